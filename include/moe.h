@@ -226,6 +226,94 @@ moe_status_t moe_layer_backward(const void* u, const void* E_gate, const void* W
                                 float* dW_shared, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* ================================================================
+ * Operators beside the layer, for the block around it and for experts of a
+ * caller's own making.  They share the conventions above except the limits:
+ * sizes need not be multiples of 64, and each operator states its own.
+ * Outputs and workspaces must not overlap any other buffer of the call unless
+ * an operator allows it.  Sums, statistics and gradients of weights are
+ * float32; every sum has a fixed order, so repeated calls give identical bits.
+ * Two calls that may run at the same time need workspaces of their own.
+ * ================================================================ */
+
+/* ---- layer norm ----
+ *   mean_t = (1/d) sum_j x_tj,  rstd_t = 1 / sqrt((1/d) sum_j (x_tj - mean_t)^2 + eps)
+ *   y_tj   = (x_tj - mean_t) rstd_t weight_j + bias_j
+ *   x [T][d] dtype, weight [d] dtype or NULL (ones), bias [d] dtype or NULL (zeros),
+ *   y [T][d] dtype, mean [T] and rstd [T] float32 or NULL (the backward needs both).
+ * Any T >= 0 and d >= 1. */
+moe_status_t moe_layer_norm(const void* x, const void* weight, const void* bias, int T, int d,
+                            float eps, int dtype, void* y, float* mean, float* rstd,
+                            void* stream);
+
+/* Gradients of sum_t dy_t . y_t (xh = (x - mean) rstd, g = dy weight):
+ *   dx = rstd (g - mean_j(g) - xh mean_j(g xh))   [T][d] dtype
+ *   dweight = sum_t dy xh, dbias = sum_t dy       [d] float32, each may be NULL
+ * mean and rstd are the forward's.  T = 0 writes nothing.  The workspace is
+ * needed where dweight or dbias is given. */
+moe_status_t moe_layer_norm_backward_workspace_size(int T, int d, int dtype, size_t* bytes);
+moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* weight,
+                                     const float* mean, const float* rstd, int T, int d, int dtype,
+                                     void* dx, float* dweight, float* dbias, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* ---- products grouped by expert, ragged ----
+ * E groups of rows, group e being rows offsets[e] .. offsets[e+1] - 1 (what
+ * moe_dispatch writes, or any non-decreasing int32 sequence in [0, M], on the
+ * device):
+ *   y[r] = w[e] x[r]     for every row r of group e
+ *   x [M][k] dtype, w [E][n][k] dtype, y [M][n] dtype.
+ * Groups may be empty.  Rows outside every group (before offsets[0], from
+ * offsets[E] on) are not read; their y is zero with zero_rest != 0 and left as
+ * it was with zero_rest == 0.  Offsets outside [0, M] are clamped into it, and
+ * one below its predecessor counts as equal to it.
+ * bfloat16: exact products, float32 sums, one rounding.  float32: products of
+ * two-float16 splits (float32 accuracy; each row of x and w is scaled on its
+ * own, so rows may differ by any factor).
+ * Limits: 1 <= E <= 1024; n, k <= 2^20. */
+moe_status_t moe_grouped_matmul_workspace_size(int M, int E, int n, int k, int dtype,
+                                               size_t* bytes);
+moe_status_t moe_grouped_matmul(const void* x, const void* w, const int32_t* offsets, int M, int E,
+                                int n, int k, int dtype, int zero_rest, void* y, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Gradients of sum_r dy_r . y_r:
+ *   dx[r] = w[e]^T dy[r]                       [M][k] dtype, may be NULL
+ *   dw[e] = sum over e's rows of dy[r] x[r]^T  [E][n][k] float32, may be NULL
+ * (not both NULL).  A group without rows gets a zero dw, M = 0 included; dx
+ * outside the groups as y above.  x may be NULL without dw, w without dx.
+ * float32: w is scaled per expert, and the rows of dy and x so that each
+ * row's product carries one scale: what lies 2^-40 below the largest value of
+ * an expert's w (the largest product of the call for dw) is lost. */
+moe_status_t moe_grouped_matmul_backward_workspace_size(int M, int E, int n, int k, int dtype,
+                                                        int want_dx, int want_dw, size_t* bytes);
+moe_status_t moe_grouped_matmul_backward(const void* x, const void* w, const int32_t* offsets,
+                                         const void* dy, int M, int E, int n, int k, int dtype,
+                                         int zero_rest, void* dx, float* dw, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* ---- orthogonalised update ----
+ * Newton-Schulz products on B matrices G [m][n], the update that the Muon
+ * optimiser makes of a weight matrix's gradient (or momentum):
+ *   X = G / (|G|_F + eps);  steps times: X <- (a I + b A + c A^2) X, A = X X^T
+ * (with m > n the same on the columns' side: A = X^T X, X <- X (a I + ..)).
+ *   x    matrix i at element i * x_stride, rows contiguous, dtype
+ *   out  matrix i at element i * out_stride, rows contiguous, out_dtype;
+ *        may be x itself (same strides and dtype)
+ * so that one call takes, say, W_down's gradients out of the blocks that
+ * moe_layer_backward wrote (x + 2*I*d with x_stride = 3*I*d).  Strides matter
+ * for B > 1 only and keep every matrix 16-byte aligned unless they are m * n.
+ * Arithmetic of float32 accuracy whatever the types; a zero matrix stays zero.
+ * Limits: B <= 65535; m, n <= 2^20; 0 <= steps <= 64; coefficients whose
+ * polynomial keeps the iterate's singular values below 32 and the factor
+ * a + b s^2 + c s^4 below 1024 (the usual a, b, c = 3.4445, -4.7750, 2.0315
+ * stay below 1.3 and 3.5). */
+moe_status_t moe_orthogonalize_workspace_size(int B, int m, int n, size_t* bytes);
+moe_status_t moe_orthogonalize(const void* x, int64_t x_stride, int B, int m, int n, int dtype,
+                               int steps, float eps, float a, float b, float c, void* out,
+                               int64_t out_stride, int out_dtype, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* ---- per-stage timing (for profiling; off by default) ----
  * When enabled, moe_layer_forward records a HIP event pair around each of its
  * kernel stages on the stream it was given.  moe_timing_read() waits for

@@ -1,0 +1,597 @@
+// Products grouped by expert with ragged sizes (gfx950), the products of an
+// expert FFN (DeepSeekMoE paper summary, papercache.org, sec. 3.2: each token
+// goes through its experts' matrices) for experts of a caller's own making:
+//
+//   forward   y[r]  = w[e] x[r]                  offsets[e] <= r < offsets[e+1]
+//   backward  dx[r] = w[e]^T dy[r],  dw[e] = sum of dy[r] x[r]^T over e's rows
+//
+// One launch covers every group: each block derives the tile table from the
+// offsets in LDS (clamped into [0, M] and made non-decreasing, so any offsets
+// stay inside the buffers and no row belongs to two groups) and takes its share
+// of the tiles.  The groups need no padding between them: an m-tile ends at its
+// group's last row, and the weight gradient's contraction over a group's rows
+// ends there by a bounded buffer range.
+//
+// bfloat16 operands are read where they are (the transposed products through
+// transposing LDS reads); float32 operands are first written as two float16
+// each (tile_gemm.h), with a power-of-two scale per row of x, dy and, in the
+// forward, w; per expert for w in the backward, whose product contracts over
+// w's rows; and for x in the weight gradient, which contracts over the rows of
+// both, the scale that makes each row's product scale the same.
+#include <algorithm>
+
+#include "ops_internal.h"
+#include "tile_gemm.h"
+
+namespace moe {
+namespace {
+
+enum : int { GR_FWD = 0, GR_DX = 1, GR_DW = 2 };
+
+// ---------------------------------------------------------------- groups
+// Offsets into s_off[0..E], clamped and non-decreasing, and the exclusive
+// prefix of tiles per group into s_tab[0..E] (dir: which product; bm, bn: its
+// tile).  All threads of the block.
+struct GroupDims {
+  int M, E, n, k;
+};
+template <int DIR>
+__device__ __forceinline__ int group_tiles(const GroupDims& g, int rows, int bm, int bn) {
+  if (DIR == GR_DW) return ((g.n + bm - 1) / bm) * ((g.k + bn - 1) / bn);
+  return ((rows + bm - 1) / bm) * (((DIR == GR_FWD ? g.n : g.k) + bn - 1) / bn);
+}
+template <int DIR>
+__device__ __forceinline__ void group_tables(const GroupDims& g, const int32_t* __restrict__ offsets,
+                                             int bm, int bn, int* s_off, int* s_tab) {
+  for (int i = threadIdx.x; i <= g.E; i += blockDim.x) s_off[i] = min(max(offsets[i], 0), g.M);
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int top = s_off[0], carry = 0;
+    for (int b = 0; b < g.E; b += 64) {
+      const int e = b + lane;
+      int hi = e < g.E ? s_off[e + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(hi, o);
+        if (lane >= o) hi = max(hi, y);
+      }
+      hi = max(hi, top);
+      const int up = __shfl_up(hi, 1);
+      const int lo = lane == 0 ? top : up;
+      const int t = e < g.E ? group_tiles<DIR>(g, hi - lo, bm, bn) : 0;
+      int inc = t;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (e < g.E) {
+        s_off[e + 1] = hi;
+        s_tab[e] = carry + inc - t;
+      }
+      carry += __shfl(inc, 63);
+      top = __shfl(hi, 63);
+    }
+    if (lane == 0) s_tab[g.E] = carry;
+  }
+  __syncthreads();
+}
+
+// The group of tile L: the last one whose first tile is at or before L.
+__device__ __forceinline__ int group_of_tile(const int* s_tab, int E, int L) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_tab[mid] <= L) lo = mid; else hi = mid - 1;
+  }
+  return uni(lo);
+}
+
+// Zeros into the rows [0, first) and [last, M) of out, this block's share.
+template <class T>
+__device__ __forceinline__ void zero_rows(T* out, int M, int width, int first, int last) {
+  const long long n0 = (long long)first * width, n1 = (long long)(M - last) * width;
+  T* tail = out + (long long)last * width;
+  const long long stride = (long long)gridDim.x * blockDim.x;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n0 + n1; i += stride)
+    (i < n0 ? out + i : tail + (i - n0))[0] = T(0);
+}
+
+// ---------------------------------------------------------------- the product
+struct GroupedProduct {
+  const uint8_t* A;        // x or dy (rows of the groups)
+  const uint8_t* B;        // w (forward, dx) or x (weight gradient)
+  uint32_t pitch_a, pitch_b;
+  const int32_t* offsets;
+  void* out;
+  const int32_t* ea;       // float32: exponents of A's rows, and of
+  const int32_t* eb;       //   w's rows (forward), experts (dx), the weight gradient's sum
+  GroupDims g;
+  int zero_rest;
+};
+
+template <class C, int DIR>
+struct GroupedTiles {
+  const GroupedProduct& p;
+  const int* s_off;
+  const int* s_tab;
+
+  struct Tile {
+    TgOperand A, B;
+    int m0, n0, steps, e, row0, rows;
+  };
+  __device__ __forceinline__ Tile tile(int L) const {
+    Tile t;
+    const GroupDims& g = p.g;
+    t.e = group_of_tile(s_tab, g.E, L);
+    t.row0 = uni(s_off[t.e]);
+    t.rows = uni(s_off[t.e + 1]) - t.row0;
+    const int local = L - uni(s_tab[t.e]);
+    const int mt = ((DIR == GR_DW ? g.n : t.rows) + C::BM - 1) / C::BM;
+    t.m0 = local % mt * C::BM;
+    t.n0 = local / mt * C::BN;
+    t.A.p = p.A + (size_t)t.row0 * p.pitch_a;
+    t.A.pitch = p.pitch_a;
+    t.A.rows = t.rows;
+    t.A.width = (g.n + 31) & ~31;
+    t.B.pitch = p.pitch_b;
+    if (DIR == GR_DW) {
+      t.B.p = p.B + (size_t)t.row0 * p.pitch_b;
+      t.B.rows = t.rows;
+      t.B.width = (g.k + 31) & ~31;
+      t.steps = (t.rows + C::KS - 1) / C::KS;
+    } else {
+      t.B.p = p.B + (size_t)t.e * g.n * p.pitch_b;
+      t.B.rows = g.n;
+      t.B.width = (g.k + 31) & ~31;
+      t.steps = ((DIR == GR_FWD ? g.k : g.n) + C::KS - 1) / C::KS;
+    }
+    if (!C::SPLIT) {  // a bfloat16 row holds what its pitch says
+      t.A.width = min(t.A.width, (int)(p.pitch_a / 2));
+      t.B.width = min(t.B.width, (int)(p.pitch_b / 2));
+    }
+    return t;
+  }
+
+  __device__ __forceinline__ void store(const Tile& t, int wm, int wn, int lane,
+                                        f32x16 (&acc)[C::FM][C::FN]) const {
+    const GroupDims& g = p.g;
+    if constexpr (DIR == GR_DW) {
+      float* out = (float*)p.out + (size_t)t.e * g.n * g.k;
+      const int ex = C::SPLIT ? -p.eb[0] : 0;
+#pragma unroll
+      for (int fm = 0; fm < C::FM; ++fm)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int m = t.m0 + tg_row<C>(wm, fm, lane, r);
+          if (m >= g.n) continue;
+#pragma unroll
+          for (int fn = 0; fn < C::FN; ++fn) {
+            const int n = t.n0 + tg_col<C>(wn, fn, lane, r);
+            if (n < g.k) {
+              const float v = acc[fm][fn][r];
+              out[(size_t)m * g.k + n] = C::SPLIT ? ldexpf(v, ex) : v;
+            }
+          }
+        }
+    } else {
+      // a lane holds four consecutive columns of one row
+      const int N = DIR == GR_FWD ? g.n : g.k;
+      const bool vec = N % 4 == 0;
+#pragma unroll
+      for (int fm = 0; fm < C::FM; ++fm) {
+        const int m = t.m0 + tg_row<C>(wm, fm, lane, 0);
+        if (m >= t.rows) continue;
+        const int ea = C::SPLIT ? p.ea[t.row0 + m] + (DIR == GR_DX ? p.eb[t.e] : 0) : 0;
+#pragma unroll
+        for (int fn = 0; fn < C::FN; ++fn)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = t.n0 + tg_col<C>(wn, fn, lane, 4 * q);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[e] = acc[fm][fn][4 * q + e];
+              if (C::SPLIT && n + e < N)
+                v[e] = ldexpf(v[e], -ea - (DIR == GR_FWD ? p.eb[(size_t)t.e * g.n + n + e] : 0));
+            }
+            if constexpr (C::SPLIT) {
+              float* c = (float*)p.out + (size_t)(t.row0 + m) * N + n;
+              if (vec) {
+                if (n < N) *(f32x4*)c = f32x4{v[0], v[1], v[2], v[3]};
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (n + e < N) c[e] = v[e];
+              }
+            } else {
+              uint16_t* c = (uint16_t*)p.out + (size_t)(t.row0 + m) * N + n;
+              if (vec) {
+                if (n < N) *(uint2*)c = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (n + e < N) c[e] = f32_to_bf16(v[e]);
+              }
+            }
+          }
+      }
+    }
+  }
+};
+
+template <class C, int DIR>
+__global__ __launch_bounds__(kTgThreads, C::SLOT > 32768 ? 2 : 4) void grouped_kernel(
+    GroupedProduct p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[C::SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[C::SLOT];
+  __shared__ int s_off[kGroupedMaxE + 1], s_tab[kGroupedMaxE + 1];
+  group_tables<DIR>(p.g, p.offsets, C::BM, C::BN, s_off, s_tab);
+  if (DIR != GR_DW && p.zero_rest) {
+    if (C::SPLIT) zero_rows((float*)p.out, p.g.M, DIR == GR_FWD ? p.g.n : p.g.k, s_off[0], s_off[p.g.E]);
+    else zero_rows((uint16_t*)p.out, p.g.M, DIR == GR_FWD ? p.g.n : p.g.k, s_off[0], s_off[p.g.E]);
+  }
+  const GroupedTiles<C, DIR> tiles{p, s_off, s_tab};
+  const TgShare sh = tg_share(uni(s_tab[p.g.E]));
+  tg_run<C>(tiles, sh.start, sh.end, sh.stride, lds0, lds1);
+}
+
+// ---------------------------------------------------------------- operand preparation
+// Exponent that brings a largest magnitude to [2^13, 2^14); `none` if all is zero.
+__device__ __forceinline__ int split_exponent(float most, int none = 0) {
+  return most > 0.f ? 13 - ilogbf(most) : none;
+}
+// The weight gradient's mark of a dy row that is all zero.
+constexpr int kNoRow = -(1 << 20);
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor(v, k));
+  return v;
+}
+
+// Writes one float32 row of `width` values as split units, scaled by 2^ex, zeros
+// in the padding.  One wavefront; lane l takes the pairs of elements 2l + 128 i.
+__device__ __forceinline__ void split_row(const float* __restrict__ src, int width, int ex,
+                                          uint8_t* __restrict__ dst, int lane) {
+  const int padded = (width + 31) & ~31;
+  for (int j = 2 * lane; j < padded; j += 128) {
+    uint16_t h[2], l[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      split_f16(j + e < width ? ldexpf(src[j + e], ex) : 0.f, h[e], l[e]);
+    uint8_t* d = dst + split_at(j);
+    *(uint32_t*)d = h[0] | ((uint32_t)h[1] << 16);
+    *(uint32_t*)(d + 64) = l[0] | ((uint32_t)l[1] << 16);
+  }
+}
+
+// Rows with a scale of their own: four rows per block.
+__global__ __launch_bounds__(256) void split_rows_kernel(const float* __restrict__ src,
+                                                         long long rows, int width,
+                                                         uint8_t* __restrict__ dst, uint32_t pitch,
+                                                         int32_t* __restrict__ ex, int none) {
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (r >= rows) return;
+  const float* s = src + r * width;
+  float m = 0.f;
+  for (int j = lane; j < width; j += 64) m = fmaxf(m, fabsf(s[j]));
+  const int e = split_exponent(wave_max(m), none);
+  if (lane == 0) ex[r] = e;
+  split_row(s, width, e == none ? 0 : e, dst + r * pitch, lane);
+}
+
+// w by expert: partial maxima of kMaxChunks row ranges per expert, then the rows
+// with their expert's scale.
+constexpr int kMaxChunks = 32;
+__global__ __launch_bounds__(256) void expert_max_kernel(const float* __restrict__ w, long long per,
+                                                         float* __restrict__ part) {
+  __shared__ float s[4];
+  const float* src = w + (long long)blockIdx.y * per;
+  const long long a = per * blockIdx.x / kMaxChunks, b = per * (blockIdx.x + 1) / kMaxChunks;
+  float m = 0.f;
+  for (long long i = a + threadIdx.x; i < b; i += 256) m = fmaxf(m, fabsf(src[i]));
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    part[blockIdx.y * kMaxChunks + blockIdx.x] = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+}
+__global__ __launch_bounds__(256) void split_experts_kernel(const float* __restrict__ w, int n,
+                                                            int k, long long rows,
+                                                            const float* __restrict__ part,
+                                                            uint8_t* __restrict__ dst,
+                                                            uint32_t pitch,
+                                                            int32_t* __restrict__ ex) {
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (r >= rows) return;
+  const int e = (int)(r / n);
+  const int x = split_exponent(wave_max(part[e * kMaxChunks + lane % kMaxChunks]));
+  if (lane == 0 && r % n == 0) ex[e] = x;
+  split_row(w + r * k, k, x, dst + r * pitch, lane);
+}
+
+// x for the weight gradient: row r is scaled by 2^(C - a_r), a_r the exponent of
+// dy's row r, so that every product of row r carries 2^C.  C brings the largest
+// of all rows into range: partial maxima of ilogb(x row) - a_r over the rows of
+// the groups (rows outside them are not read), then C = 13 - the largest.  Rows
+// whose dy is zero contribute nothing and are written as zeros.
+constexpr int kRowParts = 256;
+__device__ __forceinline__ void group_span(const int32_t* __restrict__ offsets, int E, int M,
+                                           int lane, int& first, int& last) {
+  int hi = 0;
+  for (int e = lane; e <= E; e += 64) hi = max(hi, min(max(offsets[e], 0), M));
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) hi = max(hi, __shfl_xor(hi, k));
+  first = min(max(offsets[0], 0), M);
+  last = max(hi, first);
+}
+__global__ __launch_bounds__(256) void pair_max_kernel(const float* __restrict__ x, int width,
+                                                       const int32_t* __restrict__ offsets, int E,
+                                                       int M, const int32_t* __restrict__ ea,
+                                                       int32_t* __restrict__ part) {
+  __shared__ int s[4];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int first, last, most = kNoRow;
+  group_span(offsets, E, M, lane, first, last);
+  for (long long r = first + blockIdx.x * 4 + w; r < last; r += 4 * kRowParts) {
+    float m = 0.f;
+    for (int j = lane; j < width; j += 64) m = fmaxf(m, fabsf(x[r * width + j]));
+    m = wave_max(m);
+    if (m > 0.f && ea[r] != kNoRow) most = max(most, ilogbf(m) - ea[r]);
+  }
+  if (lane == 0) s[w] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) part[blockIdx.x] = max(max(s[0], s[1]), max(s[2], s[3]));
+}
+__global__ __launch_bounds__(256) void split_pair_kernel(const float* __restrict__ x, int width,
+                                                         const int32_t* __restrict__ offsets, int E,
+                                                         int M, const int32_t* __restrict__ ea,
+                                                         const int32_t* __restrict__ part,
+                                                         uint8_t* __restrict__ dst, uint32_t pitch,
+                                                         int32_t* __restrict__ ex) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int first, last, most = kNoRow;
+  for (int i = lane; i < kRowParts; i += 64) most = max(most, part[i]);
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) most = max(most, __shfl_xor(most, k));
+  const int C = most == kNoRow ? 0 : 13 - most;
+  if (blockIdx.x == 0 && threadIdx.x == 0) ex[0] = C;
+  group_span(offsets, E, M, lane, first, last);
+  const long long r = first + (long long)blockIdx.x * 4 + w;
+  if (r >= last) return;
+  if (ea[r] != kNoRow) {
+    split_row(x + r * width, width, C - ea[r], dst + r * pitch, lane);
+  } else {
+    for (uint32_t b = 4 * lane; b < pitch; b += 256) *(uint32_t*)(dst + r * pitch + b) = 0;
+  }
+}
+
+// bfloat16 rows whose length does not suit the loads, copied into rows of whole
+// 128-byte units with zeros behind the last element.
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src,
+                                                       long long rows, int width,
+                                                       uint8_t* __restrict__ dst, uint32_t pitch) {
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (r >= rows) return;
+  const uint16_t* s = src + r * width;
+  for (int j = 2 * lane; j < (int)(pitch / 2); j += 128) {
+    const uint32_t a = j < width ? s[j] : 0, b = j + 1 < width ? s[j + 1] : 0;
+    *(uint32_t*)(dst + r * pitch + 2 * j) = a | (b << 16);
+  }
+}
+
+// ---------------------------------------------------------------- launch
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Carve {
+  uint8_t* base;
+  size_t at = 0;
+  uint8_t* take(size_t bytes) {
+    uint8_t* p = base != nullptr ? base + at : nullptr;
+    at = up256(at + bytes);
+    return p;
+  }
+};
+
+uint32_t pad_pitch(int n) { return (uint32_t)((n + 63) / 64 * 128); }
+
+// Tiles of 256 where they give every CU one; else 128 (a quarter of the work per
+// tile, two blocks per CU).
+bool tiles_128(int dir, const GroupedArgs& a) {
+  const long long per = std::max(1LL, ((long long)a.M + a.E - 1) / a.E);
+  auto ct = [](long long x, long long b) { return (x + b - 1) / b; };
+  const long long t = dir == GR_DW ? ct(a.n, 256) * ct(a.k, 256) * a.E
+                                   : ct(per, 256) * a.E * ct(dir == GR_FWD ? a.n : a.k, 256);
+  return t < device_cu_count() || (dir != GR_DW && per <= 128);
+}
+
+template <class C, int DIR>
+hipError_t run_product(const GroupedProduct& p, hipStream_t st) {
+  auto ct = [](long long x, long long b) { return (x + b - 1) / b; };
+  const GroupDims& g = p.g;
+  const long long most =
+      DIR == GR_DW ? g.E * ct(g.n, C::BM) * ct(g.k, C::BN)
+                   : (ct(g.M, C::BM) + g.E) * ct(DIR == GR_FWD ? g.n : g.k, C::BN);
+  const long long blocks = (long long)device_cu_count() * (C::SLOT > 32768 ? 1 : 2);
+  grouped_kernel<C, DIR><<<(unsigned)std::max(1LL, std::min(most, blocks)), kTgThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <int DIR, bool SPLIT>
+hipError_t pick_product(const GroupedArgs& a, const GroupedProduct& p, hipStream_t st) {
+  constexpr bool AC = DIR == GR_DW, BC = DIR != GR_FWD, SW = DIR != GR_DW;
+  if (tiles_128(DIR, a)) return run_product<TgConfig<1, 2, AC, BC, SPLIT, SW>, DIR>(p, st);
+  return run_product<TgConfig<2, 4, AC, BC, SPLIT, SW>, DIR>(p, st);
+}
+
+unsigned row_blocks(long long rows) { return (unsigned)((rows + 3) / 4); }
+
+// The workspace's regions: which are needed, and where they lie.
+struct GroupedPlan {
+  uint8_t *x = nullptr, *w = nullptr, *dy = nullptr;        // prepared operands
+  int32_t *ex = nullptr, *ew = nullptr, *ey = nullptr;      // exponents
+  int32_t* parts = nullptr;
+  float* wmax = nullptr;
+  size_t bytes = 0;
+};
+GroupedPlan plan_forward(int dtype, int M, int E, int n, int k, void* ws) {
+  GroupedPlan p;
+  Carve c{(uint8_t*)ws};
+  if (dtype == 0) {
+    p.x = c.take((size_t)M * split_pitch(k));
+    p.w = c.take((size_t)E * n * split_pitch(k));
+    p.ex = (int32_t*)c.take((size_t)M * 4);
+    p.ew = (int32_t*)c.take((size_t)E * n * 4);
+  } else if (k % 64 != 0) {
+    p.x = c.take((size_t)M * pad_pitch(k));
+    p.w = c.take((size_t)E * n * pad_pitch(k));
+  }
+  p.bytes = c.at;
+  return p;
+}
+GroupedPlan plan_backward(int dtype, int M, int E, int n, int k, bool dx, bool dw, void* ws) {
+  GroupedPlan p;
+  Carve c{(uint8_t*)ws};
+  if (dtype == 0) {
+    p.dy = c.take((size_t)M * split_pitch(n));
+    p.ey = (int32_t*)c.take((size_t)M * 4);
+    if (dx) {
+      p.w = c.take((size_t)E * n * split_pitch(k));
+      p.ew = (int32_t*)c.take((size_t)E * 4);
+      p.wmax = (float*)c.take((size_t)E * kMaxChunks * 4);
+    }
+    if (dw) {
+      p.x = c.take((size_t)M * split_pitch(k));
+      p.ex = (int32_t*)c.take(4);
+      p.parts = (int32_t*)c.take(kRowParts * 4);
+    }
+  } else {
+    if (n % (dx ? 64 : 8) != 0) p.dy = c.take((size_t)M * pad_pitch(n));
+    if (dx && k % 8 != 0) p.w = c.take((size_t)E * n * pad_pitch(k));
+    if (dw && k % 8 != 0) p.x = c.take((size_t)M * pad_pitch(k));
+  }
+  p.bytes = c.at;
+  return p;
+}
+
+}  // namespace
+
+int device_cu_count() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) == hipSuccess &&
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess &&
+      cus > 0)
+    return cus;
+  return 256;
+}
+
+size_t grouped_workspace_bytes(int dtype, int M, int E, int n, int k) {
+  return plan_forward(dtype, M, E, n, k, nullptr).bytes;
+}
+size_t grouped_backward_workspace_bytes(int dtype, int M, int E, int n, int k, bool dx, bool dw) {
+  return plan_backward(dtype, M, E, n, k, dx, dw, nullptr).bytes;
+}
+
+hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t st) {
+  const GroupedPlan w = plan_forward(dtype, a.M, a.E, a.n, a.k, ws);
+  GroupedProduct p{};
+  p.A = (const uint8_t*)a.x;
+  p.B = (const uint8_t*)a.w;
+  p.pitch_a = p.pitch_b = (uint32_t)a.k * 2;
+  p.offsets = a.offsets;
+  p.out = a.y;
+  p.g = GroupDims{a.M, a.E, a.n, a.k};
+  p.zero_rest = a.zero_rest;
+  const long long wr = (long long)a.E * a.n;
+  if (dtype == 0) {
+    p.pitch_a = p.pitch_b = (uint32_t)split_pitch(a.k);
+    split_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const float*)a.x, a.M, a.k, w.x, p.pitch_a, w.ex, 0);
+    split_rows_kernel<<<row_blocks(wr), 256, 0, st>>>((const float*)a.w, wr, a.k, w.w, p.pitch_b, w.ew, 0);
+    p.A = w.x;
+    p.B = w.w;
+    p.ea = w.ex;
+    p.eb = w.ew;
+    return pick_product<GR_FWD, true>(a, p, st);
+  }
+  if (w.x != nullptr) {
+    p.pitch_a = p.pitch_b = pad_pitch(a.k);
+    pad_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const uint16_t*)a.x, a.M, a.k, w.x, p.pitch_a);
+    pad_rows_kernel<<<row_blocks(wr), 256, 0, st>>>((const uint16_t*)a.w, wr, a.k, w.w, p.pitch_b);
+    p.A = w.x;
+    p.B = w.w;
+  }
+  return pick_product<GR_FWD, false>(a, p, st);
+}
+
+hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hipStream_t st) {
+  const bool dx = a.dx != nullptr, dw = a.dw != nullptr;
+  const GroupedPlan w = plan_backward(dtype, a.M, a.E, a.n, a.k, dx, dw, ws);
+  const long long wr = (long long)a.E * a.n;
+  GroupedProduct p{};
+  p.offsets = a.offsets;
+  p.g = GroupDims{a.M, a.E, a.n, a.k};
+  p.zero_rest = a.zero_rest;
+  const uint8_t *x = (const uint8_t*)a.x, *wt = (const uint8_t*)a.w, *dy = (const uint8_t*)a.dy;
+  uint32_t px = a.k * 2, pw = a.k * 2, py = a.n * 2;
+  if (dtype == 0) {
+    px = pw = (uint32_t)split_pitch(a.k);
+    py = (uint32_t)split_pitch(a.n);
+    if (a.M > 0)
+      split_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const float*)a.dy, a.M, a.n, w.dy, py, w.ey, kNoRow);
+    dy = w.dy;
+    if (dx) {
+      expert_max_kernel<<<dim3(kMaxChunks, a.E), 256, 0, st>>>((const float*)a.w, (long long)a.n * a.k, w.wmax);
+      split_experts_kernel<<<row_blocks(wr), 256, 0, st>>>((const float*)a.w, a.n, a.k, wr, w.wmax, w.w, pw, w.ew);
+      wt = w.w;
+    }
+    if (dw) {
+      pair_max_kernel<<<kRowParts, 256, 0, st>>>((const float*)a.x, a.k, a.offsets, a.E, a.M, w.ey, w.parts);
+      split_pair_kernel<<<std::max(1u, row_blocks(a.M)), 256, 0, st>>>((const float*)a.x, a.k, a.offsets, a.E, a.M,
+                                                        w.ey, w.parts, w.x, px, w.ex);
+      x = w.x;
+    }
+  } else {
+    if (w.dy != nullptr && a.M > 0) {
+      py = pad_pitch(a.n);
+      pad_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const uint16_t*)a.dy, a.M, a.n, w.dy, py);
+      dy = w.dy;
+    }
+    if (w.w != nullptr) {
+      pw = pad_pitch(a.k);
+      pad_rows_kernel<<<row_blocks(wr), 256, 0, st>>>((const uint16_t*)a.w, wr, a.k, w.w, pw);
+      wt = w.w;
+    }
+    if (w.x != nullptr && a.M > 0) {
+      px = pad_pitch(a.k);
+      pad_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const uint16_t*)a.x, a.M, a.k, w.x, px);
+      x = w.x;
+    }
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  p.A = dy;
+  p.pitch_a = py;
+  p.ea = w.ey;
+  if (dx && a.M > 0) {
+    p.B = wt;
+    p.pitch_b = pw;
+    p.eb = w.ew;
+    p.out = a.dx;
+    e = dtype == 0 ? pick_product<GR_DX, true>(a, p, st) : pick_product<GR_DX, false>(a, p, st);
+    if (e != hipSuccess) return e;
+  }
+  if (dw) {
+    p.B = x;
+    p.pitch_b = px;
+    p.eb = w.ex;
+    p.out = a.dw;
+    e = dtype == 0 ? pick_product<GR_DW, true>(a, p, st) : pick_product<GR_DW, false>(a, p, st);
+  }
+  return e;
+}
+
+}  // namespace moe

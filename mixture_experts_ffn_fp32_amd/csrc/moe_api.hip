@@ -10,6 +10,7 @@
 
 #include "moe.h"
 #include "moe_internal.h"
+#include "ops_internal.h"
 
 namespace {
 
@@ -457,6 +458,7 @@ hipError_t scratch_of_device(char** out) {
 }  // namespace
 
 namespace moe {
+void set_last_error(const char* msg) { g_err = msg; }
 LaunchEvents stage_launch_events() {
   if (!g_scope.active) return LaunchEvents{nullptr, nullptr};
   const LaunchEvents ev{g_scope.launched ? nullptr : g_scope.a, g_scope.b};

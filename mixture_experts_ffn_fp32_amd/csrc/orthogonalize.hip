@@ -1,0 +1,429 @@
+// Orthogonalised update of weight gradients by Newton-Schulz products (gfx950),
+// as the Muon optimiser applies it to each matrix parameter, here to every
+// expert's block of the layer's weight gradients (DeepSeekMoE paper summary,
+// papercache.org, sec. 3.2: W_gate, W_up, W_down per expert) in one call:
+//
+//   X_0 = G / (|G|_F + eps),  then `steps` times
+//   A = X X^T,  P = a I + b A + c A^2,  X <- P X     (A = X^T X, X <- X P where
+//                                                     G has more rows than columns)
+//
+// p(s) = a s + b s^3 + c s^5 acts on each singular value and drives it towards
+// 1.  Bound by the matrix products: per step p^2 q + p^3 + 2 p^2 q flops (p the
+// smaller side; A and A^2 are symmetric, so only tiles on and above the diagonal
+// are computed and each is written to both places).
+//
+// Errors of an early step grow with the singular values they fall on (a factor
+// of up to a per step), so single bfloat16 or float16 products lose what a
+// float32 gradient holds.  X, A and P are kept as two float16 per value
+// (tile_gemm.h) at fixed power-of-two scales that follow from bounds of p over
+// the steps: float32 accuracy at three float16 products, and each product's
+// epilogue writes the next one's operand directly.  The norm is summed in
+// float64 (squares of small gradients leave float32's range).
+#include <math.h>
+
+#include <algorithm>
+
+#include "ops_internal.h"
+#include "tile_gemm.h"
+
+namespace moe {
+namespace {
+
+enum : int { NS_GRAM = 0, NS_POLY = 1, NS_APPLY = 2 };
+constexpr int kNormParts = 64;  // partial norms per matrix
+
+struct NsProduct {
+  const uint8_t* A;
+  const uint8_t* B;
+  const uint8_t* G;        // POLY: A at the output's place
+  uint8_t* out;            // split rows
+  void* last;              // APPLY, last step: the result instead
+  long long stride_a, stride_b, stride_out, stride_last;  // bytes (last: elements) per matrix
+  uint32_t pitch_a, pitch_b, pitch_out;
+  int rows_a, rows_b;      // rows of the operands as they are stored
+  int width_a, width_b;    // their padded widths (column layout)
+  int M, N, K;             // output rows and columns, contraction
+  int last_dtype;
+  int count;               // matrices
+  float scale;             // of the accumulators
+  float ca, cb, cc;        // POLY: acc * scale * cc + G * cb (+ ca on the diagonal)
+};
+
+template <class C, int KIND>
+struct NsTiles {
+  const NsProduct& p;
+  struct Tile {
+    TgOperand A, B;
+    int m0, n0, steps, i;
+  };
+  static constexpr bool SYM = KIND != NS_APPLY;
+
+  __device__ __forceinline__ int per_matrix() const {
+    const int mt = (p.M + C::BM - 1) / C::BM;
+    return SYM ? mt * (mt + 1) / 2 : mt * ((p.N + C::BN - 1) / C::BN);
+  }
+  __device__ __forceinline__ Tile tile(int L) const {
+    Tile t;
+    const int per = per_matrix(), mt = (p.M + C::BM - 1) / C::BM;
+    t.i = L / per;
+    int local = L - t.i * per;
+    if (SYM) {  // row y of the upper triangle starts at tile y mt - y (y - 1) / 2
+      int y = 0;
+      while (local >= mt - y) {
+        local -= mt - y;
+        ++y;
+      }
+      t.m0 = y * C::BM;
+      t.n0 = (y + local) * C::BN;
+    } else {
+      t.m0 = local % mt * C::BM;
+      t.n0 = local / mt * C::BN;
+    }
+    t.A.p = p.A + (size_t)t.i * p.stride_a;
+    t.A.pitch = p.pitch_a;
+    t.A.rows = p.rows_a;
+    t.A.width = p.width_a;
+    t.B.p = p.B + (size_t)t.i * p.stride_b;
+    t.B.pitch = p.pitch_b;
+    t.B.rows = p.rows_b;
+    t.B.width = p.width_b;
+    t.steps = (p.K + C::KS - 1) / C::KS;
+    return t;
+  }
+
+  __device__ __forceinline__ void store(const Tile& t, int wm, int wn, int lane,
+                                        f32x16 (&acc)[C::FM][C::FN]) const {
+    uint8_t* out = p.out + (size_t)t.i * p.stride_out;
+    const int wide = (p.N + 31) & ~31;  // columns of an output row with its padding
+    if constexpr (SYM) {
+      // a lane holds four consecutive rows m .. m + 3 of one column n: written
+      // there, and (off the diagonal tiles) as columns m .. m + 3 of row n
+      const uint8_t* G = KIND == NS_POLY ? p.G + (size_t)t.i * p.stride_out : nullptr;
+#pragma unroll
+      for (int fm = 0; fm < C::FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < C::FN; ++fn) {
+          const int n = t.n0 + tg_col<C>(wn, fn, lane, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int m = t.m0 + tg_row<C>(wm, fm, lane, 4 * q);
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float v = acc[fm][fn][4 * q + e] * p.scale;
+              if constexpr (KIND == NS_POLY) {
+                float g = 0.f;
+                if (m + e < p.M && n < p.N) {
+                  const uint8_t* at = G + (size_t)(m + e) * p.pitch_out + split_at(n);
+                  g = f16_to_f32(*(const uint16_t*)at) + f16_to_f32(*(const uint16_t*)(at + 64));
+                }
+                v = p.cc * v + p.cb * g + (m + e == n ? p.ca : 0.f);
+              }
+              if (m + e >= p.M || n >= p.N) v = 0.f;
+              split_f16(v, hi[e], lo[e]);
+              if (m + e < p.M && n < wide) {
+                uint8_t* at = out + (size_t)(m + e) * p.pitch_out + split_at(n);
+                *(uint16_t*)at = hi[e];
+                *(uint16_t*)(at + 64) = lo[e];
+              }
+            }
+            if (t.m0 != t.n0 && n < p.N && m < wide) {
+              uint8_t* at = out + (size_t)n * p.pitch_out + split_at(m);
+              *(uint2*)at = uint2{hi[0] | ((uint32_t)hi[1] << 16), hi[2] | ((uint32_t)hi[3] << 16)};
+              *(uint2*)(at + 64) =
+                  uint2{lo[0] | ((uint32_t)lo[1] << 16), lo[2] | ((uint32_t)lo[3] << 16)};
+            }
+          }
+        }
+    } else {
+      const bool vec = p.N % 4 == 0;
+#pragma unroll
+      for (int fm = 0; fm < C::FM; ++fm) {
+        const int m = t.m0 + tg_row<C>(wm, fm, lane, 0);
+        if (m >= p.M) continue;
+#pragma unroll
+        for (int fn = 0; fn < C::FN; ++fn)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = t.n0 + tg_col<C>(wn, fn, lane, 4 * q);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[fm][fn][4 * q + e] * p.scale;
+            if (p.last == nullptr) {
+              if (n >= wide) continue;
+              uint16_t hi[4], lo[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) split_f16(n + e < p.N ? v[e] : 0.f, hi[e], lo[e]);
+              uint8_t* at = out + (size_t)m * p.pitch_out + split_at(n);
+              *(uint2*)at = uint2{hi[0] | ((uint32_t)hi[1] << 16), hi[2] | ((uint32_t)hi[3] << 16)};
+              *(uint2*)(at + 64) =
+                  uint2{lo[0] | ((uint32_t)lo[1] << 16), lo[2] | ((uint32_t)lo[3] << 16)};
+            } else if (p.last_dtype == 0) {
+              float* c = (float*)p.last + (size_t)t.i * p.stride_last + (size_t)m * p.N + n;
+              if (vec) {
+                if (n < p.N) *(f32x4*)c = f32x4{v[0], v[1], v[2], v[3]};
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (n + e < p.N) c[e] = v[e];
+              }
+            } else {
+              uint16_t* c = (uint16_t*)p.last + (size_t)t.i * p.stride_last + (size_t)m * p.N + n;
+              if (vec) {
+                if (n < p.N) *(uint2*)c = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (n + e < p.N) c[e] = f32_to_bf16(v[e]);
+              }
+            }
+          }
+      }
+    }
+  }
+};
+
+template <class C, int KIND>
+__global__ __launch_bounds__(kTgThreads, C::SLOT > 32768 ? 2 : 4) void ns_kernel(NsProduct p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[C::SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[C::SLOT];
+  const NsTiles<C, KIND> tiles{p};
+  const TgShare sh = tg_share(tiles.per_matrix() * p.count);
+  tg_run<C>(tiles, sh.start, sh.end, sh.stride, lds0, lds1);
+}
+
+// ---------------------------------------------------------------- the first iterate
+// Partial sums of squares: block (part, matrix) takes the part-th share of its values.
+template <class E>
+__global__ __launch_bounds__(256) void ns_norm_kernel(const void* __restrict__ x, long long stride,
+                                                      long long per, double* __restrict__ part) {
+  __shared__ double s[4];
+  const typename E::T* src = (const typename E::T*)x + (long long)blockIdx.y * stride;
+  const long long a = per * blockIdx.x / kNormParts, b = per * (blockIdx.x + 1) / kNormParts;
+  double v = 0.0;
+  for (long long i = a + threadIdx.x; i < b; i += 256) {
+    const double f = (double)load_as_f32<E>(src + i);
+    v += f * f;
+  }
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) v += __shfl_xor(v, k);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) part[blockIdx.y * kNormParts + blockIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// X_0 in split rows (zeros in the padding), scaled by 2^ex; with `last` set (no
+// steps), X_0 itself as the result.  One wavefront per row.
+template <class E>
+__global__ __launch_bounds__(256) void ns_start_kernel(const void* __restrict__ x, long long stride,
+                                                       int m, int n, long long rows,
+                                                       const double* __restrict__ part, float eps,
+                                                       float scale, uint8_t* __restrict__ out,
+                                                       uint32_t pitch, void* last,
+                                                       long long last_stride, int last_dtype) {
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (r >= rows) return;
+  const long long i = r / m, row = r % m;
+  double sq = part[i * kNormParts + lane];
+  static_assert(kNormParts == 64, "one partial norm per lane");
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) sq += __shfl_xor(sq, k);
+  const double norm = sqrt(sq) + (double)eps;
+  // an all-zero matrix stays zero
+  const double f = norm > 0.0 ? (double)scale / norm : 0.0;
+  const typename E::T* src = (const typename E::T*)x + i * stride + row * n;
+  if (last != nullptr) {
+    for (int j = lane; j < n; j += 64) {
+      const float v = (float)((double)load_as_f32<E>(src + j) * f);
+      if (last_dtype == 0) ((float*)last)[i * last_stride + row * n + j] = v;
+      else ((uint16_t*)last)[i * last_stride + row * n + j] = f32_to_bf16(v);
+    }
+    return;
+  }
+  const int padded = (n + 31) & ~31;
+  for (int j = 2 * lane; j < padded; j += 128) {
+    uint16_t h[2], l[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      split_f16(j + e < n ? (float)((double)load_as_f32<E>(src + j + e) * f) : 0.f, h[e], l[e]);
+    uint8_t* d = out + r * pitch + split_at(j);
+    *(uint32_t*)d = h[0] | ((uint32_t)h[1] << 16);
+    *(uint32_t*)(d + 64) = l[0] | ((uint32_t)l[1] << 16);
+  }
+}
+
+// ---------------------------------------------------------------- launch
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Exponent that keeps values up to `most` (in magnitude) below 2^15.
+int scale_exponent(double most) { return 14 - (int)ceil(log2(std::max(most, 1e-30))); }
+
+struct NsPlan {
+  size_t x[2], a, p, part, bytes;
+  size_t stride_x, stride_a;
+};
+NsPlan ns_plan(int B, int m, int n) {
+  NsPlan l{};
+  const int side = std::min(m, n);
+  l.stride_x = (size_t)m * split_pitch(n);
+  l.stride_a = (size_t)side * split_pitch(side);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at = up256(at + bytes);
+    return o;
+  };
+  l.x[0] = take(l.stride_x * B);
+  l.x[1] = take(l.stride_x * B);
+  l.a = take(l.stride_a * B);
+  l.p = take(l.stride_a * B);
+  l.part = take((size_t)B * kNormParts * 8);
+  l.bytes = at;
+  return l;
+}
+
+template <class C, int KIND>
+hipError_t run_ns(const NsProduct& p, hipStream_t st) {
+  const long long mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN;
+  const long long total = (KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2) * p.count;
+  const long long blocks = (long long)device_cu_count() * (C::SLOT > 32768 ? 1 : 2);
+  ns_kernel<C, KIND><<<(unsigned)std::min(total, blocks), kTgThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
+// Tiles of 256 where they give every CU one, else 128.
+template <int KIND, bool AC, bool BC, bool SW>
+hipError_t pick_ns(const NsProduct& p, hipStream_t st) {
+  const long long mt = (p.M + 255) / 256, nt = (p.N + 255) / 256;
+  const long long total = (KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2) * p.count;
+  if (total < device_cu_count()) return run_ns<TgConfig<1, 2, AC, BC, true, SW>, KIND>(p, st);
+  return run_ns<TgConfig<2, 4, AC, BC, true, SW>, KIND>(p, st);
+}
+
+}  // namespace
+
+void ortho_bounds(int steps, float a, float b, float c, double* iterate, double* factor) {
+  double s = 1.0, top = 1.0, f = 0.0;
+  for (int k = 0; k < steps; ++k) {
+    // |p| over [0, s] and |a + b t + c t^2| over [0, s^2], at 4096 points each and
+    // padded by what lies between them
+    double next = 0.0, fac = 0.0;
+    for (int i = 0; i <= 4096; ++i) {
+      const double u = s * i / 4096.0, t = u * u;
+      const double q = (double)a + (double)b * t + (double)c * t * t;
+      fac = std::max(fac, fabs(q));
+      next = std::max(next, fabs(u * q));
+    }
+    f = std::max(f, 1.01 * fac);
+    s = 1.01 * next;
+    top = std::max(top, s);
+    if (!(top <= 1e30) || !(f <= 1e30)) break;
+  }
+  *iterate = top;
+  *factor = f;
+}
+
+size_t ortho_workspace_bytes(int B, int m, int n) { return ns_plan(B, m, n).bytes; }
+
+hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
+  const NsPlan l = ns_plan(a.B, a.m, a.n);
+  uint8_t* w = (uint8_t*)ws;
+  double* part = (double*)(w + l.part);
+  const long long per = (long long)a.m * a.n, rows = (long long)a.B * a.m;
+  double most_x, most_p;
+  ortho_bounds(a.steps, a.a, a.b, a.c, &most_x, &most_p);
+  const int ex = scale_exponent(most_x), ea = scale_exponent(most_x * most_x),
+            ep = scale_exponent(most_p);
+  const uint32_t px = (uint32_t)split_pitch(a.n), pa = (uint32_t)split_pitch(std::min(a.m, a.n));
+  const float start = a.steps == 0 ? 1.f : ldexpf(1.f, ex);
+  void* direct = a.steps == 0 ? a.out : nullptr;
+  const dim3 gn(kNormParts, a.B), gs((unsigned)((rows + 3) / 4));
+  if (a.dtype == 0) {
+    ns_norm_kernel<ElemF32><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part);
+    ns_start_kernel<ElemF32><<<gs, 256, 0, st>>>(a.x, a.x_stride, a.m, a.n, rows, part, a.eps, start,
+                                                 w + l.x[0], px, direct, a.out_stride, a.out_dtype);
+  } else {
+    ns_norm_kernel<ElemBF16><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part);
+    ns_start_kernel<ElemBF16><<<gs, 256, 0, st>>>(a.x, a.x_stride, a.m, a.n, rows, part, a.eps, start,
+                                                  w + l.x[0], px, direct, a.out_stride, a.out_dtype);
+  }
+  hipError_t e = hipGetLastError();
+  const bool tall = a.m > a.n;
+  const int side = std::min(a.m, a.n), wide_x = (a.n + 31) & ~31, wide_a = (side + 31) & ~31;
+  for (int k = 0; k < a.steps && e == hipSuccess; ++k) {
+    const uint8_t* X = w + l.x[k & 1];
+    NsProduct g{};
+    g.A = g.B = X;
+    g.out = w + l.a;
+    g.stride_a = g.stride_b = l.stride_x;
+    g.stride_out = l.stride_a;
+    g.pitch_a = g.pitch_b = px;
+    g.pitch_out = pa;
+    g.rows_a = g.rows_b = a.m;
+    g.width_a = g.width_b = wide_x;
+    g.M = g.N = side;
+    g.K = tall ? a.m : a.n;
+    g.count = a.B;
+    g.scale = ldexpf(1.f, ea - 2 * ex);
+    e = tall ? pick_ns<NS_GRAM, true, true, false>(g, st) : pick_ns<NS_GRAM, false, false, false>(g, st);
+    if (e != hipSuccess) break;
+    NsProduct q{};
+    q.A = q.B = q.G = w + l.a;
+    q.out = w + l.p;
+    q.stride_a = q.stride_b = q.stride_out = l.stride_a;
+    q.pitch_a = q.pitch_b = q.pitch_out = pa;
+    q.rows_a = q.rows_b = side;
+    q.width_a = q.width_b = wide_a;
+    q.M = q.N = q.K = side;
+    q.count = a.B;
+    q.scale = ldexpf(1.f, ep - 2 * ea);
+    q.ca = ldexpf(a.a, ep);
+    q.cb = ldexpf(a.b, ep - ea);
+    q.cc = a.c;
+    e = pick_ns<NS_POLY, false, false, false>(q, st);
+    if (e != hipSuccess) break;
+    NsProduct u{};
+    u.out = w + l.x[(k + 1) & 1];
+    u.stride_out = l.stride_x;
+    u.pitch_out = px;
+    u.M = a.m;
+    u.N = a.n;
+    u.K = side;
+    u.count = a.B;
+    u.scale = ldexpf(1.f, -ep);
+    if (k + 1 == a.steps) {
+      u.last = a.out;
+      u.last_dtype = a.out_dtype;
+      u.stride_last = a.out_stride;
+      u.scale = ldexpf(1.f, -ep - ex);
+    }
+    if (tall) {  // X P
+      u.A = X;
+      u.stride_a = l.stride_x;
+      u.pitch_a = px;
+      u.rows_a = a.m;
+      u.width_a = wide_x;
+      u.B = w + l.p;
+      u.stride_b = l.stride_a;
+      u.pitch_b = pa;
+      u.rows_b = side;
+      u.width_b = wide_a;
+      e = pick_ns<NS_APPLY, false, false, true>(u, st);
+    } else {  // P X
+      u.A = w + l.p;
+      u.stride_a = l.stride_a;
+      u.pitch_a = pa;
+      u.rows_a = side;
+      u.width_a = wide_a;
+      u.B = X;
+      u.stride_b = l.stride_x;
+      u.pitch_b = px;
+      u.rows_b = a.m;
+      u.width_b = wide_x;
+      e = pick_ns<NS_APPLY, false, true, true>(u, st);
+    }
+  }
+  return e;
+}
+
+}  // namespace moe

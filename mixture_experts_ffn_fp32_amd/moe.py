@@ -24,7 +24,11 @@ EXPORTED = ("moe_last_error", "moe_workspace_size", "moe_layer_forward",
             "moe_layer_forward_static", "moe_route",
             "moe_dispatch_workspace_size", "moe_dispatch", "moe_expert_ffn_workspace_size",
             "moe_expert_ffn", "moe_combine", "moe_balance_workspace_size", "moe_balance_stats",
-            "moe_backward_workspace_size", "moe_layer_backward", "moe_timing_enable",
+            "moe_backward_workspace_size", "moe_layer_backward", "moe_layer_norm",
+            "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
+            "moe_grouped_matmul_workspace_size", "moe_grouped_matmul",
+            "moe_grouped_matmul_backward_workspace_size", "moe_grouped_matmul_backward",
+            "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_timing_enable",
             "moe_timing_read", "moe_timing_stages")
 
 
@@ -48,6 +52,7 @@ def load_library(path: str = LIB_PATH):
     L = ctypes.CDLL(path)
     vp, i, sz, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
     szp = ctypes.POINTER(ctypes.c_size_t)
+    fl, i64 = ctypes.c_float, ctypes.c_int64
     L.moe_last_error.restype = ctypes.c_char_p
     L.moe_last_error.argtypes = []
     sigs = {
@@ -66,6 +71,15 @@ def load_library(path: str = LIB_PATH):
         "moe_backward_workspace_size": [i, i, i, i, i, i, i, szp],
         "moe_layer_backward": [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp, vp, vp, vp, vp, vp,
                                sz, vp],
+        "moe_layer_norm": [vp, vp, vp, i, i, fl, i, vp, vp, vp, vp],
+        "moe_layer_norm_backward_workspace_size": [i, i, i, szp],
+        "moe_layer_norm_backward": [vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, vp, sz, vp],
+        "moe_grouped_matmul_workspace_size": [i, i, i, i, i, szp],
+        "moe_grouped_matmul": [vp, vp, vp, i, i, i, i, i, i, vp, vp, sz, vp],
+        "moe_grouped_matmul_backward_workspace_size": [i, i, i, i, i, i, i, szp],
+        "moe_grouped_matmul_backward": [vp, vp, vp, vp, i, i, i, i, i, i, vp, vp, vp, sz, vp],
+        "moe_orthogonalize_workspace_size": [i, i, i, szp],
+        "moe_orthogonalize": [vp, i64, i, i, i, i, i, fl, fl, fl, fl, vp, i64, i, vp, sz, vp],
         "moe_timing_enable": [i],
         "moe_timing_read": [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int)],
         "moe_timing_stages": [ctypes.c_uint],
@@ -299,6 +313,195 @@ def balance_stats(scores, idx, K: int, group_of=None, alpha1: float = 1.0, alpha
     if group_of is not None:
         res.update({"f_dev": fd[:D], "P_dev": Pd[:D], "L_DevBal": losses[1]})
     return res
+
+
+# ---------------------------------------------------------------- operators beside the layer
+def _operands(first, *others):
+    """Every tensor given is contiguous and on the device of the first; returns that device."""
+    _dev(first, *others)
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise MoEError(1, f"tensors on different devices: {first.device} and {t.device}")
+    return first.device
+
+
+def _typed(name: str, t, dtype, shape):
+    """t (if given) has this dtype and shape."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise MoEError(1, f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise MoEError(1, f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _dims(name: str, t, n: int):
+    if t.dim() != n:
+        raise MoEError(1, f"{name} must have {n} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _scratch(workspace, need: int, device):
+    """(pointer, bytes): the caller's workspace if it is large enough, else a new one.
+    A new one comes from PyTorch's allocator for the current stream, like the outputs."""
+    if workspace is not None:
+        if _operands(workspace) != device:
+            raise MoEError(1, f"workspace is on {workspace.device}, the operands on {device}")
+        if workspace.numel() * workspace.element_size() >= need:
+            return workspace
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _bytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def _size(query, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _check(query(*args, ctypes.byref(out)))
+    return out.value
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None):
+    """(y, mean, rstd) of layer norm over the last dimension of x [T][d]; see include/moe.h.
+
+    weight and bias [d] have x's dtype (None: ones, zeros); mean and rstd [T] are float32,
+    what layer_norm_backward needs."""
+    L = load_library()
+    T, d = _dims("x", x, 2)
+    dt = _dtype_code(x)
+    _typed("weight", weight, x.dtype, (d,))
+    _typed("bias", bias, x.dtype, (d,))
+    _typed("out", out, x.dtype, (T, d))
+    dev = _operands(x, weight, bias, out)
+    with torch.cuda.device(dev):
+        y = torch.empty_like(x) if out is None else out
+        mean = torch.empty(T, dtype=torch.float32, device=dev)
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        _check(L.moe_layer_norm(_p(x), _p(weight), _p(bias), T, d, eps, dt, _p(y), _p(mean),
+                                _p(rstd), _stream()))
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None):
+    """(dx, dweight, dbias) of sum(dy * y) for y, mean, rstd = layer_norm(x, weight, ..);
+    dx has x's dtype, dweight and dbias [d] are float32.  weight may be None (ones)."""
+    L = load_library()
+    T, d = _dims("x", x, 2)
+    dt = _dtype_code(x)
+    _typed("dy", dy, x.dtype, (T, d))
+    _typed("weight", weight, x.dtype, (d,))
+    _typed("mean", mean, torch.float32, (T,))
+    _typed("rstd", rstd, torch.float32, (T,))
+    dev = _operands(x, dy, weight, mean, rstd)
+    with torch.cuda.device(dev):
+        dx = torch.empty_like(x)
+        # an empty batch writes nothing: its weight gradients are zeros
+        alloc = torch.zeros if T == 0 else torch.empty
+        dw = alloc(d, dtype=torch.float32, device=dev)
+        db = alloc(d, dtype=torch.float32, device=dev)
+        ws = _scratch(workspace, _size(L.moe_layer_norm_backward_workspace_size, T, d, dt), dev)
+        _check(L.moe_layer_norm_backward(_p(dy), _p(x), _p(weight), _p(mean), _p(rstd), T, d, dt,
+                                         _p(dx), _p(dw), _p(db), _p(ws), _bytes(ws), _stream()))
+    return dx, dw, db
+
+
+def _grouped_shapes(x, w, offsets):
+    M, k = _dims("x", x, 2)
+    E, n, kw = _dims("w", w, 3)
+    if kw != k:
+        raise MoEError(1, f"x has rows of {k}, w of {kw}")
+    _typed("w", w, x.dtype, (E, n, k))
+    _typed("offsets", offsets, torch.int32, (E + 1,))
+    return M, E, n, k
+
+
+def grouped_matmul(x, w, offsets, out=None, workspace=None):
+    """y [M][n]: y[r] = w[e] @ x[r] for the rows offsets[e] <= r < offsets[e+1] of each group e.
+
+    x [M][k], w [E][n][k] of one dtype, offsets [E+1] int32 on the device (dispatch()'s, or any
+    non-decreasing ones).  Rows outside every group are zero in a new y and left as they were
+    in a given `out`."""
+    L = load_library()
+    M, E, n, k = _grouped_shapes(x, w, offsets)
+    dt = _dtype_code(x)
+    _typed("out", out, x.dtype, (M, n))
+    dev = _operands(x, w, offsets, out)
+    with torch.cuda.device(dev):
+        y = torch.empty((M, n), dtype=x.dtype, device=dev) if out is None else out
+        ws = _scratch(workspace, _size(L.moe_grouped_matmul_workspace_size, M, E, n, k, dt), dev)
+        _check(L.moe_grouped_matmul(_p(x), _p(w), _p(offsets), M, E, n, k, dt,
+                                    1 if out is None else 0, _p(y), _p(ws), _bytes(ws),
+                                    _stream()))
+    return y
+
+
+def grouped_matmul_backward(x, w, offsets, dy, need_dx: bool = True, need_dw: bool = True,
+                            workspace=None):
+    """(dx, dw) of sum(dy * y) for y = grouped_matmul(x, w, offsets): dx [M][k] in x's dtype
+    (zero outside the groups), dw [E][n][k] float32 (zero for a group without rows).  One that
+    is not needed is None."""
+    L = load_library()
+    M, E, n, k = _grouped_shapes(x, w, offsets)
+    dt = _dtype_code(x)
+    _typed("dy", dy, x.dtype, (M, n))
+    dev = _operands(x, w, offsets, dy)
+    with torch.cuda.device(dev):
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty((E, n, k), dtype=torch.float32, device=dev) if need_dw else None
+        ws = _scratch(workspace, _size(L.moe_grouped_matmul_backward_workspace_size, M, E, n, k,
+                                       dt, int(need_dx), int(need_dw)), dev)
+        _check(L.moe_grouped_matmul_backward(_p(x), _p(w), _p(offsets), _p(dy), M, E, n, k, dt, 1,
+                                             _p(dx), _p(dw), _p(ws), _bytes(ws), _stream()))
+    return dx, dw
+
+
+def _matrices(name: str, t):
+    """(batch, m, n, elements from one matrix to the next) of t [..][m][n]: contiguous, or
+    [B][m][n] with contiguous matrices at a larger stride (the blocks of a weight gradient)."""
+    if not t.is_cuda:
+        raise MoEError(1, "tensors must be on a GPU device")
+    if t.dim() < 2:
+        raise MoEError(1, f"{name} must have at least 2 dimensions")
+    m, n = t.shape[-2:]
+    B = 1
+    for s in t.shape[:-2]:
+        B *= s
+    if t.is_contiguous():
+        return B, m, n, m * n
+    if t.dim() != 3 or not t[0].is_contiguous() or t.stride(0) < m * n:
+        raise MoEError(1, f"{name} must hold contiguous matrices, back to back or at one stride")
+    return B, m, n, t.stride(0)
+
+
+def orthogonalize(x, steps: int = 5, eps: float = 1e-7,
+                  coefficients=(3.4445, -4.7750, 2.0315), out=None, out_dtype=None,
+                  workspace=None):
+    """The orthogonalised update of each matrix of x [..][m][n] (see include/moe.h): its
+    Newton-Schulz iterate after `steps` steps, in out_dtype (default x's dtype).
+
+    Takes gradients where they lie: x may be a view like layer_backward's
+    dW_routed.view(N, 3, I * d)[:, 2].view(N, d, I), whose matrices are contiguous at one
+    stride.  out may be x."""
+    L = load_library()
+    dt = _dtype_code(x)
+    B, m, n, xs = _matrices("x", x)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype,
+                          device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise MoEError(1, f"out: expected dtype {out_dtype}, got {out.dtype}")
+    if out.shape != x.shape:
+        raise MoEError(1, f"out: expected shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    if out.device != x.device:
+        raise MoEError(1, f"tensors on different devices: {x.device} and {out.device}")
+    os_ = _matrices("out", out)[3]
+    a, b, c = (float(v) for v in coefficients)
+    with torch.cuda.device(x.device):
+        ws = _scratch(workspace, _size(L.moe_orthogonalize_workspace_size, B, m, n), x.device)
+        _check(L.moe_orthogonalize(_p(x), xs, B, m, n, dt, steps, eps, a, b, c, _p(out), os_,
+                                   _dtype_code(out), _p(ws), _bytes(ws), _stream()))
+    return out
 
 
 def timing_enable(on: bool = True, stages=None):
