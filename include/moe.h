@@ -306,8 +306,8 @@ moe_status_t moe_grouped_matmul_backward(const void* x, const void* w, const int
  * Arithmetic of float32 accuracy whatever the types; a zero matrix stays zero.
  * Limits: B <= 65535; m, n <= 2^20; 0 <= steps <= 64; coefficients whose
  * polynomial keeps the iterate's singular values below 32 and the factor
- * a + b s^2 + c s^4 below 1024 (the usual a, b, c = 3.4445, -4.7750, 2.0315
- * stay below 1.3 and 3.5). */
+ * a + b s^2 + c s^4 below 1024, and c = 0 or b^2 <= 64 |c| (the usual a, b, c =
+ * 3.4445, -4.7750, 2.0315 stay below 1.3 and 3.5). */
 moe_status_t moe_orthogonalize_workspace_size(int B, int m, int n, size_t* bytes);
 moe_status_t moe_orthogonalize(const void* x, int64_t x_stride, int B, int m, int n, int dtype,
                                int steps, float eps, float a, float b, float c, void* out,

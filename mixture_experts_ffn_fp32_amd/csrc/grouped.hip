@@ -29,28 +29,41 @@ namespace {
 enum : int { GR_FWD = 0, GR_DX = 1, GR_DW = 2 };
 
 // ---------------------------------------------------------------- groups
-// Offsets into s_off[0..E], clamped and non-decreasing, and the exclusive
-// prefix of tiles per group into s_tab[0..E] (dir: which product; bm, bn: its
-// tile).  All threads of the block.
 struct GroupDims {
   int M, E, n, k;
 };
+// The groups as every block sees them in LDS: their rows (offsets clamped into [0, M]
+// and made non-decreasing), and the exclusive prefix of their m-tiles.
+struct GroupTables {
+  int off[kGroupedMaxE + 1], tiles[kGroupedMaxE + 1];
+};
+
 template <int DIR>
-__device__ __forceinline__ int group_tiles(const GroupDims& g, int rows, int bm, int bn) {
-  if (DIR == GR_DW) return ((g.n + bm - 1) / bm) * ((g.k + bn - 1) / bn);
-  return ((rows + bm - 1) / bm) * (((DIR == GR_FWD ? g.n : g.k) + bn - 1) / bn);
+__device__ __forceinline__ int group_tiles(const GroupDims& g, int rows, int bm) {
+  return ((DIR == GR_DW ? (rows > 0 ? g.n : 0) : rows) + bm - 1) / bm;
 }
+
+__device__ __forceinline__ int wave_prefix(int v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// All threads of the block.
 template <int DIR>
 __device__ __forceinline__ void group_tables(const GroupDims& g, const int32_t* __restrict__ offsets,
-                                             int bm, int bn, int* s_off, int* s_tab) {
-  for (int i = threadIdx.x; i <= g.E; i += blockDim.x) s_off[i] = min(max(offsets[i], 0), g.M);
+                                             int bm, GroupTables& t) {
+  for (int i = threadIdx.x; i <= g.E; i += blockDim.x) t.off[i] = min(max(offsets[i], 0), g.M);
   __syncthreads();
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
-    int top = s_off[0], carry = 0;
+    int top = t.off[0], carry = 0;
     for (int b = 0; b < g.E; b += 64) {
       const int e = b + lane;
-      int hi = e < g.E ? s_off[e + 1] : 0;
+      int hi = e < g.E ? t.off[e + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int y = __shfl_up(hi, o);
@@ -58,34 +71,33 @@ __device__ __forceinline__ void group_tables(const GroupDims& g, const int32_t* 
       }
       hi = max(hi, top);
       const int up = __shfl_up(hi, 1);
-      const int lo = lane == 0 ? top : up;
-      const int t = e < g.E ? group_tiles<DIR>(g, hi - lo, bm, bn) : 0;
-      int inc = t;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_up(inc, o);
-        if (lane >= o) inc += y;
-      }
+      const int own = e < g.E ? group_tiles<DIR>(g, hi - (lane == 0 ? top : up), bm) : 0;
+      const int sum = wave_prefix(own, lane);
       if (e < g.E) {
-        s_off[e + 1] = hi;
-        s_tab[e] = carry + inc - t;
+        t.off[e + 1] = hi;
+        t.tiles[e] = carry + sum - own;
       }
-      carry += __shfl(inc, 63);
+      carry += __shfl(sum, 63);
       top = __shfl(hi, 63);
     }
-    if (lane == 0) s_tab[g.E] = carry;
+    if (lane == 0) t.tiles[g.E] = carry;
   }
   __syncthreads();
 }
 
-// The group of tile L: the last one whose first tile is at or before L.
-__device__ __forceinline__ int group_of_tile(const int* s_tab, int E, int L) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s_tab[mid] <= L) lo = mid; else hi = mid - 1;
+// The group of the key-th m-tile of a prefix table (tab[E] > key): the last one whose
+// first is at or before it, looked for near e first (a block's tiles come in order).
+__device__ __forceinline__ int group_of(const int* tab, int E, int key, int e) {
+  if (key < uni(tab[e]) || key >= uni(tab[min(e + 4, E)])) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (uni(tab[mid]) <= key) lo = mid; else hi = mid - 1;
+    }
+    return lo;
   }
-  return uni(lo);
+  while (uni(tab[e + 1]) <= key) ++e;
+  return e;
 }
 
 // Zeros into the rows [0, first) and [last, M) of out, this block's share.
@@ -114,35 +126,43 @@ struct GroupedProduct {
 template <class C, int DIR>
 struct GroupedTiles {
   const GroupedProduct& p;
-  const int* s_off;
-  const int* s_tab;
+  const GroupTables& g_;
 
+  static constexpr bool SYM = false;
   struct Tile {
     TgOperand A, B;
-    int m0, n0, steps, e, row0, rows;
+    int m0, n0, steps, rows, cols, hint, row0, size;
   };
-  __device__ __forceinline__ Tile tile(int L) const {
-    Tile t;
+  __device__ __forceinline__ bool tri(const Tile&) const { return false; }
+  __device__ __forceinline__ int columns() const {
+    return ((DIR == GR_FWD ? p.g.n : p.g.k) + C::BN - 1) / C::BN;
+  }
+  __device__ __forceinline__ Tile tile(int L, int e) const {  // group by group, m fastest
     const GroupDims& g = p.g;
-    t.e = group_of_tile(s_tab, g.E, L);
-    t.row0 = uni(s_off[t.e]);
-    t.rows = uni(s_off[t.e + 1]) - t.row0;
-    const int local = L - uni(s_tab[t.e]);
-    const int mt = ((DIR == GR_DW ? g.n : t.rows) + C::BM - 1) / C::BM;
-    t.m0 = local % mt * C::BM;
-    t.n0 = local / mt * C::BN;
+    const int nt = columns();
+    e = uni(group_of(g_.tiles, g.E, L / nt, e));
+    const int first = uni(g_.tiles[e]), mt = uni(g_.tiles[e + 1]) - first, local = L - first * nt;
+    const int m = local % mt, n = local / mt;
+    Tile t;
+    t.hint = e;
+    t.row0 = uni(g_.off[e]);
+    t.size = uni(g_.off[e + 1]) - t.row0;
+    t.m0 = m * C::BM;
+    t.n0 = n * C::BN;
+    t.rows = (DIR == GR_DW ? g.n : t.size) - t.m0;
+    t.cols = (DIR == GR_FWD ? g.n : g.k) - t.n0;
     t.A.p = p.A + (size_t)t.row0 * p.pitch_a;
     t.A.pitch = p.pitch_a;
-    t.A.rows = t.rows;
+    t.A.rows = t.size;
     t.A.width = (g.n + 31) & ~31;
     t.B.pitch = p.pitch_b;
     if (DIR == GR_DW) {
       t.B.p = p.B + (size_t)t.row0 * p.pitch_b;
-      t.B.rows = t.rows;
+      t.B.rows = t.size;
       t.B.width = (g.k + 31) & ~31;
-      t.steps = (t.rows + C::KS - 1) / C::KS;
+      t.steps = (t.size + C::KS - 1) / C::KS;
     } else {
-      t.B.p = p.B + (size_t)t.e * g.n * p.pitch_b;
+      t.B.p = p.B + (size_t)t.hint * g.n * p.pitch_b;
       t.B.rows = g.n;
       t.B.width = (g.k + 31) & ~31;
       t.steps = ((DIR == GR_FWD ? g.k : g.n) + C::KS - 1) / C::KS;
@@ -158,7 +178,7 @@ struct GroupedTiles {
                                         f32x16 (&acc)[C::FM][C::FN]) const {
     const GroupDims& g = p.g;
     if constexpr (DIR == GR_DW) {
-      float* out = (float*)p.out + (size_t)t.e * g.n * g.k;
+      float* out = (float*)p.out + (size_t)t.hint * g.n * g.k;
       const int ex = C::SPLIT ? -p.eb[0] : 0;
 #pragma unroll
       for (int fm = 0; fm < C::FM; ++fm)
@@ -178,44 +198,62 @@ struct GroupedTiles {
     } else {
       // a lane holds four consecutive columns of one row
       const int N = DIR == GR_FWD ? g.n : g.k;
-      const bool vec = N % 4 == 0;
+      const bool vec = N % (C::SPLIT ? 4 : 8) == 0;  // whole 16-byte runs
 #pragma unroll
       for (int fm = 0; fm < C::FM; ++fm) {
-        const int m = t.m0 + tg_row<C>(wm, fm, lane, 0);
-        if (m >= t.rows) continue;
-        const int ea = C::SPLIT ? p.ea[t.row0 + m] + (DIR == GR_DX ? p.eb[t.e] : 0) : 0;
+        const int mr = tg_row<C>(wm, fm, lane, 0);
+        if (mr >= t.rows) continue;
+        const size_t row = (size_t)(t.row0 + t.m0 + mr);
+        const int ea = C::SPLIT ? p.ea[row] + (DIR == GR_DX ? p.eb[t.hint] : 0) : 0;
 #pragma unroll
-        for (int fn = 0; fn < C::FN; ++fn)
+        for (int fn = 0; fn < C::FN; ++fn) {
+          const int n0 = t.n0 + tg_col<C>(wn, fn, 0, 0);  // the fragment's first column
+          if (n0 >= N) continue;
+          if constexpr (C::SPLIT) {
+            float* c = (float*)p.out + row * N;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int n = t.n0 + tg_col<C>(wn, fn, lane, 4 * q);
-            float v[4];
+            for (int q = 0; q < 4; ++q) {
+              const int n = n0 + 8 * q + 4 * (lane >> 5);
+              float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[e] = acc[fm][fn][4 * q + e];
-              if (C::SPLIT && n + e < N)
-                v[e] = ldexpf(v[e], -ea - (DIR == GR_FWD ? p.eb[(size_t)t.e * g.n + n + e] : 0));
-            }
-            if constexpr (C::SPLIT) {
-              float* c = (float*)p.out + (size_t)(t.row0 + m) * N + n;
-              if (vec) {
-                if (n < N) *(f32x4*)c = f32x4{v[0], v[1], v[2], v[3]};
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (n + e < N) c[e] = v[e];
+              for (int e = 0; e < 4; ++e) {
+                v[e] = acc[fm][fn][4 * q + e];
+                if (n + e < N)
+                  v[e] = ldexpf(v[e], -ea - (DIR == GR_FWD ? p.eb[(size_t)t.hint * g.n + n + e] : 0));
               }
-            } else {
-              uint16_t* c = (uint16_t*)p.out + (size_t)(t.row0 + m) * N + n;
               if (vec) {
-                if (n < N) *(uint2*)c = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                if (n < N) *(f32x4*)(c + n) = f32x4{v[0], v[1], v[2], v[3]};
               } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (n + e < N) c[e] = f32_to_bf16(v[e]);
+                  if (n + e < N) c[n + e] = v[e];
+              }
+            }
+          } else {
+            uint16_t* c = (uint16_t*)p.out + row * N;
+            uint2 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = uint2{pack_bf16x2(acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1]),
+                           pack_bf16x2(acc[fm][fn][4 * q + 2], acc[fm][fn][4 * q + 3])};
+            if (vec) {
+              u32x4 r0, r1;
+              tg_runs16(w, r0, r1);
+              const int n = n0 + 8 * (lane >> 5);
+              if (n < N) *(u32x4*)(c + n) = r0;
+              if (n + 16 < N) *(u32x4*)(c + n + 16) = r1;
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int n = n0 + 8 * q + 4 * (lane >> 5);
+                const uint32_t b[2] = {w[q].x, w[q].y};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (n + e < N) c[n + e] = (uint16_t)(b[e >> 1] >> (16 * (e & 1)));
               }
             }
           }
+        }
       }
     }
   }
@@ -226,15 +264,23 @@ __global__ __launch_bounds__(kTgThreads, C::SLOT > 32768 ? 2 : 4) void grouped_k
     GroupedProduct p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[C::SLOT];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[C::SLOT];
-  __shared__ int s_off[kGroupedMaxE + 1], s_tab[kGroupedMaxE + 1];
-  group_tables<DIR>(p.g, p.offsets, C::BM, C::BN, s_off, s_tab);
+  __shared__ GroupTables t;
+  group_tables<DIR>(p.g, p.offsets, C::BM, t);
   if (DIR != GR_DW && p.zero_rest) {
-    if (C::SPLIT) zero_rows((float*)p.out, p.g.M, DIR == GR_FWD ? p.g.n : p.g.k, s_off[0], s_off[p.g.E]);
-    else zero_rows((uint16_t*)p.out, p.g.M, DIR == GR_FWD ? p.g.n : p.g.k, s_off[0], s_off[p.g.E]);
+    const int width = DIR == GR_FWD ? p.g.n : p.g.k;
+    if (C::SPLIT) zero_rows((float*)p.out, p.g.M, width, t.off[0], t.off[p.g.E]);
+    else zero_rows((uint16_t*)p.out, p.g.M, width, t.off[0], t.off[p.g.E]);
   }
-  const GroupedTiles<C, DIR> tiles{p, s_off, s_tab};
-  const TgShare sh = tg_share(uni(s_tab[p.g.E]));
-  tg_run<C>(tiles, sh.start, sh.end, sh.stride, lds0, lds1);
+  if (DIR == GR_DW) {  // groups without rows have no tiles
+    const size_t per = (size_t)p.g.n * p.g.k;
+    for (int e = 0; e < p.g.E; ++e)
+      if (t.off[e] == t.off[e + 1])
+        for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < per;
+             i += (size_t)gridDim.x * blockDim.x)
+          ((float*)p.out)[e * per + i] = 0.f;
+  }
+  const GroupedTiles<C, DIR> tiles{p, t};
+  tg_run<C>(tiles, uni(t.tiles[p.g.E]) * tiles.columns(), nullptr, lds0, lds1, nullptr);
 }
 
 // ---------------------------------------------------------------- operand preparation

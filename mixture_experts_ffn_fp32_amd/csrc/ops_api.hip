@@ -328,6 +328,9 @@ moe_status_t moe_orthogonalize(const void* x, int64_t x_stride, int B, int m, in
   if (!(iterate * iterate <= moe::kOrthoMaxBound) || !(factor <= moe::kOrthoMaxBound))
     return fail(MOE_ERR_UNSUPPORTED,
                 "the coefficients let the iterate grow past the range its products are held in");
+  // P comes from the completed square, which cancels b^2 / (4 c) against a
+  if (c != 0.f && !((double)b * b <= 64.0 * fabs((double)c)))
+    return fail(MOE_ERR_UNSUPPORTED, "the coefficients must satisfy c == 0 or b * b <= 64 |c|");
   if (B == 0) return ok();
   const int64_t per = (int64_t)m * n;
   if (B > 1 && (x_stride < per || out_stride < per))

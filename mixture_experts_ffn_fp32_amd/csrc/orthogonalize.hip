@@ -7,6 +7,10 @@
 //   A = X X^T,  P = a I + b A + c A^2,  X <- P X     (A = X^T X, X <- X P where
 //                                                     G has more rows than columns)
 //
+// With the square completed, P = c S^2 + (a - c d^2) I, S = A + d I, d = b / (2 c): the
+// first product's epilogue adds d to its diagonal and the second one needs no other
+// operand (reading A again there cost as much time as the product itself).
+//
 // p(s) = a s + b s^3 + c s^5 acts on each singular value and drives it towards
 // 1.  Bound by the matrix products: per step p^2 q + p^3 + 2 p^2 q flops (p the
 // smaller side; A and A^2 are symmetric, so only tiles on and above the diagonal
@@ -29,13 +33,13 @@
 namespace moe {
 namespace {
 
-enum : int { NS_GRAM = 0, NS_POLY = 1, NS_APPLY = 2 };
+// The two kinds of product: a symmetric one, and the last one of a step.
+enum : int { NS_SYM = 0, NS_APPLY = 1 };
 constexpr int kNormParts = 64;  // partial norms per matrix
 
 struct NsProduct {
   const uint8_t* A;
   const uint8_t* B;
-  const uint8_t* G;        // POLY: A at the output's place
   uint8_t* out;            // split rows
   void* last;              // APPLY, last step: the result instead
   long long stride_a, stride_b, stride_out, stride_last;  // bytes (last: elements) per matrix
@@ -46,7 +50,8 @@ struct NsProduct {
   int last_dtype;
   int count;               // matrices
   float scale;             // of the accumulators
-  float ca, cb, cc;        // POLY: acc * scale * cc + G * cb (+ ca on the diagonal)
+  float diag;              // SYM: added on the diagonal
+  int32_t* counters;       // tile claims (kTgCounters zeros), or NULL
 };
 
 template <class C, int KIND>
@@ -54,15 +59,17 @@ struct NsTiles {
   const NsProduct& p;
   struct Tile {
     TgOperand A, B;
-    int m0, n0, steps, i;
+    int m0, n0, steps, rows, cols, hint, i;
   };
-  static constexpr bool SYM = KIND != NS_APPLY;
+  static constexpr bool SYM = KIND == NS_SYM;
+  __device__ __forceinline__ bool tri(const Tile& t) const { return t.m0 == t.n0; }
+  __device__ __forceinline__ int hint(int) const { return 0; }
 
   __device__ __forceinline__ int per_matrix() const {
     const int mt = (p.M + C::BM - 1) / C::BM;
     return SYM ? mt * (mt + 1) / 2 : mt * ((p.N + C::BN - 1) / C::BN);
   }
-  __device__ __forceinline__ Tile tile(int L) const {
+  __device__ __forceinline__ Tile tile(int L, int) const {
     Tile t;
     const int per = per_matrix(), mt = (p.M + C::BM - 1) / C::BM;
     t.i = L / per;
@@ -79,6 +86,9 @@ struct NsTiles {
       t.m0 = local % mt * C::BM;
       t.n0 = local / mt * C::BN;
     }
+    t.hint = 0;
+    t.rows = p.M - t.m0;
+    t.cols = p.N - t.n0;
     t.A.p = p.A + (size_t)t.i * p.stride_a;
     t.A.pitch = p.pitch_a;
     t.A.rows = p.rows_a;
@@ -96,88 +106,131 @@ struct NsTiles {
     uint8_t* out = p.out + (size_t)t.i * p.stride_out;
     const int wide = (p.N + 31) & ~31;  // columns of an output row with its padding
     if constexpr (SYM) {
-      // a lane holds four consecutive rows m .. m + 3 of one column n: written
-      // there, and (off the diagonal tiles) as columns m .. m + 3 of row n
-      const uint8_t* G = KIND == NS_POLY ? p.G + (size_t)t.i * p.stride_out : nullptr;
+      // A lane holds rows m .. m + 3 (m = 8 q + 4 (lane / 32) in a fragment) of one
+      // column n.  Written as columns m .. of row n (16-byte runs), and, four
+      // lanes transposed among themselves, as columns n .. of rows m ...  A
+      // diagonal tile (its lower left quarter not computed, only mirrored)
+      // writes the second form, and the first of its upper right quarter.
+      const bool diagonal = t.m0 == t.n0, quarters = diagonal && C::FM == 2 && t.rows > C::BM / 2;
 #pragma unroll
       for (int fm = 0; fm < C::FM; ++fm)
 #pragma unroll
         for (int fn = 0; fn < C::FN; ++fn) {
+          const bool lower = tg_skip<C, C::FM == 2>(fm, fn);
+          const bool mirror = !diagonal || (quarters && fm < C::FM / 2 && fn >= C::FN / 2);
+          if (lower && quarters) continue;
           const int n = t.n0 + tg_col<C>(wn, fn, lane, 0);
+          const int m0 = t.m0 + tg_row<C>(wm, fm, 0, 0);  // the fragment's first row
+          if (m0 >= wide || t.n0 + tg_col<C>(wn, fn, 0, 0) >= wide) continue;
+          uint2 wh[4], wl[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int m = t.m0 + tg_row<C>(wm, fm, lane, 4 * q);
+            const int m = m0 + 8 * q + 4 * (lane >> 5);
             uint16_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float v = acc[fm][fn][4 * q + e] * p.scale;
-              if constexpr (KIND == NS_POLY) {
-                float g = 0.f;
-                if (m + e < p.M && n < p.N) {
-                  const uint8_t* at = G + (size_t)(m + e) * p.pitch_out + split_at(n);
-                  g = f16_to_f32(*(const uint16_t*)at) + f16_to_f32(*(const uint16_t*)(at + 64));
-                }
-                v = p.cc * v + p.cb * g + (m + e == n ? p.ca : 0.f);
-              }
+              if (m + e == n) v += p.diag;
               if (m + e >= p.M || n >= p.N) v = 0.f;
               split_f16(v, hi[e], lo[e]);
-              if (m + e < p.M && n < wide) {
-                uint8_t* at = out + (size_t)(m + e) * p.pitch_out + split_at(n);
-                *(uint16_t*)at = hi[e];
-                *(uint16_t*)(at + 64) = lo[e];
-              }
             }
-            if (t.m0 != t.n0 && n < p.N && m < wide) {
-              uint8_t* at = out + (size_t)n * p.pitch_out + split_at(m);
-              *(uint2*)at = uint2{hi[0] | ((uint32_t)hi[1] << 16), hi[2] | ((uint32_t)hi[3] << 16)};
-              *(uint2*)(at + 64) =
-                  uint2{lo[0] | ((uint32_t)lo[1] << 16), lo[2] | ((uint32_t)lo[3] << 16)};
+            wh[q] = uint2{hi[0] | ((uint32_t)hi[1] << 16), hi[2] | ((uint32_t)hi[3] << 16)};
+            wl[q] = uint2{lo[0] | ((uint32_t)lo[1] << 16), lo[2] | ((uint32_t)lo[3] << 16)};
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint2 h = tg_quad_transpose(wh[q], lane), l = tg_quad_transpose(wl[q], lane);
+            const int m = m0 + 8 * q + 4 * (lane >> 5) + (lane & 3);
+            if (m < p.M) {
+              uint8_t* at = out + (size_t)m * p.pitch_out + split_at(n & ~3);
+              *(uint2*)at = h;
+              *(uint2*)(at + 64) = l;
             }
+          }
+          if (mirror && n < p.N) {
+            u32x4 r0, r1;
+            uint8_t* at = out + (size_t)n * p.pitch_out + split_at(m0 + 8 * (lane >> 5));
+            tg_runs16(wh, r0, r1);
+            *(u32x4*)at = r0;
+            *(u32x4*)(at + 32) = r1;
+            tg_runs16(wl, r0, r1);
+            *(u32x4*)(at + 64) = r0;
+            *(u32x4*)(at + 96) = r1;
           }
         }
     } else {
-      const bool vec = p.N % 4 == 0;
+      const bool vec = p.N % 8 == 0;  // whole 16-byte runs of either type
 #pragma unroll
       for (int fm = 0; fm < C::FM; ++fm) {
         const int m = t.m0 + tg_row<C>(wm, fm, lane, 0);
         if (m >= p.M) continue;
 #pragma unroll
-        for (int fn = 0; fn < C::FN; ++fn)
+        for (int fn = 0; fn < C::FN; ++fn) {
+          const int n0 = t.n0 + tg_col<C>(wn, fn, 0, 0);  // the fragment's first column
+          if (n0 >= wide) continue;
+          if (p.last == nullptr) {
+            uint2 wh[4], wl[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int n = t.n0 + tg_col<C>(wn, fn, lane, 4 * q);
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = acc[fm][fn][4 * q + e] * p.scale;
-            if (p.last == nullptr) {
-              if (n >= wide) continue;
+            for (int q = 0; q < 4; ++q) {
+              const int n = n0 + 8 * q + 4 * (lane >> 5);
               uint16_t hi[4], lo[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) split_f16(n + e < p.N ? v[e] : 0.f, hi[e], lo[e]);
-              uint8_t* at = out + (size_t)m * p.pitch_out + split_at(n);
-              *(uint2*)at = uint2{hi[0] | ((uint32_t)hi[1] << 16), hi[2] | ((uint32_t)hi[3] << 16)};
-              *(uint2*)(at + 64) =
-                  uint2{lo[0] | ((uint32_t)lo[1] << 16), lo[2] | ((uint32_t)lo[3] << 16)};
-            } else if (p.last_dtype == 0) {
-              float* c = (float*)p.last + (size_t)t.i * p.stride_last + (size_t)m * p.N + n;
+              for (int e = 0; e < 4; ++e)
+                split_f16(n + e < p.N ? acc[fm][fn][4 * q + e] * p.scale : 0.f, hi[e], lo[e]);
+              wh[q] = uint2{hi[0] | ((uint32_t)hi[1] << 16), hi[2] | ((uint32_t)hi[3] << 16)};
+              wl[q] = uint2{lo[0] | ((uint32_t)lo[1] << 16), lo[2] | ((uint32_t)lo[3] << 16)};
+            }
+            u32x4 r0, r1;
+            uint8_t* at = out + (size_t)m * p.pitch_out + split_at(n0 + 8 * (lane >> 5));
+            tg_runs16(wh, r0, r1);
+            *(u32x4*)at = r0;
+            *(u32x4*)(at + 32) = r1;
+            tg_runs16(wl, r0, r1);
+            *(u32x4*)(at + 64) = r0;
+            *(u32x4*)(at + 96) = r1;
+            continue;
+          }
+          const size_t row = (size_t)t.i * p.stride_last + (size_t)m * p.N;
+          if (p.last_dtype == 0) {
+            float* c = (float*)p.last + row;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int n = n0 + 8 * q + 4 * (lane >> 5);
+              const f32x4 v = {acc[fm][fn][4 * q] * p.scale, acc[fm][fn][4 * q + 1] * p.scale,
+                               acc[fm][fn][4 * q + 2] * p.scale, acc[fm][fn][4 * q + 3] * p.scale};
               if (vec) {
-                if (n < p.N) *(f32x4*)c = f32x4{v[0], v[1], v[2], v[3]};
+                if (n < p.N) *(f32x4*)(c + n) = v;
               } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (n + e < p.N) c[e] = v[e];
+                  if (n + e < p.N) c[n + e] = v[e];
               }
+            }
+          } else {
+            uint16_t* c = (uint16_t*)p.last + row;
+            uint2 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = uint2{pack_bf16x2(acc[fm][fn][4 * q] * p.scale, acc[fm][fn][4 * q + 1] * p.scale),
+                           pack_bf16x2(acc[fm][fn][4 * q + 2] * p.scale, acc[fm][fn][4 * q + 3] * p.scale)};
+            if (vec) {
+              u32x4 r0, r1;
+              tg_runs16(w, r0, r1);
+              const int n = n0 + 8 * (lane >> 5);
+              if (n < p.N) *(u32x4*)(c + n) = r0;
+              if (n + 16 < p.N) *(u32x4*)(c + n + 16) = r1;
             } else {
-              uint16_t* c = (uint16_t*)p.last + (size_t)t.i * p.stride_last + (size_t)m * p.N + n;
-              if (vec) {
-                if (n < p.N) *(uint2*)c = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-              } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int n = n0 + 8 * q + 4 * (lane >> 5);
+                const uint32_t b[2] = {w[q].x, w[q].y};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (n + e < p.N) c[e] = f32_to_bf16(v[e]);
+                  if (n + e < p.N) c[n + e] = (uint16_t)(b[e >> 1] >> (16 * (e & 1)));
               }
             }
           }
+        }
       }
     }
   }
@@ -187,17 +240,20 @@ template <class C, int KIND>
 __global__ __launch_bounds__(kTgThreads, C::SLOT > 32768 ? 2 : 4) void ns_kernel(NsProduct p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[C::SLOT];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[C::SLOT];
+  __shared__ int s_claim;
   const NsTiles<C, KIND> tiles{p};
-  const TgShare sh = tg_share(tiles.per_matrix() * p.count);
-  tg_run<C>(tiles, sh.start, sh.end, sh.stride, lds0, lds1);
+  tg_run<C>(tiles, tiles.per_matrix() * p.count, p.counters, lds0, lds1, &s_claim);
 }
 
 // ---------------------------------------------------------------- the first iterate
-// Partial sums of squares: block (part, matrix) takes the part-th share of its values.
+// Partial sums of squares (and the products' claim counters zeroed): block (part, matrix) takes the part-th share of its values.
 template <class E>
 __global__ __launch_bounds__(256) void ns_norm_kernel(const void* __restrict__ x, long long stride,
-                                                      long long per, double* __restrict__ part) {
+                                                      long long per, double* __restrict__ part,
+                                                      int32_t* __restrict__ counters, int claims) {
   __shared__ double s[4];
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < claims; i += 256) counters[i] = 0;
   const typename E::T* src = (const typename E::T*)x + (long long)blockIdx.y * stride;
   const long long a = per * blockIdx.x / kNormParts, b = per * (blockIdx.x + 1) / kNormParts;
   double v = 0.0;
@@ -260,9 +316,10 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 int scale_exponent(double most) { return 14 - (int)ceil(log2(std::max(most, 1e-30))); }
 
 struct NsPlan {
-  size_t x[2], a, p, part, bytes;
+  size_t x[2], a, p, part, counters, bytes;
   size_t stride_x, stride_a;
 };
+constexpr int kMaxSteps = 64;
 NsPlan ns_plan(int B, int m, int n) {
   NsPlan l{};
   const int side = std::min(m, n);
@@ -279,15 +336,17 @@ NsPlan ns_plan(int B, int m, int n) {
   l.a = take(l.stride_a * B);
   l.p = take(l.stride_a * B);
   l.part = take((size_t)B * kNormParts * 8);
+  l.counters = take((size_t)kMaxSteps * 3 * kTgCounters * 4);
   l.bytes = at;
   return l;
 }
 
 template <class C, int KIND>
-hipError_t run_ns(const NsProduct& p, hipStream_t st) {
+hipError_t run_ns(NsProduct p, hipStream_t st) {
   const long long mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN;
   const long long total = (KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2) * p.count;
   const long long blocks = (long long)device_cu_count() * (C::SLOT > 32768 ? 1 : 2);
+  if (total <= blocks) p.counters = nullptr;  // one tile each
   ns_kernel<C, KIND><<<(unsigned)std::min(total, blocks), kTgThreads, 0, st>>>(p);
   return hipGetLastError();
 }
@@ -330,20 +389,26 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
   uint8_t* w = (uint8_t*)ws;
   double* part = (double*)(w + l.part);
   const long long per = (long long)a.m * a.n, rows = (long long)a.B * a.m;
+  int32_t* counters = (int32_t*)(w + l.counters);
+  const int claims = a.steps * 3 * kTgCounters;
   double most_x, most_p;
   ortho_bounds(a.steps, a.a, a.b, a.c, &most_x, &most_p);
-  const int ex = scale_exponent(most_x), ea = scale_exponent(most_x * most_x),
+  // d of the completed square; c = 0: the first product gives P = a I + b A itself
+  const double d = a.c != 0.f ? (double)a.b / (2.0 * a.c) : 0.0;
+  const int ex = scale_exponent(most_x), ea = scale_exponent(most_x * most_x + fabs(d)),
             ep = scale_exponent(most_p);
   const uint32_t px = (uint32_t)split_pitch(a.n), pa = (uint32_t)split_pitch(std::min(a.m, a.n));
   const float start = a.steps == 0 ? 1.f : ldexpf(1.f, ex);
   void* direct = a.steps == 0 ? a.out : nullptr;
   const dim3 gn(kNormParts, a.B), gs((unsigned)((rows + 3) / 4));
   if (a.dtype == 0) {
-    ns_norm_kernel<ElemF32><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part);
+    ns_norm_kernel<ElemF32><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part,
+                                                counters, claims);
     ns_start_kernel<ElemF32><<<gs, 256, 0, st>>>(a.x, a.x_stride, a.m, a.n, rows, part, a.eps, start,
                                                  w + l.x[0], px, direct, a.out_stride, a.out_dtype);
   } else {
-    ns_norm_kernel<ElemBF16><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part);
+    ns_norm_kernel<ElemBF16><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part,
+                                                counters, claims);
     ns_start_kernel<ElemBF16><<<gs, 256, 0, st>>>(a.x, a.x_stride, a.m, a.n, rows, part, a.eps, start,
                                                   w + l.x[0], px, direct, a.out_stride, a.out_dtype);
   }
@@ -352,9 +417,10 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
   const int side = std::min(a.m, a.n), wide_x = (a.n + 31) & ~31, wide_a = (side + 31) & ~31;
   for (int k = 0; k < a.steps && e == hipSuccess; ++k) {
     const uint8_t* X = w + l.x[k & 1];
+    int32_t* cnt = counters + k * 3 * kTgCounters;
     NsProduct g{};
     g.A = g.B = X;
-    g.out = w + l.a;
+    g.out = w + (a.c != 0.f ? l.a : l.p);
     g.stride_a = g.stride_b = l.stride_x;
     g.stride_out = l.stride_a;
     g.pitch_a = g.pitch_b = px;
@@ -364,24 +430,32 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
     g.M = g.N = side;
     g.K = tall ? a.m : a.n;
     g.count = a.B;
-    g.scale = ldexpf(1.f, ea - 2 * ex);
-    e = tall ? pick_ns<NS_GRAM, true, true, false>(g, st) : pick_ns<NS_GRAM, false, false, false>(g, st);
+    g.counters = cnt;
+    if (a.c != 0.f) {
+      g.scale = ldexpf(1.f, ea - 2 * ex);
+      g.diag = (float)ldexp(d, ea);
+    } else {
+      g.scale = ldexpf(a.b, ep - 2 * ex);
+      g.diag = ldexpf(a.a, ep);
+    }
+    e = tall ? pick_ns<NS_SYM, true, true, false>(g, st) : pick_ns<NS_SYM, false, false, false>(g, st);
     if (e != hipSuccess) break;
-    NsProduct q{};
-    q.A = q.B = q.G = w + l.a;
-    q.out = w + l.p;
-    q.stride_a = q.stride_b = q.stride_out = l.stride_a;
-    q.pitch_a = q.pitch_b = q.pitch_out = pa;
-    q.rows_a = q.rows_b = side;
-    q.width_a = q.width_b = wide_a;
-    q.M = q.N = q.K = side;
-    q.count = a.B;
-    q.scale = ldexpf(1.f, ep - 2 * ea);
-    q.ca = ldexpf(a.a, ep);
-    q.cb = ldexpf(a.b, ep - ea);
-    q.cc = a.c;
-    e = pick_ns<NS_POLY, false, false, false>(q, st);
-    if (e != hipSuccess) break;
+    if (a.c != 0.f) {
+      NsProduct q{};
+      q.A = q.B = w + l.a;
+      q.out = w + l.p;
+      q.stride_a = q.stride_b = q.stride_out = l.stride_a;
+      q.pitch_a = q.pitch_b = q.pitch_out = pa;
+      q.rows_a = q.rows_b = side;
+      q.width_a = q.width_b = wide_a;
+      q.M = q.N = q.K = side;
+      q.count = a.B;
+      q.counters = cnt + kTgCounters;
+      q.scale = ldexpf(a.c, ep - 2 * ea);
+      q.diag = (float)ldexp(a.a - a.c * d * d, ep);
+      e = pick_ns<NS_SYM, false, false, false>(q, st);
+      if (e != hipSuccess) break;
+    }
     NsProduct u{};
     u.out = w + l.x[(k + 1) & 1];
     u.stride_out = l.stride_x;
@@ -390,6 +464,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
     u.N = a.n;
     u.K = side;
     u.count = a.B;
+    u.counters = cnt + 2 * kTgCounters;
     u.scale = ldexpf(1.f, -ep);
     if (k + 1 == a.steps) {
       u.last = a.out;

@@ -64,22 +64,16 @@ struct TgOperand {
 struct TgLoad {
   const uint8_t* base;
   uint32_t step;   // bytes from one k-step to the next
-  int rows;        // column layout: contraction rows; row layout: -1
+  int rows;        // column layout: contraction rows; row layout: -(k-steps)
   uint32_t pitch;
 };
 
-// Position of the 16-byte chunk `c` of contraction row k in a column-layout
-// tile of W columns.  A transposing read of 32 lanes touches 64 bytes of each of
-// four consecutive rows: rotating by four chunks per row puts them on distinct
-// banks.
-template <int W>
-__device__ __forceinline__ int tg_col_offset(int k, int n) {
-  return k * (W * 2) + (((n >> 3) ^ ((k & 3) << 2)) << 4) + (n & 7) * 2;
-}
-
+// In a column-layout tile the 16-byte chunk c of contraction row k lies at position
+// c ^ 4 (k & 3): a transposing read of 32 lanes touches 64 bytes of each of four
+// consecutive rows, and the rotation puts them on distinct banks.
 template <class C, bool COL>
-__device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int t0, int w, int lane,
-                                                  uint32_t (&off)[C::NI]) {
+__device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int t0, int steps, int w,
+                                                  int lane, uint32_t (&off)[C::NI]) {
   constexpr int W = C::BM;
   TgLoad l;
   l.pitch = uni((int)o.pitch);
@@ -104,7 +98,8 @@ __device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int t0, in
     const int r0 = min(t0, o.rows - 1);
     l.base = uni(o.p + (size_t)r0 * o.pitch);
     l.step = 128;
-    l.rows = -1;
+    // a wavefront whose rows all lie past the last one loads nothing (range 0)
+    l.rows = t0 + w * C::NI * 8 < o.rows ? -uni(steps) : 0;
 #pragma unroll
     for (int i = 0; i < C::NI; ++i) {
       const int r = (w * C::NI + i) * 8 + (lane >> 3);
@@ -119,15 +114,16 @@ __device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int t0, in
 // This wavefront's loads of a tile at (m0, n0): wavefronts 0-3 A, 4-7 B.
 template <class C>
 __device__ __forceinline__ TgLoad tg_prepare(const TgOperand& A, const TgOperand& B, int m0, int n0,
-                                             int wave, int lane, uint32_t (&off)[C::NI]) {
-  if (wave < 4) return tg_prepare_side<C, C::ACOL>(A, m0, wave, lane, off);
-  return tg_prepare_side<C, C::BCOL>(B, n0, wave - 4, lane, off);
+                                             int steps, int wave, int lane,
+                                             uint32_t (&off)[C::NI]) {
+  if (wave < 4) return tg_prepare_side<C, C::ACOL>(A, m0, steps, wave, lane, off);
+  return tg_prepare_side<C, C::BCOL>(B, n0, steps, wave - 4, lane, off);
 }
 
 // Bytes from the k-step's base that its loads may touch; later ones read zeros.
 template <class C>
 __device__ __forceinline__ int tg_range(const TgLoad& l, int s) {
-  if (l.rows < 0) return 0x7fffffff;
+  if (l.rows < 0) return s < -l.rows ? 0x7fffffff : 0;
   return min(max(l.rows - C::KS * s, 0), C::KS) * (int)l.pitch;
 }
 
@@ -137,44 +133,62 @@ __device__ __forceinline__ uint2 tg_read_tr(const uint8_t* p) {
   return __builtin_bit_cast(uint2, v);
 }
 
-// Fragment of k-group kg (16 indices), 32 rows (columns) from `at`: lane l
-// holds row l % 32, indices 8 (l / 32) .. of the group.  Transposing reads:
-// within each 16-lane group lane l names contraction row (l % 16) / 4 (+ 4 for
-// the upper four) at column 16 ((l / 16) % 2) + 4 (l % 4).
+// Fragment of k-group kg (16 indices), 32 rows (columns) of a tile, at 32 u: lane l
+// holds row l % 32, indices 8 (l / 32) .. of the group.
+//
+// Column layout, transposing reads: within each 16-lane group lane l names contraction
+// row k = 8 (l / 32) + (l % 16) / 4 (+ 4 for the upper four) of the group at column
+// 16 ((l / 16) % 2) + 4 (l % 4) of the fragment.  Its chunk is 4 u + c, c < 4, rotated
+// to 4 (u ^ (k & 3)) + c: everything but u % 4 and the lane is a constant offset.
 template <int W, bool COL>
-__device__ __forceinline__ u32x4 tg_frag(const uint8_t* rd, int kg, int at, int lane) {
+__device__ __forceinline__ u32x4 tg_frag(const uint8_t* rd, int kg, int u_const, int u_wave,
+                                         int lane) {
   if constexpr (COL) {
-    const int k = kg * 16 + 8 * (lane >> 5) + ((lane & 15) >> 2);
-    const int n = at + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-    const uint2 lo = tg_read_tr(rd + tg_col_offset<W>(k, n));
-    const uint2 hi = tg_read_tr(rd + tg_col_offset<W>(k + 4, n));
+    const int k = 8 * (lane >> 5) + ((lane & 15) >> 2), n = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    // u = u_const + u_wave: the low two bits of u_const + u_wave, without a carry
+    const int low = ((u_const & 3) + u_wave) ^ (k & 3);
+    const uint8_t* p = rd + k * (2 * W) + low * 64 + (n >> 3) * 16 + (n & 7) * 2 +
+                       (kg * 16 * (2 * W) + (u_const >> 2) * 256);
+    const uint2 lo = tg_read_tr(p), hi = tg_read_tr(p + 4 * 2 * W);
     return u32x4{lo.x, lo.y, hi.x, hi.y};
   } else {
-    return *(const u32x4*)(rd + lds_chunk_offset(at + (lane & 31), kg * 2 + (lane >> 5)));
+    return *(const u32x4*)(rd + lds_chunk_offset(u_wave * 32 + (lane & 31), kg * 2 + (lane >> 5)) +
+                           u_const * 32 * 128);
   }
 }
 
-template <class C>
+// The wavefronts' fragments interleave: fragment (fm, fn) of wavefront (wm, wn) is
+// rows (4 fm + wm) 32 .. and columns (2 fn + wn) 32 .. of the tile, so a tile whose
+// matrix ends after half its rows (or half its columns) leaves out whole fragments
+// of every wavefront, and the eight stay balanced.
+template <class C, int FMA>
 __device__ __forceinline__ void tg_frags_a(const uint8_t* __restrict__ rd, int kg, int wm, int lane,
                                            u32x4 (&f)[C::FM]) {
 #pragma unroll
-  for (int i = 0; i < C::FM; ++i) f[i] = tg_frag<C::BM, C::ACOL>(rd, kg, (wm * C::FM + i) * 32, lane);
+  for (int i = 0; i < FMA; ++i) f[i] = tg_frag<C::BM, C::ACOL>(rd, kg, 4 * i, wm, lane);
 }
-template <class C>
+template <class C, int FNA>
 __device__ __forceinline__ void tg_frags_b(const uint8_t* __restrict__ rd, int kg, int wn, int lane,
                                            u32x4 (&f)[C::FN]) {
 #pragma unroll
-  for (int i = 0; i < C::FN; ++i)
-    f[i] = tg_frag<C::BN, C::BCOL>(rd + C::BM * 128, kg, (wn * C::FN + i) * 32, lane);
+  for (int i = 0; i < FNA; ++i)
+    f[i] = tg_frag<C::BN, C::BCOL>(rd + C::BM * 128, kg, 2 * i, wn, lane);
 }
 
-template <class C>
+// The fragments a tile multiplies: FMA x FNA of the configuration's FM x FN;
+// TRI leaves out the lower left quarter (a symmetric product's diagonal tile).
+template <class C, bool TRI>
+__device__ __forceinline__ constexpr bool tg_skip(int fm, int fn) {
+  return TRI && fm >= C::FM / 2 && fn < C::FN / 2;
+}
+template <class C, int FMA, int FNA, bool TRI>
 __device__ __forceinline__ void tg_products(const u32x4 (&a)[C::FM], const u32x4 (&b)[C::FN],
                                             f32x16 (&acc)[C::FM][C::FN]) {
 #pragma unroll
-  for (int fm = 0; fm < C::FM; ++fm)
+  for (int fm = 0; fm < FMA; ++fm)
 #pragma unroll
-    for (int fn = 0; fn < C::FN; ++fn) {
+    for (int fn = 0; fn < FNA; ++fn) {
+      if (tg_skip<C, TRI>(fm, fn)) continue;
       const u32x4 x = C::SWAP ? b[fn] : a[fm], y = C::SWAP ? a[fm] : b[fn];
       if constexpr (C::SPLIT)
         acc[fm][fn] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
@@ -185,115 +199,288 @@ __device__ __forceinline__ void tg_products(const u32x4 (&a)[C::FM], const u32x4
     }
 }
 
-// Order of one group of FM * FN MFMAs with NR LDS reads and ND loads spread over it.
+// Order of one group of MF MFMAs with NR LDS reads and ND loads: the reads directly
+// behind the first MFMAs (one each, two where there are more), so that the rest of the
+// group covers their latency, also before a barrier that waits for them; the loads
+// behind the reads, which the next group needs first.
 template <int MF, int NR, int ND>
 __device__ __forceinline__ void tg_order() {
+  constexpr int PER = (NR + MF - 1) / MF > 1 || (ND > 0 && MF > 2) ? 2 : 1;
+  constexpr int RM = PER > 0 ? (NR + PER - 1) / PER : 0;            // MFMAs followed by reads
+  constexpr int DM = MF - (RM < MF ? RM : MF - 1);                  // MFMAs followed by loads
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
 #pragma unroll
-    for (int r = m * NR / MF; r < (m + 1) * NR / MF; ++r)
+    for (int r = m * PER; r < (m + 1) * PER && r < NR; ++r)
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (m >= MF - DM) {
+      const int i = m - (MF - DM);
 #pragma unroll
-    for (int r = m * ND / MF; r < (m + 1) * ND / MF; ++r)
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      for (int r = i * ND / DM; r < (i + 1) * ND / DM; ++r)
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
   }
+#pragma unroll
+  for (int r = MF * PER; r < NR; ++r) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
 }
 
-// One k-step out of ring slot `rd`, the next one's loads (`db` + off into `wr`,
-// range `nrec`: 0 reads zeros without touching memory) issued under its first
-// MFMAs, every fragment read one group ahead of its use.
+// Fragments that pass from one k-step to the next: on entry a[0] / b[0] hold the first
+// group of 16 indices (split: of its hi halves).
 template <class C>
-__device__ __forceinline__ void tg_step(const uint8_t* __restrict__ rd, int wm, int wn, int lane,
-                                        f32x16 (&acc)[C::FM][C::FN], const uint8_t* db,
-                                        const uint32_t (&off)[C::NI], uint8_t* __restrict__ wr,
-                                        int nrec) {
-  constexpr int MF = C::FM * C::FN, HALF = C::NI / 2;
-  constexpr int RA = C::FM * (C::ACOL ? 2 : 1), RB = C::FN * (C::BCOL ? 2 : 1);
+struct TgFrags {
+  u32x4 a[2][C::FM], b[2][C::FN];
+};
+
+// One k-step out of ring slot `rd`, every fragment read one group ahead of its use.
+// The barrier stands before the last group, whose fragments are in registers by
+// then: `rd` is free, the next k-step (slot `nx`) has landed, and the last group's
+// MFMAs cover both the reads of the next k-step's first fragments and the loads of
+// the one after it (`db` + off into `wr`, range `nrec`: 0 reads zeros without
+// touching memory).  `wr` is `rd` again, under a name of its own: with the loads and
+// the reads in separate restrict scopes the compiler does not make every fragment
+// read wait for the loads in flight, and the barrier's fences keep their order.
+template <class C, int FMA, int FNA, bool TRI>
+__device__ __forceinline__ void tg_step(const uint8_t* __restrict__ rd,
+                                        const uint8_t* __restrict__ nx, int wm, int wn, int lane,
+                                        TgFrags<C>& f, f32x16 (&acc)[C::FM][C::FN],
+                                        const uint8_t* db, const uint32_t (&off)[C::NI],
+                                        uint8_t* __restrict__ wr, int nrec, bool first) {
+  constexpr int MF = FMA * FNA - (TRI ? C::FM * C::FN / 4 : 0);
+  constexpr int RA = FMA * (C::ACOL ? 2 : 1), RB = FNA * (C::BCOL ? 2 : 1);
   if constexpr (C::SPLIT) {
     // per 16 indices: hi hi', hi lo', lo hi'
-    u32x4 ah[2][C::FM], bh[2][C::FN], al[2][C::FM], bl[2][C::FN];
-    tg_frags_a<C>(rd, 0, wm, lane, ah[0]);
-    tg_frags_b<C>(rd, 0, wn, lane, bh[0]);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int i = h * HALF; i < (h + 1) * HALF; ++i) dma16(db, off[i], wr + i * 1024, nrec);
-      tg_frags_b<C>(rd, 2 + h, wn, lane, bl[h]);
-      tg_products<C>(ah[h], bh[h], acc);
-      tg_frags_a<C>(rd, 2 + h, wm, lane, al[h]);
-      tg_products<C>(ah[h], bl[h], acc);
-      if (h == 0) {
-        tg_frags_a<C>(rd, 1, wm, lane, ah[1]);
-        tg_frags_b<C>(rd, 1, wn, lane, bh[1]);
-      }
-      tg_products<C>(al[h], bh[h], acc);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x100, RA + RB, 0);
-    tg_order<MF, RB, HALF>();
+    u32x4 al[C::FM], bl[C::FN];
+    tg_frags_b<C, FNA>(rd, 2, wn, lane, bl);
+    tg_products<C, FMA, FNA, TRI>(f.a[0], f.b[0], acc);
+    tg_frags_a<C, FMA>(rd, 2, wm, lane, al);
+    tg_products<C, FMA, FNA, TRI>(f.a[0], bl, acc);
+    tg_frags_a<C, FMA>(rd, 1, wm, lane, f.a[1]);
+    tg_frags_b<C, FNA>(rd, 1, wn, lane, f.b[1]);
+    tg_products<C, FMA, FNA, TRI>(al, f.b[0], acc);
+    tg_frags_b<C, FNA>(rd, 3, wn, lane, bl);
+    tg_products<C, FMA, FNA, TRI>(f.a[1], f.b[1], acc);
+    tg_frags_a<C, FMA>(rd, 3, wm, lane, al);
+    tg_products<C, FMA, FNA, TRI>(f.a[1], bl, acc);
+    tg_order<MF, RB, 0>();
     tg_order<MF, RA, 0>();
     tg_order<MF, RA + RB, 0>();
-    tg_order<MF, RB, HALF>();
+    tg_order<MF, RB, 0>();
     tg_order<MF, RA, 0>();
-    tg_order<MF, 0, 0>();
+    if (!first) MOE_WAIT_VMCNT(0);
+    lds_sync();
+    tg_frags_a<C, FMA>(nx, 0, wm, lane, f.a[0]);
+    tg_frags_b<C, FNA>(nx, 0, wn, lane, f.b[0]);
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) dma16(db, off[i], wr + i * 1024, nrec);
+    tg_products<C, FMA, FNA, TRI>(al, f.b[1], acc);
+    tg_order<MF, RA + RB, C::NI>();
   } else {
-    u32x4 a[2][C::FM], b[2][C::FN];
-    tg_frags_a<C>(rd, 0, wm, lane, a[0]);
-    tg_frags_b<C>(rd, 0, wn, lane, b[0]);
 #pragma unroll
-    for (int kg = 0; kg < 4; ++kg) {
-      if (kg < 2) {
-#pragma unroll
-        for (int i = kg * HALF; i < (kg + 1) * HALF; ++i) dma16(db, off[i], wr + i * 1024, nrec);
-      }
-      if (kg < 3) {
-        tg_frags_a<C>(rd, kg + 1, wm, lane, a[(kg + 1) & 1]);
-        tg_frags_b<C>(rd, kg + 1, wn, lane, b[(kg + 1) & 1]);
-      }
-      tg_products<C>(a[kg & 1], b[kg & 1], acc);
+    for (int kg = 0; kg < 3; ++kg) {
+      tg_frags_a<C, FMA>(rd, kg + 1, wm, lane, f.a[(kg + 1) & 1]);
+      tg_frags_b<C, FNA>(rd, kg + 1, wn, lane, f.b[(kg + 1) & 1]);
+      tg_products<C, FMA, FNA, TRI>(f.a[kg & 1], f.b[kg & 1], acc);
     }
-    __builtin_amdgcn_sched_group_barrier(0x100, RA + RB, 0);
-    tg_order<MF, RA + RB, HALF>();
-    tg_order<MF, RA + RB, HALF>();
     tg_order<MF, RA + RB, 0>();
-    tg_order<MF, 0, 0>();
+    tg_order<MF, RA + RB, 0>();
+    tg_order<MF, RA + RB, 0>();
+    if (!first) MOE_WAIT_VMCNT(0);
+    lds_sync();
+    tg_frags_a<C, FMA>(nx, 0, wm, lane, f.a[0]);
+    tg_frags_b<C, FNA>(nx, 0, wn, lane, f.b[0]);
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) dma16(db, off[i], wr + i * 1024, nrec);
+    tg_products<C, FMA, FNA, TRI>(f.a[1], f.b[1], acc);
+    tg_order<MF, RA + RB, C::NI>();
   }
 }
 
 // Row and column (inside the tile) of accumulator register r of fragment (fm, fn).
 template <class C>
 __device__ __forceinline__ int tg_row(int wm, int fm, int lane, int r) {
-  return (wm * C::FM + fm) * 32 + (C::SWAP ? (lane & 31) : 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3));
+  return (4 * fm + wm) * 32 + (C::SWAP ? (lane & 31) : 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3));
 }
 template <class C>
 __device__ __forceinline__ int tg_col(int wn, int fn, int lane, int r) {
-  return (wn * C::FN + fn) * 32 + (C::SWAP ? 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) : (lane & 31));
+  return (2 * fn + wn) * 32 + (C::SWAP ? 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) : (lane & 31));
 }
 
-// The persistent loop over the tiles start, start + stride, .. < end of problem P:
-//   P::Tile        { TgOperand A, B; int m0, n0, steps; ... }
-//   p.tile(L)      the L-th tile (wavefront-uniform)
-//   p.store(t, wm, wn, lane, acc)   the epilogue, from registers
-// After a tile's last k-step the next tile's first one is already loading
-// while the tile is written out.
+// The four 8-byte groups a lane holds of a fragment's 32 consecutive elements
+// (group g: elements 8g + 4 (lane / 32) ..) as two 16-byte runs: after exchanging
+// halves between lanes l and l + 32, r0 is elements 8 (lane / 32) .. and r1 the same
+// 16 further on.
+__device__ __forceinline__ void tg_runs16(uint2 (&w)[4], u32x4& r0, u32x4& r1) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w[0].x, w[1].x, false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(w[0].y, w[1].y, false, false);
+  const auto c = __builtin_amdgcn_permlane32_swap(w[2].x, w[3].x, false, false);
+  const auto d = __builtin_amdgcn_permlane32_swap(w[2].y, w[3].y, false, false);
+  r0 = u32x4{a[0], b[0], a[1], b[1]};
+  r1 = u32x4{c[0], d[0], c[1], d[1]};
+}
+
+// Transposes the 4 x 4 16-bit values of four neighbouring lanes: lane j holds
+// values (0..3, j) and receives (j, 0..3).
+__device__ __forceinline__ uint2 tg_quad_transpose(uint2 v, int lane) {
+  const bool odd = lane & 1, up = lane & 2;
+  // with lane ^ 1: even lanes take values 0 and 2, odd ones 1 and 3, of both
+  const uint32_t tx = __builtin_amdgcn_mov_dpp(v.x, 0xB1, 0xf, 0xf, true);
+  const uint32_t ty = __builtin_amdgcn_mov_dpp(v.y, 0xB1, 0xf, 0xf, true);
+  const uint32_t a = odd ? (tx >> 16) | (v.x & 0xffff0000u) : (v.x & 0xffffu) | (tx << 16);
+  const uint32_t b = odd ? (ty >> 16) | (v.y & 0xffff0000u) : (v.y & 0xffffu) | (ty << 16);
+  // with lane ^ 2
+  const uint32_t r = __builtin_amdgcn_mov_dpp(up ? a : b, 0x4E, 0xf, 0xf, true);
+  return up ? uint2{r, b} : uint2{a, r};
+}
+
+// A block's tiles.  The blocks are dealt to the eight XCDs round-robin, and each XCD
+// owns a contiguous range of the tiles, whose neighbours share operands in its L2.  A
+// block starts with the tile of its XCD's range by its index there.  With `counters`
+// (8 zeros) it claims the following ones, from its XCD's range first and then from the
+// others' (the tiles differ in length and the XCDs in clock), else it takes every P-th
+// (P: the XCD's blocks).  Wavefront 0 claims the tile after the next one at a tile's
+// start and passes it on through LDS at its end.
+// (Taking the shorter tiles last for an even end costs more than it saves: a short tile
+// shares its operands with its neighbours, prefill product 328 -> 352 us.)
+struct TgTiles {
+  int n, X, x, y, own;       // y: the range to claim from; own: the block's place in its XCD
+  int32_t* counters;
+
+  __device__ __forceinline__ int blocks(int xcd) const { return ((int)gridDim.x - xcd + X - 1) / X; }
+  // The j-th tile of an XCD's range, or -1.
+  __device__ __forceinline__ int at(int xcd, int j) const {
+    const int a = (int)((long long)n * xcd / X), b = (int)((long long)n * (xcd + 1) / X);
+    return j < b - a ? a + j : -1;
+  }
+  __device__ __forceinline__ void init(int tiles, int32_t* c) {
+    n = tiles;
+    counters = c;
+    X = min(8, (int)gridDim.x);
+    x = y = blockIdx.x % X;
+    own = blockIdx.x / X;
+  }
+  // One whole wavefront: the next tile, or -1.  A range's first entries are the tiles
+  // its own blocks started with, so claims begin behind those.  Once its XCD's range is
+  // used up, eight lanes look at all the counters at once.
+  __device__ __forceinline__ int claim(int lane) {
+    while (true) {
+      int j = 0;
+      if (lane == 0) j = atomicAdd(counters + y, 1);
+      const int t = at(y, blocks(y) + uni(j));
+      if (t >= 0) return t;
+      bool some = false;
+      const int z = (x + lane) % X;
+      if (lane < X)
+        some = at(z, blocks(z) + __hip_atomic_load(counters + z, __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_AGENT)) >= 0;
+      const uint64_t left = __ballot(some);
+      if (left == 0) return -1;
+      y = (x + __builtin_ctzll(left)) % X;
+    }
+  }
+};
+constexpr int kTgCounters = 8;
+constexpr int kTgMinSteps = 3;
+
+// The loads' place in the stream of k-steps of a block's tiles, two k-steps ahead of
+// the multiplication.  Plain scalars: with the tile itself in it the structure ends
+// up in scratch memory.
+struct TgCursor {
+  int hint;
+  int s, steps;      // the tile's next k-step, its k-steps (0: the stream has ended)
+};
+
+// The cursor to tile L (-1: the stream has ended).
 template <class C, class P>
-__device__ __forceinline__ void tg_run(const P& p, int start, int end, int stride,
-                                       uint8_t* __restrict__ lds0, uint8_t* __restrict__ lds1) {
+__device__ __forceinline__ void tg_seek(const P& p, int L, TgCursor& c, TgLoad& ld,
+                                        uint32_t (&off)[C::NI], int wave, int lane) {
+  c.s = 0;
+  c.steps = 0;
+  if (L < 0) return;
+  const typename P::Tile t = p.tile(L, c.hint);
+  c.hint = uni(t.hint);
+  c.steps = max(uni(t.steps), kTgMinSteps);
+  ld = tg_prepare<C>(t.A, t.B, t.m0, t.n0, t.steps, wave, lane, off);
+}
+
+// The k-steps of a tile.  There are at least three (after a short contraction come
+// k-steps of zeros), so the cursor, two ahead, passes to the next tile, which is
+// next(), while this one is multiplied, behind its first barrier.
+template <class C, int FMA, int FNA, bool TRI, class P, class Next>
+__device__ __forceinline__ void tg_tile(const P& p, int steps, int& ph, int wave, int lane,
+                                        Next next, TgCursor& c, TgLoad& ld,
+                                        uint32_t (&off)[C::NI], f32x16 (&acc)[C::FM][C::FN],
+                                        uint8_t* __restrict__ lds0, uint8_t* __restrict__ lds1) {
+  const int wm = wave >> 1, wn = wave & 1;
+  // (opaque: the fragments' LDS addresses stay inside the tile, where they are few,
+  // and do not spill what the epilogue keeps)
+  asm volatile("" : "+v"(lane));
+  // (not carried over from the last tile: that may have read fewer fragments)
+  TgFrags<C> f;
+  tg_frags_a<C, FMA>(ph ? lds1 : lds0, 0, wm, lane, f.a[0]);
+  tg_frags_b<C, FNA>(ph ? lds1 : lds0, 0, wn, lane, f.b[0]);
+  const int all = max(steps, kTgMinSteps);
+  for (int s = 0; s < all; ++s) {
+    const uint8_t* rd = ph ? lds1 : lds0;
+    const uint8_t* nx = ph ? lds0 : lds1;
+    uint8_t* wr = (ph ? lds1 : lds0) + wave * C::NI * 1024;
+    const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
+    const int nrec = uni(c.steps > 0 ? tg_range<C>(ld, c.s) : 0);
+    tg_step<C, FMA, FNA, TRI>(rd, nx, wm, wn, lane, f, acc, db, off, wr, nrec, s == 0);
+    c.s = uni(c.s + 1);
+    if (c.s == c.steps) tg_seek<C>(p, next(), c, ld, off, wave, lane);
+    ph ^= 1;
+  }
+}
+
+// The persistent loop over a block's tiles of problem P:
+//   P::Tile   { TgOperand A, B; int m0, n0, steps, rows, cols, hint; ... }, rows and
+//             cols being the tile's that exist (any number above BM, BN counts as all)
+//   p.tile(L, hint)    the L-th tile; uniform.  hint: an earlier tile's, or 0
+//   p.tri(t)           whether its lower left quarter is left out
+//   p.store(t, wm, wn, lane, acc)   the epilogue, from registers
+template <class C, class P>
+__device__ __forceinline__ void tg_run(const P& p, int tiles, int32_t* counters,
+                                       uint8_t* __restrict__ lds0, uint8_t* __restrict__ lds1,
+                                       int* s_claim) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uni(tid >> 6), wm = wave >> 1, wn = wave & 1;
-  if (start >= end) return;
-  typename P::Tile cur = p.tile(start);
-  uint32_t off[C::NI];
-  TgLoad ld = tg_prepare<C>(cur.A, cur.B, cur.m0, cur.n0, wave, lane, off);
-  int ph = 0;  // ring slot of the current tile's k-step 0
-  {
-    uint8_t* w = lds0 + wave * C::NI * 1024;
-    const int nrec = cur.steps > 0 ? tg_range<C>(ld, 0) : 0;
+  TgTiles q;
+  q.init(tiles, counters);
+  int mine = q.own;
+  int L = q.at(q.x, mine);
+  if (L < 0) return;
+  TgCursor c{0, 0, 0};
+  TgLoad ld{};
+  uint32_t off[C::NI] = {};
+  tg_seek<C>(p, L, c, ld, off, wave, lane);
+  int ph = 0;  // ring slot of the next k-step
 #pragma unroll
-    for (int i = 0; i < C::NI; ++i) dma16(ld.base, off[i], w + i * 1024, nrec);
+  for (int k = 0; k < 2; ++k) {
+    uint8_t* w = (k ? lds1 : lds0) + wave * C::NI * 1024;
+    const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
+    const int nrec = uni(tg_range<C>(ld, c.s));
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) dma16(db, off[i], w + i * 1024, nrec);
+    c.s = uni(c.s + 1);
   }
-  for (int L = start;;) {
-    const int Ln = L + stride;
+  // the next tile
+  if (counters != nullptr && wave == 0) {
+    const int p1 = q.claim(lane);
+    if (lane == 0) *s_claim = p1;
+  }
+  pipe_sync();
+  int L1 = -1;
+  auto next = [&]() -> int {
+    L1 = counters != nullptr ? uni(*s_claim) : q.at(q.x, mine += q.blocks(q.x));
+    return L1;
+  };
+  int hint = 0;
+  while (true) {
+    const typename P::Tile t = p.tile(L, hint);
+    hint = t.hint;
+    int claimed = -1;
+    if (counters != nullptr && wave == 0) claimed = q.claim(lane);
     f32x16 acc[C::FM][C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
@@ -301,61 +488,27 @@ __device__ __forceinline__ void tg_run(const P& p, int start, int end, int strid
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    typename P::Tile nxt = cur;
-    if (cur.steps == 0) {
-      // nothing to multiply: the wait lands the zero loads of this slot before the
-      // next tile's first k-step is loaded into it
-      pipe_sync();
-      if (Ln < end) {
-        nxt = p.tile(Ln);
-        ld = tg_prepare<C>(nxt.A, nxt.B, nxt.m0, nxt.n0, wave, lane, off);
-        uint8_t* w = ((ph & 1) ? lds1 : lds0) + wave * C::NI * 1024;
-        const int nrec = nxt.steps > 0 ? tg_range<C>(ld, 0) : 0;
-#pragma unroll
-        for (int i = 0; i < C::NI; ++i) dma16(ld.base, off[i], w + i * 1024, nrec);
-      }
+    if constexpr (C::FM == 2) {
+      const bool hm = t.rows <= C::BM / 2, hn = t.cols <= C::BN / 2;
+      if (hm && hn) tg_tile<C, 1, 2, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+      else if (hm) tg_tile<C, 1, 4, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+      else if (hn) tg_tile<C, 2, 2, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+      else if (P::SYM && p.tri(t))
+        tg_tile<C, 2, 4, P::SYM>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+      else tg_tile<C, 2, 4, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+    } else {
+      if (t.cols <= C::BN / 2)
+        tg_tile<C, 1, 1, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+      else tg_tile<C, 1, 2, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
     }
-    for (int s = 0; s < cur.steps; ++s) {
-      pipe_sync();  // k-step s has landed; every wavefront is done with the other slot
-      const int q = (ph + s) & 1;
-      const uint8_t* rd = q ? lds1 : lds0;
-      uint8_t* wr = (q ? lds0 : lds1) + wave * C::NI * 1024;
-      const uint8_t* db = ld.base + (size_t)(s + 1) * ld.step;
-      int nrec = tg_range<C>(ld, s + 1);
-      if (s + 1 == cur.steps) {
-        nrec = 0;
-        db = ld.base;
-        if (Ln < end) {
-          nxt = p.tile(Ln);
-          ld = tg_prepare<C>(nxt.A, nxt.B, nxt.m0, nxt.n0, wave, lane, off);
-          db = ld.base;
-          if (nxt.steps > 0) nrec = tg_range<C>(ld, 0);
-        }
-      }
-      tg_step<C>(rd, wm, wn, lane, acc, uni(db), off, wr, uni(nrec));
-    }
-    p.store(cur, wm, wn, lane, acc);
-    ph += cur.steps;
-    if (Ln >= end) break;
-    L = Ln;
-    cur = nxt;
+    // the loads in flight are waited for here (the next tile's second k-step; the first
+    // one landed before the last barrier), so its loop needs no wait of its own for them
+    MOE_WAIT_VMCNT(0);
+    if (counters != nullptr && tid == 0) *s_claim = claimed;  // read behind its first barrier
+    p.store(t, wm, wn, lane, acc);
+    if (L1 < 0) break;
+    L = L1;
   }
-  MOE_WAIT_VMCNT(0);  // no direct-to-LDS load outlives the block
-}
-
-// The tiles [start, end) and stride of this block: the blocks are dealt to the
-// eight XCDs round-robin, and each XCD takes a contiguous range, whose
-// neighbouring tiles share operands in its L2.
-struct TgShare {
-  int start, end, stride;
-};
-__device__ __forceinline__ TgShare tg_share(int total) {
-  const int g = gridDim.x, X = min(8, g), x = blockIdx.x % X;
-  TgShare s;
-  s.end = (int)((long long)total * (x + 1) / X);
-  s.start = (int)((long long)total * x / X) + blockIdx.x / X;
-  s.stride = (g - x + X - 1) / X;
-  return s;
 }
 
 // v * 2^e as two float16.
