@@ -284,6 +284,12 @@ __global__ __launch_bounds__(kTgThreads, C::SLOT > 32768 ? 2 : 4) void grouped_k
 }
 
 // ---------------------------------------------------------------- operand preparation
+// float32 rows -> split rows.  One wavefront per row; lane l takes the 8-element chunks
+// l, l + 64, ..: 32 bytes read, 16 bytes of hi and of lo written, each row read once
+// (it stays in registers between the maximum and the split; longer ones are read
+// again).  HBM bound.
+constexpr int kRowChunks = 4;  // chunks per lane held in registers: rows up to 2048
+
 // Exponent that brings a largest magnitude to [2^13, 2^14); `none` if all is zero.
 __device__ __forceinline__ int split_exponent(float most, int none = 0) {
   return most > 0.f ? 13 - ilogbf(most) : none;
@@ -296,67 +302,108 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// Writes one float32 row of `width` values as split units, scaled by 2^ex, zeros
-// in the padding.  One wavefront; lane l takes the pairs of elements 2l + 128 i.
-__device__ __forceinline__ void split_row(const float* __restrict__ src, int width, int ex,
-                                          uint8_t* __restrict__ dst, int lane) {
-  const int padded = (width + 31) & ~31;
-  for (int j = 2 * lane; j < padded; j += 128) {
-    uint16_t h[2], l[2];
+__device__ __forceinline__ float chunk_max(const float (&f)[8]) {
+  float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      split_f16(j + e < width ? ldexpf(src[j + e], ex) : 0.f, h[e], l[e]);
-    uint8_t* d = dst + split_at(j);
-    *(uint32_t*)d = h[0] | ((uint32_t)h[1] << 16);
-    *(uint32_t*)(d + 64) = l[0] | ((uint32_t)l[1] << 16);
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+  return m;
+}
+// Splits one row; `exponent` gives the scale from the row's largest magnitude.
+template <class F>
+__device__ __forceinline__ int split_row(const float* __restrict__ src, int width,
+                                         uint8_t* __restrict__ dst, int lane, F exponent) {
+  const int padded = (width + 31) & ~31;
+  float f[kRowChunks][8], m = 0.f;
+#pragma unroll
+  for (int c = 0; c < kRowChunks; ++c) load_chunk<ElemF32>(src, 8 * (lane + 64 * c), width, f[c]);
+#pragma unroll
+  for (int c = 0; c < kRowChunks; ++c) m = fmaxf(m, chunk_max(f[c]));
+  for (int j = 8 * (lane + 64 * kRowChunks); j < width; j += 512) {
+    float g[8];
+    load_chunk<ElemF32>(src, j, width, g);
+    m = fmaxf(m, chunk_max(g));
   }
+  const int ex = exponent(wave_max(m));
+#pragma unroll
+  for (int c = 0; c < kRowChunks; ++c) {
+    const int j = 8 * (lane + 64 * c);
+    if (j < padded) store_chunk(f[c], dst, j, ex);
+  }
+  for (int j = 8 * (lane + 64 * kRowChunks); j < padded; j += 512) {
+    float g[8];
+    load_chunk<ElemF32>(src, j, width, g);
+    store_chunk(g, dst, j, ex);
+  }
+  return ex;
 }
 
-// Rows with a scale of their own: four rows per block.
-__global__ __launch_bounds__(256) void split_rows_kernel(const float* __restrict__ src,
-                                                         long long rows, int width,
-                                                         uint8_t* __restrict__ dst, uint32_t pitch,
-                                                         int32_t* __restrict__ ex, int none) {
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+// One kind of rows of a launch: four rows per block.
+struct SplitRows {
+  const float* src;
+  uint8_t* dst;
+  int32_t* ex;      // per row
+  long long rows;
+  uint32_t pitch;
+  int width, none;  // none: the exponent of an all-zero row
+};
+__host__ __device__ inline unsigned blocks_of(long long rows) { return (unsigned)((rows + 3) / 4); }
+__device__ __forceinline__ void split_rows(const SplitRows& a, unsigned block) {
+  const long long r = (long long)block * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  if (r >= rows) return;
-  const float* s = src + r * width;
-  float m = 0.f;
-  for (int j = lane; j < width; j += 64) m = fmaxf(m, fabsf(s[j]));
-  const int e = split_exponent(wave_max(m), none);
-  if (lane == 0) ex[r] = e;
-  split_row(s, width, e == none ? 0 : e, dst + r * pitch, lane);
+  if (r >= a.rows) return;
+  const float* src = a.src + r * a.width;
+  int mark = 0;
+  split_row(src, a.width, a.dst + r * a.pitch, lane, [&](float m) {
+    mark = split_exponent(m, a.none);
+    return m > 0.f ? mark : 0;
+  });
+  if (lane == 0) a.ex[r] = mark;
+}
+// The forward's operands, in one launch.
+__global__ __launch_bounds__(256) void split_two_kernel(SplitRows a, SplitRows b) {
+  const unsigned n = blocks_of(a.rows);
+  if (blockIdx.x < n) split_rows(a, blockIdx.x);
+  else split_rows(b, blockIdx.x - n);
 }
 
 // w by expert: partial maxima of kMaxChunks row ranges per expert, then the rows
 // with their expert's scale.
-constexpr int kMaxChunks = 32;
-__global__ __launch_bounds__(256) void expert_max_kernel(const float* __restrict__ w, long long per,
-                                                         float* __restrict__ part) {
+constexpr int kMaxChunks = 64;
+struct SplitExperts {
+  const float* w;
+  float* part;      // [E][kMaxChunks]
+  uint8_t* dst;
+  int32_t* ex;      // [E]
+  long long rows;   // E * n
+  uint32_t pitch;
+  int E, n, k;
+};
+__device__ __forceinline__ void expert_max(const SplitExperts& a, unsigned block) {
   __shared__ float s[4];
-  const float* src = w + (long long)blockIdx.y * per;
-  const long long a = per * blockIdx.x / kMaxChunks, b = per * (blockIdx.x + 1) / kMaxChunks;
+  const int e = block / kMaxChunks, c = block % kMaxChunks, lane = threadIdx.x & 63;
+  const float* src = a.w + (long long)e * a.n * a.k;
+  const int lo = (int)((long long)a.n * c / kMaxChunks), hi = (int)((long long)a.n * (c + 1) / kMaxChunks);
   float m = 0.f;
-  for (long long i = a + threadIdx.x; i < b; i += 256) m = fmaxf(m, fabsf(src[i]));
+  for (int r = lo + (threadIdx.x >> 6); r < hi; r += 4)
+    for (int j = 8 * lane; j < a.k; j += 512) {
+      float g[8];
+      load_chunk<ElemF32>(src + (long long)r * a.k, j, a.k, g);
+      m = fmaxf(m, chunk_max(g));
+    }
   m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
+  if (lane == 0) s[threadIdx.x >> 6] = m;
   __syncthreads();
-  if (threadIdx.x == 0)
-    part[blockIdx.y * kMaxChunks + blockIdx.x] = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+  if (threadIdx.x == 0) a.part[block] = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
 }
-__global__ __launch_bounds__(256) void split_experts_kernel(const float* __restrict__ w, int n,
-                                                            int k, long long rows,
-                                                            const float* __restrict__ part,
-                                                            uint8_t* __restrict__ dst,
-                                                            uint32_t pitch,
-                                                            int32_t* __restrict__ ex) {
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+__device__ __forceinline__ void split_expert_rows(const SplitExperts& a, unsigned block) {
+  const long long r = (long long)block * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  if (r >= rows) return;
-  const int e = (int)(r / n);
-  const int x = split_exponent(wave_max(part[e * kMaxChunks + lane % kMaxChunks]));
-  if (lane == 0 && r % n == 0) ex[e] = x;
-  split_row(w + r * k, k, x, dst + r * pitch, lane);
+  if (r >= a.rows) return;
+  const int e = (int)(r / a.n);
+  static_assert(kMaxChunks == 64, "one partial maximum per lane");
+  const int x = split_exponent(wave_max(a.part[e * kMaxChunks + lane]));
+  if (lane == 0 && r % a.n == 0) a.ex[e] = x;
+  split_row(a.w + r * a.k, a.k, a.dst + r * a.pitch, lane, [&](float) { return x; });
 }
 
 // x for the weight gradient: row r is scaled by 2^(C - a_r), a_r the exponent of
@@ -365,54 +412,72 @@ __global__ __launch_bounds__(256) void split_experts_kernel(const float* __restr
 // the groups (rows outside them are not read), then C = 13 - the largest.  Rows
 // whose dy is zero contribute nothing and are written as zeros.
 constexpr int kRowParts = 256;
-__device__ __forceinline__ void group_span(const int32_t* __restrict__ offsets, int E, int M,
-                                           int lane, int& first, int& last) {
+struct SplitPairs {
+  const float* x;
+  const int32_t* offsets;
+  const int32_t* ea;  // a_r
+  int32_t* part;      // [kRowParts]
+  uint8_t* dst;
+  int32_t* ex;        // C
+  uint32_t pitch;
+  int width, E, M;
+};
+__device__ __forceinline__ void group_span(const SplitPairs& a, int lane, int& first, int& last) {
   int hi = 0;
-  for (int e = lane; e <= E; e += 64) hi = max(hi, min(max(offsets[e], 0), M));
+  for (int e = lane; e <= a.E; e += 64) hi = max(hi, min(max(a.offsets[e], 0), a.M));
 #pragma unroll
   for (int k = 32; k > 0; k >>= 1) hi = max(hi, __shfl_xor(hi, k));
-  first = min(max(offsets[0], 0), M);
+  first = min(max(a.offsets[0], 0), a.M);
   last = max(hi, first);
 }
-__global__ __launch_bounds__(256) void pair_max_kernel(const float* __restrict__ x, int width,
-                                                       const int32_t* __restrict__ offsets, int E,
-                                                       int M, const int32_t* __restrict__ ea,
-                                                       int32_t* __restrict__ part) {
+__device__ __forceinline__ void pair_max(const SplitPairs& a, unsigned block) {
   __shared__ int s[4];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int first, last, most = kNoRow;
-  group_span(offsets, E, M, lane, first, last);
-  for (long long r = first + blockIdx.x * 4 + w; r < last; r += 4 * kRowParts) {
+  group_span(a, lane, first, last);
+  for (long long r = first + block * 4 + w; r < last; r += 4 * kRowParts) {
     float m = 0.f;
-    for (int j = lane; j < width; j += 64) m = fmaxf(m, fabsf(x[r * width + j]));
+    for (int j = 8 * lane; j < a.width; j += 512) {
+      float g[8];
+      load_chunk<ElemF32>(a.x + r * a.width, j, a.width, g);
+      m = fmaxf(m, chunk_max(g));
+    }
     m = wave_max(m);
-    if (m > 0.f && ea[r] != kNoRow) most = max(most, ilogbf(m) - ea[r]);
+    if (m > 0.f && a.ea[r] != kNoRow) most = max(most, ilogbf(m) - a.ea[r]);
   }
   if (lane == 0) s[w] = most;
   __syncthreads();
-  if (threadIdx.x == 0) part[blockIdx.x] = max(max(s[0], s[1]), max(s[2], s[3]));
+  if (threadIdx.x == 0) a.part[block] = max(max(s[0], s[1]), max(s[2], s[3]));
 }
-__global__ __launch_bounds__(256) void split_pair_kernel(const float* __restrict__ x, int width,
-                                                         const int32_t* __restrict__ offsets, int E,
-                                                         int M, const int32_t* __restrict__ ea,
-                                                         const int32_t* __restrict__ part,
-                                                         uint8_t* __restrict__ dst, uint32_t pitch,
-                                                         int32_t* __restrict__ ex) {
+__global__ __launch_bounds__(256) void split_pair_kernel(SplitPairs a) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int first, last, most = kNoRow;
-  for (int i = lane; i < kRowParts; i += 64) most = max(most, part[i]);
+  for (int i = lane; i < kRowParts; i += 64) most = max(most, a.part[i]);
 #pragma unroll
   for (int k = 32; k > 0; k >>= 1) most = max(most, __shfl_xor(most, k));
   const int C = most == kNoRow ? 0 : 13 - most;
-  if (blockIdx.x == 0 && threadIdx.x == 0) ex[0] = C;
-  group_span(offsets, E, M, lane, first, last);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.ex[0] = C;
+  group_span(a, lane, first, last);
   const long long r = first + (long long)blockIdx.x * 4 + w;
   if (r >= last) return;
-  if (ea[r] != kNoRow) {
-    split_row(x + r * width, width, C - ea[r], dst + r * pitch, lane);
+  if (a.ea[r] != kNoRow) {
+    split_row(a.x + r * a.width, a.width, a.dst + r * a.pitch, lane, [&](float) { return C - a.ea[r]; });
   } else {
-    for (uint32_t b = 4 * lane; b < pitch; b += 256) *(uint32_t*)(dst + r * pitch + b) = 0;
+    for (uint32_t b = 4 * lane; b < a.pitch; b += 256) *(uint32_t*)(a.dst + r * a.pitch + b) = 0;
   }
+}
+
+// The backward's operands in two launches before the last one's: what needs nothing
+// (dy's rows, w's maxima), then what needs those (w's rows, the pairs' maxima).
+__global__ __launch_bounds__(256) void backward_first_kernel(SplitRows dy, SplitExperts w) {
+  const unsigned n = blocks_of(dy.rows);
+  if (blockIdx.x < n) split_rows(dy, blockIdx.x);
+  else expert_max(w, blockIdx.x - n);
+}
+__global__ __launch_bounds__(256) void backward_second_kernel(SplitExperts w, SplitPairs x) {
+  const unsigned n = blocks_of(w.rows);
+  if (blockIdx.x < n) split_expert_rows(w, blockIdx.x);
+  else pair_max(x, blockIdx.x - n);
 }
 
 // bfloat16 rows whose length does not suit the loads, copied into rows of whole
@@ -474,7 +539,7 @@ hipError_t pick_product(const GroupedArgs& a, const GroupedProduct& p, hipStream
   return run_product<TgConfig<2, 4, AC, BC, SPLIT, SW>, DIR>(p, st);
 }
 
-unsigned row_blocks(long long rows) { return (unsigned)((rows + 3) / 4); }
+unsigned row_blocks(long long rows) { return blocks_of(rows); }
 
 // The workspace's regions: which are needed, and where they lie.
 struct GroupedPlan {
@@ -555,8 +620,9 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
   const long long wr = (long long)a.E * a.n;
   if (dtype == 0) {
     p.pitch_a = p.pitch_b = (uint32_t)split_pitch(a.k);
-    split_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const float*)a.x, a.M, a.k, w.x, p.pitch_a, w.ex, 0);
-    split_rows_kernel<<<row_blocks(wr), 256, 0, st>>>((const float*)a.w, wr, a.k, w.w, p.pitch_b, w.ew, 0);
+    const SplitRows rx{(const float*)a.x, w.x, w.ex, a.M, p.pitch_a, a.k, 0};
+    const SplitRows rw{(const float*)a.w, w.w, w.ew, wr, p.pitch_b, a.k, 0};
+    split_two_kernel<<<row_blocks(a.M) + row_blocks(wr), 256, 0, st>>>(rx, rw);
     p.A = w.x;
     p.B = w.w;
     p.ea = w.ex;
@@ -586,20 +652,18 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   if (dtype == 0) {
     px = pw = (uint32_t)split_pitch(a.k);
     py = (uint32_t)split_pitch(a.n);
-    if (a.M > 0)
-      split_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const float*)a.dy, a.M, a.n, w.dy, py, w.ey, kNoRow);
+    const SplitRows ry{(const float*)a.dy, w.dy, w.ey, a.M, py, a.n, kNoRow};
+    SplitExperts we{};
+    if (dx) we = {(const float*)a.w, w.wmax, w.w, w.ew, wr, pw, a.E, a.n, a.k};
+    const SplitPairs xp{(const float*)a.x, a.offsets, w.ey, w.parts, w.x, w.ex, px, a.k, a.E, a.M};
+    const unsigned b1 = row_blocks(a.M) + (dx ? a.E * kMaxChunks : 0);
+    const unsigned b2 = (dx ? row_blocks(wr) : 0) + (dw ? kRowParts : 0);
+    if (b1 > 0) backward_first_kernel<<<b1, 256, 0, st>>>(ry, we);
+    backward_second_kernel<<<b2, 256, 0, st>>>(we, xp);
+    if (dw) split_pair_kernel<<<std::max(1u, row_blocks(a.M)), 256, 0, st>>>(xp);
     dy = w.dy;
-    if (dx) {
-      expert_max_kernel<<<dim3(kMaxChunks, a.E), 256, 0, st>>>((const float*)a.w, (long long)a.n * a.k, w.wmax);
-      split_experts_kernel<<<row_blocks(wr), 256, 0, st>>>((const float*)a.w, a.n, a.k, wr, w.wmax, w.w, pw, w.ew);
-      wt = w.w;
-    }
-    if (dw) {
-      pair_max_kernel<<<kRowParts, 256, 0, st>>>((const float*)a.x, a.k, a.offsets, a.E, a.M, w.ey, w.parts);
-      split_pair_kernel<<<std::max(1u, row_blocks(a.M)), 256, 0, st>>>((const float*)a.x, a.k, a.offsets, a.E, a.M,
-                                                        w.ey, w.parts, w.x, px, w.ex);
-      x = w.x;
-    }
+    wt = w.w;
+    x = w.x;
   } else {
     if (w.dy != nullptr && a.M > 0) {
       py = pad_pitch(a.n);

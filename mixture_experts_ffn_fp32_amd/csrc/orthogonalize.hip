@@ -255,11 +255,19 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const void* __restrict__ x
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < claims; i += 256) counters[i] = 0;
   const typename E::T* src = (const typename E::T*)x + (long long)blockIdx.y * stride;
-  const long long a = per * blockIdx.x / kNormParts, b = per * (blockIdx.x + 1) / kNormParts;
+  const long long chunks = (per + 7) / 8;
+  const long long a = chunks * blockIdx.x / kNormParts, b = chunks * (blockIdx.x + 1) / kNormParts;
+  const bool aligned = stride % E::kPerChunk == 0;
   double v = 0.0;
   for (long long i = a + threadIdx.x; i < b; i += 256) {
-    const double f = (double)load_as_f32<E>(src + i);
-    v += f * f;
+    float f[8];
+    // (matrices back to back at an odd size are read element by element)
+    if (aligned) load_chunk<E>(src, 8 * i, per, f);
+    else
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = 8 * i + e < per ? load_as_f32<E>(src + 8 * i + e) : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v += (double)f[e] * (double)f[e];
   }
 #pragma unroll
   for (int k = 32; k > 0; k >>= 1) v += __shfl_xor(v, k);
@@ -298,14 +306,12 @@ __global__ __launch_bounds__(256) void ns_start_kernel(const void* __restrict__ 
     return;
   }
   const int padded = (n + 31) & ~31;
-  for (int j = 2 * lane; j < padded; j += 128) {
-    uint16_t h[2], l[2];
+  for (int j = 8 * lane; j < padded; j += 512) {
+    float v[8];
+    load_chunk<E>(src, j, n, v);
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      split_f16(j + e < n ? (float)((double)load_as_f32<E>(src + j + e) * f) : 0.f, h[e], l[e]);
-    uint8_t* d = out + r * pitch + split_at(j);
-    *(uint32_t*)d = h[0] | ((uint32_t)h[1] << 16);
-    *(uint32_t*)(d + 64) = l[0] | ((uint32_t)l[1] << 16);
+    for (int e = 0; e < 8; ++e) v[e] = (float)((double)v[e] * f);
+    store_chunk(v, out + r * pitch, j);
   }
 }
 

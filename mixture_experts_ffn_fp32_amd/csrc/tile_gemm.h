@@ -511,7 +511,7 @@ __device__ __forceinline__ void tg_run(const P& p, int tiles, int32_t* counters,
   }
 }
 
-// v * 2^e as two float16.
+// A value as two float16.
 __device__ __forceinline__ void split_f16(float v, uint16_t& hi, uint16_t& lo) {
   const _Float16 h = (_Float16)v;
   const _Float16 l = (_Float16)(v - (float)h);
@@ -526,6 +526,51 @@ __device__ __forceinline__ float f16_to_f32(uint16_t b) {
 // is 64 bytes further).
 __host__ __device__ inline long long split_pitch(int n) { return (long long)((n + 31) / 32) * 128; }
 __device__ __forceinline__ long long split_at(int j) { return (long long)(j >> 5) * 128 + (j & 31) * 2; }
+
+
+// Elements j .. j + 7 of a row of `width` as float32, zeros past its end.  Rows whose
+// width is a whole number of 16 bytes start 16-byte aligned.
+template <class E>
+__device__ __forceinline__ void load_chunk(const typename E::T* __restrict__ src, long long j,
+                                           long long width, float (&f)[8]) {
+  if (j + 8 <= width && width % E::kPerChunk == 0) {
+    if constexpr (sizeof(typename E::T) == 4) {
+      const f32x4 a = *(const f32x4*)(src + j), b = *(const f32x4*)(src + j + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[e] = a[e];
+        f[4 + e] = b[e];
+      }
+    } else {
+      const u32x4 v = *(const u32x4*)(src + j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(v[e] << 16);
+        f[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = j + e < width ? load_as_f32<E>(src + j + e) : 0.f;
+  }
+}
+
+// Eight values times 2^ex into a split row from element j (a multiple of 8).
+__device__ __forceinline__ void store_chunk(const float (&f)[8], uint8_t* __restrict__ dst, int j,
+                                            int ex = 0) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint16_t h0, l0, h1, l1;
+    split_f16(ldexpf(f[2 * e], ex), h0, l0);
+    split_f16(ldexpf(f[2 * e + 1], ex), h1, l1);
+    h[e] = h0 | ((uint32_t)h1 << 16);
+    l[e] = l0 | ((uint32_t)l1 << 16);
+  }
+  uint8_t* d = dst + split_at(j);
+  *(u32x4*)d = u32x4{h[0], h[1], h[2], h[3]};
+  *(u32x4*)(d + 64) = u32x4{l[0], l[1], l[2], l[3]};
+}
 
 }  // namespace
 }  // namespace moe
