@@ -260,10 +260,9 @@ struct GroupedTiles {
 };
 
 template <class C, int DIR>
-__global__ __launch_bounds__(kTgThreads, C::SLOT > 32768 ? 2 : 4) void grouped_kernel(
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void grouped_kernel(
     GroupedProduct p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds0[C::SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds1[C::SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS];
   __shared__ GroupTables t;
   group_tables<DIR>(p.g, p.offsets, C::BM, t);
   if (DIR != GR_DW && p.zero_rest) {
@@ -280,7 +279,9 @@ __global__ __launch_bounds__(kTgThreads, C::SLOT > 32768 ? 2 : 4) void grouped_k
           ((float*)p.out)[e * per + i] = 0.f;
   }
   const GroupedTiles<C, DIR> tiles{p, t};
-  tg_run<C>(tiles, uni(t.tiles[p.g.E]) * tiles.columns(), nullptr, lds0, lds1, nullptr);
+  const int n = uni(t.tiles[p.g.E]) * tiles.columns();
+  if constexpr (C::SMALL) tg_run_small<C>(tiles, n, lds);
+  else tg_run<C>(tiles, n, nullptr, lds, nullptr);
 }
 
 // ---------------------------------------------------------------- operand preparation
@@ -510,14 +511,12 @@ struct Carve {
 
 uint32_t pad_pitch(int n) { return (uint32_t)((n + 63) / 64 * 128); }
 
-// Tiles of 256 where they give every CU one; else 128 (a quarter of the work per
-// tile, two blocks per CU).
-bool tiles_128(int dir, const GroupedArgs& a) {
-  const long long per = std::max(1LL, ((long long)a.M + a.E - 1) / a.E);
-  auto ct = [](long long x, long long b) { return (x + b - 1) / b; };
-  const long long t = dir == GR_DW ? ct(a.n, 256) * ct(a.k, 256) * a.E
-                                   : ct(per, 256) * a.E * ct(dir == GR_FWD ? a.n : a.k, 256);
-  return t < device_cu_count() || (dir != GR_DW && per <= 128);
+// Tiles of a product in tiles of b x b, its rows taken as spread evenly.
+long long tiles_of(int dir, const GroupedArgs& a, long long b) {
+  auto ct = [](long long x, long long y) { return (x + y - 1) / y; };
+  const long long per = std::max(1LL, ct(a.M, a.E)), groups = std::min(a.M, a.E);
+  if (dir == GR_DW) return ct(a.n, b) * ct(a.k, b) * groups;
+  return ct(per, b) * groups * ct(dir == GR_FWD ? a.n : a.k, b);
 }
 
 template <class C, int DIR>
@@ -527,16 +526,21 @@ hipError_t run_product(const GroupedProduct& p, hipStream_t st) {
   const long long most =
       DIR == GR_DW ? g.E * ct(g.n, C::BM) * ct(g.k, C::BN)
                    : (ct(g.M, C::BM) + g.E) * ct(DIR == GR_FWD ? g.n : g.k, C::BN);
-  const long long blocks = (long long)device_cu_count() * (C::SLOT > 32768 ? 1 : 2);
-  grouped_kernel<C, DIR><<<(unsigned)std::max(1LL, std::min(most, blocks)), kTgThreads, 0, st>>>(p);
+  const long long blocks = (long long)device_cu_count() * C::BPC;
+  grouped_kernel<C, DIR><<<(unsigned)std::max(1LL, std::min(most, blocks)), C::THREADS, 0, st>>>(p);
   return hipGetLastError();
 }
 
 template <int DIR, bool SPLIT>
 hipError_t pick_product(const GroupedArgs& a, const GroupedProduct& p, hipStream_t st) {
   constexpr bool AC = DIR == GR_DW, BC = DIR != GR_FWD, SW = DIR != GR_DW;
-  if (tiles_128(DIR, a)) return run_product<TgConfig<1, 2, AC, BC, SPLIT, SW>, DIR>(p, st);
-  return run_product<TgConfig<2, 4, AC, BC, SPLIT, SW>, DIR>(p, st);
+  const int cus = device_cu_count();
+  // the largest tiles that give every CU one
+  if (tiles_of(DIR, a, 256) >= cus && (DIR == GR_DW || a.M > 128LL * a.E))
+    return run_product<TgConfig<TgBig, AC, BC, SPLIT, SW>, DIR>(p, st);
+  if (tiles_of(DIR, a, 128) >= cus)
+    return run_product<TgConfig<TgMid, AC, BC, SPLIT, SW>, DIR>(p, st);
+  return run_product<TgConfig<TgSmall, AC, BC, SPLIT, SW>, DIR>(p, st);
 }
 
 unsigned row_blocks(long long rows) { return blocks_of(rows); }

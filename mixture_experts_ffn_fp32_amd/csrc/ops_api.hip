@@ -94,8 +94,8 @@ moe_status_t check_grouped(int M, int E, int n, int k, int dtype) {
   if (row > moe::kGroupedMaxRowBytes)
     return fail(MOE_ERR_UNSUPPORTED, "n and k must stay at or below " +
                                          std::to_string(moe::kGroupedMaxRowBytes / 4));
-  const long long tiles = ((long long)M / 128 + 1 + E) * ((std::max(n, k) + 127LL) / 128);
-  const long long wtiles = (long long)E * ((n + 127LL) / 128) * ((k + 127LL) / 128);
+  const long long tiles = ((long long)M / 64 + 1 + E) * ((std::max(n, k) + 63LL) / 64);
+  const long long wtiles = (long long)E * ((n + 63LL) / 64) * ((k + 63LL) / 64);
   if (std::max(tiles, wtiles) > 0x3fffffffLL || (long long)E * n > 0x7fffffffLL)
     return fail(MOE_ERR_UNSUPPORTED, "M, E, n, k give too many tiles");
   return MOE_OK;
@@ -108,7 +108,7 @@ moe_status_t check_ortho(int B, int m, int n) {
   if (m < 1 || n < 1) return fail(MOE_ERR_INVALID_ARG, "m and n must be positive");
   if (m > (1 << 20) || n > (1 << 20))
     return fail(MOE_ERR_UNSUPPORTED, "m and n must stay at or below 2^20");
-  const long long mt = (m + 127LL) / 128, nt = (n + 127LL) / 128;
+  const long long mt = (m + 63LL) / 64, nt = (n + 63LL) / 64;
   if (mt * nt * std::max(B, 1) > 0x3fffffffLL || (long long)B * m > 0x7fffffffLL)
     return fail(MOE_ERR_UNSUPPORTED, "B, m, n give too many tiles");
   return MOE_OK;

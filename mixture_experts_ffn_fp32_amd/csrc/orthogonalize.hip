@@ -237,12 +237,13 @@ struct NsTiles {
 };
 
 template <class C, int KIND>
-__global__ __launch_bounds__(kTgThreads, C::SLOT > 32768 ? 2 : 4) void ns_kernel(NsProduct p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds0[C::SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds1[C::SLOT];
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void ns_kernel(NsProduct p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS];
   __shared__ int s_claim;
   const NsTiles<C, KIND> tiles{p};
-  tg_run<C>(tiles, tiles.per_matrix() * p.count, p.counters, lds0, lds1, &s_claim);
+  const int n = tiles.per_matrix() * p.count;
+  if constexpr (C::SMALL) tg_run_small<C>(tiles, n, lds);
+  else tg_run<C>(tiles, n, p.counters, lds, &s_claim);
 }
 
 // ---------------------------------------------------------------- the first iterate
@@ -351,18 +352,22 @@ template <class C, int KIND>
 hipError_t run_ns(NsProduct p, hipStream_t st) {
   const long long mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN;
   const long long total = (KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2) * p.count;
-  const long long blocks = (long long)device_cu_count() * (C::SLOT > 32768 ? 1 : 2);
+  const long long blocks = (long long)device_cu_count() * C::BPC;
   if (total <= blocks) p.counters = nullptr;  // one tile each
-  ns_kernel<C, KIND><<<(unsigned)std::min(total, blocks), kTgThreads, 0, st>>>(p);
+  ns_kernel<C, KIND><<<(unsigned)std::min(total, blocks), C::THREADS, 0, st>>>(p);
   return hipGetLastError();
 }
-// Tiles of 256 where they give every CU one, else 128.
+// The largest tiles that give every CU one.
 template <int KIND, bool AC, bool BC, bool SW>
 hipError_t pick_ns(const NsProduct& p, hipStream_t st) {
-  const long long mt = (p.M + 255) / 256, nt = (p.N + 255) / 256;
-  const long long total = (KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2) * p.count;
-  if (total < device_cu_count()) return run_ns<TgConfig<1, 2, AC, BC, true, SW>, KIND>(p, st);
-  return run_ns<TgConfig<2, 4, AC, BC, true, SW>, KIND>(p, st);
+  auto tiles = [&](long long b) {
+    const long long mt = (p.M + b - 1) / b, nt = (p.N + b - 1) / b;
+    return (KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2) * p.count;
+  };
+  const int cus = device_cu_count();
+  if (tiles(256) >= cus) return run_ns<TgConfig<TgBig, AC, BC, true, SW>, KIND>(p, st);
+  if (tiles(128) >= cus) return run_ns<TgConfig<TgMid, AC, BC, true, SW>, KIND>(p, st);
+  return run_ns<TgConfig<TgSmall, AC, BC, true, SW>, KIND>(p, st);
 }
 
 }  // namespace

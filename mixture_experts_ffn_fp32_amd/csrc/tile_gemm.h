@@ -1,7 +1,7 @@
 // MFMA tile pipeline of the products beside the layer (grouped products,
 // Newton-Schulz products): one (BM x BN) tile of C = A B^T per block at a
-// time, eight wavefronts (4 x 2), k-steps landing in a two-slot LDS ring by
-// direct-to-LDS loads while the other slot is multiplied.
+// time, k-steps landing in an LDS ring by direct-to-LDS loads while an earlier
+// slot is multiplied.  Three sizes of tile (TgBig, TgMid, TgSmall below).
 //
 // An operand is read in one of two layouts:
 //   row layout     its rows are contiguous along the contraction; a k-step is
@@ -34,20 +34,45 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef short tg_v4s __attribute__((ext_vector_type(4)));
 
-constexpr int kTgThreads = 512;
+// WM x WN wavefronts of FM x FN fragments of 32 x 32; a ring of S k-steps, S - 1 of
+// them in flight; ACOL / BCOL: operand in column layout; SWAP: B as the MFMA's first
+// operand, so that a lane holds four consecutive columns of one row instead of four
+// consecutive rows of one column.
+template <int WM_, int WN_, int FM_, int FN_, int S_, int BPC_, bool AHEAD_>
+struct TgShape {
+  static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, S = S_, BPC = BPC_;
+  static constexpr bool AHEAD = AHEAD_;  // fragments a whole k-step ahead (tg_step_ahead)
+  static constexpr int BM = WM * FM * 32, BN = WN * FN * 32, THREADS = WM * WN * 64;
+  static constexpr int SLOT = (BM + BN) * 128;        // bytes of a ring slot
+  static constexpr int NI = BM / (4 * WM * WN);       // loads per wavefront per k-step
+  static_assert(BM == BN, "the first half of the wavefronts loads A, the other B");
+};
+// 64 x 64, the k-steps dealt to the four wavefronts, each multiplying whole tiles of its
+// own k-steps (4 fragments, 1 LDS read per MFMA) from a ring of its own: no barrier in
+// the loop.  Their sums are added through LDS, in wavefront order; then each wavefront
+// writes one fragment (WM, WN, FM, FN are those of the epilogue).
+struct TgSmall {
+  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, S = 2, BPC = 1, WAVES = 4;
+  static constexpr bool AHEAD = false;
+  static constexpr int BM = 64, BN = 64, THREADS = 256;
+  static constexpr int SLOT = (BM + BN) * 128;
+  static constexpr int NI = BM / 8;                   // loads per operand per k-step
+};
+// 256 x 256, eight wavefronts of 64 x 128, one block per CU: 0.75 LDS reads per MFMA.
+// Below a tile per CU it leaves CUs idle; 128 x 128 (four wavefronts of 64 x 64, 1 read
+// per MFMA, two blocks per CU that fill each other's barriers and epilogues) is next,
+// its fragments a whole k-step ahead (one group of four MFMAs does not cover an LDS
+// read), then TgSmall.
+using TgBig = TgShape<4, 2, 2, 4, 2, 1, false>;
+using TgMid = TgShape<2, 2, 2, 2, 2, 2, true>;
 
-// FM x FN fragments of 32 x 32 per wavefront; ACOL / BCOL: operand in column
-// layout; SWAP: B as the MFMA's first operand, so that a lane holds four
-// consecutive columns of one row instead of four consecutive rows of one
-// column.
-template <int FM_, int FN_, bool ACOL_, bool BCOL_, bool SPLIT_, bool SWAP_>
-struct TgConfig {
-  static constexpr int FM = FM_, FN = FN_, BM = FM_ * 128, BN = FN_ * 64;
+template <class Shape, bool ACOL_, bool BCOL_, bool SPLIT_, bool SWAP_>
+struct TgConfig : Shape {
   static constexpr bool ACOL = ACOL_, BCOL = BCOL_, SPLIT = SPLIT_, SWAP = SWAP_;
   static constexpr int KS = SPLIT ? 32 : 64;          // contraction indices per k-step
-  static constexpr int SLOT = (BM + BN) * 128;        // bytes of a ring slot
-  static constexpr int NI = BM / 32;                  // loads per wavefront per k-step
-  static_assert(BM == BN, "wavefronts 0-3 load A, 4-7 load B, NI loads each");
+  static constexpr bool SMALL = Shape::BM == TgSmall::BM;
+  static constexpr int LDS = Shape::S * Shape::SLOT * (SMALL ? TgSmall::WAVES : 1);
+  static constexpr int WAVES_PER_SIMD = Shape::BPC * Shape::THREADS / 256;
 };
 
 // One operand of a tile.  Row layout: `rows` rows of `pitch` bytes, k-step s at
@@ -68,9 +93,14 @@ struct TgLoad {
   uint32_t pitch;
 };
 
-// In a column-layout tile the 16-byte chunk c of contraction row k lies at position
-// c ^ 4 (k & 3): a transposing read of 32 lanes touches 64 bytes of each of four
-// consecutive rows, and the rotation puts them on distinct banks.
+// In a column-layout tile of W columns the 16-byte chunk c of contraction row k lies at
+// position c ^ 4 j(k): a transposing read of 32 lanes touches 64 bytes of each of four
+// consecutive rows, and the rotation puts them on distinct banks (rows of 128 bytes
+// share a bank window in pairs).
+template <int W>
+__device__ __forceinline__ int tg_rotation(int k) {
+  return W >= 128 ? k & 3 : (k >> 1) & 1;
+}
 template <class C, bool COL>
 __device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int t0, int steps, int w,
                                                   int lane, uint32_t (&off)[C::NI]) {
@@ -86,7 +116,7 @@ __device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int t0, in
 #pragma unroll
     for (int i = 0; i < C::NI; ++i) {
       const int k = (w * C::NI + i) * RPI + lane / CPR;  // LDS row 0..63
-      const int c = (lane % CPR) ^ ((k & 3) << 2);
+      const int c = (lane % CPR) ^ (tg_rotation<W>(k) << 2);
       // columns past the last one reread the last chunk (never stored)
       const int col = min(t0 + 8 * c, o.width - 8);
       if constexpr (C::SPLIT)
@@ -111,13 +141,14 @@ __device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int t0, in
   return l;
 }
 
-// This wavefront's loads of a tile at (m0, n0): wavefronts 0-3 A, 4-7 B.
+// This wavefront's loads of a tile at (m0, n0): A in the first half of them, B in the other.
 template <class C>
 __device__ __forceinline__ TgLoad tg_prepare(const TgOperand& A, const TgOperand& B, int m0, int n0,
                                              int steps, int wave, int lane,
                                              uint32_t (&off)[C::NI]) {
-  if (wave < 4) return tg_prepare_side<C, C::ACOL>(A, m0, steps, wave, lane, off);
-  return tg_prepare_side<C, C::BCOL>(B, n0, steps, wave - 4, lane, off);
+  constexpr int H = C::WM * C::WN / 2;
+  if (wave < H) return tg_prepare_side<C, C::ACOL>(A, m0, steps, wave, lane, off);
+  return tg_prepare_side<C, C::BCOL>(B, n0, steps, wave - H, lane, off);
 }
 
 // Bytes from the k-step's base that its loads may touch; later ones read zeros.
@@ -139,14 +170,14 @@ __device__ __forceinline__ uint2 tg_read_tr(const uint8_t* p) {
 // Column layout, transposing reads: within each 16-lane group lane l names contraction
 // row k = 8 (l / 32) + (l % 16) / 4 (+ 4 for the upper four) of the group at column
 // 16 ((l / 16) % 2) + 4 (l % 4) of the fragment.  Its chunk is 4 u + c, c < 4, rotated
-// to 4 (u ^ (k & 3)) + c: everything but u % 4 and the lane is a constant offset.
+// to 4 (u ^ j(k)) + c: everything but u % 4 and the lane is a constant offset.
 template <int W, bool COL>
 __device__ __forceinline__ u32x4 tg_frag(const uint8_t* rd, int kg, int u_const, int u_wave,
                                          int lane) {
   if constexpr (COL) {
     const int k = 8 * (lane >> 5) + ((lane & 15) >> 2), n = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
     // u = u_const + u_wave: the low two bits of u_const + u_wave, without a carry
-    const int low = ((u_const & 3) + u_wave) ^ (k & 3);
+    const int low = ((u_const & 3) + u_wave) ^ tg_rotation<W>(k);
     const uint8_t* p = rd + k * (2 * W) + low * 64 + (n >> 3) * 16 + (n & 7) * 2 +
                        (kg * 16 * (2 * W) + (u_const >> 2) * 256);
     const uint2 lo = tg_read_tr(p), hi = tg_read_tr(p + 4 * 2 * W);
@@ -158,21 +189,21 @@ __device__ __forceinline__ u32x4 tg_frag(const uint8_t* rd, int kg, int u_const,
 }
 
 // The wavefronts' fragments interleave: fragment (fm, fn) of wavefront (wm, wn) is
-// rows (4 fm + wm) 32 .. and columns (2 fn + wn) 32 .. of the tile, so a tile whose
+// rows (WM fm + wm) 32 .. and columns (WN fn + wn) 32 .. of the tile, so a tile whose
 // matrix ends after half its rows (or half its columns) leaves out whole fragments
-// of every wavefront, and the eight stay balanced.
+// of every wavefront, and they stay balanced.
 template <class C, int FMA>
 __device__ __forceinline__ void tg_frags_a(const uint8_t* __restrict__ rd, int kg, int wm, int lane,
                                            u32x4 (&f)[C::FM]) {
 #pragma unroll
-  for (int i = 0; i < FMA; ++i) f[i] = tg_frag<C::BM, C::ACOL>(rd, kg, 4 * i, wm, lane);
+  for (int i = 0; i < FMA; ++i) f[i] = tg_frag<C::BM, C::ACOL>(rd, kg, C::WM * i, wm, lane);
 }
 template <class C, int FNA>
 __device__ __forceinline__ void tg_frags_b(const uint8_t* __restrict__ rd, int kg, int wn, int lane,
                                            u32x4 (&f)[C::FN]) {
 #pragma unroll
   for (int i = 0; i < FNA; ++i)
-    f[i] = tg_frag<C::BN, C::BCOL>(rd + C::BM * 128, kg, 2 * i, wn, lane);
+    f[i] = tg_frag<C::BN, C::BCOL>(rd + C::BM * 128, kg, C::WN * i, wn, lane);
 }
 
 // The fragments a tile multiplies: FMA x FNA of the configuration's FM x FN;
@@ -245,7 +276,7 @@ __device__ __forceinline__ void tg_step(const uint8_t* __restrict__ rd,
                                         const uint8_t* __restrict__ nx, int wm, int wn, int lane,
                                         TgFrags<C>& f, f32x16 (&acc)[C::FM][C::FN],
                                         const uint8_t* db, const uint32_t (&off)[C::NI],
-                                        uint8_t* __restrict__ wr, int nrec, bool first) {
+                                        uint8_t* __restrict__ wr, int nrec, bool landed) {
   constexpr int MF = FMA * FNA - (TRI ? C::FM * C::FN / 4 : 0);
   constexpr int RA = FMA * (C::ACOL ? 2 : 1), RB = FNA * (C::BCOL ? 2 : 1);
   if constexpr (C::SPLIT) {
@@ -267,7 +298,7 @@ __device__ __forceinline__ void tg_step(const uint8_t* __restrict__ rd,
     tg_order<MF, RA + RB, 0>();
     tg_order<MF, RB, 0>();
     tg_order<MF, RA, 0>();
-    if (!first) MOE_WAIT_VMCNT(0);
+    if (!landed) MOE_WAIT_VMCNT((C::S - 2) * C::NI);
     lds_sync();
     tg_frags_a<C, FMA>(nx, 0, wm, lane, f.a[0]);
     tg_frags_b<C, FNA>(nx, 0, wn, lane, f.b[0]);
@@ -285,7 +316,7 @@ __device__ __forceinline__ void tg_step(const uint8_t* __restrict__ rd,
     tg_order<MF, RA + RB, 0>();
     tg_order<MF, RA + RB, 0>();
     tg_order<MF, RA + RB, 0>();
-    if (!first) MOE_WAIT_VMCNT(0);
+    if (!landed) MOE_WAIT_VMCNT((C::S - 2) * C::NI);
     lds_sync();
     tg_frags_a<C, FMA>(nx, 0, wm, lane, f.a[0]);
     tg_frags_b<C, FNA>(nx, 0, wn, lane, f.b[0]);
@@ -296,14 +327,60 @@ __device__ __forceinline__ void tg_step(const uint8_t* __restrict__ rd,
   }
 }
 
+// All fragments of a k-step.
+template <class C>
+struct TgWhole {
+  u32x4 a[4][C::FM], b[4][C::FN];
+};
+template <class C, int FMA, int FNA>
+__device__ __forceinline__ void tg_read_whole(const uint8_t* __restrict__ rd, int wm, int wn,
+                                              int lane, TgWhole<C>& f) {
+#pragma unroll
+  for (int kg = 0; kg < 4; ++kg) {
+    tg_frags_a<C, FMA>(rd, kg, wm, lane, f.a[kg]);
+    tg_frags_b<C, FNA>(rd, kg, wn, lane, f.b[kg]);
+  }
+}
+
+// One k-step from registers (f), the next one's fragments (slot `nx`) read into g
+// meanwhile.  The barrier stands before it: every wavefront has read this k-step's
+// slot, which takes the loads of the k-step S further on (as in tg_step).
+template <class C, int FMA, int FNA, bool TRI>
+__device__ __forceinline__ void tg_step_ahead(const uint8_t* __restrict__ nx, int wm, int wn,
+                                              int lane, const TgWhole<C>& f, TgWhole<C>& g,
+                                              f32x16 (&acc)[C::FM][C::FN], const uint8_t* db,
+                                              const uint32_t (&off)[C::NI],
+                                              uint8_t* __restrict__ wr, int nrec, bool landed) {
+  constexpr int MF = FMA * FNA - (TRI ? C::FM * C::FN / 4 : 0);
+  constexpr int NR = 4 * (FMA * (C::ACOL ? 2 : 1) + FNA * (C::BCOL ? 2 : 1));
+  if (!landed) MOE_WAIT_VMCNT((C::S - 2) * C::NI);
+  lds_sync();
+  tg_read_whole<C, FMA, FNA>(nx, wm, wn, lane, g);
+#pragma unroll
+  for (int i = 0; i < C::NI; ++i) dma16(db, off[i], wr + i * 1024, nrec);
+  if constexpr (C::SPLIT) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      tg_products<C, FMA, FNA, TRI>(f.a[h], f.b[h], acc);
+      tg_products<C, FMA, FNA, TRI>(f.a[h], f.b[2 + h], acc);
+      tg_products<C, FMA, FNA, TRI>(f.a[2 + h], f.b[h], acc);
+    }
+    tg_order<6 * MF, NR, C::NI>();
+  } else {
+#pragma unroll
+    for (int kg = 0; kg < 4; ++kg) tg_products<C, FMA, FNA, TRI>(f.a[kg], f.b[kg], acc);
+    tg_order<4 * MF, NR, C::NI>();
+  }
+}
+
 // Row and column (inside the tile) of accumulator register r of fragment (fm, fn).
 template <class C>
 __device__ __forceinline__ int tg_row(int wm, int fm, int lane, int r) {
-  return (4 * fm + wm) * 32 + (C::SWAP ? (lane & 31) : 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3));
+  return (C::WM * fm + wm) * 32 + (C::SWAP ? (lane & 31) : 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3));
 }
 template <class C>
 __device__ __forceinline__ int tg_col(int wn, int fn, int lane, int r) {
-  return (2 * fn + wn) * 32 + (C::SWAP ? 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) : (lane & 31));
+  return (C::WN * fn + wn) * 32 + (C::SWAP ? 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) : (lane & 31));
 }
 
 // The four 8-byte groups a lane holds of a fragment's 32 consecutive elements
@@ -380,15 +457,22 @@ struct TgTiles {
   }
 };
 constexpr int kTgCounters = 8;
-constexpr int kTgMinSteps = 3;
 
-// The loads' place in the stream of k-steps of a block's tiles, two k-steps ahead of
-// the multiplication.  Plain scalars: with the tile itself in it the structure ends
+// The loads' place in the stream of k-steps of a block's tiles, S k-steps ahead of the
+// multiplication.  Plain scalars: with the tile itself in it the structure ends
 // up in scratch memory.
 struct TgCursor {
   int hint;
   int s, steps;      // the tile's next k-step, its k-steps (0: the stream has ended)
 };
+
+// k-steps of a tile: S + 1 at least (after a short contraction come k-steps of zeros),
+// and an even number where the fragments go through two sets of registers.
+template <class C>
+__device__ __forceinline__ int tg_steps(int steps) {
+  const int n = max(steps, C::S + 1);
+  return C::AHEAD ? (n + 1) & ~1 : n;
+}
 
 // The cursor to tile L (-1: the stream has ended).
 template <class C, class P>
@@ -399,37 +483,55 @@ __device__ __forceinline__ void tg_seek(const P& p, int L, TgCursor& c, TgLoad& 
   if (L < 0) return;
   const typename P::Tile t = p.tile(L, c.hint);
   c.hint = uni(t.hint);
-  c.steps = max(uni(t.steps), kTgMinSteps);
+  c.steps = tg_steps<C>(uni(t.steps));
   ld = tg_prepare<C>(t.A, t.B, t.m0, t.n0, t.steps, wave, lane, off);
 }
 
-// The k-steps of a tile.  There are at least three (after a short contraction come
-// k-steps of zeros), so the cursor, two ahead, passes to the next tile, which is
-// next(), while this one is multiplied, behind its first barrier.
+// The k-steps of a tile.  As there are at least S + 1, the cursor, S ahead, passes to
+// the next tile, which is next(), while this one is multiplied, behind its first barrier.
 template <class C, int FMA, int FNA, bool TRI, class P, class Next>
 __device__ __forceinline__ void tg_tile(const P& p, int steps, int& ph, int wave, int lane,
                                         Next next, TgCursor& c, TgLoad& ld,
                                         uint32_t (&off)[C::NI], f32x16 (&acc)[C::FM][C::FN],
-                                        uint8_t* __restrict__ lds0, uint8_t* __restrict__ lds1) {
-  const int wm = wave >> 1, wn = wave & 1;
+                                        uint8_t* __restrict__ lds) {
+  const int wm = wave / C::WN, wn = wave % C::WN;
   // (opaque: the fragments' LDS addresses stay inside the tile, where they are few,
   // and do not spill what the epilogue keeps)
   asm volatile("" : "+v"(lane));
-  // (not carried over from the last tile: that may have read fewer fragments)
-  TgFrags<C> f;
-  tg_frags_a<C, FMA>(ph ? lds1 : lds0, 0, wm, lane, f.a[0]);
-  tg_frags_b<C, FNA>(ph ? lds1 : lds0, 0, wn, lane, f.b[0]);
-  const int all = max(steps, kTgMinSteps);
-  for (int s = 0; s < all; ++s) {
-    const uint8_t* rd = ph ? lds1 : lds0;
-    const uint8_t* nx = ph ? lds0 : lds1;
-    uint8_t* wr = (ph ? lds1 : lds0) + wave * C::NI * 1024;
+  // The first fragments are not carried over from the last tile, which may have read
+  // fewer.
+  const int all = tg_steps<C>(steps);
+  auto issue = [&](auto step) {
+    const int after = ph + 1 < C::S ? ph + 1 : 0;
     const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
     const int nrec = uni(c.steps > 0 ? tg_range<C>(ld, c.s) : 0);
-    tg_step<C, FMA, FNA, TRI>(rd, nx, wm, wn, lane, f, acc, db, off, wr, nrec, s == 0);
+    step(lds + ph * C::SLOT, lds + after * C::SLOT, db, nrec);
     c.s = uni(c.s + 1);
     if (c.s == c.steps) tg_seek<C>(p, next(), c, ld, off, wave, lane);
-    ph ^= 1;
+    ph = after;
+  };
+  if constexpr (C::AHEAD) {
+    TgWhole<C> f, g;
+    tg_read_whole<C, FMA, FNA>(lds + ph * C::SLOT, wm, wn, lane, f);
+    for (int s = 0; s < all; s += 2) {
+      issue([&](uint8_t* rd, const uint8_t* nx, const uint8_t* db, int nrec) {
+        tg_step_ahead<C, FMA, FNA, TRI>(nx, wm, wn, lane, f, g, acc, db, off,
+                                        rd + wave * C::NI * 1024, nrec, s < C::S - 1);
+      });
+      issue([&](uint8_t* rd, const uint8_t* nx, const uint8_t* db, int nrec) {
+        tg_step_ahead<C, FMA, FNA, TRI>(nx, wm, wn, lane, g, f, acc, db, off,
+                                        rd + wave * C::NI * 1024, nrec, s + 1 < C::S - 1);
+      });
+    }
+  } else {
+    TgFrags<C> f;
+    tg_frags_a<C, FMA>(lds + ph * C::SLOT, 0, wm, lane, f.a[0]);
+    tg_frags_b<C, FNA>(lds + ph * C::SLOT, 0, wn, lane, f.b[0]);
+    for (int s = 0; s < all; ++s)
+      issue([&](uint8_t* rd, const uint8_t* nx, const uint8_t* db, int nrec) {
+        tg_step<C, FMA, FNA, TRI>(rd, nx, wm, wn, lane, f, acc, db, off, rd + wave * C::NI * 1024,
+                                  nrec, s < C::S - 1);
+      });
   }
 }
 
@@ -441,10 +543,9 @@ __device__ __forceinline__ void tg_tile(const P& p, int steps, int& ph, int wave
 //   p.store(t, wm, wn, lane, acc)   the epilogue, from registers
 template <class C, class P>
 __device__ __forceinline__ void tg_run(const P& p, int tiles, int32_t* counters,
-                                       uint8_t* __restrict__ lds0, uint8_t* __restrict__ lds1,
-                                       int* s_claim) {
+                                       uint8_t* __restrict__ lds, int* s_claim) {
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = uni(tid >> 6), wm = wave >> 1, wn = wave & 1;
+  const int wave = uni(tid >> 6), wm = wave / C::WN, wn = wave % C::WN;
   TgTiles q;
   q.init(tiles, counters);
   int mine = q.own;
@@ -456,8 +557,8 @@ __device__ __forceinline__ void tg_run(const P& p, int tiles, int32_t* counters,
   tg_seek<C>(p, L, c, ld, off, wave, lane);
   int ph = 0;  // ring slot of the next k-step
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    uint8_t* w = (k ? lds1 : lds0) + wave * C::NI * 1024;
+  for (int k = 0; k < C::S; ++k) {
+    uint8_t* w = lds + k * C::SLOT + wave * C::NI * 1024;
     const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
     const int nrec = uni(tg_range<C>(ld, c.s));
 #pragma unroll
@@ -489,25 +590,136 @@ __device__ __forceinline__ void tg_run(const P& p, int tiles, int32_t* counters,
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     if constexpr (C::FM == 2) {
+      constexpr int H = C::FN / 2;
       const bool hm = t.rows <= C::BM / 2, hn = t.cols <= C::BN / 2;
-      if (hm && hn) tg_tile<C, 1, 2, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
-      else if (hm) tg_tile<C, 1, 4, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
-      else if (hn) tg_tile<C, 2, 2, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+      if (hm && hn) tg_tile<C, 1, H, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
+      else if (hm) tg_tile<C, 1, C::FN, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
+      else if (hn) tg_tile<C, 2, H, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
       else if (P::SYM && p.tri(t))
-        tg_tile<C, 2, 4, P::SYM>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
-      else tg_tile<C, 2, 4, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+        tg_tile<C, 2, C::FN, P::SYM>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
+      else tg_tile<C, 2, C::FN, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
     } else {
-      if (t.cols <= C::BN / 2)
-        tg_tile<C, 1, 1, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
-      else tg_tile<C, 1, 2, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds0, lds1);
+      tg_tile<C, C::FM, C::FN, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
     }
-    // the loads in flight are waited for here (the next tile's second k-step; the first
-    // one landed before the last barrier), so its loop needs no wait of its own for them
+    // the loads in flight are waited for here (the next tile's first k-steps; the very
+    // first one landed before the last barrier): its loop needs no wait for them
     MOE_WAIT_VMCNT(0);
     if (counters != nullptr && tid == 0) *s_claim = claimed;  // read behind its first barrier
     p.store(t, wm, wn, lane, acc);
     if (L1 < 0) break;
     L = L1;
+  }
+}
+
+// One wavefront of TgSmall in its loop: a whole tile of 2 x 2 fragments.
+template <class C>
+struct TgOne : C {
+  static constexpr int WM = 1, WN = 1, FM = 2, FN = 2;
+};
+
+// A wavefront's `mine` k-steps (wave, wave + 4, ..) of a 64 x 64 tile: two in its ring;
+// a k-step's fragments are read, its slot takes the loads two further on, then they are
+// multiplied.
+template <class C, class One>
+__device__ __forceinline__ void tg_small_loop(const TgLoad& la, const TgLoad& lb,
+                                              const uint32_t (&oa)[C::NI],
+                                              const uint32_t (&ob)[C::NI], int mine, int wave,
+                                              int lane, f32x16 (&acc)[2][2],
+                                              uint8_t* __restrict__ slot0,
+                                              uint8_t* __restrict__ slot1) {
+  constexpr int W = TgSmall::WAVES, NI = C::NI;
+  auto issue = [&](int i, uint8_t* slot) {
+    const int s = wave + W * i;
+    const int na = uni(i < mine ? tg_range<C>(la, s) : 0), nb = uni(i < mine ? tg_range<C>(lb, s) : 0);
+    const uint8_t* da = uni(la.base + (size_t)s * la.step);
+    const uint8_t* db = uni(lb.base + (size_t)s * lb.step);
+#pragma unroll
+    for (int k = 0; k < NI; ++k) dma16(da, oa[k], slot + k * 1024, na);
+#pragma unroll
+    for (int k = 0; k < NI; ++k) dma16(db, ob[k], slot + C::BM * 128 + k * 1024, nb);
+  };
+  issue(0, slot0);
+  issue(1, slot1);
+  for (int i = 0; i < mine; ++i) {
+    uint8_t* slot = i & 1 ? slot1 : slot0;
+    MOE_WAIT_VMCNT(2 * NI);  // this k-step has landed, the next one may be in flight
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    TgWhole<One> f;
+    tg_read_whole<One, 2, 2>(slot, 0, 0, lane, f);
+    MOE_WAIT_LGKMCNT0();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    issue(i + 2, slot);
+    if constexpr (C::SPLIT) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        tg_products<One, 2, 2, false>(f.a[h], f.b[h], acc);
+        tg_products<One, 2, 2, false>(f.a[h], f.b[2 + h], acc);
+        tg_products<One, 2, 2, false>(f.a[2 + h], f.b[h], acc);
+      }
+    } else {
+#pragma unroll
+      for (int kg = 0; kg < 4; ++kg) tg_products<One, 2, 2, false>(f.a[kg], f.b[kg], acc);
+    }
+  }
+  MOE_WAIT_VMCNT(0);  // the sums go through the ring
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// The same for TgSmall.
+template <class C, class P>
+__device__ __forceinline__ void tg_run_small(const P& p, int tiles, uint8_t* __restrict__ lds) {
+  constexpr int W = TgSmall::WAVES, NI = C::NI;
+  using One = TgOne<C>;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uni(tid >> 6);
+  uint8_t* ring = lds + wave * (C::S * C::SLOT);
+  TgTiles q;
+  q.init(tiles, nullptr);
+  int hint = 0;
+  for (int j = q.own;; j += q.blocks(q.x)) {
+    const int L = q.at(q.x, j);
+    if (L < 0) break;
+    const typename P::Tile t = p.tile(L, hint);
+    hint = t.hint;
+    uint32_t oa[NI], ob[NI];
+    const TgLoad la = tg_prepare_side<C, C::ACOL>(t.A, t.m0, t.steps, 0, lane, oa);
+    const TgLoad lb = tg_prepare_side<C, C::BCOL>(t.B, t.n0, t.steps, 0, lane, ob);
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][k][r] = 0.f;
+    const int mine = t.steps > wave ? (t.steps - wave + W - 1) / W : 0;
+    tg_small_loop<C, One>(la, lb, oa, ob, mine, wave, lane, acc, ring, ring + C::SLOT);
+    // the four sums through this wavefront's ring, every fragment as 16-byte runs
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *(f32x4*)(ring + f * 4096 + r * 1024 + lane * 16) =
+            f32x4{acc[f >> 1][f & 1][4 * r], acc[f >> 1][f & 1][4 * r + 1],
+                  acc[f >> 1][f & 1][4 * r + 2], acc[f >> 1][f & 1][4 * r + 3]};
+    __syncthreads();
+    f32x16 sum[1][1];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const f32x4 o = *(const f32x4*)(lds + w * (C::S * C::SLOT) + wave * 4096 + r * 1024 + lane * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += o[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[0][0][4 * r + e] = v[e];
+    }
+    __syncthreads();  // the rings take the next tile's loads
+    p.store(t, wave / C::WN, wave % C::WN, lane, sum);
   }
 }
 
