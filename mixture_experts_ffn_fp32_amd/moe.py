@@ -98,7 +98,7 @@ def _check(status: int):
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _dev(*tensors, dtype=None):
@@ -316,13 +316,51 @@ def balance_stats(scores, idx, K: int, group_of=None, alpha1: float = 1.0, alpha
 
 
 # ---------------------------------------------------------------- operators beside the layer
+# A call on a few rows takes about as long as the host needs for it, so the calls below avoid
+# what costs microseconds: torch.cuda.current_stream() builds a Stream object (2.6 us; the raw
+# handle takes 0.1), and a device guard is only entered where the operands' device is not the
+# current one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+class _Same:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME = _Same()
+
+
+def _on(device):
+    """Context in which `device` is the current device."""
+    return _SAME if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _stream_of(device):
+    """The current stream of `device`."""
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _operands(first, *others):
     """Every tensor given is contiguous and on the device of the first; returns that device."""
-    _dev(first, *others)
+    device = first.device
+    if device.type != "cuda":
+        raise MoEError(1, "tensors must be on a GPU device")
+    if not first.is_contiguous():
+        raise MoEError(1, "tensors must be contiguous")
     for t in others:
-        if t is not None and t.device != first.device:
-            raise MoEError(1, f"tensors on different devices: {first.device} and {t.device}")
-    return first.device
+        if t is None:
+            continue
+        if t.device != device:
+            raise MoEError(1, f"tensors on different devices: {device} and {t.device}")
+        if not t.is_contiguous():
+            raise MoEError(1, "tensors must be contiguous")
+    return device
 
 
 def _typed(name: str, t, dtype, shape):
@@ -342,18 +380,18 @@ def _dims(name: str, t, n: int):
 
 
 def _scratch(workspace, need: int, device):
-    """(pointer, bytes): the caller's workspace if it is large enough, else a new one.
+    """The caller's workspace if it is large enough, else a new one (None: none needed).
     A new one comes from PyTorch's allocator for the current stream, like the outputs."""
     if workspace is not None:
         if _operands(workspace) != device:
             raise MoEError(1, f"workspace is on {workspace.device}, the operands on {device}")
         if workspace.numel() * workspace.element_size() >= need:
             return workspace
-    return torch.empty(need, dtype=torch.uint8, device=device)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
 
 
 def _bytes(t) -> int:
-    return t.numel() * t.element_size()
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _size(query, *args) -> int:
@@ -374,12 +412,12 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None):
     _typed("bias", bias, x.dtype, (d,))
     _typed("out", out, x.dtype, (T, d))
     dev = _operands(x, weight, bias, out)
-    with torch.cuda.device(dev):
+    with _on(dev):
         y = torch.empty_like(x) if out is None else out
         mean = torch.empty(T, dtype=torch.float32, device=dev)
         rstd = torch.empty(T, dtype=torch.float32, device=dev)
         _check(L.moe_layer_norm(_p(x), _p(weight), _p(bias), T, d, eps, dt, _p(y), _p(mean),
-                                _p(rstd), _stream()))
+                                _p(rstd), _stream_of(dev)))
     return y, mean, rstd
 
 
@@ -394,7 +432,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None):
     _typed("mean", mean, torch.float32, (T,))
     _typed("rstd", rstd, torch.float32, (T,))
     dev = _operands(x, dy, weight, mean, rstd)
-    with torch.cuda.device(dev):
+    with _on(dev):
         dx = torch.empty_like(x)
         # an empty batch writes nothing: its weight gradients are zeros
         alloc = torch.zeros if T == 0 else torch.empty
@@ -402,7 +440,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None):
         db = alloc(d, dtype=torch.float32, device=dev)
         ws = _scratch(workspace, _size(L.moe_layer_norm_backward_workspace_size, T, d, dt), dev)
         _check(L.moe_layer_norm_backward(_p(dy), _p(x), _p(weight), _p(mean), _p(rstd), T, d, dt,
-                                         _p(dx), _p(dw), _p(db), _p(ws), _bytes(ws), _stream()))
+                                         _p(dx), _p(dw), _p(db), _p(ws), _bytes(ws), _stream_of(dev)))
     return dx, dw, db
 
 
@@ -427,12 +465,12 @@ def grouped_matmul(x, w, offsets, out=None, workspace=None):
     dt = _dtype_code(x)
     _typed("out", out, x.dtype, (M, n))
     dev = _operands(x, w, offsets, out)
-    with torch.cuda.device(dev):
+    with _on(dev):
         y = torch.empty((M, n), dtype=x.dtype, device=dev) if out is None else out
         ws = _scratch(workspace, _size(L.moe_grouped_matmul_workspace_size, M, E, n, k, dt), dev)
         _check(L.moe_grouped_matmul(_p(x), _p(w), _p(offsets), M, E, n, k, dt,
                                     1 if out is None else 0, _p(y), _p(ws), _bytes(ws),
-                                    _stream()))
+                                    _stream_of(dev)))
     return y
 
 
@@ -446,13 +484,13 @@ def grouped_matmul_backward(x, w, offsets, dy, need_dx: bool = True, need_dw: bo
     dt = _dtype_code(x)
     _typed("dy", dy, x.dtype, (M, n))
     dev = _operands(x, w, offsets, dy)
-    with torch.cuda.device(dev):
+    with _on(dev):
         dx = torch.empty_like(x) if need_dx else None
         dw = torch.empty((E, n, k), dtype=torch.float32, device=dev) if need_dw else None
         ws = _scratch(workspace, _size(L.moe_grouped_matmul_backward_workspace_size, M, E, n, k,
                                        dt, int(need_dx), int(need_dw)), dev)
         _check(L.moe_grouped_matmul_backward(_p(x), _p(w), _p(offsets), _p(dy), M, E, n, k, dt, 1,
-                                             _p(dx), _p(dw), _p(ws), _bytes(ws), _stream()))
+                                             _p(dx), _p(dw), _p(ws), _bytes(ws), _stream_of(dev)))
     return dx, dw
 
 
@@ -497,10 +535,10 @@ def orthogonalize(x, steps: int = 5, eps: float = 1e-7,
         raise MoEError(1, f"tensors on different devices: {x.device} and {out.device}")
     os_ = _matrices("out", out)[3]
     a, b, c = (float(v) for v in coefficients)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         ws = _scratch(workspace, _size(L.moe_orthogonalize_workspace_size, B, m, n), x.device)
         _check(L.moe_orthogonalize(_p(x), xs, B, m, n, dt, steps, eps, a, b, c, _p(out), os_,
-                                   _dtype_code(out), _p(ws), _bytes(ws), _stream()))
+                                   _dtype_code(out), _p(ws), _bytes(ws), _stream_of(x.device)))
     return out
 
 
