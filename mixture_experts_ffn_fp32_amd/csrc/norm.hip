@@ -9,8 +9,7 @@
 //
 // Both directions are bound by HBM: x (and dy) once in, y or dx once out.  A
 // row therefore stays in registers between its reductions: TPR threads hold
-// NCH chunks of CH elements each (the widest aligned load that divides d: 16
-// bytes, for bfloat16 with even d 4 bytes, else one element).  The variance is
+// NCH chunks of 16 bytes each.  The variance is
 // the mean of squared deviations from the mean, a second sum over registers
 // (no cancellation).  Statistics, gradients and every sum are float32.
 //
@@ -19,6 +18,7 @@
 // block writes one partial row; a second launch adds the partial rows in a
 // fixed order (repeated calls give identical bits).
 #include <algorithm>
+#include <type_traits>
 
 #include "lds_dma.h"
 #include "ops_internal.h"
@@ -26,63 +26,69 @@
 namespace moe {
 namespace {
 
-// CH consecutive elements as raw bits, and their float32 values.
-template <class E, int CH>
-struct Raw;
-template <>
-struct Raw<ElemF32, 4> {
-  using V = u32x4;
-};
-template <>
-struct Raw<ElemF32, 1> {
-  using V = uint32_t;
-};
-template <>
-struct Raw<ElemBF16, 8> {
-  using V = u32x4;
-};
-template <>
-struct Raw<ElemBF16, 2> {
-  using V = uint32_t;
-};
-template <>
-struct Raw<ElemBF16, 1> {
-  using V = uint16_t;
-};
+// A 16-byte chunk of a row: CH elements as raw bits.  Rows of any width start at any
+// element, so the accesses claim an element's alignment only (the hardware takes
+// 16-byte accesses at any address; where the width is a whole number of chunks they are
+// aligned anyway).  The row's last chunk is read and written element by element unless
+// WHOLE says that the width is a multiple of a chunk (8192 x 2048 bfloat16: 15.2 ->
+// 14.4 us without that branch).
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+template <class E, bool WHOLE>
+struct Chunk {
+  static constexpr int CH = E::kPerChunk;
+  using T = typename E::T;
+  using V = std::conditional_t<sizeof(T) == 4, u32x4_at4, u32x4_at2>;
 
-template <class E, int CH>
-__device__ __forceinline__ void unpack(typename Raw<E, CH>::V v, float (&f)[CH]) {
-  if constexpr (CH == 1) {
-    if constexpr (sizeof(v) == 4) f[0] = __uint_as_float(v);
-    else f[0] = bf16_to_f32(v);
-  } else if constexpr (sizeof(typename E::T) == 4) {
+  static __device__ __forceinline__ u32x4 load(const T* __restrict__ row, int j, int d) {
+    if (WHOLE || j + CH <= d) return *(const V*)(row + j);
+    u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < CH; ++i) f[i] = __uint_as_float(v[i]);
-  } else if constexpr (CH == 2) {
-    f[0] = __uint_as_float(v << 16);
-    f[1] = __uint_as_float(v & 0xffff0000u);
-  } else {
+    for (int e = 0; e < CH; ++e)
+      if (j + e < d) {
+        if constexpr (sizeof(T) == 4) v[e] = __float_as_uint(row[j + e]);
+        else v[e >> 1] |= (uint32_t)row[j + e] << (16 * (e & 1));
+      }
+    return v;
+  }
+  static __device__ __forceinline__ void unpack(u32x4 v, float (&f)[CH]) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < CH / 2; ++i) {
-      f[2 * i] = __uint_as_float(v[i] << 16);
-      f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+      for (int i = 0; i < CH; ++i) f[i] = __uint_as_float(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH / 2; ++i) {
+        f[2 * i] = __uint_as_float(v[i] << 16);
+        f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+      }
     }
   }
-}
-template <class E, int CH>
-__device__ __forceinline__ typename Raw<E, CH>::V pack(const float (&f)[CH]) {
-  if constexpr (sizeof(typename E::T) == 4) {
-    if constexpr (CH == 1) return __float_as_uint(f[0]);
-    else return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-  } else if constexpr (CH == 1) {
-    return f32_to_bf16(f[0]);
-  } else if constexpr (CH == 2) {
-    return pack_bf16x2(f[0], f[1]);
-  } else {
-    return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                 pack_bf16x2(f[6], f[7])};
+  static __device__ __forceinline__ u32x4 pack(const float (&f)[CH]) {
+    u32x4 v;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) v[i] = __float_as_uint(f[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH / 2; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+    return v;
   }
-}
+  static __device__ __forceinline__ void store(T* __restrict__ row, int j, int d,
+                                               const float (&f)[CH]) {
+    const u32x4 v = pack(f);
+    if (WHOLE || j + CH <= d) {
+      *(V*)(row + j) = v;
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < CH; ++e)
+      if (j + e < d) {
+        if constexpr (sizeof(T) == 4) row[j + e] = __uint_as_float(v[e]);
+        else row[j + e] = (T)(v[e >> 1] >> (16 * (e & 1)));
+      }
+  }
+};
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -121,11 +127,13 @@ constexpr int norm_threads() {
 }
 
 // Chunk c of this thread starts at column (c * TPR + i) * CH (i: the thread's index in
-// its row), so a wavefront's load is contiguous.
-template <class E, int CH, int TPR, int NCH>
+// its row), so a wavefront's load is contiguous.  A chunk's elements past the row's end
+// are zeros.
+template <class E, int TPR, int NCH, bool WHOLE>
 __global__ __launch_bounds__(norm_threads<TPR>()) void norm_fwd_kernel(NormArgs a) {
-  using V = typename Raw<E, CH>::V;
+  using K = Chunk<E, WHOLE>;
   using T = typename E::T;
+  constexpr int CH = K::CH;
   __shared__ float s[2 * TPR / 64];
   constexpr int RPB = norm_threads<TPR>() / TPR;  // rows per block
   const int i = threadIdx.x % TPR, d = a.d;
@@ -133,17 +141,17 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_fwd_kernel(NormArgs 
   for (long long r = (long long)blockIdx.x * RPB + threadIdx.x / TPR; r < a.T;
        r += (long long)gridDim.x * RPB) {
     const T* x = (const T*)a.x + r * d;
-    V xv[NCH];
+    u32x4 xv[NCH];
     float sum = 0.f, zero = 0.f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int j = (c * TPR + i) * CH;
-      xv[c] = j < d ? *(const V*)(x + j) : V{};
+      xv[c] = j < d ? K::load(x, j, d) : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       float f[CH];
-      unpack<E, CH>(xv[c], f);
+      K::unpack(xv[c], f);
 #pragma unroll
       for (int e = 0; e < CH; ++e) sum += f[e];
     }
@@ -152,12 +160,11 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_fwd_kernel(NormArgs 
     float sq = 0.f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
+      const int j = (c * TPR + i) * CH;
       float f[CH];
-      unpack<E, CH>(xv[c], f);
-      if ((c * TPR + i) * CH < d) {
+      K::unpack(xv[c], f);
 #pragma unroll
-        for (int e = 0; e < CH; ++e) sq += (f[e] - mean) * (f[e] - mean);
-      }
+      for (int e = 0; e < CH; ++e) sq += (WHOLE ? j : j + e) < d ? (f[e] - mean) * (f[e] - mean) : 0.f;
     }
     row_sum2<TPR>(sq, zero, s);
     const float rstd = 1.f / sqrtf(sq * inv_d + a.eps);
@@ -171,26 +178,27 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_fwd_kernel(NormArgs 
       const int j = (c * TPR + i) * CH;
       if (j >= d) continue;
       float f[CH], w[CH], b[CH];
-      unpack<E, CH>(xv[c], f);
+      K::unpack(xv[c], f);
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         w[e] = 1.f;
         b[e] = 0.f;
       }
-      if (a.weight != nullptr) unpack<E, CH>(*(const V*)((const T*)a.weight + j), w);
-      if (a.bias != nullptr) unpack<E, CH>(*(const V*)((const T*)a.bias + j), b);
+      if (a.weight != nullptr) K::unpack(K::load((const T*)a.weight, j, d), w);
+      if (a.bias != nullptr) K::unpack(K::load((const T*)a.bias, j, d), b);
 #pragma unroll
       for (int e = 0; e < CH; ++e) f[e] = (f[e] - mean) * rstd * w[e] + b[e];
-      *(V*)(y + j) = pack<E, CH>(f);
+      K::store(y, j, d, f);
     }
   }
 }
 
 // DW: also the block's partial weight and bias gradients (part row blockIdx.x).
-template <class E, int CH, int TPR, int NCH, bool DW>
+template <class E, int TPR, int NCH, bool WHOLE, bool DW>
 __global__ __launch_bounds__(norm_threads<TPR>()) void norm_bwd_kernel(NormArgs a) {
-  using V = typename Raw<E, CH>::V;
+  using K = Chunk<E, WHOLE>;
   using T = typename E::T;
+  constexpr int CH = K::CH;
   constexpr int RPB = norm_threads<TPR>() / TPR;
   // row sums, and (RPB > 1) the rows' column sums on their way into the block's
   __shared__ float s[2 * TPR / 64];
@@ -204,41 +212,38 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_bwd_kernel(NormArgs 
 #pragma unroll
       for (int e = 0; e < CH; ++e) dw[c][e] = db[c][e] = 0.f;
   }
-  V wv[NCH];
-  if (a.weight != nullptr) {
+  u32x4 wv[NCH];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int j = (c * TPR + i) * CH;
-      wv[c] = j < d ? *(const V*)((const T*)a.weight + j) : V{};
-    }
-  } else {
+  for (int c = 0; c < NCH; ++c) {
+    const int j = (c * TPR + i) * CH;
     float one[CH];
 #pragma unroll
     for (int e = 0; e < CH; ++e) one[e] = 1.f;
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) wv[c] = pack<E, CH>(one);
+    wv[c] = a.weight == nullptr ? K::pack(one)
+            : j < d             ? K::load((const T*)a.weight, j, d)
+                                : u32x4{0u, 0u, 0u, 0u};
   }
   for (long long r = (long long)blockIdx.x * RPB + threadIdx.x / TPR; r < a.T;
        r += (long long)gridDim.x * RPB) {
     const T* x = (const T*)a.x + r * d;
     const T* dy = (const T*)a.dy + r * d;
-    V xv[NCH], yv[NCH];
+    u32x4 xv[NCH], yv[NCH];
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int j = (c * TPR + i) * CH;
-      xv[c] = j < d ? *(const V*)(x + j) : V{};
-      yv[c] = j < d ? *(const V*)(dy + j) : V{};
+      xv[c] = j < d ? K::load(x, j, d) : u32x4{0u, 0u, 0u, 0u};
+      yv[c] = j < d ? K::load(dy, j, d) : u32x4{0u, 0u, 0u, 0u};
     }
     const float mean = a.mean[r], rstd = a.rstd[r];
     float c1 = 0.f, c2 = 0.f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       float f[CH], g[CH], w[CH];
-      unpack<E, CH>(xv[c], f);
-      unpack<E, CH>(yv[c], g);
-      unpack<E, CH>(wv[c], w);
+      K::unpack(xv[c], f);
+      K::unpack(yv[c], g);
+      K::unpack(wv[c], w);
 #pragma unroll
-      for (int e = 0; e < CH; ++e) {  // (columns past d: dy = 0)
+      for (int e = 0; e < CH; ++e) {  // (past the row's end dy = 0)
         const float xh = (f[e] - mean) * rstd, gw = g[e] * w[e];
         c1 += gw;
         c2 += gw * xh;
@@ -257,15 +262,15 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_bwd_kernel(NormArgs 
       const int j = (c * TPR + i) * CH;
       if (j >= d) continue;
       float f[CH], g[CH], w[CH];
-      unpack<E, CH>(xv[c], f);
-      unpack<E, CH>(yv[c], g);
-      unpack<E, CH>(wv[c], w);
+      K::unpack(xv[c], f);
+      K::unpack(yv[c], g);
+      K::unpack(wv[c], w);
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         const float xh = (f[e] - mean) * rstd;
         f[e] = rstd * (g[e] * w[e] - c1 - xh * c2);
       }
-      *(V*)(dx + j) = pack<E, CH>(f);
+      K::store(dx, j, d, f);
     }
   }
   if constexpr (DW) {
@@ -293,9 +298,16 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_bwd_kernel(NormArgs 
             }
           }
         }
-        if (threadIdx.x < TPR && j < d) {
+        if (threadIdx.x < TPR) {
+          if (WHOLE ? j < d : j + CH <= d && d % 4 == 0) {
 #pragma unroll
-          for (int e = 0; e < CH; ++e) part[which * d + j + e] = f[e];
+            for (int e = 0; e < CH; e += 4)
+              *(f32x4*)(part + which * d + j + e) = f32x4{f[e], f[e + 1], f[e + 2], f[e + 3]};
+          } else {
+#pragma unroll
+            for (int e = 0; e < CH; ++e)
+              if (!WHOLE && j + e < d) part[which * d + j + e] = f[e];
+          }
         }
       }
   }
@@ -379,46 +391,39 @@ __global__ __launch_bounds__(256) void norm_cols_long_kernel(NormArgs a) {
   part[d + j] = db;
 }
 
-// dweight and dbias: column sums of the `chunks` partial rows, 64 columns per
-// block, 16 wavefronts over the rows, then the 16 sums in order.
+// dweight and dbias: column sums of the `chunks` partial rows, 32 columns per block, 32
+// threads a column over the rows, then the 32 sums in order.
 __global__ __launch_bounds__(1024) void norm_cols_kernel(NormArgs a, int chunks) {
-  __shared__ float s[16][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const long long j = (long long)blockIdx.x * 64 + lane, w2 = 2LL * a.d;
+  __shared__ float s[32][33];
+  const int col = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const long long w2 = 2LL * a.d, j = (long long)blockIdx.x * 32 + col;
   float sum = 0.f;
-  if (j < w2)
-    for (int p = w; p < chunks; p += 16) sum += a.part[p * w2 + j];
-  s[w][lane] = sum;
+  if (j < w2) {
+#pragma unroll 8
+    for (int p = g; p < chunks; p += 32) sum += a.part[p * w2 + j];
+  }
+  s[g][col] = sum;
   __syncthreads();
-  if (w != 0 || j >= w2) return;
+  if (g != 0 || j >= w2) return;
   sum = 0.f;
 #pragma unroll
-  for (int q = 0; q < 16; ++q) sum += s[q][lane];
+  for (int q = 0; q < 32; ++q) sum += s[q][col];
   float* out = j < a.d ? a.dweight : a.dbias;
   if (out != nullptr) out[j < a.d ? j : j - a.d] = sum;
 }
 
 // ---------------------------------------------------------------- launch rules
-// The widest load that divides d, then the smallest (threads per row, chunks)
-// that hold the row: one wavefront per row up to 4 chunks a lane, so small
-// rows need no barrier, then 256 and 1024 threads.
+// The smallest (threads per row, chunks) that hold the row: one wavefront per row up to
+// 4 chunks a lane, so small rows need no barrier, then 256 and 1024 threads.
 struct NormPlan {
-  int ch, tpr, nch;  // nch = 0: the row does not fit registers
+  int tpr, nch;  // nch = 0: the row does not fit registers
 };
 NormPlan norm_plan(int dtype, int d) {
-  NormPlan p;
-  if (dtype == 0) p.ch = d % 4 == 0 ? 4 : 1;
-  else p.ch = d % 8 == 0 ? 8 : d % 2 == 0 ? 2 : 1;
-  static const int options[][2] = {{64, 1}, {64, 2}, {64, 4}, {256, 2}, {256, 4}, {1024, 4}, {1024, 8}};
+  const int ch = dtype == 0 ? 4 : 8;
+  static const int options[][2] = {{64, 1}, {64, 2}, {64, 4}, {256, 2}, {256, 4}, {1024, 2}};
   for (const auto& o : options)
-    if ((long long)o[0] * o[1] * p.ch >= d) {
-      p.tpr = o[0];
-      p.nch = o[1];
-      return p;
-    }
-  p.tpr = 1024;
-  p.nch = 0;
-  return p;
+    if ((long long)o[0] * o[1] * ch >= d) return NormPlan{o[0], o[1]};
+  return NormPlan{1024, 0};
 }
 
 int norm_rows_per_block(const NormPlan& p) { return p.tpr < 256 ? 256 / p.tpr : 1; }
@@ -431,26 +436,25 @@ unsigned norm_grid(const NormPlan& p, int T, int most) {
   return (unsigned)std::min<long long>(((long long)T + rpb - 1) / rpb, most);
 }
 
-template <class E, int CH, int TPR, int NCH>
+template <class E, int TPR, int NCH, bool WHOLE>
 hipError_t run_norm(bool bwd, bool dw, unsigned grid, const NormArgs& a, hipStream_t st) {
   const dim3 b(norm_threads<TPR>());
-  if (!bwd) norm_fwd_kernel<E, CH, TPR, NCH><<<grid, b, 0, st>>>(a);
-  else if (dw) norm_bwd_kernel<E, CH, TPR, NCH, true><<<grid, b, 0, st>>>(a);
-  else norm_bwd_kernel<E, CH, TPR, NCH, false><<<grid, b, 0, st>>>(a);
+  if (!bwd) norm_fwd_kernel<E, TPR, NCH, WHOLE><<<grid, b, 0, st>>>(a);
+  else if (dw) norm_bwd_kernel<E, TPR, NCH, WHOLE, true><<<grid, b, 0, st>>>(a);
+  else norm_bwd_kernel<E, TPR, NCH, WHOLE, false><<<grid, b, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <class E, int CH>
+template <class E, bool WHOLE>
 hipError_t pick_norm(const NormPlan& p, bool bwd, bool dw, unsigned grid, const NormArgs& a,
                      hipStream_t st) {
   switch (p.tpr * 16 + p.nch) {
-    case 64 * 16 + 1: return run_norm<E, CH, 64, 1>(bwd, dw, grid, a, st);
-    case 64 * 16 + 2: return run_norm<E, CH, 64, 2>(bwd, dw, grid, a, st);
-    case 64 * 16 + 4: return run_norm<E, CH, 64, 4>(bwd, dw, grid, a, st);
-    case 256 * 16 + 2: return run_norm<E, CH, 256, 2>(bwd, dw, grid, a, st);
-    case 256 * 16 + 4: return run_norm<E, CH, 256, 4>(bwd, dw, grid, a, st);
-    case 1024 * 16 + 4: return run_norm<E, CH, 1024, 4>(bwd, dw, grid, a, st);
-    case 1024 * 16 + 8: return run_norm<E, CH, 1024, 8>(bwd, dw, grid, a, st);
+    case 64 * 16 + 1: return run_norm<E, 64, 1, WHOLE>(bwd, dw, grid, a, st);
+    case 64 * 16 + 2: return run_norm<E, 64, 2, WHOLE>(bwd, dw, grid, a, st);
+    case 64 * 16 + 4: return run_norm<E, 64, 4, WHOLE>(bwd, dw, grid, a, st);
+    case 256 * 16 + 2: return run_norm<E, 256, 2, WHOLE>(bwd, dw, grid, a, st);
+    case 256 * 16 + 4: return run_norm<E, 256, 4, WHOLE>(bwd, dw, grid, a, st);
+    case 1024 * 16 + 2: return run_norm<E, 1024, 2, WHOLE>(bwd, dw, grid, a, st);
     default: return hipErrorInvalidValue;
   }
 }
@@ -458,11 +462,10 @@ hipError_t pick_norm(const NormPlan& p, bool bwd, bool dw, unsigned grid, const 
 hipError_t run_plan(int dtype, const NormPlan& p, bool bwd, bool dw, unsigned grid,
                     const NormArgs& a, hipStream_t st) {
   if (dtype == 0)
-    return p.ch == 4 ? pick_norm<ElemF32, 4>(p, bwd, dw, grid, a, st)
-                     : pick_norm<ElemF32, 1>(p, bwd, dw, grid, a, st);
-  if (p.ch == 8) return pick_norm<ElemBF16, 8>(p, bwd, dw, grid, a, st);
-  return p.ch == 2 ? pick_norm<ElemBF16, 2>(p, bwd, dw, grid, a, st)
-                   : pick_norm<ElemBF16, 1>(p, bwd, dw, grid, a, st);
+    return a.d % ElemF32::kPerChunk == 0 ? pick_norm<ElemF32, true>(p, bwd, dw, grid, a, st)
+                                         : pick_norm<ElemF32, false>(p, bwd, dw, grid, a, st);
+  return a.d % ElemBF16::kPerChunk == 0 ? pick_norm<ElemBF16, true>(p, bwd, dw, grid, a, st)
+                                        : pick_norm<ElemBF16, false>(p, bwd, dw, grid, a, st);
 }
 
 }  // namespace
@@ -502,7 +505,7 @@ hipError_t launch_layer_norm_backward(int dtype, const NormArgs& a, hipStream_t 
     }
   }
   if (e != hipSuccess || !dw) return e;
-  norm_cols_kernel<<<(unsigned)((2LL * a.d + 63) / 64), 1024, 0, st>>>(a, chunks);
+  norm_cols_kernel<<<(unsigned)((2LL * a.d + 31) / 32), 1024, 0, st>>>(a, chunks);
   return hipGetLastError();
 }
 
