@@ -370,6 +370,8 @@ moe_status_t moe_orthogonalize(const void* x, int64_t x_stride, int B, int m, in
   o.a = a;
   o.b = b;
   o.c = c;
+  o.most_x = iterate;
+  o.most_p = factor;
   return launched(moe::launch_orthogonalize(o, workspace, (hipStream_t)stream),
                   "orthogonalise launch");
 }

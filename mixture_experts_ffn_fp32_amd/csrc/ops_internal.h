@@ -57,6 +57,7 @@ struct OrthoArgs {
   int B, m, n, steps;
   int dtype, out_dtype;
   float eps, a, b, c;
+  double most_x, most_p;  // ortho_bounds of these steps and coefficients
 };
 // Largest bounds of the iterate and of the polynomial factor over the steps, for
 // coefficients (a, b, c) and a first iterate of Frobenius norm 1.
@@ -64,6 +65,18 @@ void ortho_bounds(int steps, float a, float b, float c, double* iterate, double*
 constexpr double kOrthoMaxBound = 1024.0;
 size_t ortho_workspace_bytes(int B, int m, int n);
 hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st);
+
+// Power-of-two scales and constants of the products (see launch_orthogonalize): X is
+// held times 2^ex (`first`), S = A + d I times 2^ea, P times 2^ep; each product's
+// accumulators times its scale are the next operand.
+struct OrthoScales {
+  float first, s_scale, s_diag, p_scale, p_diag, x_scale, last_scale;
+};
+// orthogonalize_small.hip: whether these matrices go there, and the launch.
+bool ortho_small_fits(int B, int m, int n);
+size_t ortho_small_workspace_bytes(int B, int m, int n);
+hipError_t launch_orthogonalize_small(const OrthoArgs& a, const OrthoScales& s, void* ws,
+                                      hipStream_t st);
 
 int device_cu_count();
 

@@ -372,55 +372,79 @@ hipError_t pick_ns(const NsProduct& p, hipStream_t st) {
 
 }  // namespace
 
-void ortho_bounds(int steps, float a, float b, float c, double* iterate, double* factor) {
+void ortho_bounds(int steps, float af, float bf, float cf, double* iterate, double* factor) {
+  const double a = af, b = bf, c = cf;
   double s = 1.0, top = 1.0, f = 0.0;
-  for (int k = 0; k < steps; ++k) {
-    // |p| over [0, s] and |a + b t + c t^2| over [0, s^2], at 4096 points each and
-    // padded by what lies between them
-    double next = 0.0, fac = 0.0;
-    for (int i = 0; i <= 4096; ++i) {
-      const double u = s * i / 4096.0, t = u * u;
-      const double q = (double)a + (double)b * t + (double)c * t * t;
-      fac = std::max(fac, fabs(q));
-      next = std::max(next, fabs(u * q));
+  for (int k = 0; k < steps && top <= 1e30 && f <= 1e30; ++k) {
+    // q = |a + b t + c t^2| and |u q(u^2)| = |a u + b u^3 + c u^5| over u in [0, s],
+    // t = u^2: at the ends of the range and where their derivatives vanish
+    const double end = s * s;
+    double fac = fabs(a), next = 0.0;
+    auto at = [&](double t) {
+      if (!(t >= 0.0) || t > end) return;
+      const double q = fabs(a + b * t + c * t * t);
+      fac = std::max(fac, q);
+      next = std::max(next, sqrt(t) * q);
+    };
+    at(end);
+    if (c != 0.0) {
+      at(-b / (2.0 * c));
+      const double root = 9.0 * b * b - 20.0 * a * c;  // of a + 3 b t + 5 c t^2
+      if (root >= 0.0) {
+        at((-3.0 * b + sqrt(root)) / (10.0 * c));
+        at((-3.0 * b - sqrt(root)) / (10.0 * c));
+      }
+    } else if (b != 0.0) {
+      at(-a / (3.0 * b));
     }
+    // (1.01: what the products' rounding adds, and that of these points)
     f = std::max(f, 1.01 * fac);
     s = 1.01 * next;
     top = std::max(top, s);
-    if (!(top <= 1e30) || !(f <= 1e30)) break;
   }
   *iterate = top;
   *factor = f;
 }
 
-size_t ortho_workspace_bytes(int B, int m, int n) { return ns_plan(B, m, n).bytes; }
+size_t ortho_workspace_bytes(int B, int m, int n) {
+  // (no steps: the general path's norm and division, whatever the size)
+  return std::max(ortho_small_fits(B, m, n) ? ortho_small_workspace_bytes(B, m, n) : 0,
+                  ns_plan(B, m, n).bytes);
+}
 
 hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
+  // d of the completed square; c = 0: the first product gives P = a I + b A itself
+  const double d = a.c != 0.f ? (double)a.b / (2.0 * a.c) : 0.0;
+  const int ex = scale_exponent(a.most_x), ea = scale_exponent(a.most_x * a.most_x + fabs(d)),
+            ep = scale_exponent(a.most_p);
+  OrthoScales sc{};
+  sc.first = a.steps == 0 ? 1.f : ldexpf(1.f, ex);
+  sc.s_scale = ldexpf(1.f, ea - 2 * ex);
+  sc.s_diag = (float)ldexp(d, ea);
+  sc.p_scale = a.c != 0.f ? ldexpf(a.c, ep - 2 * ea) : ldexpf(a.b, ep - 2 * ex);
+  sc.p_diag = (float)ldexp(a.a - a.c * d * d, ep);
+  sc.x_scale = ldexpf(1.f, -ep);
+  sc.last_scale = ldexpf(1.f, -ep - ex);
+  if (a.steps > 0 && ortho_small_fits(a.B, a.m, a.n))
+    return launch_orthogonalize_small(a, sc, ws, st);
   const NsPlan l = ns_plan(a.B, a.m, a.n);
   uint8_t* w = (uint8_t*)ws;
   double* part = (double*)(w + l.part);
   const long long per = (long long)a.m * a.n, rows = (long long)a.B * a.m;
   int32_t* counters = (int32_t*)(w + l.counters);
   const int claims = a.steps * 3 * kTgCounters;
-  double most_x, most_p;
-  ortho_bounds(a.steps, a.a, a.b, a.c, &most_x, &most_p);
-  // d of the completed square; c = 0: the first product gives P = a I + b A itself
-  const double d = a.c != 0.f ? (double)a.b / (2.0 * a.c) : 0.0;
-  const int ex = scale_exponent(most_x), ea = scale_exponent(most_x * most_x + fabs(d)),
-            ep = scale_exponent(most_p);
   const uint32_t px = (uint32_t)split_pitch(a.n), pa = (uint32_t)split_pitch(std::min(a.m, a.n));
-  const float start = a.steps == 0 ? 1.f : ldexpf(1.f, ex);
   void* direct = a.steps == 0 ? a.out : nullptr;
   const dim3 gn(kNormParts, a.B), gs((unsigned)((rows + 3) / 4));
   if (a.dtype == 0) {
     ns_norm_kernel<ElemF32><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part,
                                                 counters, claims);
-    ns_start_kernel<ElemF32><<<gs, 256, 0, st>>>(a.x, a.x_stride, a.m, a.n, rows, part, a.eps, start,
+    ns_start_kernel<ElemF32><<<gs, 256, 0, st>>>(a.x, a.x_stride, a.m, a.n, rows, part, a.eps, sc.first,
                                                  w + l.x[0], px, direct, a.out_stride, a.out_dtype);
   } else {
     ns_norm_kernel<ElemBF16><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part,
                                                 counters, claims);
-    ns_start_kernel<ElemBF16><<<gs, 256, 0, st>>>(a.x, a.x_stride, a.m, a.n, rows, part, a.eps, start,
+    ns_start_kernel<ElemBF16><<<gs, 256, 0, st>>>(a.x, a.x_stride, a.m, a.n, rows, part, a.eps, sc.first,
                                                   w + l.x[0], px, direct, a.out_stride, a.out_dtype);
   }
   hipError_t e = hipGetLastError();
@@ -442,13 +466,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
     g.K = tall ? a.m : a.n;
     g.count = a.B;
     g.counters = cnt;
-    if (a.c != 0.f) {
-      g.scale = ldexpf(1.f, ea - 2 * ex);
-      g.diag = (float)ldexp(d, ea);
-    } else {
-      g.scale = ldexpf(a.b, ep - 2 * ex);
-      g.diag = ldexpf(a.a, ep);
-    }
+    g.scale = a.c != 0.f ? sc.s_scale : sc.p_scale;
+    g.diag = a.c != 0.f ? sc.s_diag : sc.p_diag;
     e = tall ? pick_ns<NS_SYM, true, true, false>(g, st) : pick_ns<NS_SYM, false, false, false>(g, st);
     if (e != hipSuccess) break;
     if (a.c != 0.f) {
@@ -462,8 +481,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
       q.M = q.N = q.K = side;
       q.count = a.B;
       q.counters = cnt + kTgCounters;
-      q.scale = ldexpf(a.c, ep - 2 * ea);
-      q.diag = (float)ldexp(a.a - a.c * d * d, ep);
+      q.scale = sc.p_scale;
+      q.diag = sc.p_diag;
       e = pick_ns<NS_SYM, false, false, false>(q, st);
       if (e != hipSuccess) break;
     }
@@ -476,12 +495,12 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
     u.K = side;
     u.count = a.B;
     u.counters = cnt + 2 * kTgCounters;
-    u.scale = ldexpf(1.f, -ep);
+    u.scale = sc.x_scale;
     if (k + 1 == a.steps) {
       u.last = a.out;
       u.last_dtype = a.out_dtype;
       u.stride_last = a.out_stride;
-      u.scale = ldexpf(1.f, -ep - ex);
+      u.scale = sc.last_scale;
     }
     if (tall) {  // X P
       u.A = X;
