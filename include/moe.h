@@ -241,7 +241,7 @@ moe_status_t moe_layer_backward(const void* u, const void* E_gate, const void* W
  *   y_tj   = (x_tj - mean_t) rstd_t weight_j + bias_j
  *   x [T][d] dtype, weight [d] dtype or NULL (ones), bias [d] dtype or NULL (zeros),
  *   y [T][d] dtype, mean [T] and rstd [T] float32 or NULL (the backward needs both).
- * Any T >= 0 and d >= 1. */
+ * Any T >= 0; 1 <= d <= 2^24. */
 moe_status_t moe_layer_norm(const void* x, const void* weight, const void* bias, int T, int d,
                             float eps, int dtype, void* y, float* mean, float* rstd,
                             void* stream);
@@ -249,8 +249,8 @@ moe_status_t moe_layer_norm(const void* x, const void* weight, const void* bias,
 /* Gradients of sum_t dy_t . y_t (xh = (x - mean) rstd, g = dy weight):
  *   dx = rstd (g - mean_j(g) - xh mean_j(g xh))   [T][d] dtype
  *   dweight = sum_t dy xh, dbias = sum_t dy       [d] float32, each may be NULL
- * mean and rstd are the forward's.  T = 0 writes nothing.  The workspace is
- * needed where dweight or dbias is given. */
+ * mean and rstd are the forward's.  T = 0 gives zero dweight and dbias.  The
+ * workspace is needed where dweight or dbias is given (not for T = 0). */
 moe_status_t moe_layer_norm_backward_workspace_size(int T, int d, int dtype, size_t* bytes);
 moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* weight,
                                      const float* mean, const float* rstd, int T, int d, int dtype,
@@ -269,7 +269,8 @@ moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* 
  * one below its predecessor counts as equal to it.
  * bfloat16: exact products, float32 sums, one rounding.  float32: products of
  * two-float16 splits (float32 accuracy; each row of x and w is scaled on its
- * own, so rows may differ by any factor).
+ * own, so rows may differ by any factor).  An infinity or NaN reaches the
+ * results of its own products only.
  * Limits: 1 <= E <= 1024; n, k <= 2^20. */
 moe_status_t moe_grouped_matmul_workspace_size(int M, int E, int n, int k, int dtype,
                                                size_t* bytes);

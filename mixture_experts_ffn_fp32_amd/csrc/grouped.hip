@@ -18,6 +18,8 @@
 // forward, w; per expert for w in the backward, whose product contracts over
 // w's rows; and for x in the weight gradient, which contracts over the rows of
 // both, the scale that makes each row's product scale the same.
+#include <float.h>
+
 #include <algorithm>
 
 #include "ops_internal.h"
@@ -303,10 +305,12 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
+// (of the finite values: an infinity or NaN stays one in its own products and takes no
+// other value's scale)
 __device__ __forceinline__ float chunk_max(const float (&f)[8]) {
   float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]) <= FLT_MAX ? fabsf(f[e]) : 0.f);
   return m;
 }
 // Splits one row; `exponent` gives the scale from the row's largest magnitude.

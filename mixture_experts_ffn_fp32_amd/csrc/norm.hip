@@ -379,7 +379,7 @@ __global__ __launch_bounds__(256) void norm_cols_long_kernel(NormArgs a) {
   using T = typename E::T;
   const int j = blockIdx.x * 256 + threadIdx.x, d = a.d;
   if (j >= d) return;
-  const int R = long_rows(a.T), r0 = blockIdx.y * R, r1 = min(r0 + R, a.T);
+  const int R = long_rows(a.T), r0 = blockIdx.y * R, r1 = r0 + min(R, a.T - r0);
   float dw = 0.f, db = 0.f;
   for (int r = r0; r < r1; ++r) {
     const float g = load_as_f32<E>((const T*)a.dy + (long long)r * d + j);
@@ -488,9 +488,10 @@ int layer_norm_chunks(int dtype, int T, int d) {
 hipError_t launch_layer_norm_backward(int dtype, const NormArgs& a, hipStream_t st) {
   const NormPlan p = norm_plan(dtype, a.d);
   const bool dw = a.dweight != nullptr || a.dbias != nullptr;
-  const int chunks = layer_norm_chunks(dtype, a.T, a.d);
-  hipError_t e;
-  if (p.nch != 0) {
+  const int chunks = layer_norm_chunks(dtype, a.T, a.d);  // T = 0: none, so zero sums
+  hipError_t e = hipSuccess;
+  if (a.T == 0) {
+  } else if (p.nch != 0) {
     e = run_plan(dtype, p, true, dw, norm_grid(p, a.T, kNormBwdBlocks), a, st);
   } else {
     const unsigned grid = norm_grid(p, a.T, kNormFwdBlocks);

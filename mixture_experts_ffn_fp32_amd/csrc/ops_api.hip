@@ -2,6 +2,7 @@
 // checks and launches.  As in the layer's own entry points, validation runs
 // before any HIP call, no device memory is allocated and nothing waits.
 #include <math.h>
+#include <stdint.h>
 
 #include <algorithm>
 #include <string>
@@ -73,6 +74,7 @@ moe_status_t check_norm(int T, int d, int dtype) {
   if (s != MOE_OK) return s;
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T must be >= 0");
   if (d < 1) return fail(MOE_ERR_INVALID_ARG, "d must be positive");
+  if (d > (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "d > 2^24 is not supported");
   return MOE_OK;
 }
 size_t norm_bwd_bytes(int T, int d, int dtype) {
@@ -163,13 +165,12 @@ moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* 
                                      size_t workspace_bytes, void* stream) {
   moe_status_t s = check_norm(T, d, dtype);
   if (s != MOE_OK) return s;
-  if (T == 0) return ok();
-  if ((s = check_ptr("dy", dy, true)) != MOE_OK) return s;
-  if ((s = check_ptr("x", x, true)) != MOE_OK) return s;
+  if ((s = check_ptr("dy", dy, T > 0)) != MOE_OK) return s;
+  if ((s = check_ptr("x", x, T > 0)) != MOE_OK) return s;
   if ((s = check_ptr("weight", weight, false)) != MOE_OK) return s;
-  if ((s = check_ptr("mean", mean, true)) != MOE_OK) return s;
-  if ((s = check_ptr("rstd", rstd, true)) != MOE_OK) return s;
-  if ((s = check_ptr("dx", dx, true)) != MOE_OK) return s;
+  if ((s = check_ptr("mean", mean, T > 0)) != MOE_OK) return s;
+  if ((s = check_ptr("rstd", rstd, T > 0)) != MOE_OK) return s;
+  if ((s = check_ptr("dx", dx, T > 0)) != MOE_OK) return s;
   if ((s = check_ptr("dweight", dweight, false)) != MOE_OK) return s;
   if ((s = check_ptr("dbias", dbias, false)) != MOE_OK) return s;
   const size_t need = dweight != nullptr || dbias != nullptr ? norm_bwd_bytes(T, d, dtype) : 0;
@@ -335,6 +336,8 @@ moe_status_t moe_orthogonalize(const void* x, int64_t x_stride, int B, int m, in
   const int64_t per = (int64_t)m * n;
   if (B > 1 && (x_stride < per || out_stride < per))
     return fail(MOE_ERR_INVALID_ARG, "x_stride and out_stride must be at least m * n");
+  if (B > 1 && std::max(x_stride, out_stride) > INT64_MAX / 8 / B)
+    return fail(MOE_ERR_INVALID_ARG, "x_stride and out_stride reach past the address space");
   const size_t es = elem_size(dtype), eo = elem_size(out_dtype);
   if (B > 1 && ((x_stride * es) % 16 != 0 || (out_stride * eo) % 16 != 0) &&
       (x_stride != per || out_stride != per))

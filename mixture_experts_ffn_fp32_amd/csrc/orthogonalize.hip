@@ -296,7 +296,7 @@ __global__ __launch_bounds__(256) void ns_start_kernel(const void* __restrict__ 
   for (int k = 32; k > 0; k >>= 1) sq += __shfl_xor(sq, k);
   const double norm = sqrt(sq) + (double)eps;
   // an all-zero matrix stays zero
-  const double f = norm > 0.0 ? (double)scale / norm : 0.0;
+  const double f = norm == 0.0 ? 0.0 : (double)scale / norm;
   const typename E::T* src = (const typename E::T*)x + i * stride + row * n;
   if (last != nullptr) {
     for (int j = lane; j < n; j += 64) {

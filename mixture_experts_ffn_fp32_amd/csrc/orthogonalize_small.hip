@@ -382,7 +382,7 @@ __global__ __launch_bounds__(NsSmall<PP>::THREADS) void ns_small_kernel(NsSmallA
   // X_0 = x f0, f0 = scale 2^raise: the power of two first, exact on the smallest values (an
   // all-zero matrix stays zero; f0's rounding scales the whole matrix by 1 +- 2^-24)
   int raise = 0;
-  const float scale = (float)frexp(norm > 0.0 ? (double)a.first / norm : 0.0, &raise);
+  const float scale = (float)frexp(norm == 0.0 ? 0.0 : (double)a.first / norm, &raise);
   __syncthreads();
 
   // this lane's 16 bytes of a chunk: instruction i covers rows 8 i .. of one of its units

@@ -31,7 +31,6 @@ namespace moe {
 namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef short tg_v4s __attribute__((ext_vector_type(4)));
 
 // WM x WN wavefronts of FM x FN fragments of 32 x 32; a ring of S k-steps, S - 1 of

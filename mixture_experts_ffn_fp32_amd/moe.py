@@ -434,10 +434,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None):
     dev = _operands(x, dy, weight, mean, rstd)
     with _on(dev):
         dx = torch.empty_like(x)
-        # an empty batch writes nothing: its weight gradients are zeros
-        alloc = torch.zeros if T == 0 else torch.empty
-        dw = alloc(d, dtype=torch.float32, device=dev)
-        db = alloc(d, dtype=torch.float32, device=dev)
+        dw = torch.empty(d, dtype=torch.float32, device=dev)
+        db = torch.empty(d, dtype=torch.float32, device=dev)
         ws = _scratch(workspace, _size(L.moe_layer_norm_backward_workspace_size, T, d, dt), dev)
         _check(L.moe_layer_norm_backward(_p(dy), _p(x), _p(weight), _p(mean), _p(rstd), T, d, dt,
                                          _p(dx), _p(dw), _p(db), _p(ws), _bytes(ws), _stream_of(dev)))

@@ -7,8 +7,7 @@ Tolerances, per element, u = 2^-24:
           the left-out lo lo' product u) and 2^-38 of the largest product for values far below
           their row's largest;
   stats   a row sum goes through at most 64 additions in a thread and 26 across threads: 96 u;
-  store   half a step of the stored type: 2^-9 (bf16: eps / 2 = 2^-8 as a bound of the relative
-          error), u for float32.
+  store   half a step of the stored type, relative: 2^-8 for bfloat16, u for float32.
 """
 import numpy as np
 import pytest

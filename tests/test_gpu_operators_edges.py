@@ -1,0 +1,237 @@
+"""The operators beside the layer where they can go wrong: infinities and NaN among the
+operands, tensors past 2^32 bytes, workspaces shared by captured graphs, empty batches, and
+the orthogonalised update on both sides of its size rule.  Tolerances are those of
+test_gpu_operators.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import operators as ref
+from parity_helpers import say
+from test_gpu_operators import (STORE, U, _bits, _grouped_inputs, _growth, _offsets, _sum_tol, dev,
+                                host, mx, within)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- values that are not finite
+def _same_where_finite(got, want, tol, label):
+    """got is not finite exactly where want is not, and within tol elsewhere."""
+    g = host(got)
+    assert (np.isfinite(g) == np.isfinite(want)).all(), label
+    ok = np.isfinite(want)
+    within(np.where(ok, g, 0.0), np.where(ok, want, 0.0), np.where(ok, tol, 1.0), label)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,k", [(48, 72), (320, 256)])
+def test_grouped_bad_values_reach_their_own_results_only(n, k, dtype):
+    sizes = [30, 150, 0, 9]
+    x, w, off, dy, _ = _grouped_inputs(sizes, 2, 3, n, k, dtype, 21)
+    x[2 + 5, 7] = float("inf")
+    x[2 + 31, 0] = float("nan")
+    w[1, 3, 11] = -float("inf")
+    w[3, n - 1, k - 1] = float("nan")
+    dy[2 + 40, 6] = float("inf")
+    dy[2 + 182] = float("nan")               # a whole row
+    say(f"grouped bad values n={n} k={k} {dtype}")
+    y = mx.grouped_matmul(x, w, off)
+    dx, dw = mx.grouped_matmul_backward(x, w, off, dy)
+    torch.cuda.synchronize()
+    offs = off.cpu().numpy()
+    fx, fw, fdy = (np.where(np.isfinite(host(t)), np.abs(host(t)), 0.0) for t in (x, w, dy))
+    most = fx[2:191].max() * fdy[2:191].max()
+    with np.errstate(invalid="ignore"):
+        for e, (a, b) in enumerate(ref.group_rows(offs, x.shape[0])):
+            X, W, DY = host(x)[a:b], host(w)[e], host(dy)[a:b]
+            t = _sum_tol(fx[a:b], fw[e], k, dtype)
+            want = X @ W.T
+            _same_where_finite(y[a:b], want, t + STORE[dtype] * (np.abs(want) + t), f"y {e}")
+            t = _sum_tol(fdy[a:b], fw[e].T, n, dtype)
+            want = DY @ W
+            _same_where_finite(dx[a:b], want, t + STORE[dtype] * (np.abs(want) + t), f"dx {e}")
+            t = _sum_tol(fdy[a:b].T, fx[a:b].T, b - a, dtype)
+            t = t + (b - a) * 2.0 ** -37 * most * (dtype == "f32")
+            want = DY.T @ X
+            _same_where_finite(dw[e], want, t + U * np.abs(want), f"dw {e}")
+
+
+@pytest.mark.parametrize("steps", [0, 1, 5])
+@pytest.mark.parametrize("m,n", [(33, 64), (96, 100), (200, 300)])
+def test_orthogonalize_keeps_a_bad_matrix_to_itself(m, n, steps):
+    r = np.random.default_rng(22)
+    x = dev(r.normal(size=(4, m, n)))
+    clean = mx.orthogonalize(x, steps=steps)
+    x[1, 2, 3] = float("nan")
+    x[3, m - 1, n - 1] = float("inf")
+    say(f"orthogonalize bad values {m}x{n}")
+    out = mx.orthogonalize(x, steps=steps)
+    torch.cuda.synchronize()
+    for i in (0, 2):
+        assert torch.equal(_bits(out[i]), _bits(clean[i]))
+    assert torch.isnan(out[1]).all()
+    if steps:                                 # (without steps a / inf is a zero)
+        assert torch.isnan(out[3]).all()
+    else:
+        assert torch.isnan(out[3, m - 1, n - 1]) and not out[3].nan_to_num().any()
+
+
+def test_layer_norm_backward_of_an_empty_batch():
+    for dt in (torch.float32, torch.bfloat16):
+        for d in (5, 512, 20000):
+            say(f"layer_norm T=0 d={d}")
+            x = torch.empty(0, d, device="cuda", dtype=dt)
+            w = torch.ones(d, device="cuda", dtype=dt)
+            y, mean, rstd = mx.layer_norm(x, w)
+            dx, dw, db = mx.layer_norm_backward(x, x, w, mean, rstd)
+            torch.cuda.synchronize()
+            assert y.shape == dx.shape == (0, d) and mean.shape == rstd.shape == (0,)
+            assert dw.shape == db.shape == (d,) and not dw.any() and not db.any()
+
+
+# ---------------------------------------------------------------- the update's two paths
+# (batches and sides around 64, 128 and the rule's limits; tall and wide; odd sizes)
+PATHS = [(1, 1, 300), (2, 64, 65), (1, 65, 65), (3, 63, 449), (1, 64, 513), (1, 513, 64), (2, 128, 129),
+         (2, 129, 128), (1, 128, 257), (3, 129, 131), (127, 20, 2500), (128, 20, 2500), (17, 128, 1000),
+         (130, 130, 65), (140, 100, 700), (300, 9, 10), (2, 500, 130), (1, 1100, 700)]
+
+
+def _check_update(got, g, steps, coef, dtype, label):
+    want = ref.orthogonalize(g, steps, 1e-7, coef)
+    delta = 2 * U * 3 * 11 * np.sqrt(max(g.shape))
+    tol = (delta * _growth(g, steps, coef) + 2 * U + (STORE["bf16"] if dtype == "bf16" else 0))
+    err = np.linalg.norm(host(got) - want)
+    assert err <= tol * np.linalg.norm(want), (label, err, tol * np.linalg.norm(want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,m,n", PATHS)
+def test_orthogonalize_both_paths(B, m, n, dtype):
+    r = np.random.default_rng(B + 1000 * m + n)
+    x = dev(r.normal(size=(B, m, n)) * 10.0 ** r.uniform(-6, 6, (B, 1, 1)), dtype)
+    usual = (3.4445, -4.7750, 2.0315)
+    for steps, coef in ((5, usual), (1, usual), (3, (1.5, -0.5, 0.0))):
+        say(f"orthogonalize B={B} {m}x{n} {dtype} steps={steps}")
+        out = mx.orthogonalize(x, steps=steps, coefficients=coef)
+        again = mx.orthogonalize(x, steps=steps, coefficients=coef)
+        torch.cuda.synchronize()
+        assert torch.equal(_bits(out), _bits(again))
+        for i in sorted({0, B // 2, B - 1}):
+            _check_update(out[i], host(x[i]), steps, coef, dtype, (i, steps))
+    mine = x.clone()
+    assert mx.orthogonalize(mine, out=mine) is mine
+    want = mx.orthogonalize(x)
+    other = mx.orthogonalize(x, out_dtype=torch.float32 if dtype == "bf16" else torch.bfloat16)
+    torch.cuda.synchronize()
+    assert torch.equal(_bits(mine), _bits(want))
+    low = (other if dtype == "f32" else want)
+    assert torch.equal(_bits(low), _bits((want if dtype == "f32" else other).to(torch.bfloat16)))
+
+
+# ---------------------------------------------------------------- past 2^32 bytes
+def _rows_match(got, want, a, b, n, dtype, label):
+    t = _sum_tol(np.abs(a), np.abs(b), n, dtype)
+    within(got, want, t + STORE[dtype] * (np.abs(want) + t), label)
+
+
+def test_grouped_rows_past_4_gib():
+    M, k, n, E = 300_001, 8192, 24, 3
+    torch.manual_seed(1)
+    x = torch.randn(M, k, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(E, n, k, device="cuda", dtype=torch.bfloat16)
+    off = torch.tensor([0, 100, 299_990, 300_000], dtype=torch.int32, device="cuda")
+    say("grouped x of 4.9 GB")
+    y = mx.grouped_matmul(x, w, off)
+    dy = torch.randn(M, n, device="cuda", dtype=torch.bfloat16)
+    dx, _ = mx.grouped_matmul_backward(x, w, off, dy, need_dw=False)
+    torch.cuda.synchronize()
+    for e, (a, b) in enumerate([(0, 100), (299_900, 299_990), (299_990, 300_000)]):
+        X, W, DY = host(x[a:b]), host(w[e]), host(dy[a:b])
+        _rows_match(y[a:b], X @ W.T, X, W, k, "bf16", f"y {e}")
+        _rows_match(dx[a:b], DY @ W, DY, W.T, n, "bf16", f"dx {e}")
+    assert not y[-1].any() and not dx[-1].any()
+
+
+def test_grouped_weights_and_their_gradient_past_4_gib():
+    E, n, k = 600, 1024, 2048
+    torch.manual_seed(2)
+    sizes = np.zeros(E, int)
+    sizes[[0, 300, 598, 599]] = 3, 70, 1, 6
+    M = int(sizes.sum())
+    x = torch.randn(M, k, device="cuda")
+    w = torch.randn(E, n, k, device="cuda")
+    dy = torch.randn(M, n, device="cuda")
+    off = torch.from_numpy(_offsets(sizes)).cuda()
+    say("grouped w of 5 GB")
+    y = mx.grouped_matmul(x, w, off)
+    dx, dw = mx.grouped_matmul_backward(x, w, off, dy)
+    torch.cuda.synchronize()
+    most = np.abs(host(x)).max() * np.abs(host(dy)).max()
+    for e, (a, b) in enumerate(ref.group_rows(off.cpu().numpy(), M)):
+        if a == b:
+            continue
+        X, W, DY = host(x[a:b]), host(w[e]), host(dy[a:b])
+        _rows_match(y[a:b], X @ W.T, X, W, k, "f32", f"y {e}")
+        _rows_match(dx[a:b], DY @ W, DY, W.T, n, "f32", f"dx {e}")
+        t = _sum_tol(np.abs(DY).T, np.abs(X).T, b - a, "f32") + (b - a) * 2.0 ** -37 * most
+        within(dw[e], DY.T @ X, t + U * np.abs(DY.T @ X), f"dw {e}")
+    assert not dw[1:300].any() and not dw[301:598].any()
+
+
+def test_layer_norm_past_4_gib():
+    T, d = 600_003, 4096
+    torch.manual_seed(3)
+    x = torch.randn(T, d, device="cuda", dtype=torch.bfloat16)
+    say("layer_norm of 4.9 GB")
+    y, mean, rstd = mx.layer_norm(x)
+    dx, _, _ = mx.layer_norm_backward(x, x, None, mean, rstd)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 4), slice(T - 4, T)):
+        small, m, s = mx.layer_norm(x[rows].clone())
+        again = mx.layer_norm_backward(x[rows].clone(), x[rows].clone(), None, m, s)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(_bits(y[rows]), _bits(small)) and torch.equal(mean[rows], m)
+        assert torch.equal(rstd[rows], s) and torch.equal(_bits(dx[rows]), _bits(again))
+
+
+# ---------------------------------------------------------------- captured graphs
+def test_graphs_that_share_a_workspace():
+    """Every operator that needs one, captured into graphs of its own over one workspace and
+    replayed in turn, with eager calls on the same workspace between."""
+    r = np.random.default_rng(31)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    gx, gw, off, gdy, _ = _grouped_inputs([100, 0, 33, 200], 0, 4, 192, 136, "f32", 4)
+    hx, hw, hoff, hdy, _ = _grouped_inputs([64, 7, 300], 1, 0, 200, 150, "bf16", 5)
+    x, w = dev(r.normal(size=(300, 256)), "bf16"), dev(r.normal(size=256), "bf16")
+    _, mean, rstd = mx.layer_norm(x, w)
+    small, large = dev(r.normal(size=(3, 96, 160))), dev(r.normal(size=(2, 700, 600)))
+    calls = [
+        lambda: (mx.grouped_matmul(gx, gw, off, workspace=ws),),
+        lambda: mx.grouped_matmul_backward(gx, gw, off, gdy, workspace=ws),
+        lambda: (mx.grouped_matmul(hx, hw, hoff, workspace=ws),),
+        lambda: mx.grouped_matmul_backward(hx, hw, hoff, hdy, workspace=ws),
+        lambda: mx.layer_norm_backward(x, x, w, mean, rstd, workspace=ws),
+        lambda: (mx.orthogonalize(small, workspace=ws),),
+        lambda: (mx.orthogonalize(large, workspace=ws),),
+    ]
+    want = [[t.clone() for t in c()] for c in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i, c in enumerate(calls):
+        say(f"capture {i}")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+    for k in range(3):
+        ws.fill_(255)                        # what other calls left there does not matter
+        for i in ((0, 1, 2, 3, 4, 5, 6), (6, 0, 5, 2, 4, 1, 3), (3, 3, 6, 6, 1, 0, 5))[k]:
+            say(f"replay {k} {i}")
+            for t in outs[i]:
+                t.zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            for a, b in zip(outs[i], want[i]):
+                assert torch.equal(_bits(a), _bits(b)), (k, i)
+            for a, b in zip(calls[i](), want[i]):
+                assert torch.equal(_bits(a), _bits(b)), (k, i)
