@@ -12,10 +12,11 @@
 //
 // X lives in the workspace, which this CU's L2 share holds; chunks land by direct-to-LDS
 // loads, two ahead, and X' of one chunk is multiplied while the next is formed.  One CU
-// then does 6 p^2 q multiply-adds on 32 x 32 tiles per wavefront, where LDS reads (p = 64)
-// or MFMAs and LDS reads alike (p = 128) bound a chunk: 1.2 us and 2.2 us at 2.5 GHz, of
-// which the MFMAs are 0.4 and 1.3.  16 float32 matrices of 128 x 256, five steps: 88 us
-// (110 us in 17 launches), of 64 x 64: 19 us (93 us).
+// then does 6 p^2 q multiply-adds with 32 x 32 tiles per wavefront: a chunk takes 1.2 us at
+// p = 64 and 2.1 us at p = 128 (2.5 GHz), of which the MFMAs are 0.4 and 1.3; the rest is
+// the chain from barrier to LDS read to MFMA to split to LDS write, which one or two
+// wavefronts per SIMD do not hide (MFMAs busy 32% on a CU in use, LDS 26%).  16 float32
+// matrices of 128 x 256, five steps: 75 us (110 us in 17 launches), of 64 x 64: 18 us (93 us).
 #include <math.h>
 
 #include <algorithm>
@@ -60,6 +61,14 @@ __device__ __forceinline__ f32x16 ns_mfma(u32x4 a, u32x4 b, f32x16 c) {
                                                 __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// Byte of 16-byte chunk c of row r of a unit: chunk positions are rotated by the row so that
+// reads along the rows (16 rows of one chunk) and transposing ones (32 bytes of four
+// rows, the second pair's 64 bytes away) meet each bank once.
+__device__ __forceinline__ uint32_t ns_place(int r, int c) {
+  const int turn = ((r >> 1) & 1) * 4 | ((r >> 2) & 1) * 2 | ((r >> 3) & 1);
+  return r * 128 + ((c ^ turn) << 4);
+}
+
 // A lane's addresses of fragments, from row 0 of a unit on: the rotation of a row's chunks
 // does not change over 16 rows, so everything else is a constant offset.
 struct NsLane {
@@ -73,8 +82,8 @@ struct NsLane {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        rows[i][j] = lds_chunk_offset(lane & 31, j * 4 + i * 2 + (lane >> 5));
-        cols[i][j] = lds_chunk_offset(r + 4 * j, i * 4 + (n >> 3)) + (n & 7) * 2;
+        rows[i][j] = ns_place(lane & 31, j * 4 + i * 2 + (lane >> 5));
+        cols[i][j] = ns_place(r + 4 * j, i * 4 + (n >> 3)) + (n & 7) * 2;
       }
     keep();
   }
@@ -108,9 +117,9 @@ __device__ __forceinline__ void ns_put4(uint8_t* m, int row, int j, const float 
   for (int e = 0; e < 4; ++e) split_f16(v[e], h[e], l[e]);
   uint8_t* u = m + (j >> 5) * NsSmall<PP>::UNIT + (j & 7) * 2;
   const int c = (j & 31) >> 3;
-  *(uint2*)(u + lds_chunk_offset(row, c)) =
+  *(uint2*)(u + ns_place(row, c)) =
       uint2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
-  *(uint2*)(u + lds_chunk_offset(row, 4 + c)) =
+  *(uint2*)(u + ns_place(row, 4 + c)) =
       uint2{l[0] | ((uint32_t)l[1] << 16), l[2] | ((uint32_t)l[3] << 16)};
 }
 
@@ -325,6 +334,42 @@ __device__ __forceinline__ void ns_chunk(const NsWave<PP>& w, NsLane at, const u
   if constexpr (ADD) ns_save<PP>(done, to, c - 1, w.wave, w.lane, w.off);
 }
 
+// The result's columns of chunk c: a lane holds columns j .. j + 3 of its row.  Whole runs of
+// four where a row is made of them (its start is aligned to them then), else element by
+// element; of a tall matrix neighbouring lanes hold neighbouring elements.
+__device__ __forceinline__ void ns_write(float* to, float v) { *to = v; }
+__device__ __forceinline__ void ns_write(uint16_t* to, float v) { *to = f32_to_bf16(v); }
+__device__ __forceinline__ void ns_write4(float* to, const float (&v)[4]) {
+  *(f32x4*)to = f32x4{v[0], v[1], v[2], v[3]};
+}
+__device__ __forceinline__ void ns_write4(uint16_t* to, const float (&v)[4]) {
+  *(uint2*)to = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+template <int PP, class O>
+__device__ __forceinline__ void ns_result(const NsSmallArgs& a, O* out, const NsWave<PP>& w, int c,
+                                          const f32x16& y) {
+  int lane = w.lane;
+  asm volatile("" : "+v"(lane));  // (addresses derived here, not kept)
+  const int r = w.row + (lane & 31), j0 = c * 64 + w.half * 32 + 4 * (lane >> 5);
+  if (r >= a.p) return;
+  const int row_step = a.tall ? 1 : a.q, col_step = a.tall ? a.p : 1;
+  const bool runs = !a.tall && a.q % 4 == 0, whole = c * 64 + 64 <= a.q;
+  O* to = out + (long long)blockIdx.x * a.out_stride + r * row_step + j0 * col_step;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = y[4 * q + e] * a.last_scale;
+    if (runs) {
+      if (whole || j0 + 8 * q < a.q) ns_write4(to + 8 * q, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (whole || j0 + 8 * q + e < a.q) ns_write(to + (8 * q + e) * col_step, v[e]);
+    }
+  }
+}
+
 template <class E, int PP>
 __global__ __launch_bounds__(NsSmall<PP>::THREADS) void ns_small_kernel(NsSmallArgs a) {
   using N = NsSmall<PP>;
@@ -395,7 +440,7 @@ __global__ __launch_bounds__(NsSmall<PP>::THREADS) void ns_small_kernel(NsSmallA
 #pragma unroll
   for (int i = 0; i < N::NI; ++i) {
     const int g = wave * N::NI + i, u = g / (PP / 8), r = g % (PP / 8) * 8 + (lane >> 3);
-    w.off[i] = (uint32_t)r * pitch + u * 128 + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    w.off[i] = (uint32_t)r * pitch + u * 128 + (ns_place(r, lane & 7) & 127);
   }
   const NsLane at(lane);
   f32x16 acc[N::TA];
@@ -497,22 +542,8 @@ __global__ __launch_bounds__(NsSmall<PP>::THREADS) void ns_small_kernel(NsSmallA
       slot = uni(slot == 2 ? 0 : slot + 1);
       if constexpr (apply.value) {
         if (last) {
-          int mine = lane;
-          asm volatile("" : "+v"(mine));
-          const int r = w.row + (mine & 31);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int j = c * 64 + w.half * 32 + 8 * q + 4 * (mine >> 5);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (r < a.p && j + e < a.q) {
-                const float v = y[4 * q + e] * a.last_scale;
-                const long long el = (long long)blockIdx.x * a.out_stride +
-                                     (a.tall ? (j + e) * a.p + r : r * a.q + j + e);
-                if (a.out_dtype == 0) ((float*)a.out)[el] = v;
-                else ((uint16_t*)a.out)[el] = f32_to_bf16(v);
-              }
-          }
+          if (a.out_dtype == 0) ns_result<PP>(a, (float*)a.out, w, c, y);
+          else ns_result<PP>(a, (uint16_t*)a.out, w, c, y);
         }
       }
     };
@@ -544,15 +575,17 @@ long long plane_bytes(int m, int n) {
 }  // namespace
 
 // Whether one block per matrix is faster than the general path, whose launches take 90 us
-// or more but spread a matrix over many blocks.  float32, five steps, general -> this one:
-// 64 x 512 98 -> 71 us, 64 x 1024 109 -> 130 us, 128 x 256 104 -> 88 us, 128 x 512
-// 109 -> 145 us; 64 matrices of 64 x 2048 346 -> 276 us, of 128 x 512 167 -> 165 us, of 128 x
-// 1024 234 -> 287 us; 256 of 128 x 4096 2423 -> 1690 us, of 64 x 64 163 -> 23 us.
+// or more but spread a matrix over many blocks.  Measured (float32, five steps), general -> this
+// one: one matrix of 64 x 512 98 -> 61 us, of 64 x 1024 109 -> 110 us, of 128 x 256 104 -> 74 us, of
+// 128 x 512 109 -> 120 us; 16 of 64 x 1024 117 -> 112 us, of 128 x 512 114 -> 122 us; 64 of
+// 64 x 4096 467 -> 459 us, of 128 x 1024 234 -> 237 us; 256 of 64 x 64 163 -> 22 us, of 128 x
+// 4096 2423 -> 1543 us.  That is a limit of chunks (of 128 rows: twice) that grows with the
+// CUs that the matrices occupy.
 bool ortho_small_fits(int B, int m, int n) {
   const int side = std::min(m, n);
   if (side > 128) return false;
   const int work = ((std::max(m, n) + 63) / 64) * (padded_side(side) / 64);
-  return B >= 128 || work <= 8 + B / 4;
+  return work <= 12 + (long long)B * B / 64;
 }
 
 size_t ortho_small_workspace_bytes(int B, int m, int n) { return (size_t)B * 2 * plane_bytes(m, n); }
