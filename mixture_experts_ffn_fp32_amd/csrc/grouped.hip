@@ -515,12 +515,13 @@ struct Carve {
 
 uint32_t pad_pitch(int n) { return (uint32_t)((n + 63) / 64 * 128); }
 
-// Tiles of a product in tiles of b x b, its rows taken as spread evenly.
+// About how many tiles of b x b a product has: the offsets are on the device, so half a
+// tile's rows are taken as lost per group, and every row as in a group.
 long long tiles_of(int dir, const GroupedArgs& a, long long b) {
   auto ct = [](long long x, long long y) { return (x + y - 1) / y; };
-  const long long per = std::max(1LL, ct(a.M, a.E)), groups = std::min(a.M, a.E);
+  const long long groups = std::min(a.M, a.E);
   if (dir == GR_DW) return ct(a.n, b) * ct(a.k, b) * groups;
-  return ct(per, b) * groups * ct(dir == GR_FWD ? a.n : a.k, b);
+  return std::max(groups, a.M / b + groups / 2) * ct(dir == GR_FWD ? a.n : a.k, b);
 }
 
 template <class C, int DIR>
@@ -539,10 +540,14 @@ template <int DIR, bool SPLIT>
 hipError_t pick_product(const GroupedArgs& a, const GroupedProduct& p, hipStream_t st) {
   constexpr bool AC = DIR == GR_DW, BC = DIR != GR_FWD, SW = DIR != GR_DW;
   const int cus = device_cu_count();
-  // the largest tiles that give every CU one
-  if (tiles_of(DIR, a, 256) >= cus && (DIR == GR_DW || a.M > 128LL * a.E))
+  // The largest tiles that give three quarters of the CUs one (tile_gemm.h; ragged groups
+  // fill fewer than half: 8190 rows in 16 uneven groups, y 896 x 1280 float32, 160 tiles of 256
+  // rows 137 us, of 128 rows 115 us), and 256 rows only where groups hold more than half of
+  // that (64 groups of 64 rows, y 1408 x 2048 bfloat16: 118 us, of 128 rows 107 us; 64 of
+  // 256: 138 and 147 us).
+  if (4 * tiles_of(DIR, a, 256) >= 3 * cus && (DIR == GR_DW || a.M > 128LL * a.E))
     return run_product<TgConfig<TgBig, AC, BC, SPLIT, SW>, DIR>(p, st);
-  if (tiles_of(DIR, a, 128) >= cus)
+  if (4 * tiles_of(DIR, a, 128) >= 3 * cus)
     return run_product<TgConfig<TgMid, AC, BC, SPLIT, SW>, DIR>(p, st);
   return run_product<TgConfig<TgSmall, AC, BC, SPLIT, SW>, DIR>(p, st);
 }

@@ -357,7 +357,7 @@ hipError_t run_ns(NsProduct p, hipStream_t st) {
   ns_kernel<C, KIND><<<(unsigned)std::min(total, blocks), C::THREADS, 0, st>>>(p);
   return hipGetLastError();
 }
-// The largest tiles that give every CU one.
+// The largest tiles that give more than half of the CUs one (tile_gemm.h).
 template <int KIND, bool AC, bool BC, bool SW>
 hipError_t pick_ns(const NsProduct& p, hipStream_t st) {
   auto tiles = [&](long long b) {
@@ -365,8 +365,8 @@ hipError_t pick_ns(const NsProduct& p, hipStream_t st) {
     return (KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2) * p.count;
   };
   const int cus = device_cu_count();
-  if (tiles(256) >= cus) return run_ns<TgConfig<TgBig, AC, BC, true, SW>, KIND>(p, st);
-  if (tiles(128) >= cus) return run_ns<TgConfig<TgMid, AC, BC, true, SW>, KIND>(p, st);
+  if (2 * tiles(256) > cus) return run_ns<TgConfig<TgBig, AC, BC, true, SW>, KIND>(p, st);
+  if (2 * tiles(128) > cus) return run_ns<TgConfig<TgMid, AC, BC, true, SW>, KIND>(p, st);
   return run_ns<TgConfig<TgSmall, AC, BC, true, SW>, KIND>(p, st);
 }
 

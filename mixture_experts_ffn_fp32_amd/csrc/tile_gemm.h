@@ -58,10 +58,18 @@ struct TgSmall {
   static constexpr int NI = BM / 8;                   // loads per operand per k-step
 };
 // 256 x 256, eight wavefronts of 64 x 128, one block per CU: 0.75 LDS reads per MFMA.
-// Below a tile per CU it leaves CUs idle; 128 x 128 (four wavefronts of 64 x 64, 1 read
-// per MFMA, two blocks per CU that fill each other's barriers and epilogues) is next,
-// its fragments a whole k-step ahead (one group of four MFMAs does not cover an LDS
-// read), then TgSmall.
+// 128 x 128, four wavefronts of 64 x 64, 1 read per MFMA, two blocks per CU that fill each
+// other's barriers and epilogues; its fragments are read a whole k-step ahead (one group
+// of four MFMAs does not cover an LDS read).  Then TgSmall.
+//
+// The larger tile is taken as soon as it gives more than half of the CUs one: a CU's time
+// is then one such tile, and the next smaller size needs as many rounds at a lower rate
+// (four tiles for one, over two blocks or the same CUs).  Measured, larger | smaller:
+//   256 | 128  update of 8 matrices of 1408 x 2048, symmetric products of 168 tiles on 256
+//              CUs, 2357 | 2637 us; of one of 4096 x 4096, 136 tiles, 3974 | 4325 us; grouped
+//              y (bfloat16), 192 tiles, 51 | 58 us; 128 tiles, 36 | 29 us
+//   128 | 64   update of 64 matrices of 256 x 512, 192 tiles, 362 | 384 us; of one of 2048 x
+//              2048, 136 tiles, 861 | 858 us; grouped y (float32), 128 tiles, 50 | 40 us
 using TgBig = TgShape<4, 2, 2, 4, 2, 1, false>;
 using TgMid = TgShape<2, 2, 2, 2, 2, 2, true>;
 
