@@ -503,6 +503,225 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
 // ---------------------------------------------------------------- launch
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// ---------------------------------------------------------------- float32, few rows per group
+// With few rows the product is bound by reading w once (64 groups of 6 rows, w 2048 x 1408:
+// 738 MB), and writing w's split form and reading it back would treble that.  Here w's
+// rows go from memory to registers and are split there, into three bfloat16:
+//   v = hi + mid + lo exactly (3 x 8 bits, each the rounded rest of the one before), and
+//   hi hi' + hi mid' + mid hi' + mid mid' + hi lo' + lo hi' leaves out at most
+//   2 mid lo' <= 2^-23 |v v'|,
+// which, having float32's exponents, need no scale of w's rows (whose maximum would take a
+// read of its own).  x is split likewise beforehand (it is small), its rows' largest
+// value scaled to 2^-12, so that sums of products with the largest w stay finite.
+//
+// A block takes 64 columns of y and up to 32 rows of a group; its four wavefronts deal the
+// k-steps of 32 indices among themselves, each with four fragments of 16 w rows against one
+// or two of x rows, loads two k-steps ahead and no barrier; the four sums are added through
+// LDS in wavefront order.  Loads of fragments touch many rows, and what they cost is lines:
+// a lane of quarter g takes the indices 4 g .. 4 g + 3 and 16 + 4 g .. of a k-step (any order
+// does that x and w share), so a load takes 64 bytes of 16 rows, and x lies in that order
+// (fragments of 32 rows, 32 bytes of each per load, and x by rows: 209 us for the 174 below).
+constexpr int kFewRows = 32, kFewCols = 64;
+struct FewProduct {
+  const float* w;
+  const u32x4* x;          // [k-step][quarter][hi, mid, lo][M]: a lane's eight values of a row
+  const int32_t* ex;       // x's exponents
+  const int32_t* offsets;
+  float* out;
+  GroupDims g;
+  int zero_rest;
+};
+// Bytes of x's split row.
+__host__ __device__ inline long long few_pitch(int k) { return (long long)((k + 31) / 32) * 192; }
+
+struct Split3 {
+  u32x4 hi, mid, lo;
+};
+__device__ __forceinline__ Split3 split_three(const float (&v)[8]) {
+  Split3 s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
+    s.hi[i] = pack_bf16x2(a, b);
+    a -= __uint_as_float(s.hi[i] << 16);
+    b -= __uint_as_float(s.hi[i] & 0xffff0000u);
+    s.mid[i] = pack_bf16x2(a, b);
+    a -= __uint_as_float(s.mid[i] << 16);
+    b -= __uint_as_float(s.mid[i] & 0xffff0000u);
+    s.lo[i] = pack_bf16x2(a, b);
+  }
+  return s;
+}
+// x's rows (of a multiple of 4 values), one wavefront each.
+__global__ __launch_bounds__(256) void split_three_kernel(const float* __restrict__ x, int rows, int k,
+                                                          u32x4* __restrict__ out,
+                                                          int32_t* __restrict__ ex) {
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (r >= rows) return;
+  const float* src = x + r * k;
+  float m = 0.f, f[8];
+  for (int j = 8 * lane; j < k; j += 512) {
+    load_chunk<ElemF32>(src, j, k, f);
+    m = fmaxf(m, chunk_max(f));
+  }
+  m = wave_max(m);
+  const int e = m > 0.f ? -12 - ilogbf(m) : 0;
+  if (lane == 0) ex[r] = e;
+  for (int c = lane; c < (k + 31) / 32 * 4; c += 64) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = c / 4 * 32 + h * 16 + c % 4 * 4;
+      const f32x4 v = j < k ? *(const f32x4*)(src + j) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[4 * h + i] = ldexpf(v[i], e);
+    }
+    const Split3 s = split_three(f);
+    u32x4* to = out + (long long)c * 3 * rows + r;
+    to[0] = s.hi;
+    to[rows] = s.mid;
+    to[2LL * rows] = s.lo;
+  }
+}
+
+__device__ __forceinline__ f32x4 few_mfma(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// A wavefront's operands of a k-step.
+template <int RF>
+struct FewLoad {
+  f32x4 w[4][2];
+  Split3 x[RF];
+};
+// The sums of this wavefront's k-steps for 64 columns and 16 RF rows.
+template <int RF>
+__device__ __forceinline__ void few_tile(const FewProduct& p, int e, int row0, int rows, int n0,
+                                         int wave, int lane, f32x4 (&acc)[4][RF]) {
+  const int k = p.g.k, steps = (k + 31) / 32, g = lane >> 4, i16 = lane & 15;
+  // rows past the last one (of w, of the group) reread it and are never stored
+  const float* w[4];
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+    w[f] = p.w + ((size_t)e * p.g.n + min(n0 + 16 * f + i16, p.g.n - 1)) * k;
+  const u32x4* x[RF];
+#pragma unroll
+  for (int f = 0; f < RF; ++f) x[f] = p.x + row0 + min(16 * f + i16, rows - 1);
+  auto load = [&](int s, FewLoad<RF>& d) {
+    s = min(s, steps - 1);
+#pragma unroll
+    for (int f = 0; f < RF; ++f) {
+      const u32x4* from = x[f] + (size_t)(s * 4 + g) * 3 * p.g.M;
+      d.x[f] = Split3{from[0], from[p.g.M], from[2LL * p.g.M]};
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // (k is a multiple of 4: four values are inside the row or past it)
+        const int j = 32 * s + 16 * h + 4 * g;
+        d.w[f][h] = *(const f32x4*)(w[f] + (j < k ? j : 0));
+      }
+  };
+  auto multiply = [&](int s, const FewLoad<RF>& d) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      float v[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * h + i] = 32 * s + 16 * h + 4 * g < k ? d.w[f][h][i] : 0.f;
+      const Split3 t = split_three(v);
+#pragma unroll
+      for (int r = 0; r < RF; ++r) {
+        acc[f][r] = few_mfma(t.lo, d.x[r].hi, acc[f][r]);
+        acc[f][r] = few_mfma(t.hi, d.x[r].lo, acc[f][r]);
+        acc[f][r] = few_mfma(t.mid, d.x[r].mid, acc[f][r]);
+        acc[f][r] = few_mfma(t.mid, d.x[r].hi, acc[f][r]);
+        acc[f][r] = few_mfma(t.hi, d.x[r].mid, acc[f][r]);
+        acc[f][r] = few_mfma(t.hi, d.x[r].hi, acc[f][r]);
+      }
+    }
+  };
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int r = 0; r < RF; ++r) acc[f][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  FewLoad<RF> a, b;
+  load(2 * wave, a);
+  load(2 * wave + 1, b);
+  for (int s = 2 * wave; s < steps; s += 8) {
+    multiply(s, a);
+    load(s + 8, a);
+    if (s + 1 < steps) multiply(s + 1, b);
+    load(s + 9, b);
+  }
+}
+// Sums and stores a tile: wavefront f fragment f, a lane four columns of one row.
+template <int RF>
+__device__ __forceinline__ void few_store(const FewProduct& p, int row0, int rows, int n0, int wave,
+                                          int lane, const f32x4 (&acc)[4][RF],
+                                          f32x4 (*__restrict__ sum)[4][2][64]) {
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int r = 0; r < RF; ++r) sum[wave][f][r][lane] = acc[f][r];
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < RF; ++r) {
+    const int i = 16 * r + (lane & 15), n = n0 + 16 * wave + 4 * (lane >> 4);
+    if (i >= rows || n >= p.g.n) continue;
+    f32x4 v = sum[0][wave][r][lane];
+#pragma unroll
+    for (int o = 1; o < 4; ++o) v += sum[o][wave][r][lane];
+    const int ex = p.ex[row0 + i];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = ldexpf(v[c], -ex);
+    float* y = p.out + (size_t)(row0 + i) * p.g.n + n;
+    if (p.g.n % 4 == 0) {
+      *(f32x4*)y = v;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (n + c < p.g.n) y[c] = v[c];
+    }
+  }
+  __syncthreads();
+}
+__global__ __launch_bounds__(256, 2) void grouped_few_kernel(FewProduct p) {
+  __shared__ GroupTables t;
+  __shared__ f32x4 sum[4][4][2][64];
+  group_tables<GR_FWD>(p.g, p.offsets, kFewRows, t);
+  if (p.zero_rest) zero_rows(p.out, p.g.M, p.g.n, t.off[0], t.off[p.g.E]);
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+  const int nt = (p.g.n + kFewCols - 1) / kFewCols, total = uni(t.tiles[p.g.E]) * nt;
+  int e = 0;
+  for (int L = blockIdx.x; L < total; L += gridDim.x) {
+    e = uni(group_of(t.tiles, p.g.E, L / nt, e));
+    const int first = uni(t.tiles[e]), mt = uni(t.tiles[e + 1]) - first, local = L - first * nt;
+    const int row0 = uni(t.off[e]) + local % mt * kFewRows, n0 = local / mt * kFewCols;
+    const int rows = uni(t.off[e + 1]) - row0;
+    if (rows > 16) {
+      f32x4 acc[4][2];
+      few_tile<2>(p, e, row0, rows, n0, wave, lane, acc);
+      few_store<2>(p, row0, rows, n0, wave, lane, acc, sum);
+    } else {
+      f32x4 acc[4][1];
+      few_tile<1>(p, e, row0, rows, n0, wave, lane, acc);
+      few_store<1>(p, row0, rows, n0, wave, lane, acc, sum);
+    }
+  }
+}
+
+// Up to 64 rows per group on average; w 2048 x 1408 and 64 groups, general path -> this one: 6 rows
+// 432 -> 174 us (4.3 TB/s), 1 row 161 us (4.6 TB/s); 1408 x 2048, 32 rows 470 -> 221 us, 64 rows
+// 499 -> 368 us; of 96 rows it would read w three times (513 us there).  From 32 columns on: below,
+// its workspace would not shrink with the rows, and most of its 64 columns would be empty.
+bool few_rows(int dtype, int M, int E, int n, int k) {
+  return dtype == 0 && k % 4 == 0 && n >= 32 && M <= 64LL * E;
+}
+
 struct Carve {
   uint8_t* base;
   size_t at = 0;
@@ -565,7 +784,10 @@ struct GroupedPlan {
 GroupedPlan plan_forward(int dtype, int M, int E, int n, int k, void* ws) {
   GroupedPlan p;
   Carve c{(uint8_t*)ws};
-  if (dtype == 0) {
+  if (few_rows(dtype, M, E, n, k)) {
+    p.x = c.take((size_t)M * few_pitch(k));
+    p.ex = (int32_t*)c.take((size_t)M * 4);
+  } else if (dtype == 0) {
     p.x = c.take((size_t)M * split_pitch(k));
     p.w = c.take((size_t)E * n * split_pitch(k));
     p.ex = (int32_t*)c.take((size_t)M * 4);
@@ -631,6 +853,14 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
   p.g = GroupDims{a.M, a.E, a.n, a.k};
   p.zero_rest = a.zero_rest;
   const long long wr = (long long)a.E * a.n;
+  if (few_rows(dtype, a.M, a.E, a.n, a.k)) {
+    const FewProduct f{(const float*)a.w, (u32x4*)w.x, w.ex, a.offsets, (float*)a.y, p.g, a.zero_rest};
+    split_three_kernel<<<row_blocks(a.M), 256, 0, st>>>((const float*)a.x, a.M, a.k, (u32x4*)w.x, w.ex);
+    const long long most = ((long long)a.M / kFewRows + std::min(a.M, a.E)) * ((a.n + kFewCols - 1) / kFewCols);
+    const long long room = 2LL * device_cu_count();
+    grouped_few_kernel<<<(unsigned)std::min(most, room), 256, 0, st>>>(f);
+    return hipGetLastError();
+  }
   if (dtype == 0) {
     p.pitch_a = p.pitch_b = (uint32_t)split_pitch(a.k);
     const SplitRows rx{(const float*)a.x, w.x, w.ex, a.M, p.pitch_a, a.k, 0};

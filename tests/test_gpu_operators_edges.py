@@ -235,3 +235,40 @@ def test_graphs_that_share_a_workspace():
                 assert torch.equal(_bits(a), _bits(b)), (k, i)
             for a, b in zip(calls[i](), want[i]):
                 assert torch.equal(_bits(a), _bits(b)), (k, i)
+
+
+# ---------------------------------------------------------------- float32 products of few rows
+FEW = [([1], 0, 0, 32, 4), ([2, 0, 1], 1, 2, 33, 8), ([33, 0, 0, 1, 64, 65, 0, 3], 0, 4, 70, 36),
+       ([150] + [0] * 7, 0, 0, 129, 100), ([1] * 64, 0, 0, 64, 1000), ([31, 32, 33, 64, 96], 3, 0, 260, 516),
+       ([64] * 3, 0, 0, 96, 2052), ([64] * 3 + [1], 0, 1, 31, 2052), ([5, 9], 0, 0, 200, 30),
+       ([0, 0, 7, 0], 2, 1, 1408, 2048), ([3] * 200 + [0] * 300, 5, 5, 40, 68)]
+
+
+@pytest.mark.parametrize("case", range(len(FEW)))
+def test_grouped_f32_few_rows(case):
+    from test_gpu_operators import _grouped_check
+    _grouped_check(*FEW[case], "f32", seed=100 + case)
+
+
+def test_grouped_f32_few_rows_at_the_ends_of_the_range():
+    """Weights and rows near float32's largest and smallest values: no product leaves the
+    range on the way to a result inside it."""
+    r = np.random.default_rng(41)
+    M, E, n, k = 12, 3, 64, 128
+    x, w = r.normal(size=(M, k)), r.normal(size=(E, n, k))
+    x[0] *= 1e-36
+    w[0, 0] = 3e38 * np.sign(w[0, 0])          # sums of 128 such products with a small row
+    w[1] *= 1e-28
+    x[5] *= 1e30
+    w[2, 3] = 0.0
+    x[11] = 0.0
+    x, w = dev(x), dev(w)
+    off = torch.tensor([0, 1, 8, 12], dtype=torch.int32, device="cuda")
+    say("grouped f32 few rows, ends of the range")
+    y = mx.grouped_matmul(x, w, off)
+    torch.cuda.synchronize()
+    ry, _ = ref.grouped_matmul(host(x), host(w), off.cpu().numpy())
+    for e, (a, b) in enumerate([(0, 1), (1, 8), (8, 12)]):
+        ax, aw = np.abs(host(x)[a:b]), np.abs(host(w)[e])
+        t = (2 * (k + 8) + 3) * U * (ax @ aw.T)
+        within(y[a:b], ry[a:b], t + U * np.abs(ry[a:b]), f"group {e}")
