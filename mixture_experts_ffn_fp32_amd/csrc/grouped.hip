@@ -521,10 +521,15 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // a lane of quarter g takes the indices 4 g .. 4 g + 3 and 16 + 4 g .. of a k-step (any order
 // does that x and w share), so a load takes 64 bytes of 16 rows, and x lies in that order
 // (fragments of 32 rows, 32 bytes of each per load, and x by rows: 209 us for the 174 below).
+//
+// dx = w^T dy likewise, contracting over w's rows: a lane of quarter g and index i loads 4
+// consecutive values of the rows 4 g .. 4 g + 3 and 16 + 4 g .. of a k-step, from column 4 i of
+// the tile on, a load 256 bytes of four rows; fragment c takes the c-th of each four (its row i
+// is column 4 i + c of the tile), so that a lane ends with runs of four columns.
 constexpr int kFewRows = 32, kFewCols = 64;
 struct FewProduct {
   const float* w;
-  const u32x4* x;          // [k-step][quarter][hi, mid, lo][M]: a lane's eight values of a row
+  const u32x4* x;          // (dx: dy) [k-step][quarter][hi, mid, lo][M]: a lane's eight values of a row
   const int32_t* ex;       // x's exponents
   const int32_t* offsets;
   float* out;
@@ -596,18 +601,24 @@ struct FewLoad {
   Split3 x[RF];
 };
 // The sums of this wavefront's k-steps for 64 columns and 16 RF rows.
-template <int RF>
+template <bool DX, int RF>
 __device__ __forceinline__ void few_tile(const FewProduct& p, int e, int row0, int rows, int n0,
                                          int wave, int lane, f32x4 (&acc)[4][RF]) {
-  const int k = p.g.k, steps = (k + 31) / 32, g = lane >> 4, i16 = lane & 15;
+  const int n = p.g.n, k = p.g.k, length = DX ? n : k;
+  const int steps = (length + 31) / 32, g = lane >> 4, i16 = lane & 15;
   // rows past the last one (of w, of the group) reread it and are never stored
-  const float* w[4];
+  const float* w[DX ? 1 : 4];
+  if constexpr (DX) {
+    w[0] = p.w + (size_t)e * n * k + (n0 + 4 * i16 < k ? n0 + 4 * i16 : 0);
+  } else {
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
-    w[f] = p.w + ((size_t)e * p.g.n + min(n0 + 16 * f + i16, p.g.n - 1)) * k;
+    for (int f = 0; f < 4; ++f) w[f] = p.w + ((size_t)e * n + min(n0 + 16 * f + i16, n - 1)) * k;
+  }
   const u32x4* x[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f) x[f] = p.x + row0 + min(16 * f + i16, rows - 1);
+  // index j of a lane's eight in a k-step (four of them are inside the contraction or past it)
+  auto index = [&](int s, int j) { return 32 * s + 16 * (j >> 2) + 4 * g + (j & 3); };
   auto load = [&](int s, FewLoad<RF>& d) {
     s = min(s, steps - 1);
 #pragma unroll
@@ -619,9 +630,12 @@ __device__ __forceinline__ void few_tile(const FewProduct& p, int e, int row0, i
     for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // (k is a multiple of 4: four values are inside the row or past it)
-        const int j = 32 * s + 16 * h + 4 * g;
-        d.w[f][h] = *(const f32x4*)(w[f] + (j < k ? j : 0));
+        if constexpr (DX) {
+          d.w[f][h] = *(const f32x4*)(w[0] + (size_t)min(index(s, 4 * h + f), n - 1) * k);
+        } else {
+          const int j = index(s, 4 * h);
+          d.w[f][h] = *(const f32x4*)(w[f] + (j < k ? j : 0));
+        }
       }
   };
   auto multiply = [&](int s, const FewLoad<RF>& d) {
@@ -631,7 +645,8 @@ __device__ __forceinline__ void few_tile(const FewProduct& p, int e, int row0, i
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * h + i] = 32 * s + 16 * h + 4 * g < k ? d.w[f][h][i] : 0.f;
+        for (int i = 0; i < 4; ++i)
+          v[4 * h + i] = index(s, 4 * h) < length ? (DX ? d.w[i][h][f] : d.w[f][h][i]) : 0.f;
       const Split3 t = split_three(v);
 #pragma unroll
       for (int r = 0; r < RF; ++r) {
@@ -658,11 +673,13 @@ __device__ __forceinline__ void few_tile(const FewProduct& p, int e, int row0, i
     load(s + 9, b);
   }
 }
-// Sums and stores a tile: wavefront f fragment f, a lane four columns of one row.
-template <int RF>
+// Sums and stores a tile, a lane four columns of one row: wavefront q fragment q's (dx: the
+// q-th values of the four fragments, which are neighbours).
+template <bool DX, int RF>
 __device__ __forceinline__ void few_store(const FewProduct& p, int row0, int rows, int n0, int wave,
                                           int lane, const f32x4 (&acc)[4][RF],
                                           f32x4 (*__restrict__ sum)[4][2][64]) {
+  const int width = DX ? p.g.k : p.g.n;
 #pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
@@ -670,32 +687,42 @@ __device__ __forceinline__ void few_store(const FewProduct& p, int row0, int row
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < RF; ++r) {
-    const int i = 16 * r + (lane & 15), n = n0 + 16 * wave + 4 * (lane >> 4);
-    if (i >= rows || n >= p.g.n) continue;
-    f32x4 v = sum[0][wave][r][lane];
+    const int i = 16 * r + (lane & 15);
+    const int n = n0 + (DX ? 16 * (lane >> 4) + 4 * wave : 16 * wave + 4 * (lane >> 4));
+    if (i >= rows || n >= width) continue;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int o = 1; o < 4; ++o) v += sum[o][wave][r][lane];
+    for (int o = 0; o < 4; ++o) {
+      if constexpr (DX) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] += ((const float*)&sum[o][c][r][lane])[wave];
+      } else {
+        v += sum[o][wave][r][lane];
+      }
+    }
     const int ex = p.ex[row0 + i];
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = ldexpf(v[c], -ex);
-    float* y = p.out + (size_t)(row0 + i) * p.g.n + n;
-    if (p.g.n % 4 == 0) {
+    float* y = p.out + (size_t)(row0 + i) * width + n;
+    if (DX || width % 4 == 0) {
       *(f32x4*)y = v;
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (n + c < p.g.n) y[c] = v[c];
+        if (n + c < width) y[c] = v[c];
     }
   }
   __syncthreads();
 }
+template <bool DX>
 __global__ __launch_bounds__(256, 2) void grouped_few_kernel(FewProduct p) {
   __shared__ GroupTables t;
   __shared__ f32x4 sum[4][4][2][64];
+  const int width = DX ? p.g.k : p.g.n;
   group_tables<GR_FWD>(p.g, p.offsets, kFewRows, t);
-  if (p.zero_rest) zero_rows(p.out, p.g.M, p.g.n, t.off[0], t.off[p.g.E]);
+  if (p.zero_rest) zero_rows(p.out, p.g.M, width, t.off[0], t.off[p.g.E]);
   const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
-  const int nt = (p.g.n + kFewCols - 1) / kFewCols, total = uni(t.tiles[p.g.E]) * nt;
+  const int nt = (width + kFewCols - 1) / kFewCols, total = uni(t.tiles[p.g.E]) * nt;
   int e = 0;
   for (int L = blockIdx.x; L < total; L += gridDim.x) {
     e = uni(group_of(t.tiles, p.g.E, L / nt, e));
@@ -704,22 +731,40 @@ __global__ __launch_bounds__(256, 2) void grouped_few_kernel(FewProduct p) {
     const int rows = uni(t.off[e + 1]) - row0;
     if (rows > 16) {
       f32x4 acc[4][2];
-      few_tile<2>(p, e, row0, rows, n0, wave, lane, acc);
-      few_store<2>(p, row0, rows, n0, wave, lane, acc, sum);
+      few_tile<DX, 2>(p, e, row0, rows, n0, wave, lane, acc);
+      few_store<DX, 2>(p, row0, rows, n0, wave, lane, acc, sum);
     } else {
       f32x4 acc[4][1];
-      few_tile<1>(p, e, row0, rows, n0, wave, lane, acc);
-      few_store<1>(p, row0, rows, n0, wave, lane, acc, sum);
+      few_tile<DX, 1>(p, e, row0, rows, n0, wave, lane, acc);
+      few_store<DX, 1>(p, row0, rows, n0, wave, lane, acc, sum);
     }
   }
+}
+// `in`: x or dy, split into `planes` and `ex` first.
+template <bool DX>
+hipError_t run_few(const GroupedArgs& a, const void* in, uint8_t* planes, int32_t* ex, void* out,
+                   hipStream_t st) {
+  const int width = DX ? a.k : a.n, length = DX ? a.n : a.k;
+  const FewProduct p{(const float*)a.w, (const u32x4*)planes, ex, a.offsets, (float*)out,
+                     GroupDims{a.M, a.E, a.n, a.k}, a.zero_rest};
+  split_three_kernel<<<blocks_of(a.M), 256, 0, st>>>((const float*)in, a.M, length, (u32x4*)planes, ex);
+  const long long most =
+      ((long long)a.M / kFewRows + std::min(a.M, a.E)) * ((width + kFewCols - 1) / kFewCols);
+  const long long room = 2LL * device_cu_count();
+  grouped_few_kernel<DX><<<(unsigned)std::min(most, room), 256, 0, st>>>(p);
+  return hipGetLastError();
 }
 
 // Up to 64 rows per group on average; w 2048 x 1408 and 64 groups, general path -> this one: 6 rows
 // 432 -> 174 us (4.3 TB/s), 1 row 161 us (4.6 TB/s); 1408 x 2048, 32 rows 470 -> 221 us, 64 rows
-// 499 -> 368 us; of 96 rows it would read w three times (513 us there).  From 32 columns on: below,
-// its workspace would not shrink with the rows, and most of its 64 columns would be empty.
+// 499 -> 368 us; of 96 rows it would read w three times (513 | 532 us).  dx, 6 rows 580 -> 162 us, 32 rows
+// 559 -> 199 us, 64 rows 576 -> 310 us, 96 rows 595 us either way.  The widths keep the
+// workspace of fewer rows the smaller one, and the tile's 64 columns in use.
 bool few_rows(int dtype, int M, int E, int n, int k) {
   return dtype == 0 && k % 4 == 0 && n >= 32 && M <= 64LL * E;
+}
+bool few_rows_dx(int dtype, int M, int E, int n, int k) {
+  return few_rows(dtype, M, E, n, k) && n % 4 == 0 && k >= 192;
 }
 
 struct Carve {
@@ -776,6 +821,8 @@ unsigned row_blocks(long long rows) { return blocks_of(rows); }
 // The workspace's regions: which are needed, and where they lie.
 struct GroupedPlan {
   uint8_t *x = nullptr, *w = nullptr, *dy = nullptr;        // prepared operands
+  uint8_t* few = nullptr;                                   // dy, few rows per group
+  int32_t* efew = nullptr;
   int32_t *ex = nullptr, *ew = nullptr, *ey = nullptr;      // exponents
   int32_t* parts = nullptr;
   float* wmax = nullptr;
@@ -802,7 +849,13 @@ GroupedPlan plan_forward(int dtype, int M, int E, int n, int k, void* ws) {
 GroupedPlan plan_backward(int dtype, int M, int E, int n, int k, bool dx, bool dw, void* ws) {
   GroupedPlan p;
   Carve c{(uint8_t*)ws};
-  if (dtype == 0) {
+  if (M == 0) dx = false;
+  if (dx && few_rows_dx(dtype, M, E, n, k)) {
+    p.few = c.take((size_t)M * few_pitch(n));
+    p.efew = (int32_t*)c.take((size_t)M * 4);
+    dx = false;
+  }
+  if (dtype == 0 && (dx || dw)) {
     p.dy = c.take((size_t)M * split_pitch(n));
     p.ey = (int32_t*)c.take((size_t)M * 4);
     if (dx) {
@@ -815,7 +868,7 @@ GroupedPlan plan_backward(int dtype, int M, int E, int n, int k, bool dx, bool d
       p.ex = (int32_t*)c.take(4);
       p.parts = (int32_t*)c.take(kRowParts * 4);
     }
-  } else {
+  } else if (dtype != 0) {
     if (n % (dx ? 64 : 8) != 0) p.dy = c.take((size_t)M * pad_pitch(n));
     if (dx && k % 8 != 0) p.w = c.take((size_t)E * n * pad_pitch(k));
     if (dw && k % 8 != 0) p.x = c.take((size_t)M * pad_pitch(k));
@@ -854,12 +907,7 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
   p.zero_rest = a.zero_rest;
   const long long wr = (long long)a.E * a.n;
   if (few_rows(dtype, a.M, a.E, a.n, a.k)) {
-    const FewProduct f{(const float*)a.w, (u32x4*)w.x, w.ex, a.offsets, (float*)a.y, p.g, a.zero_rest};
-    split_three_kernel<<<row_blocks(a.M), 256, 0, st>>>((const float*)a.x, a.M, a.k, (u32x4*)w.x, w.ex);
-    const long long most = ((long long)a.M / kFewRows + std::min(a.M, a.E)) * ((a.n + kFewCols - 1) / kFewCols);
-    const long long room = 2LL * device_cu_count();
-    grouped_few_kernel<<<(unsigned)std::min(most, room), 256, 0, st>>>(f);
-    return hipGetLastError();
+    return run_few<false>(a, a.x, w.x, w.ex, a.y, st);
   }
   if (dtype == 0) {
     p.pitch_a = p.pitch_b = (uint32_t)split_pitch(a.k);
@@ -883,8 +931,14 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
 }
 
 hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hipStream_t st) {
-  const bool dx = a.dx != nullptr, dw = a.dw != nullptr;
+  bool dx = a.dx != nullptr;
+  const bool dw = a.dw != nullptr;
   const GroupedPlan w = plan_backward(dtype, a.M, a.E, a.n, a.k, dx, dw, ws);
+  if (w.few != nullptr) {
+    const hipError_t e = run_few<true>(a, a.dy, w.few, w.efew, a.dx, st);
+    if (e != hipSuccess || !dw) return e;
+    dx = false;
+  }
   const long long wr = (long long)a.E * a.n;
   GroupedProduct p{};
   p.offsets = a.offsets;

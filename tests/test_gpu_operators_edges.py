@@ -272,3 +272,35 @@ def test_grouped_f32_few_rows_at_the_ends_of_the_range():
         ax, aw = np.abs(host(x)[a:b]), np.abs(host(w)[e])
         t = (2 * (k + 8) + 3) * U * (ax @ aw.T)
         within(y[a:b], ry[a:b], t + U * np.abs(ry[a:b]), f"group {e}")
+
+
+# (rows of one group past a tile, widths past a k-step and a tile, both gradients and dx alone)
+FEW_DX = [([1], 0, 0, 32, 192), ([2, 0, 1], 1, 2, 36, 196), ([33, 0, 0, 1, 64, 65, 0, 3], 0, 4, 100, 260),
+          ([150] + [0] * 7, 0, 0, 132, 708), ([3] * 200 + [0] * 300, 5, 5, 40, 192), ([64] * 3, 0, 0, 96, 2052),
+          ([64] * 3 + [1], 0, 1, 96, 2052), ([0, 0, 7, 0], 2, 1, 1408, 2048)]
+
+
+@pytest.mark.parametrize("case", range(len(FEW_DX)))
+def test_grouped_f32_few_rows_gradients(case):
+    from test_gpu_operators import _grouped_check
+    sizes, before, behind, n, k = FEW_DX[case]
+    _grouped_check(sizes, before, behind, n, k, "f32", seed=200 + case)
+    x, w, off, dy, _ = _grouped_inputs(sizes, before, behind, n, k, "f32", 200 + case)
+    both = mx.grouped_matmul_backward(x, w, off, dy)
+    dx, _ = mx.grouped_matmul_backward(x, w, off, dy, need_dw=False)
+    _, dw = mx.grouped_matmul_backward(x, w, off, dy, need_dx=False)
+    torch.cuda.synchronize()
+    assert torch.equal(_bits(dx), _bits(both[0])) and torch.equal(_bits(dw), _bits(both[1]))
+
+
+def test_grouped_f32_few_rows_gradient_keeps_bad_weights_to_their_columns():
+    x, w, off, dy, _ = _grouped_inputs([9, 40], 0, 0, 44, 200, "f32", 51)
+    clean = mx.grouped_matmul_backward(x, w, off, dy, need_dw=False)[0]
+    w[0, 43, 7] = float("inf")               # the last row, which padding must not reach
+    w[1, 0, 199] = float("nan")
+    dx = mx.grouped_matmul_backward(x, w, off, dy, need_dw=False)[0]
+    torch.cuda.synchronize()
+    bad = torch.zeros_like(dx, dtype=torch.bool)
+    bad[:9, 7] = True
+    bad[9:, 199] = True
+    assert (~torch.isfinite(dx) == bad).all() and torch.equal(dx[~bad], clean[~bad])
