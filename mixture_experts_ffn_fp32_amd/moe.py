@@ -373,9 +373,14 @@ def _typed(name: str, t, dtype, shape):
         raise MoEError(1, f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+INT_MAX = 2 ** 31 - 1
+
+
 def _dims(name: str, t, n: int):
     if t.dim() != n:
         raise MoEError(1, f"{name} must have {n} dimensions, got {t.dim()}")
+    if max(t.shape) > INT_MAX:             # the ABI's sizes are int
+        raise MoEError(2, f"{name}: sizes past 2^31 - 1 are not supported, got {tuple(t.shape)}")
     return t.shape
 
 
@@ -495,14 +500,16 @@ def grouped_matmul_backward(x, w, offsets, dy, need_dx: bool = True, need_dw: bo
 def _matrices(name: str, t):
     """(batch, m, n, elements from one matrix to the next) of t [..][m][n]: contiguous, or
     [B][m][n] with contiguous matrices at a larger stride (the blocks of a weight gradient)."""
-    if not t.is_cuda:
-        raise MoEError(1, "tensors must be on a GPU device")
     if t.dim() < 2:
         raise MoEError(1, f"{name} must have at least 2 dimensions")
     m, n = t.shape[-2:]
     B = 1
     for s in t.shape[:-2]:
         B *= s
+    if max(B, m, n) > INT_MAX:
+        raise MoEError(2, f"{name}: sizes past 2^31 - 1 are not supported, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise MoEError(1, "tensors must be on a GPU device")
     if t.is_contiguous():
         return B, m, n, m * n
     if t.dim() != 3 or not t[0].is_contiguous() or t.stride(0) < m * n:

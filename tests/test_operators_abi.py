@@ -231,3 +231,17 @@ def test_binding_refuses_wrong_tensors():
     ):
         with pytest.raises(mx.MoEError):
             call()
+
+
+def test_binding_refuses_sizes_past_int():
+    """A size that the ABI's int would wrap around (here to 5) is refused, not shortened."""
+    wide = (1 << 32) + 5
+    x = torch.empty(wide, 8, device="meta")
+    w, off = torch.empty(2, 6, 8, device="meta"), torch.empty(3, dtype=torch.int32, device="meta")
+    stat = torch.empty(wide, device="meta")
+    for call in (lambda: mx.layer_norm(x), lambda: mx.layer_norm_backward(x, x, None, stat, stat),
+                 lambda: mx.grouped_matmul(x, w, off),
+                 lambda: mx.grouped_matmul_backward(x, w, off, torch.empty(wide, 6, device="meta")),
+                 lambda: mx.orthogonalize(x), lambda: mx.orthogonalize(torch.empty(1 << 17, 1 << 16, 2, 2, device="meta"))):
+        with pytest.raises(mx.MoEError, match="2\\^31"):
+            call()
