@@ -16,7 +16,7 @@
 // p = 64 and 2.1 us at p = 128 (2.5 GHz), of which the MFMAs are 0.4 and 1.3; the rest is
 // the chain from barrier to LDS read to MFMA to split to LDS write, which one or two
 // wavefronts per SIMD do not hide (MFMAs busy 32% on a CU in use, LDS 26%).  16 float32
-// matrices of 128 x 256, five steps: 75 us (110 us in 17 launches), of 64 x 64: 18 us (93 us).
+// matrices of 128 x 256, five steps: 83 us (110 us in 17 launches), of 64 x 64: 19 us (93 us).
 #include <math.h>
 
 #include <algorithm>
@@ -40,6 +40,11 @@ struct NsSmall {
   static constexpr int SLOTS = 3;               // chunks of X
   static constexpr int NI = 2 * PP / 8 / NW;    // loads per wavefront per chunk
   static constexpr int TA = RB / 2;             // tiles of A per wavefront
+  // lo lo' too: where sums are short, what it leaves out (2^-24.5 of a product) is what their
+  // error consists of (8 x 16: 1.2e-6 -> 1.0e-6 relative, 64 x 64 1.4e-6 -> 1.2e-6, where float32 products
+  // have 0.7e-6 and 1.2e-6; 5% of the time).  For sides past 64 it costs 12% and their error is
+  // that of float32 products without it.
+  static constexpr bool FOUR = PP == 64;
 };
 
 struct NsSmallArgs {
@@ -139,7 +144,7 @@ __device__ __forceinline__ void ns_gram_read(const uint8_t* m, int row, int col,
   for (int t = 0; t < TA; ++t) g.bl[t] = ns_rows<PP>(m, col + 32 * t, kg, 1, at);
   g.al = ns_rows<PP>(m, row, kg, 1, at);
 }
-template <int TA>
+template <int PP, int TA>
 __device__ __forceinline__ void ns_gram_add(const NsGram<TA>& g, f32x16 (&acc)[TA]) {
 #pragma unroll
   for (int t = 0; t < TA; ++t) acc[t] = ns_mfma(g.ah, g.bh[t], acc[t]);
@@ -147,27 +152,44 @@ __device__ __forceinline__ void ns_gram_add(const NsGram<TA>& g, f32x16 (&acc)[T
   for (int t = 0; t < TA; ++t) acc[t] = ns_mfma(g.ah, g.bl[t], acc[t]);
 #pragma unroll
   for (int t = 0; t < TA; ++t) acc[t] = ns_mfma(g.al, g.bh[t], acc[t]);
-}
-// The same over `kgs` groups, each one's fragments read ahead of the products before.
-template <int PP, int KGS, int TA>
-__device__ __forceinline__ void ns_gram(const uint8_t* m, int row, int col, const NsLane& at,
-                                        f32x16 (&acc)[TA]) {
-  NsGram<TA> g[2];
-  ns_gram_read<PP>(m, row, col, 0, at, g[0]);
+  if constexpr (NsSmall<PP>::FOUR) {
 #pragma unroll
-  for (int kg = 0; kg < KGS; ++kg) {
-    if (kg + 1 < KGS) ns_gram_read<PP>(m, row, col, kg + 1, at, g[(kg + 1) & 1]);
-    ns_gram_add(g[kg & 1], acc);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int t = 0; t < TA; ++t) acc[t] = ns_mfma(g.al, g.bl[t], acc[t]);
   }
 }
-
 template <int TA>
 __device__ __forceinline__ void ns_clear(f32x16 (&acc)[TA]) {
 #pragma unroll
   for (int t = 0; t < TA; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
+}
+// Sums over 64 indices are added up apart from the total: a chain's rounding then is that of
+// 12 products and of one addition per 64 indices, not of every product against the total
+// (30 x 500: error 2.1e-6 -> 1.2e-6 relative, 64 x 700 1.8e-6 -> 1.4e-6, where float32 products have
+// 1.6e-6 and 1.5e-6; 16 matrices of 128 x 256 75 -> 80 us, of 64 x 64 unchanged).
+template <int TA>
+__device__ __forceinline__ void ns_add(const f32x16 (&part)[TA], f32x16 (&acc)[TA]) {
+#pragma unroll
+  for (int t = 0; t < TA; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[t][r] += part[t][r];
+}
+// The same over KGS groups, each one's fragments read ahead of the products before.
+template <int PP, int KGS, int TA>
+__device__ __forceinline__ void ns_gram(const uint8_t* m, int row, int col, const NsLane& at,
+                                        f32x16 (&acc)[TA]) {
+  NsGram<TA> g[2];
+  f32x16 part[TA];
+  ns_gram_read<PP>(m, row, col, 0, at, g[0]);
+#pragma unroll
+  for (int kg = 0; kg < KGS; ++kg) {
+    if (kg % 4 == 0) ns_clear(part);
+    if (kg + 1 < KGS) ns_gram_read<PP>(m, row, col, kg + 1, at, g[(kg + 1) & 1]);
+    ns_gram_add<PP>(g[kg & 1], part);
+    if (kg % 4 == 3) ns_add(part, acc);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 // A symmetric accumulator tile as rows of m: a lane holds rows i .. i + 3 of column j,
@@ -279,6 +301,8 @@ __device__ __forceinline__ void ns_chunk(const NsWave<PP>& w, NsLane at, const u
                                          bool last, float scale,
                                          const u32x4 (&ph)[PP / 16], const u32x4 (&pl)[PP / 16],
                                          f32x16& y, f32x16 (&acc)[NsSmall<PP>::TA]) {
+  // (the stores first: the next barrier's wait then leaves the loads outstanding, not them)
+  if constexpr (ADD) ns_save<PP>(done, to, c - 1, w.wave, w.lane, w.off);
   ns_load<PP>(base, bound, w.wave, w.off, wr);
   if constexpr (APPLY) {
 #pragma unroll
@@ -304,16 +328,19 @@ __device__ __forceinline__ void ns_chunk(const NsWave<PP>& w, NsLane at, const u
       y = ns_mfma(xh[kg & 1], ph[kg], y);
       y = ns_mfma(xh[kg & 1], pl[kg], y);
       y = ns_mfma(xl[kg & 1], ph[kg], y);
+      if constexpr (NsSmall<PP>::FOUR) y = ns_mfma(xl[kg & 1], pl[kg], y);
       __builtin_amdgcn_sched_barrier(0);
     }
   } else {
     ns_gram_read<PP>(done, w.row, w.col, 0, at, g[0]);
   }
+  f32x16 part[TA];
   if constexpr (ADD) {
+    ns_clear(part);
 #pragma unroll
     for (int kg = 0; kg < 4; ++kg) {
       if (kg + 1 < 4) ns_gram_read<PP>(done, w.row, w.col, kg + 1, at, g[(kg + 1) & 1]);
-      ns_gram_add(g[kg & 1], acc);
+      ns_gram_add<PP>(g[kg & 1], part);
       if (kg + 1 < 4) __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -331,7 +358,7 @@ __device__ __forceinline__ void ns_chunk(const NsWave<PP>& w, NsLane at, const u
       }
     }
   }
-  if constexpr (ADD) ns_save<PP>(done, to, c - 1, w.wave, w.lane, w.off);
+  if constexpr (ADD) ns_add(part, acc);
 }
 
 // The result's columns of chunk c: a lane holds columns j .. j + 3 of its row.  Whole runs of
@@ -530,9 +557,10 @@ __global__ __launch_bounds__(NsSmall<PP>::THREADS) void ns_small_kernel(NsSmallA
     // the slots of chunk c - 1 and of X' c - 2 (and, at first, P) are free.
     int slot = 0;  // of chunk c
     auto step = [&](int c, auto apply, auto add) {
-      // accesses retire in order; each chunk's loads are followed by one chunk's stores
-      if (!last && c >= 2) MOE_WAIT_VMCNT(2 * N::NI);
-      else MOE_WAIT_VMCNT(N::NI);
+      // Loads land in order among themselves, so that with as many accesses outstanding as
+      // chunk c + 1 has loads, chunk c has landed.  The count names no stores: whether those
+      // retire in order with loads is not relied upon.
+      MOE_WAIT_VMCNT(N::NI);
       lds_sync();
       f32x16 y;
       ns_chunk<PP, apply.value, add.value>(
@@ -576,16 +604,16 @@ long long plane_bytes(int m, int n) {
 
 // Whether one block per matrix is faster than the general path, whose launches take 90 us
 // or more but spread a matrix over many blocks.  Measured (float32, five steps), general -> this
-// one: one matrix of 64 x 512 98 -> 61 us, of 64 x 1024 109 -> 110 us, of 128 x 256 104 -> 74 us, of
-// 128 x 512 109 -> 120 us; 16 of 64 x 1024 117 -> 112 us, of 128 x 512 114 -> 122 us; 64 of
-// 64 x 4096 467 -> 459 us, of 128 x 1024 234 -> 237 us; 256 of 64 x 64 163 -> 22 us, of 128 x
-// 4096 2423 -> 1543 us.  That is a limit of chunks (of 128 rows: twice) that grows with the
+// one: one matrix of 64 x 512 98 -> 68 us, of 64 x 1024 109 -> 118 us, of 128 x 256 104 -> 81 us, of
+// 128 x 512 109 -> 128 us; 16 of 64 x 1024 117 -> 127 us, of 128 x 512 114 -> 133 us; 64 of
+// 64 x 2048 346 -> 263 us, of 128 x 1024 234 -> 263 us; 256 of 64 x 64 163 -> 23 us, of 128 x
+// 4096 2423 -> 1580 us.  That is a limit of chunks (of 128 rows: twice) that grows with the
 // CUs that the matrices occupy.
 bool ortho_small_fits(int B, int m, int n) {
   const int side = std::min(m, n);
   if (side > 128) return false;
   const int work = ((std::max(m, n) + 63) / 64) * (padded_side(side) / 64);
-  return work <= 12 + (long long)B * B / 64;
+  return work <= 10 + (long long)B * B / 64;
 }
 
 size_t ortho_small_workspace_bytes(int B, int m, int n) { return (size_t)B * 2 * plane_bytes(m, n); }

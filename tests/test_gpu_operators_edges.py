@@ -304,3 +304,35 @@ def test_grouped_f32_few_rows_gradient_keeps_bad_weights_to_their_columns():
     bad[:9, 7] = True
     bad[9:, 199] = True
     assert (~torch.isfinite(dx) == bad).all() and torch.equal(dx[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("m,n", [(8, 16), (20, 30), (30, 500), (64, 64), (64, 700), (100, 120), (128, 256)])
+def test_orthogonalize_small_matrices_are_as_exact_as_float32_products(m, n):
+    """Root mean square over 16 matrices of the error against 64 bits: at most twice that of the
+    same steps in float32 (operands of 22 bits and more against 24, sums of the same length)."""
+    r = np.random.default_rng(m + n)
+    x = dev(r.normal(size=(16, m, n)))
+    out = mx.orthogonalize(x)
+    torch.cuda.synchronize()
+    own, plain = [], []
+    for i in range(16):
+        want = ref.orthogonalize(host(x[i]))
+        own.append(np.linalg.norm(host(out[i]) - want))
+        plain.append(np.linalg.norm(ref.orthogonalize(host(x[i]), dtype=np.float32) - want))
+    assert np.square(own).sum() <= 4 * np.square(plain).sum(), (own, plain)
+
+
+@pytest.mark.parametrize("m,n", [(128, 1500), (64, 2100), (700, 100)])
+def test_orthogonalize_many_matrices_repeat_their_bits(m, n):
+    """One block per matrix on every CU, iterates past the caches: what a chunk's loads and the
+    stores of another do to each other shows as bits that change from call to call."""
+    torch.manual_seed(61)
+    x = torch.randn(512, m, n, device="cuda")
+    want = mx.orthogonalize(x)
+    for k in range(4):
+        say(f"orthogonalize 512 x {m} x {n}, call {k}")
+        got = mx.orthogonalize(x)
+        torch.cuda.synchronize()
+        assert torch.equal(_bits(got), _bits(want)), k
+    for i in (0, 255, 511):
+        _check_update(want[i], host(x[i]), 5, (3.4445, -4.7750, 2.0315), "f32", i)
