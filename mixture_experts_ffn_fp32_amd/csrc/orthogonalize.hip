@@ -67,7 +67,6 @@ struct NsTiles {
   };
   static constexpr bool SYM = KIND == NS_SYM;
   __device__ __forceinline__ bool tri(const Tile& t) const { return t.m0 == t.n0; }
-  __device__ __forceinline__ int hint(int) const { return 0; }
 
   __device__ __forceinline__ int per_matrix() const {
     const int mt = (p.M + C::BM - 1) / C::BM;

@@ -496,7 +496,7 @@ __global__ __launch_bounds__(NsSmall<PP>::THREADS) void ns_small_kernel(NsSmallA
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
             const int jv = j + v * E::kPerChunk;
-            g.raw[h][v] = *(const u32x4*)(x + ((r < a.p) & (jv < a.q) ? r * a.q + jv : 0));
+            g.raw[h][v] = *(const u32x4*)(x + (((r < a.p) & (jv < a.q)) ? r * a.q + jv : 0));
           }
         } else {
 #pragma unroll
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(NsSmall<PP>::THREADS) void ns_small_kernel(NsSmallA
           if (vec) ns_unpack<E>(g.raw[h][v], g.one[h] + v * E::kPerChunk);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          f[h][e] = (r < a.p) & (j + e < a.q) ? ldexpf(g.one[h][e], raise) * scale : 0.f;
+          f[h][e] = ((r < a.p) & (j + e < a.q)) ? ldexpf(g.one[h][e], raise) * scale : 0.f;
       }
       fetch(g, min(c + 2, nc - 1));
 #pragma unroll

@@ -737,9 +737,6 @@ __device__ __forceinline__ void split_f16(float v, uint16_t& hi, uint16_t& lo) {
   hi = __builtin_bit_cast(uint16_t, h);
   lo = __builtin_bit_cast(uint16_t, l);
 }
-__device__ __forceinline__ float f16_to_f32(uint16_t b) {
-  return (float)__builtin_bit_cast(_Float16, b);
-}
 
 // Bytes of a split row of n values, and the place of element j's hi in it (its lo
 // is 64 bytes further).
