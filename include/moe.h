@@ -282,7 +282,7 @@ moe_status_t moe_grouped_matmul(const void* x, const void* w, const int32_t* off
 /* Gradients of sum_r dy_r . y_r:
  *   dx[r] = w[e]^T dy[r]                       [M][k] dtype, may be NULL
  *   dw[e] = sum over e's rows of dy[r] x[r]^T  [E][n][k] float32, may be NULL
- * (not both NULL).  A group without rows gets a zero dw, M = 0 included; dx
+ * (not both NULL unless M = 0).  A group without rows gets a zero dw, M = 0 included; dx
  * outside the groups as y above.  x may be NULL without dw, w without dx.
  * float32: w is scaled per expert, and the rows of dy and x so that each
  * row's product carries one scale: what lies 2^-40 below the largest value of

@@ -263,9 +263,10 @@ moe_status_t moe_grouped_matmul_backward(const void* x, const void* w, const int
                                          size_t workspace_bytes, void* stream) {
   moe_status_t s = check_grouped(M, E, n, k, dtype);
   if (s != MOE_OK) return s;
+  // (without rows dx has no elements, and its pointer may be NULL)
+  if (M == 0 && dw == nullptr) return ok();
   if (dx == nullptr && dw == nullptr)
     return fail(MOE_ERR_INVALID_ARG, "dx and dw are both NULL: nothing to compute");
-  if (M == 0 && dw == nullptr) return ok();
   if ((s = check_ptr("x", x, M > 0 && dw != nullptr)) != MOE_OK) return s;
   if ((s = check_ptr("w", w, M > 0 && dx != nullptr)) != MOE_OK) return s;
   if ((s = check_ptr("offsets", offsets, true)) != MOE_OK) return s;

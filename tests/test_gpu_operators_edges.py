@@ -89,6 +89,19 @@ def test_layer_norm_backward_of_an_empty_batch():
             assert dw.shape == db.shape == (d,) and not dw.any() and not db.any()
 
 
+def test_grouped_empty_batch_one_gradient_only():
+    for dt in (torch.float32, torch.bfloat16):
+        say(f"grouped M = 0 {dt}")
+        w = torch.randn(3, 32, 200, device="cuda").to(dt)
+        off = torch.zeros(4, dtype=torch.int32, device="cuda")
+        x, dy = torch.empty(0, 200, device="cuda", dtype=dt), torch.empty(0, 32, device="cuda", dtype=dt)
+        dx, none = mx.grouped_matmul_backward(x, w, off, dy, need_dw=False)
+        assert dx.shape == (0, 200) and none is None
+        none, dw = mx.grouped_matmul_backward(x, w, off, dy, need_dx=False)
+        torch.cuda.synchronize()
+        assert none is None and dw.shape == w.shape and not dw.any()
+
+
 # ---------------------------------------------------------------- the update's two paths
 # (batches and sides around 64, 128 and the rule's limits; tall and wide; odd sizes)
 PATHS = [(1, 1, 300), (2, 64, 65), (1, 65, 65), (3, 63, 449), (1, 64, 513), (1, 513, 64), (2, 128, 129),

@@ -140,6 +140,13 @@ def test_grouped_backward_refusals(lib):
     assert _grouped_bwd(lib, M=0, dw=None, x=None, w=None, dy=None, off=None, ws=None, wsb=0) == OK
 
 
+def test_grouped_backward_of_an_empty_batch_needs_no_dx_pointer(lib):
+    """dx of no rows has no elements, and a framework's empty tensor no address."""
+    for dt in (0, 1):
+        assert _grouped_bwd(lib, M=0, dt=dt, dx=None, dw=None, x=None, w=None, dy=None, ws=None, wsb=0) == OK
+        assert _grouped_bwd(lib, M=1, dt=dt, dx=None, dw=None) == INVALID
+
+
 def test_workspaces_grow_with_the_rows(lib):
     """A workspace for the largest batch holds every smaller one."""
     rows = [0, 1, 2, 31, 64, 65, 127, 500, 512, 513, 4096, 8191, 8192, 100_000]
