@@ -19,6 +19,12 @@
 // w's rows; and for x in the weight gradient, which contracts over the rows of
 // both, the scale that makes each row's product scale the same.
 //
+// The parts of an infinity are an infinity and NaN, so a float32 result with one among its
+// operands comes out as NaN, and what leaves float32's range on the way as either.  Every
+// float32 result that is not finite is therefore summed again from the operands themselves,
+// in float64 (grouped_again).  The search of the results in registers takes up to 1% of y's and
+// dx's time where all are finite.
+//
 // Measured: y of 49152 rows in 64 groups, 1408 x 2048 bfloat16, 315 us (902 TFLOP/s of the 1338 that one
 // dense product reaches here; MFMAs busy 45%); of 384 rows, 2048 x 1408, 69 us (HBM bound, 5.4
 // TB/s); both gradients of 28672 rows in 63 groups, 896 x 1280, 245 us (dw's 289 MB written at
@@ -129,7 +135,19 @@ struct GroupedProduct {
   const int32_t* eb;       //   w's rows (forward), experts (dx), the weight gradient's sum
   GroupDims g;
   int zero_rest;
+  const float *ra, *rb;    // float32: A's and B's operands as the caller gave them
 };
+
+__device__ __forceinline__ bool not_finite(float v) { return !(fabsf(v) <= FLT_MAX); }
+
+// sum of a[i sa] b[i sb] over n terms in float64: products are exact, no partial sum leaves the
+// range, infinities and NaN come out as in any order of summation.
+__device__ __forceinline__ float grouped_again(const float* a, size_t sa, const float* b, size_t sb,
+                                               int n) {
+  double s = 0.0;
+  for (int i = 0; i < n && s == s; ++i, a += sa, b += sb) s = fma((double)*a, (double)*b, s);
+  return (float)s;
+}
 
 template <class C, int DIR>
 struct GroupedTiles {
@@ -188,6 +206,7 @@ struct GroupedTiles {
     if constexpr (DIR == GR_DW) {
       float* out = (float*)p.out + (size_t)t.hint * g.n * g.k;
       const int ex = C::SPLIT ? -p.eb[0] : 0;
+      bool bad = false;
 #pragma unroll
       for (int fm = 0; fm < C::FM; ++fm)
 #pragma unroll
@@ -198,14 +217,17 @@ struct GroupedTiles {
           for (int fn = 0; fn < C::FN; ++fn) {
             const int n = t.n0 + tg_col<C>(wn, fn, lane, r);
             if (n < g.k) {
-              const float v = acc[fm][fn][r];
-              out[(size_t)m * g.k + n] = C::SPLIT ? ldexpf(v, ex) : v;
+              const float v = C::SPLIT ? ldexpf(acc[fm][fn][r], ex) : acc[fm][fn][r];
+              out[(size_t)m * g.k + n] = v;
+              bad |= not_finite(v);
             }
           }
         }
+      if (C::SPLIT && bad) again(t, wm, wn, lane);
     } else {
       // a lane holds four consecutive columns of one row
       const int N = DIR == GR_FWD ? g.n : g.k;
+      bool bad = false;
       const bool vec = N % (C::SPLIT ? 4 : 8) == 0;  // whole 16-byte runs
 #pragma unroll
       for (int fm = 0; fm < C::FM; ++fm) {
@@ -226,8 +248,10 @@ struct GroupedTiles {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 v[e] = acc[fm][fn][4 * q + e];
-                if (n + e < N)
+                if (n + e < N) {
                   v[e] = ldexpf(v[e], -ea - (DIR == GR_FWD ? p.eb[(size_t)t.hint * g.n + n + e] : 0));
+                  bad |= not_finite(v[e]);
+                }
               }
               if (vec) {
                 if (n < N) *(f32x4*)(c + n) = f32x4{v[0], v[1], v[2], v[3]};
@@ -263,6 +287,26 @@ struct GroupedTiles {
           }
         }
       }
+      if (C::SPLIT && bad) again(t, wm, wn, lane);
+    }
+  }
+
+  // This lane's float32 results that are not finite, as it stored them, summed again.
+  __device__ __forceinline__ void again(const Tile& t, int wm, int wn, int lane) const {
+    const GroupDims& g = p.g;
+    const int M = DIR == GR_DW ? g.n : t.size, N = DIR == GR_FWD ? g.n : g.k;
+    float* out = (float*)p.out + (DIR == GR_DW ? (size_t)t.hint * g.n : (size_t)t.row0) * N;
+    const float* a = p.ra + (size_t)t.row0 * (DIR == GR_FWD ? g.k : g.n);
+    const float* b = p.rb + (DIR == GR_DW ? (size_t)t.row0 : (size_t)t.hint * g.n) * g.k;
+    for (int i = 0; i < C::FM * C::FN * 16; ++i) {
+      const int f = i >> 4, m = t.m0 + tg_row<C>(wm, f / C::FN, lane, i & 15);
+      const int n = t.n0 + tg_col<C>(wn, f % C::FN, lane, i & 15);
+      if (m >= M || n >= N) continue;
+      float* to = out + (size_t)m * N + n;
+      if (!not_finite(*to)) continue;
+      if (DIR == GR_FWD) *to = grouped_again(a + (size_t)m * g.k, 1, b + (size_t)n * g.k, 1, g.k);
+      if (DIR == GR_DX) *to = grouped_again(a + (size_t)m * g.n, 1, b + n, g.k, g.n);
+      if (DIR == GR_DW) *to = grouped_again(a + m, g.n, b + n, g.k, t.size);
     }
   }
 };
@@ -541,6 +585,7 @@ struct FewProduct {
   float* out;
   GroupDims g;
   int zero_rest;
+  const float* rows;       // x or dy themselves
 };
 // Bytes of x's split row.
 __host__ __device__ inline long long few_pitch(int k) { return (long long)((k + 31) / 32) * 192; }
@@ -682,7 +727,7 @@ __device__ __forceinline__ void few_tile(const FewProduct& p, int e, int row0, i
 // Sums and stores a tile, a lane four columns of one row: wavefront q fragment q's (dx: the
 // q-th values of the four fragments, which are neighbours).
 template <bool DX, int RF>
-__device__ __forceinline__ void few_store(const FewProduct& p, int row0, int rows, int n0, int wave,
+__device__ __forceinline__ void few_store(const FewProduct& p, int e, int row0, int rows, int n0, int wave,
                                           int lane, const f32x4 (&acc)[4][RF],
                                           f32x4 (*__restrict__ sum)[4][2][64]) {
   const int width = DX ? p.g.k : p.g.n;
@@ -710,12 +755,26 @@ __device__ __forceinline__ void few_store(const FewProduct& p, int row0, int row
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = ldexpf(v[c], -ex);
     float* y = p.out + (size_t)(row0 + i) * width + n;
+    bool bad = false;
     if (DX || width % 4 == 0) {
       *(f32x4*)y = v;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) bad |= not_finite(v[c]);
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (n + c < width) y[c] = v[c];
+        if (n + c < width) {
+          y[c] = v[c];
+          bad |= not_finite(v[c]);
+        }
+    }
+    if (bad) {
+      const float* a = p.rows + (size_t)(row0 + i) * (DX ? p.g.n : p.g.k);
+      const float* w = p.w + (size_t)e * p.g.n * p.g.k;
+      for (int c = 0; c < 4 && n + c < width; ++c)
+        if (not_finite(y[c]))
+          y[c] = DX ? grouped_again(a, 1, w + n + c, p.g.k, p.g.n)
+                    : grouped_again(a, 1, w + (size_t)(n + c) * p.g.k, 1, p.g.k);
     }
   }
   __syncthreads();
@@ -738,11 +797,11 @@ __global__ __launch_bounds__(256, 2) void grouped_few_kernel(FewProduct p) {
     if (rows > 16) {
       f32x4 acc[4][2];
       few_tile<DX, 2>(p, e, row0, rows, n0, wave, lane, acc);
-      few_store<DX, 2>(p, row0, rows, n0, wave, lane, acc, sum);
+      few_store<DX, 2>(p, e, row0, rows, n0, wave, lane, acc, sum);
     } else {
       f32x4 acc[4][1];
       few_tile<DX, 1>(p, e, row0, rows, n0, wave, lane, acc);
-      few_store<DX, 1>(p, row0, rows, n0, wave, lane, acc, sum);
+      few_store<DX, 1>(p, e, row0, rows, n0, wave, lane, acc, sum);
     }
   }
 }
@@ -752,7 +811,7 @@ hipError_t run_few(const GroupedArgs& a, const void* in, uint8_t* planes, int32_
                    hipStream_t st) {
   const int width = DX ? a.k : a.n, length = DX ? a.n : a.k;
   const FewProduct p{(const float*)a.w, (const u32x4*)planes, ex, a.offsets, (float*)out,
-                     GroupDims{a.M, a.E, a.n, a.k}, a.zero_rest};
+                     GroupDims{a.M, a.E, a.n, a.k}, a.zero_rest, (const float*)in};
   split_three_kernel<<<blocks_of(a.M), 256, 0, st>>>((const float*)in, a.M, length, (u32x4*)planes, ex);
   const long long most =
       ((long long)a.M / kFewRows + std::min(a.M, a.E)) * ((width + kFewCols - 1) / kFewCols);
@@ -924,6 +983,8 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
     p.B = w.w;
     p.ea = w.ex;
     p.eb = w.ew;
+    p.ra = (const float*)a.x;
+    p.rb = (const float*)a.w;
     return pick_product<GR_FWD, true>(a, p, st);
   }
   if (w.x != nullptr) {
@@ -989,8 +1050,10 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   p.A = dy;
   p.pitch_a = py;
   p.ea = w.ey;
+  p.ra = (const float*)a.dy;
   if (dx && a.M > 0) {
     p.B = wt;
+    p.rb = (const float*)a.w;
     p.pitch_b = pw;
     p.eb = w.ew;
     p.out = a.dx;
@@ -999,6 +1062,7 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   }
   if (dw) {
     p.B = x;
+    p.rb = (const float*)a.x;
     p.pitch_b = px;
     p.eb = w.ex;
     p.out = a.dw;

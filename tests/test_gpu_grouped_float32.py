@@ -1,0 +1,130 @@
+"""float32 grouped products over everything float32 holds: infinities, NaN and the ends of the
+range, and operands whose experts, rows and channels differ by any factor.
+
+Each test runs on both sides of the rules that send a product with few rows per group to a
+path of its own (`_few`, `_few_dx`, checked against the workspace that the library asks for).
+
+Tolerances per element, u = 2^-24, for a sum of n products: operands in three parts are exact
+(a float32 value is hi + mid + lo); of the nine products of parts six are taken, the others are at
+most 2^-22.99 < 2.02 u of the product; every addition rounds by at most 2 u of the partial sum,
+and there are 6 (n + 8) of them: (12 (n + 8) + 3) u sum|products|, and u |result| for the store.
+Operands in two float16 parts lose 2 u each and lo lo' <= 4 u of a product, 8 u where 3 u stand
+above, and with half as many additions the same bound holds; what lies far below its row's
+largest value is held to 2^-38 of that.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import operators as ref
+from parity_helpers import say
+from test_gpu_operators import U, _bits, _offsets, dev, host, mx
+
+pytestmark = pytest.mark.gpu
+
+
+def _few(M, E, n, k):
+    return k % 4 == 0 and n >= 32 and M <= 64 * E
+
+
+def _few_dx(M, E, n, k):
+    return _few(M, E, n, k) and n % 4 == 0 and k >= 192
+
+
+def _size(query, *args):
+    out = ctypes.c_size_t(0)
+    assert query(*args, ctypes.byref(out)) == 0
+    return out.value
+
+
+def _side(M, E, n, k, few, few_dx):
+    """The shape falls on the expected side of both rules: without a prepared w the workspace
+    does not grow with the experts."""
+    L = mx.load_library()
+    assert (_few(M, E, n, k), _few_dx(M, E, n, k)) == (few, few_dx)
+    more = min(1024, 2 * E)
+    assert few == (_size(L.moe_grouped_matmul_workspace_size, M, E, n, k, 0) ==
+                   _size(L.moe_grouped_matmul_workspace_size, M, more, n, k, 0))
+    q = L.moe_grouped_matmul_backward_workspace_size
+    assert few_dx == (_size(q, M, E, n, k, 0, 1, 0) == _size(q, M, more, n, k, 0, 1, 0))
+
+
+def _tol(a, b, n):
+    """Tolerance of a @ b^T (absolute values) over n terms."""
+    return (12 * (n + 8) + 8) * U * (a @ b.T)
+
+
+def _same(got, want, tol, label):
+    """NaN and infinities where the definition has them, within tol elsewhere."""
+    g = host(got)
+    assert (np.isnan(g) == np.isnan(want)).all(), f"{label}: NaN"
+    big = np.abs(want) > 3.4028236e38                  # rounds to an infinity
+    assert (np.isinf(g) == big).all() and (g[big] * want[big] > 0).all(), f"{label}: infinities"
+    ok = np.isfinite(want) & ~big
+    err = np.abs(np.where(ok, g, 0.0) - np.where(ok, want, 0.0))
+    bad = ~(err <= np.where(ok, tol + U * np.abs(want), 1.0))
+    assert not bad.any(), (label, int(bad.sum()), float(err[bad].max()))
+
+
+def _check_all(x, w, off, dy, label, floor=0.0):
+    """y, dx and dw against the definition in float64.  floor: of a row's largest value, for y on
+    the path with two parts."""
+    say(label)
+    y = mx.grouped_matmul(x, w, off)
+    dx, dw = mx.grouped_matmul_backward(x, w, off, dy)
+    torch.cuda.synchronize()
+    X, W, DY = host(x), host(w), host(dy)
+    fx, fw, fdy = (np.where(np.isfinite(t), np.abs(t), 0.0) for t in (X, W, DY))
+    M, k = X.shape
+    n = W.shape[1]
+    with np.errstate(invalid="ignore", over="ignore"):
+        for e, (a, b) in enumerate(ref.group_rows(off.cpu().numpy(), M)):
+            t = _tol(fx[a:b], fw[e], k)
+            if floor:
+                t = t + floor * (fx[a:b].max(1, initial=0)[:, None] * fw[e].sum(1) +
+                                 fx[a:b].sum(1)[:, None] * fw[e].max(1))
+            _same(y[a:b], X[a:b] @ W[e].T, t, f"{label} y {e}")
+            _same(dx[a:b], DY[a:b] @ W[e], _tol(fdy[a:b], fw[e].T, n), f"{label} dx {e}")
+            _same(dw[e], DY[a:b].T @ X[a:b], _tol(fdy[a:b].T, fx[a:b].T, b - a), f"{label} dw {e}")
+
+
+# rows of the groups, n, k, and the sides of the rules: few rows, few rows with a width for y only, an odd
+# width, many rows (tiles of 64), and of tiles of 128 and 256
+SHAPES = {
+    "few": ([30, 64, 0, 9], 48, 200, True, True),
+    "few y": ([30, 64, 0, 9], 48, 72, True, False),
+    "odd width": ([30, 64, 0, 9], 50, 203, False, False),
+    "many rows": ([300, 150, 0, 9], 72, 200, False, False),
+    "tiles of 128": ([600, 300, 0, 700, 650], 640, 520, False, False),
+    "tiles of 256": ([700, 530, 0, 1100, 900], 2060, 1544, False, False),
+}
+
+
+def _normal(name, seed):
+    sizes, n, k, few, few_dx = SHAPES[name]
+    M, E = sum(sizes) + 3, len(sizes)
+    _side(M, E, n, k, few, few_dx)
+    r = np.random.default_rng(seed)
+    x, w, dy = r.normal(size=(M, k)), 0.3 * r.normal(size=(E, n, k)), r.normal(size=(M, n))
+    return x, w, torch.from_numpy(_offsets(sizes, 2)).cuda(), dy, r
+
+
+@pytest.mark.parametrize("name", SHAPES)
+def test_infinities_and_nan_come_out_as_in_float32(name):
+    x, w, off, dy, _ = _normal(name, 1)
+    last = len(w) - 1
+    a = int(off[last])                                  # a row of the last group
+    x[2 + 5, 7] = np.inf
+    x[2 + 6, 7], x[2 + 6, 9] = np.inf, -np.inf
+    x[2 + 31, 0] = np.nan
+    x[a, 3] = -np.inf
+    w[1, 3, 11] = -np.inf
+    w[1, 4, 11] = 0.0
+    w[last, -1, -1] = np.nan
+    dy[2 + 12, 6] = np.inf
+    dy[a + 2, 1] = -np.inf
+    dy[a + 3, 1] = np.inf
+    dy[a + 4] = np.nan
+    _check_all(dev(x), dev(w), off, dev(dy), name, floor=2.0 ** -37)
