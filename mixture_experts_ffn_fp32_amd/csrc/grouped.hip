@@ -13,11 +13,12 @@
 // ends there by a bounded buffer range.
 //
 // bfloat16 operands are read where they are (the transposed products through
-// transposing LDS reads); float32 operands are first written as two float16
-// each (tile_gemm.h), with a power-of-two scale per row of x, dy and, in the
-// forward, w; per expert for w in the backward, whose product contracts over
-// w's rows; and for x in the weight gradient, which contracts over the rows of
-// both, the scale that makes each row's product scale the same.
+// transposing LDS reads).  float32 operands of y and dx are first written as two
+// float16 each (tile_gemm.h), with a power-of-two scale per row of x, dy and, in the
+// forward, w; per expert for w in dx, whose product contracts over w's rows.  The
+// weight gradient contracts over the rows of both dy and x, where no scale of a row can
+// be taken out again and experts, rows and channels differ by any factor: its operands
+// are written as three bfloat16 each, which need no scale.
 //
 // The parts of an infinity are an infinity and NaN, so a float32 result with one among its
 // operands comes out as NaN, and what leaves float32's range on the way as either.  Every
@@ -129,10 +130,11 @@ struct GroupedProduct {
   const uint8_t* A;        // x or dy (rows of the groups)
   const uint8_t* B;        // w (forward, dx) or x (weight gradient)
   uint32_t pitch_a, pitch_b;
+  uint32_t plane_a, plane_b;  // three parts: bytes of one in a row
   const int32_t* offsets;
   void* out;
-  const int32_t* ea;       // float32: exponents of A's rows, and of
-  const int32_t* eb;       //   w's rows (forward), experts (dx), the weight gradient's sum
+  const int32_t* ea;       // two parts: exponents of A's rows, and of
+  const int32_t* eb;       //   w's rows (forward), experts (dx)
   GroupDims g;
   int zero_rest;
   const float *ra, *rb;    // float32: A's and B's operands as the caller gave them
@@ -181,7 +183,9 @@ struct GroupedTiles {
     t.A.pitch = p.pitch_a;
     t.A.rows = t.size;
     t.A.width = (g.n + 31) & ~31;
+    t.A.plane = p.plane_a;
     t.B.pitch = p.pitch_b;
+    t.B.plane = p.plane_b;
     if (DIR == GR_DW) {
       t.B.p = p.B + (size_t)t.row0 * p.pitch_b;
       t.B.rows = t.size;
@@ -193,9 +197,13 @@ struct GroupedTiles {
       t.B.width = (g.k + 31) & ~31;
       t.steps = ((DIR == GR_FWD ? g.k : g.n) + C::KS - 1) / C::KS;
     }
-    if (!C::SPLIT) {  // a bfloat16 row holds what its pitch says
+    if (C::PARTS == 1) {  // a bfloat16 row holds what its pitch says
       t.A.width = min(t.A.width, (int)(p.pitch_a / 2));
       t.B.width = min(t.B.width, (int)(p.pitch_b / 2));
+    } else if (C::PARTS == 3) {
+      t.steps *= kTgProducts;
+      t.A.width = min(t.A.width, (int)(p.plane_a / 2));
+      t.B.width = min(t.B.width, (int)(p.plane_b / 2));
     }
     return t;
   }
@@ -205,7 +213,6 @@ struct GroupedTiles {
     const GroupDims& g = p.g;
     if constexpr (DIR == GR_DW) {
       float* out = (float*)p.out + (size_t)t.hint * g.n * g.k;
-      const int ex = C::SPLIT ? -p.eb[0] : 0;
       bool bad = false;
 #pragma unroll
       for (int fm = 0; fm < C::FM; ++fm)
@@ -217,13 +224,13 @@ struct GroupedTiles {
           for (int fn = 0; fn < C::FN; ++fn) {
             const int n = t.n0 + tg_col<C>(wn, fn, lane, r);
             if (n < g.k) {
-              const float v = C::SPLIT ? ldexpf(acc[fm][fn][r], ex) : acc[fm][fn][r];
+              const float v = C::PARTS == 3 ? acc[fm][fn][r] * kTgUnlift : acc[fm][fn][r];
               out[(size_t)m * g.k + n] = v;
               bad |= not_finite(v);
             }
           }
         }
-      if (C::SPLIT && bad) again(t, wm, wn, lane);
+      if (C::PARTS == 3 && bad) again(t, wm, wn, lane);
     } else {
       // a lane holds four consecutive columns of one row
       const int N = DIR == GR_FWD ? g.n : g.k;
@@ -343,12 +350,10 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void grouped_kernel(
 // again).  HBM bound.
 constexpr int kRowChunks = 4;  // chunks per lane held in registers: rows up to 2048
 
-// Exponent that brings a largest magnitude to [2^13, 2^14); `none` if all is zero.
-__device__ __forceinline__ int split_exponent(float most, int none = 0) {
-  return most > 0.f ? 13 - ilogbf(most) : none;
+// Exponent that brings a largest magnitude to [2^13, 2^14); 0 if all is zero.
+__device__ __forceinline__ int split_exponent(float most) {
+  return most > 0.f ? 13 - ilogbf(most) : 0;
 }
-// The weight gradient's mark of a dy row that is all zero.
-constexpr int kNoRow = -(1 << 20);
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int k = 32; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor(v, k));
@@ -399,7 +404,7 @@ struct SplitRows {
   int32_t* ex;      // per row
   long long rows;
   uint32_t pitch;
-  int width, none;  // none: the exponent of an all-zero row
+  int width;
 };
 __host__ __device__ inline unsigned blocks_of(long long rows) { return (unsigned)((rows + 3) / 4); }
 __device__ __forceinline__ void split_rows(const SplitRows& a, unsigned block) {
@@ -407,12 +412,8 @@ __device__ __forceinline__ void split_rows(const SplitRows& a, unsigned block) {
   const int lane = threadIdx.x & 63;
   if (r >= a.rows) return;
   const float* src = a.src + r * a.width;
-  int mark = 0;
-  split_row(src, a.width, a.dst + r * a.pitch, lane, [&](float m) {
-    mark = split_exponent(m, a.none);
-    return m > 0.f ? mark : 0;
-  });
-  if (lane == 0) a.ex[r] = mark;
+  const int ex = split_row(src, a.width, a.dst + r * a.pitch, lane, [](float m) { return split_exponent(m); });
+  if (lane == 0) a.ex[r] = ex;
 }
 // The forward's operands, in one launch.
 __global__ __launch_bounds__(256) void split_two_kernel(SplitRows a, SplitRows b) {
@@ -461,78 +462,54 @@ __device__ __forceinline__ void split_expert_rows(const SplitExperts& a, unsigne
   split_row(a.w + r * a.k, a.k, a.dst + r * a.pitch, lane, [&](float) { return x; });
 }
 
-// x for the weight gradient: row r is scaled by 2^(C - a_r), a_r the exponent of
-// dy's row r, so that every product of row r carries 2^C.  C brings the largest
-// of all rows into range: partial maxima of ilogb(x row) - a_r over the rows of
-// the groups (rows outside them are not read), then C = 13 - the largest.  Rows
-// whose dy is zero contribute nothing and are written as zeros.
-constexpr int kRowParts = 256;
-struct SplitPairs {
-  const float* x;
-  const int32_t* offsets;
-  const int32_t* ea;  // a_r
-  int32_t* part;      // [kRowParts]
-  uint8_t* dst;
-  int32_t* ex;        // C
-  uint32_t pitch;
-  int width, E, M;
-};
-__device__ __forceinline__ void group_span(const SplitPairs& a, int lane, int& first, int& last) {
-  int hi = 0;
-  for (int e = lane; e <= a.E; e += 64) hi = max(hi, min(max(a.offsets[e], 0), a.M));
-#pragma unroll
-  for (int k = 32; k > 0; k >>= 1) hi = max(hi, __shfl_xor(hi, k));
-  first = min(max(a.offsets[0], 0), a.M);
-  last = max(hi, first);
-}
-__device__ __forceinline__ void pair_max(const SplitPairs& a, unsigned block) {
-  __shared__ int s[4];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int first, last, most = kNoRow;
-  group_span(a, lane, first, last);
-  for (long long r = first + block * 4 + w; r < last; r += 4 * kRowParts) {
-    float m = 0.f;
-    for (int j = 8 * lane; j < a.width; j += 512) {
-      float g[8];
-      load_chunk<ElemF32>(a.x + r * a.width, j, a.width, g);
-      m = fmaxf(m, chunk_max(g));
-    }
-    m = wave_max(m);
-    if (m > 0.f && a.ea[r] != kNoRow) most = max(most, ilogbf(m) - a.ea[r]);
-  }
-  if (lane == 0) s[w] = most;
-  __syncthreads();
-  if (threadIdx.x == 0) a.part[block] = max(max(s[0], s[1]), max(s[2], s[3]));
-}
-__global__ __launch_bounds__(256) void split_pair_kernel(SplitPairs a) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int first, last, most = kNoRow;
-  for (int i = lane; i < kRowParts; i += 64) most = max(most, a.part[i]);
-#pragma unroll
-  for (int k = 32; k > 0; k >>= 1) most = max(most, __shfl_xor(most, k));
-  const int C = most == kNoRow ? 0 : 13 - most;
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.ex[0] = C;
-  group_span(a, lane, first, last);
-  const long long r = first + (long long)blockIdx.x * 4 + w;
-  if (r >= last) return;
-  if (a.ea[r] != kNoRow) {
-    split_row(a.x + r * a.width, a.width, a.dst + r * a.pitch, lane, [&](float) { return C - a.ea[r]; });
-  } else {
-    for (uint32_t b = 4 * lane; b < a.pitch; b += 256) *(uint32_t*)(a.dst + r * a.pitch + b) = 0;
-  }
-}
-
-// The backward's operands in two launches before the last one's: what needs nothing
-// (dy's rows, w's maxima), then what needs those (w's rows, the pairs' maxima).
-__global__ __launch_bounds__(256) void backward_first_kernel(SplitRows dy, SplitExperts w) {
+// dx's operands in two launches: dy's rows and w's maxima, then w's rows.
+__global__ __launch_bounds__(256) void dx_first_kernel(SplitRows dy, SplitExperts w) {
   const unsigned n = blocks_of(dy.rows);
   if (blockIdx.x < n) split_rows(dy, blockIdx.x);
   else expert_max(w, blockIdx.x - n);
 }
-__global__ __launch_bounds__(256) void backward_second_kernel(SplitExperts w, SplitPairs x) {
-  const unsigned n = blocks_of(w.rows);
-  if (blockIdx.x < n) split_expert_rows(w, blockIdx.x);
-  else pair_max(x, blockIdx.x - n);
+__global__ __launch_bounds__(256) void dx_second_kernel(SplitExperts w) {
+  split_expert_rows(w, blockIdx.x);
+}
+
+// float32 rows as three bfloat16 each (tile_gemm.h), times kTgLift, zeros behind the last
+// element; a lane takes 8 elements, 2^shift lanes a row.  HBM bound: 4 bytes read, 6 written.
+struct PartRows {
+  const float* src;
+  uint8_t* dst;
+  long long rows;
+  uint32_t plane;    // bytes of a row's part, a multiple of 16; three of them a row
+  int width, shift;
+  unsigned blocks;
+};
+PartRows part_rows(const void* src, uint8_t* dst, long long rows, int width, uint32_t plane) {
+  PartRows a{(const float*)src, dst, rows, plane, width, 0, 0};
+  while (a.shift < 6 && (16u << a.shift) < plane) ++a.shift;
+  const long long per = 4 << (6 - a.shift);  // rows per block
+  a.blocks = (unsigned)((rows + per - 1) / per);
+  return a;
+}
+__device__ __forceinline__ void part_rows(const PartRows& a, unsigned block) {
+  const int lane = threadIdx.x & 63;
+  const long long r = (((long long)block * 4 + (threadIdx.x >> 6)) << (6 - a.shift)) + (lane >> a.shift);
+  if (r >= a.rows) return;
+  const float* src = a.src + r * a.width;
+  uint8_t* dst = a.dst + 3 * r * a.plane;
+  for (int j = 8 * (lane & ((1 << a.shift) - 1)); j < (int)(a.plane / 2); j += 8 << a.shift) {
+    float f[8];
+    load_chunk<ElemF32>(src, j, a.width, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= kTgLift;
+    const Split3 s = split_three(f);
+    uint8_t* to = dst + 2 * (size_t)j;
+    *(u32x4*)to = s.hi;
+    *(u32x4*)(to + a.plane) = s.mid;
+    *(u32x4*)(to + 2 * (size_t)a.plane) = s.lo;
+  }
+}
+__global__ __launch_bounds__(256) void parts_kernel(PartRows a, PartRows b) {
+  if (blockIdx.x < a.blocks) part_rows(a, blockIdx.x);
+  else part_rows(b, blockIdx.x - a.blocks);
 }
 
 // bfloat16 rows whose length does not suit the loads, copied into rows of whole
@@ -557,11 +534,8 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // With few rows the product is bound by reading w once (64 groups of 6 rows, w 2048 x 1408:
 // 738 MB), and writing w's split form and reading it back would treble that.  Here w's
 // rows go from memory to registers and are split there, into three bfloat16:
-//   v = hi + mid + lo exactly (3 x 8 bits, each the rounded rest of the one before), and
-//   hi hi' + hi mid' + mid hi' + mid mid' + hi lo' + lo hi' leaves out at most
-//   2 mid lo' <= 2^-23 |v v'|,
-// which, having float32's exponents, need no scale of w's rows (whose maximum would take a
-// read of its own).  x is split likewise beforehand (it is small), its rows' largest
+// (the triple precision of tile_gemm.h), which need no scale of w's rows (whose maximum
+// would take a read of its own).  x is split likewise beforehand (it is small), its rows' largest
 // value scaled to 2^-12, so that sums of products with the largest w stay finite.
 //
 // A block takes 64 columns of y and up to 32 rows of a group; its four wavefronts deal the
@@ -590,24 +564,6 @@ struct FewProduct {
 // Bytes of x's split row.
 __host__ __device__ inline long long few_pitch(int k) { return (long long)((k + 31) / 32) * 192; }
 
-struct Split3 {
-  u32x4 hi, mid, lo;
-};
-__device__ __forceinline__ Split3 split_three(const float (&v)[8]) {
-  Split3 s;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = v[2 * i], b = v[2 * i + 1];
-    s.hi[i] = pack_bf16x2(a, b);
-    a -= __uint_as_float(s.hi[i] << 16);
-    b -= __uint_as_float(s.hi[i] & 0xffff0000u);
-    s.mid[i] = pack_bf16x2(a, b);
-    a -= __uint_as_float(s.mid[i] << 16);
-    b -= __uint_as_float(s.mid[i] & 0xffff0000u);
-    s.lo[i] = pack_bf16x2(a, b);
-  }
-  return s;
-}
 // x's rows (of a multiple of 4 values), one wavefront each.
 __global__ __launch_bounds__(256) void split_three_kernel(const float* __restrict__ x, int rows, int k,
                                                           u32x4* __restrict__ out,
@@ -843,6 +799,7 @@ struct Carve {
 };
 
 uint32_t pad_pitch(int n) { return (uint32_t)((n + 63) / 64 * 128); }
+uint32_t part_plane(int n) { return (uint32_t)((n + 7) / 8 * 16); }
 
 // About how many tiles of b x b a product has: the offsets are on the device, so half a
 // tile's rows are taken as lost per group, and every row as in a group.
@@ -865,7 +822,7 @@ hipError_t run_product(const GroupedProduct& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int DIR, bool SPLIT>
+template <int DIR, int PARTS>
 hipError_t pick_product(const GroupedArgs& a, const GroupedProduct& p, hipStream_t st) {
   constexpr bool AC = DIR == GR_DW, BC = DIR != GR_FWD, SW = DIR != GR_DW;
   const int cus = device_cu_count();
@@ -875,10 +832,10 @@ hipError_t pick_product(const GroupedArgs& a, const GroupedProduct& p, hipStream
   // that (64 groups of 64 rows, y 1408 x 2048 bfloat16: 118 us, of 128 rows 107 us; 64 of
   // 256: 138 and 147 us).
   if (4 * tiles_of(DIR, a, 256) >= 3 * cus && (DIR == GR_DW || a.M > 128LL * a.E))
-    return run_product<TgConfig<TgBig, AC, BC, SPLIT, SW>, DIR>(p, st);
+    return run_product<TgConfig<TgBig, AC, BC, PARTS, SW>, DIR>(p, st);
   if (4 * tiles_of(DIR, a, 128) >= 3 * cus)
-    return run_product<TgConfig<TgMid, AC, BC, SPLIT, SW>, DIR>(p, st);
-  return run_product<TgConfig<TgSmall, AC, BC, SPLIT, SW>, DIR>(p, st);
+    return run_product<TgConfig<TgMid, AC, BC, PARTS, SW>, DIR>(p, st);
+  return run_product<TgConfig<TgSmall, AC, BC, PARTS, SW>, DIR>(p, st);
 }
 
 unsigned row_blocks(long long rows) { return blocks_of(rows); }
@@ -886,10 +843,10 @@ unsigned row_blocks(long long rows) { return blocks_of(rows); }
 // The workspace's regions: which are needed, and where they lie.
 struct GroupedPlan {
   uint8_t *x = nullptr, *w = nullptr, *dy = nullptr;        // prepared operands
+  uint8_t* dyp = nullptr;                                   // dy in three parts
   uint8_t* few = nullptr;                                   // dy, few rows per group
   int32_t* efew = nullptr;
   int32_t *ex = nullptr, *ew = nullptr, *ey = nullptr;      // exponents
-  int32_t* parts = nullptr;
   float* wmax = nullptr;
   size_t bytes = 0;
 };
@@ -920,18 +877,17 @@ GroupedPlan plan_backward(int dtype, int M, int E, int n, int k, bool dx, bool d
     p.efew = (int32_t*)c.take((size_t)M * 4);
     dx = false;
   }
-  if (dtype == 0 && (dx || dw)) {
-    p.dy = c.take((size_t)M * split_pitch(n));
-    p.ey = (int32_t*)c.take((size_t)M * 4);
+  if (dtype == 0) {
     if (dx) {
+      p.dy = c.take((size_t)M * split_pitch(n));
+      p.ey = (int32_t*)c.take((size_t)M * 4);
       p.w = c.take((size_t)E * n * split_pitch(k));
       p.ew = (int32_t*)c.take((size_t)E * 4);
       p.wmax = (float*)c.take((size_t)E * kMaxChunks * 4);
     }
     if (dw) {
-      p.x = c.take((size_t)M * split_pitch(k));
-      p.ex = (int32_t*)c.take(4);
-      p.parts = (int32_t*)c.take(kRowParts * 4);
+      p.dyp = c.take(3 * (size_t)M * part_plane(n));
+      p.x = c.take(3 * (size_t)M * part_plane(k));
     }
   } else if (dtype != 0) {
     if (n % (dx ? 64 : 8) != 0) p.dy = c.take((size_t)M * pad_pitch(n));
@@ -976,8 +932,8 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
   }
   if (dtype == 0) {
     p.pitch_a = p.pitch_b = (uint32_t)split_pitch(a.k);
-    const SplitRows rx{(const float*)a.x, w.x, w.ex, a.M, p.pitch_a, a.k, 0};
-    const SplitRows rw{(const float*)a.w, w.w, w.ew, wr, p.pitch_b, a.k, 0};
+    const SplitRows rx{(const float*)a.x, w.x, w.ex, a.M, p.pitch_a, a.k};
+    const SplitRows rw{(const float*)a.w, w.w, w.ew, wr, p.pitch_b, a.k};
     split_two_kernel<<<row_blocks(a.M) + row_blocks(wr), 256, 0, st>>>(rx, rw);
     p.A = w.x;
     p.B = w.w;
@@ -985,7 +941,7 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
     p.eb = w.ew;
     p.ra = (const float*)a.x;
     p.rb = (const float*)a.w;
-    return pick_product<GR_FWD, true>(a, p, st);
+    return pick_product<GR_FWD, 2>(a, p, st);
   }
   if (w.x != nullptr) {
     p.pitch_a = p.pitch_b = pad_pitch(a.k);
@@ -994,7 +950,7 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
     p.A = w.x;
     p.B = w.w;
   }
-  return pick_product<GR_FWD, false>(a, p, st);
+  return pick_product<GR_FWD, 1>(a, p, st);
 }
 
 hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hipStream_t st) {
@@ -1014,20 +970,21 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   const uint8_t *x = (const uint8_t*)a.x, *wt = (const uint8_t*)a.w, *dy = (const uint8_t*)a.dy;
   uint32_t px = a.k * 2, pw = a.k * 2, py = a.n * 2;
   if (dtype == 0) {
-    px = pw = (uint32_t)split_pitch(a.k);
-    py = (uint32_t)split_pitch(a.n);
-    const SplitRows ry{(const float*)a.dy, w.dy, w.ey, a.M, py, a.n, kNoRow};
-    SplitExperts we{};
-    if (dx) we = {(const float*)a.w, w.wmax, w.w, w.ew, wr, pw, a.E, a.n, a.k};
-    const SplitPairs xp{(const float*)a.x, a.offsets, w.ey, w.parts, w.x, w.ex, px, a.k, a.E, a.M};
-    const unsigned b1 = row_blocks(a.M) + (dx ? a.E * kMaxChunks : 0);
-    const unsigned b2 = (dx ? row_blocks(wr) : 0) + (dw ? kRowParts : 0);
-    if (b1 > 0) backward_first_kernel<<<b1, 256, 0, st>>>(ry, we);
-    backward_second_kernel<<<b2, 256, 0, st>>>(we, xp);
-    if (dw) split_pair_kernel<<<std::max(1u, row_blocks(a.M)), 256, 0, st>>>(xp);
+    if (dx && a.M > 0) {
+      pw = (uint32_t)split_pitch(a.k);
+      py = (uint32_t)split_pitch(a.n);
+      const SplitRows ry{(const float*)a.dy, w.dy, w.ey, a.M, py, a.n};
+      const SplitExperts we{(const float*)a.w, w.wmax, w.w, w.ew, wr, pw, a.E, a.n, a.k};
+      dx_first_kernel<<<row_blocks(a.M) + a.E * kMaxChunks, 256, 0, st>>>(ry, we);
+      dx_second_kernel<<<row_blocks(wr), 256, 0, st>>>(we);
+    }
+    if (dw && a.M > 0) {
+      const PartRows ry = part_rows(a.dy, w.dyp, a.M, a.n, part_plane(a.n));
+      const PartRows rx = part_rows(a.x, w.x, a.M, a.k, part_plane(a.k));
+      parts_kernel<<<ry.blocks + rx.blocks, 256, 0, st>>>(ry, rx);
+    }
     dy = w.dy;
     wt = w.w;
-    x = w.x;
   } else {
     if (w.dy != nullptr && a.M > 0) {
       py = pad_pitch(a.n);
@@ -1047,26 +1004,38 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  p.A = dy;
-  p.pitch_a = py;
-  p.ea = w.ey;
-  p.ra = (const float*)a.dy;
   if (dx && a.M > 0) {
+    p.A = dy;
+    p.pitch_a = py;
+    p.ea = w.ey;
     p.B = wt;
-    p.rb = (const float*)a.w;
     p.pitch_b = pw;
     p.eb = w.ew;
+    p.ra = (const float*)a.dy;
+    p.rb = (const float*)a.w;
     p.out = a.dx;
-    e = dtype == 0 ? pick_product<GR_DX, true>(a, p, st) : pick_product<GR_DX, false>(a, p, st);
+    e = dtype == 0 ? pick_product<GR_DX, 2>(a, p, st) : pick_product<GR_DX, 1>(a, p, st);
     if (e != hipSuccess) return e;
   }
   if (dw) {
-    p.B = x;
-    p.rb = (const float*)a.x;
-    p.pitch_b = px;
-    p.eb = w.ex;
     p.out = a.dw;
-    e = dtype == 0 ? pick_product<GR_DW, true>(a, p, st) : pick_product<GR_DW, false>(a, p, st);
+    if (dtype == 0) {
+      p.A = w.dyp;
+      p.B = w.x;
+      p.plane_a = part_plane(a.n);
+      p.plane_b = part_plane(a.k);
+      p.pitch_a = 3 * p.plane_a;
+      p.pitch_b = 3 * p.plane_b;
+      p.ra = (const float*)a.dy;
+      p.rb = (const float*)a.x;
+      e = pick_product<GR_DW, 3>(a, p, st);
+    } else {
+      p.A = dy;
+      p.pitch_a = py;
+      p.B = x;
+      p.pitch_b = px;
+      e = pick_product<GR_DW, 1>(a, p, st);
+    }
   }
   return e;
 }

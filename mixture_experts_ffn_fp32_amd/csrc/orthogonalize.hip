@@ -368,9 +368,9 @@ hipError_t pick_ns(const NsProduct& p, hipStream_t st) {
     return (KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2) * p.count;
   };
   const int cus = device_cu_count();
-  if (2 * tiles(256) > cus) return run_ns<TgConfig<TgBig, AC, BC, true, SW>, KIND>(p, st);
-  if (2 * tiles(128) > cus) return run_ns<TgConfig<TgMid, AC, BC, true, SW>, KIND>(p, st);
-  return run_ns<TgConfig<TgSmall, AC, BC, true, SW>, KIND>(p, st);
+  if (2 * tiles(256) > cus) return run_ns<TgConfig<TgBig, AC, BC, 2, SW>, KIND>(p, st);
+  if (2 * tiles(128) > cus) return run_ns<TgConfig<TgMid, AC, BC, 2, SW>, KIND>(p, st);
+  return run_ns<TgConfig<TgSmall, AC, BC, 2, SW>, KIND>(p, st);
 }
 
 }  // namespace

@@ -9,7 +9,7 @@
 //   column layout  its rows run along the contraction (a transposed operand in
 //                  its stored order); a k-step is 64 rows of BM columns, and
 //                  MFMA fragments come from transposing LDS reads.
-// and in one of two precisions:
+// and in one of three precisions (1, 2 or 3 parts a value):
 //   single  bfloat16, 64 contraction indices per k-step.
 //   split   a float32 value v as two float16, hi = f16(v), lo = f16(v - hi):
 //           22 bits of v survive (|v - hi - lo| <= 2^-24 |v| while lo is a
@@ -22,6 +22,16 @@
 //           the 32 lo of the same indices; a k-step is one unit of each row
 //           (32 contraction indices), so both precisions load alike, and the
 //           two halves of a unit are read from LDS once for three products.
+//   triple  a float32 value v as three bfloat16, each the rounded rest of the ones before:
+//           v = hi + mid + lo exactly (8 significant bits each; |mid| <= 2^-8 |v|, |lo| <=
+//           2^-16 |v|), and hi hi' + hi mid' + mid hi' + mid mid' + hi lo' + lo hi' leaves
+//           out mid lo' + lo mid' + lo lo' <= 2^-22.99 |v v'|.  Having float32's exponents the
+//           parts need no scale, so a product is as exact as a float32 one whatever its
+//           neighbours along the contraction or in other rows are; that costs six bfloat16
+//           products for the three of `split`.  Values are stored times 2^24 (kTgLift), which
+//           keeps the parts of the smallest ones normal numbers.  The parts of a matrix are
+//           planes in its rows, and a block of 64 contraction indices takes six k-steps of the
+//           single kind, one per product (tg_offset).
 #pragma once
 
 #include "lds_dma.h"
@@ -73,9 +83,10 @@ struct TgSmall {
 using TgBig = TgShape<4, 2, 2, 4, 2, 1, false>;
 using TgMid = TgShape<2, 2, 2, 2, 2, 2, true>;
 
-template <class Shape, bool ACOL_, bool BCOL_, bool SPLIT_, bool SWAP_>
+template <class Shape, bool ACOL_, bool BCOL_, int PARTS_, bool SWAP_>
 struct TgConfig : Shape {
-  static constexpr bool ACOL = ACOL_, BCOL = BCOL_, SPLIT = SPLIT_, SWAP = SWAP_;
+  static constexpr int PARTS = PARTS_;
+  static constexpr bool ACOL = ACOL_, BCOL = BCOL_, SPLIT = PARTS == 2, SWAP = SWAP_;
   static constexpr int KS = SPLIT ? 32 : 64;          // contraction indices per k-step
   static constexpr bool SMALL = Shape::BM == TgSmall::BM;
   static constexpr int LDS = Shape::S * Shape::SLOT * (SMALL ? TgSmall::WAVES : 1);
@@ -90,7 +101,18 @@ struct TgOperand {
   const uint8_t* p;
   uint32_t pitch;
   int rows, width;
+  uint32_t plane;  // triple: bytes from one part of a row to the next
 };
+
+// Triple: which part of A and of B the j-th k-step of a block takes, two bits each (hi 0,
+// mid 1, lo 2); neighbours share an operand.
+constexpr int kTgProducts = 6;
+constexpr int tg_parts(int a, int b, int c, int d, int e, int f) {
+  return a | b << 2 | c << 4 | d << 6 | e << 8 | f << 10;
+}
+constexpr int kTgPartsA = tg_parts(0, 0, 0, 1, 1, 2), kTgPartsB = tg_parts(2, 1, 0, 0, 1, 0);
+// The power of two that stored values carry, and what takes it back out of a product.
+constexpr float kTgLift = 0x1p24f, kTgUnlift = 0x1p-48f;
 
 // Loading state of one wavefront for a tile.
 struct TgLoad {
@@ -98,7 +120,18 @@ struct TgLoad {
   uint32_t step;   // bytes from one k-step to the next
   int rows;        // column layout: contraction rows; row layout: -(k-steps)
   uint32_t pitch;
+  uint32_t plane;  // triple
+  int parts;       // triple: kTgPartsA or kTgPartsB
 };
+// Bytes from its base to k-step s.
+template <class C>
+__device__ __forceinline__ size_t tg_offset(const TgLoad& l, int s) {
+  if constexpr (C::PARTS == 3) {
+    const int b = s / kTgProducts, part = (l.parts >> (2 * (s - kTgProducts * b))) & 3;
+    return (size_t)b * l.step + (size_t)part * l.plane;
+  }
+  return (size_t)s * l.step;
+}
 
 // In a column-layout tile of W columns the 16-byte chunk c of contraction row k lies at
 // position c ^ 4 j(k): a transposing read of 32 lanes touches 64 bytes of each of four
@@ -109,11 +142,13 @@ __device__ __forceinline__ int tg_rotation(int k) {
   return W >= 128 ? k & 3 : (k >> 1) & 1;
 }
 template <class C, bool COL>
-__device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int t0, int steps, int w,
-                                                  int lane, uint32_t (&off)[C::NI]) {
+__device__ __forceinline__ TgLoad tg_prepare_side(const TgOperand& o, int parts, int t0, int steps,
+                                                  int w, int lane, uint32_t (&off)[C::NI]) {
   constexpr int W = C::BM;
   TgLoad l;
   l.pitch = uni((int)o.pitch);
+  l.plane = C::PARTS == 3 ? uni((int)o.plane) : 0;
+  l.parts = parts;
   if constexpr (COL) {
     constexpr int RPI = 1024 / (2 * W);  // contraction rows per load instruction
     constexpr int CPR = W / 8;           // chunks per row
@@ -154,14 +189,15 @@ __device__ __forceinline__ TgLoad tg_prepare(const TgOperand& A, const TgOperand
                                              int steps, int wave, int lane,
                                              uint32_t (&off)[C::NI]) {
   constexpr int H = C::WM * C::WN / 2;
-  if (wave < H) return tg_prepare_side<C, C::ACOL>(A, m0, steps, wave, lane, off);
-  return tg_prepare_side<C, C::BCOL>(B, n0, steps, wave - H, lane, off);
+  if (wave < H) return tg_prepare_side<C, C::ACOL>(A, kTgPartsA, m0, steps, wave, lane, off);
+  return tg_prepare_side<C, C::BCOL>(B, kTgPartsB, n0, steps, wave - H, lane, off);
 }
 
 // Bytes from the k-step's base that its loads may touch; later ones read zeros.
 template <class C>
 __device__ __forceinline__ int tg_range(const TgLoad& l, int s) {
   if (l.rows < 0) return s < -l.rows ? 0x7fffffff : 0;
+  if constexpr (C::PARTS == 3) s /= kTgProducts;
   return min(max(l.rows - C::KS * s, 0), C::KS) * (int)l.pitch;
 }
 
@@ -510,7 +546,7 @@ __device__ __forceinline__ void tg_tile(const P& p, int steps, int& ph, int wave
   const int all = tg_steps<C>(steps);
   auto issue = [&](auto step) {
     const int after = ph + 1 < C::S ? ph + 1 : 0;
-    const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
+    const uint8_t* db = uni(ld.base + tg_offset<C>(ld, c.s));
     const int nrec = uni(c.steps > 0 ? tg_range<C>(ld, c.s) : 0);
     step(lds + ph * C::SLOT, lds + after * C::SLOT, db, nrec);
     c.s = uni(c.s + 1);
@@ -566,7 +602,7 @@ __device__ __forceinline__ void tg_run(const P& p, int tiles, int32_t* counters,
 #pragma unroll
   for (int k = 0; k < C::S; ++k) {
     uint8_t* w = lds + k * C::SLOT + wave * C::NI * 1024;
-    const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
+    const uint8_t* db = uni(ld.base + tg_offset<C>(ld, c.s));
     const int nrec = uni(tg_range<C>(ld, c.s));
 #pragma unroll
     for (int i = 0; i < C::NI; ++i) dma16(db, off[i], w + i * 1024, nrec);
@@ -638,8 +674,8 @@ __device__ __forceinline__ void tg_small_loop(const TgLoad& la, const TgLoad& lb
   auto issue = [&](int i, uint8_t* slot) {
     const int s = wave + W * i;
     const int na = uni(i < mine ? tg_range<C>(la, s) : 0), nb = uni(i < mine ? tg_range<C>(lb, s) : 0);
-    const uint8_t* da = uni(la.base + (size_t)s * la.step);
-    const uint8_t* db = uni(lb.base + (size_t)s * lb.step);
+    const uint8_t* da = uni(la.base + tg_offset<C>(la, s));
+    const uint8_t* db = uni(lb.base + tg_offset<C>(lb, s));
 #pragma unroll
     for (int k = 0; k < NI; ++k) dma16(da, oa[k], slot + k * 1024, na);
 #pragma unroll
@@ -692,8 +728,8 @@ __device__ __forceinline__ void tg_run_small(const P& p, int tiles, uint8_t* __r
     const typename P::Tile t = p.tile(L, hint);
     hint = t.hint;
     uint32_t oa[NI], ob[NI];
-    const TgLoad la = tg_prepare_side<C, C::ACOL>(t.A, t.m0, t.steps, 0, lane, oa);
-    const TgLoad lb = tg_prepare_side<C, C::BCOL>(t.B, t.n0, t.steps, 0, lane, ob);
+    const TgLoad la = tg_prepare_side<C, C::ACOL>(t.A, kTgPartsA, t.m0, t.steps, 0, lane, oa);
+    const TgLoad lb = tg_prepare_side<C, C::BCOL>(t.B, kTgPartsB, t.n0, t.steps, 0, lane, ob);
     f32x16 acc[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -728,6 +764,26 @@ __device__ __forceinline__ void tg_run_small(const P& p, int tiles, uint8_t* __r
     __syncthreads();  // the rings take the next tile's loads
     p.store(t, wave / C::WN, wave % C::WN, lane, sum);
   }
+}
+
+// Eight values as three bfloat16 each.
+struct Split3 {
+  u32x4 hi, mid, lo;
+};
+__device__ __forceinline__ Split3 split_three(const float (&v)[8]) {
+  Split3 s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
+    s.hi[i] = pack_bf16x2(a, b);
+    a -= __uint_as_float(s.hi[i] << 16);
+    b -= __uint_as_float(s.hi[i] & 0xffff0000u);
+    s.mid[i] = pack_bf16x2(a, b);
+    a -= __uint_as_float(s.mid[i] << 16);
+    b -= __uint_as_float(s.mid[i] & 0xffff0000u);
+    s.lo[i] = pack_bf16x2(a, b);
+  }
+  return s;
 }
 
 // A value as two float16.

@@ -97,8 +97,8 @@ SHAPES = {
     "few y": ([30, 64, 0, 9], 48, 72, True, False),
     "odd width": ([30, 64, 0, 9], 50, 203, False, False),
     "many rows": ([300, 150, 0, 9], 72, 200, False, False),
-    "tiles of 128": ([600, 300, 0, 700, 650], 640, 520, False, False),
-    "tiles of 256": ([700, 530, 0, 1100, 900], 2060, 1544, False, False),
+    "tiles of 128": ([900, 830, 0, 1100, 900], 1000, 780, False, False),
+    "tiles of 256": ([1700, 1530, 0, 1100, 900], 2060, 2060, False, False),
 }
 
 
@@ -128,3 +128,57 @@ def test_infinities_and_nan_come_out_as_in_float32(name):
     dy[a + 3, 1] = np.inf
     dy[a + 4] = np.nan
     _check_all(dev(x), dev(w), off, dev(dy), name, floor=2.0 ** -37)
+
+
+# ---------------------------------------------------------------- operands of uneven scale
+def _check_dw(x, w, off, dy, label):
+    say(label)
+    _, dw = mx.grouped_matmul_backward(x, w, off, dy, need_dx=False)
+    both = mx.grouped_matmul_backward(x, w, off, dy)[1]
+    torch.cuda.synchronize()
+    assert torch.equal(_bits(dw), _bits(both))
+    X, DY = host(x), host(dy)
+    for e, (a, b) in enumerate(ref.group_rows(off.cpu().numpy(), len(X))):
+        t = _tol(np.abs(DY[a:b]).T, np.abs(X[a:b]).T, b - a)
+        _same(dw[e], DY[a:b].T @ X[a:b], t, f"{label} dw {e}")
+
+
+@pytest.mark.parametrize("name", SHAPES)
+def test_weight_gradients_of_experts_rows_and_channels_of_any_scale(name):
+    x, w, off, dy, r = _normal(name, 3)
+    at = off.cpu().numpy()
+    rows, n, k = len(x), dy.shape[1], x.shape[1]
+    w = dev(w)
+    # experts whose gradients differ by 2^-14 .. 2^-60, and one far above the others
+    scaled = dy.copy()
+    for e, p in zip(range(len(at) - 1), (0, -30, 0, -60, 20) if len(at) > 5 else (0, -30, 0, -14)):
+        scaled[at[e]:at[e + 1]] *= 2.0 ** p
+    _check_dw(dev(x), w, off, dev(scaled), f"{name}: experts")
+    # channels of dy and of x
+    sy, sx = 2.0 ** np.floor(r.uniform(-40, 20, n)), 2.0 ** np.floor(r.uniform(-40, 20, k))
+    _check_dw(dev(x * sx), w, off, dev(dy * sy), f"{name}: channels")
+    # rows whose dy and x are each other's opposite, and one row above all others
+    s = 2.0 ** np.floor(r.uniform(-60, 60, (rows, 1)))
+    _check_dw(dev(x / s), w, off, dev(dy * s), f"{name}: balanced rows")
+    loud = dy.copy()
+    loud[at[0] + 3] *= 2.0 ** 40
+    _check_dw(dev(x), w, off, dev(loud), f"{name}: one row")
+    # the smallest values: subnormal ones on one side
+    _check_dw(dev(x * 2.0 ** 100), w, off, dev(dy * 2.0 ** -140), f"{name}: small dy")
+    _check_dw(dev(x * 2.0 ** -140), w, off, dev(dy * 2.0 ** 100), f"{name}: small x")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", SHAPES)
+def test_weight_gradients_show_bad_rows_under_a_zero_gradient(name, dtype):
+    """0 x NaN and 0 x infinity are NaN: a row of x that broke shows even where dy is zero."""
+    x, w, off, dy, _ = _normal(name, 4)
+    x[2 + 3, 5], x[2 + 4, 6] = np.nan, np.inf
+    dy[2 + 3:2 + 5] = 0.0
+    x, w, dy = dev(x, dtype), dev(w, dtype), dev(dy, dtype)
+    say(f"{name} {dtype}: zero gradient")
+    dw = mx.grouped_matmul_backward(x, w, off, dy, need_dx=False)[1]
+    torch.cuda.synchronize()
+    want = torch.zeros_like(dw, dtype=torch.bool)
+    want[0, :, 5:7] = True
+    assert (torch.isnan(dw) == want).all() and torch.isfinite(dw[~want]).all()
