@@ -269,11 +269,11 @@ moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* 
  * one below its predecessor counts as equal to it.
  * bfloat16: exact products, float32 sums, one rounding.  float32: products of
  * two-float16 splits (float32 accuracy; each row of x and w is scaled on its
- * own, so rows may differ by any factor), or, with few rows per group, of
- * three-bfloat16 splits of the same accuracy.  A float32 result that is not finite
- * is summed again in float64, so it is infinite or NaN only where its operands make
- * it so or it leaves float32's range itself.  An infinity or NaN reaches the results
- * of its own products only.
+ * own, so rows may differ by any factor; a value is held to 2^-38 of its row's
+ * largest), or, with few rows per group, of three-bfloat16 splits (the same whatever
+ * the scales are).  A float32 result that is not finite is summed again in float64, so
+ * it is infinite or NaN only where its operands make it so or it leaves float32's
+ * range itself.  An infinity or NaN reaches the results of its own products only.
  * Limits: 1 <= E <= 1024; n, k <= 2^20. */
 moe_status_t moe_grouped_matmul_workspace_size(int M, int E, int n, int k, int dtype,
                                                size_t* bytes);

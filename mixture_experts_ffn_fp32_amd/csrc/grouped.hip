@@ -535,8 +535,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // 738 MB), and writing w's split form and reading it back would treble that.  Here w's
 // rows go from memory to registers and are split there, into three bfloat16:
 // (the triple precision of tile_gemm.h), which need no scale of w's rows (whose maximum
-// would take a read of its own).  x is split likewise beforehand (it is small), its rows' largest
-// value scaled to 2^-12, so that sums of products with the largest w stay finite.
+// would take a read of its own).  x is split likewise beforehand (it is small).
 //
 // A block takes 64 columns of y and up to 32 rows of a group; its four wavefronts deal the
 // k-steps of 32 indices among themselves, each with four fragments of 16 w rows against one
@@ -554,7 +553,6 @@ constexpr int kFewRows = 32, kFewCols = 64;
 struct FewProduct {
   const float* w;
   const u32x4* x;          // (dx: dy) [k-step][quarter][hi, mid, lo][M]: a lane's eight values of a row
-  const int32_t* ex;       // x's exponents
   const int32_t* offsets;
   float* out;
   GroupDims g;
@@ -566,27 +564,19 @@ __host__ __device__ inline long long few_pitch(int k) { return (long long)((k + 
 
 // x's rows (of a multiple of 4 values), one wavefront each.
 __global__ __launch_bounds__(256) void split_three_kernel(const float* __restrict__ x, int rows, int k,
-                                                          u32x4* __restrict__ out,
-                                                          int32_t* __restrict__ ex) {
+                                                          u32x4* __restrict__ out) {
   const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (r >= rows) return;
   const float* src = x + r * k;
-  float m = 0.f, f[8];
-  for (int j = 8 * lane; j < k; j += 512) {
-    load_chunk<ElemF32>(src, j, k, f);
-    m = fmaxf(m, chunk_max(f));
-  }
-  m = wave_max(m);
-  const int e = m > 0.f ? -12 - ilogbf(m) : 0;
-  if (lane == 0) ex[r] = e;
+  float f[8];
   for (int c = lane; c < (k + 31) / 32 * 4; c += 64) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int j = c / 4 * 32 + h * 16 + c % 4 * 4;
       const f32x4 v = j < k ? *(const f32x4*)(src + j) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[4 * h + i] = ldexpf(v[i], e);
+      for (int i = 0; i < 4; ++i) f[4 * h + i] = v[i] * kTgLift;
     }
     const Split3 s = split_three(f);
     u32x4* to = out + (long long)c * 3 * rows + r;
@@ -653,7 +643,7 @@ __device__ __forceinline__ void few_tile(const FewProduct& p, int e, int row0, i
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          v[4 * h + i] = index(s, 4 * h) < length ? (DX ? d.w[i][h][f] : d.w[f][h][i]) : 0.f;
+          v[4 * h + i] = index(s, 4 * h) < length ? (DX ? d.w[i][h][f] : d.w[f][h][i]) * kTgLift : 0.f;
       const Split3 t = split_three(v);
 #pragma unroll
       for (int r = 0; r < RF; ++r) {
@@ -707,9 +697,8 @@ __device__ __forceinline__ void few_store(const FewProduct& p, int e, int row0, 
         v += sum[o][wave][r][lane];
       }
     }
-    const int ex = p.ex[row0 + i];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = ldexpf(v[c], -ex);
+    for (int c = 0; c < 4; ++c) v[c] *= kTgUnlift;
     float* y = p.out + (size_t)(row0 + i) * width + n;
     bool bad = false;
     if (DX || width % 4 == 0) {
@@ -761,14 +750,13 @@ __global__ __launch_bounds__(256, 2) void grouped_few_kernel(FewProduct p) {
     }
   }
 }
-// `in`: x or dy, split into `planes` and `ex` first.
+// `in`: x or dy, split into `planes` first.
 template <bool DX>
-hipError_t run_few(const GroupedArgs& a, const void* in, uint8_t* planes, int32_t* ex, void* out,
-                   hipStream_t st) {
+hipError_t run_few(const GroupedArgs& a, const void* in, uint8_t* planes, void* out, hipStream_t st) {
   const int width = DX ? a.k : a.n, length = DX ? a.n : a.k;
-  const FewProduct p{(const float*)a.w, (const u32x4*)planes, ex, a.offsets, (float*)out,
+  const FewProduct p{(const float*)a.w, (const u32x4*)planes, a.offsets, (float*)out,
                      GroupDims{a.M, a.E, a.n, a.k}, a.zero_rest, (const float*)in};
-  split_three_kernel<<<blocks_of(a.M), 256, 0, st>>>((const float*)in, a.M, length, (u32x4*)planes, ex);
+  split_three_kernel<<<blocks_of(a.M), 256, 0, st>>>((const float*)in, a.M, length, (u32x4*)planes);
   const long long most =
       ((long long)a.M / kFewRows + std::min(a.M, a.E)) * ((width + kFewCols - 1) / kFewCols);
   const long long room = 2LL * device_cu_count();
@@ -845,7 +833,6 @@ struct GroupedPlan {
   uint8_t *x = nullptr, *w = nullptr, *dy = nullptr;        // prepared operands
   uint8_t* dyp = nullptr;                                   // dy in three parts
   uint8_t* few = nullptr;                                   // dy, few rows per group
-  int32_t* efew = nullptr;
   int32_t *ex = nullptr, *ew = nullptr, *ey = nullptr;      // exponents
   float* wmax = nullptr;
   size_t bytes = 0;
@@ -855,7 +842,6 @@ GroupedPlan plan_forward(int dtype, int M, int E, int n, int k, void* ws) {
   Carve c{(uint8_t*)ws};
   if (few_rows(dtype, M, E, n, k)) {
     p.x = c.take((size_t)M * few_pitch(k));
-    p.ex = (int32_t*)c.take((size_t)M * 4);
   } else if (dtype == 0) {
     p.x = c.take((size_t)M * split_pitch(k));
     p.w = c.take((size_t)E * n * split_pitch(k));
@@ -874,7 +860,6 @@ GroupedPlan plan_backward(int dtype, int M, int E, int n, int k, bool dx, bool d
   if (M == 0) dx = false;
   if (dx && few_rows_dx(dtype, M, E, n, k)) {
     p.few = c.take((size_t)M * few_pitch(n));
-    p.efew = (int32_t*)c.take((size_t)M * 4);
     dx = false;
   }
   if (dtype == 0) {
@@ -928,7 +913,7 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
   p.zero_rest = a.zero_rest;
   const long long wr = (long long)a.E * a.n;
   if (few_rows(dtype, a.M, a.E, a.n, a.k)) {
-    return run_few<false>(a, a.x, w.x, w.ex, a.y, st);
+    return run_few<false>(a, a.x, w.x, a.y, st);
   }
   if (dtype == 0) {
     p.pitch_a = p.pitch_b = (uint32_t)split_pitch(a.k);
@@ -958,7 +943,7 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   const bool dw = a.dw != nullptr;
   const GroupedPlan w = plan_backward(dtype, a.M, a.E, a.n, a.k, dx, dw, ws);
   if (w.few != nullptr) {
-    const hipError_t e = run_few<true>(a, a.dy, w.few, w.efew, a.dx, st);
+    const hipError_t e = run_few<true>(a, a.dy, w.few, a.dx, st);
     if (e != hipSuccess || !dw) return e;
     dx = false;
   }

@@ -182,3 +182,34 @@ def test_weight_gradients_show_bad_rows_under_a_zero_gradient(name, dtype):
     want = torch.zeros_like(dw, dtype=torch.bool)
     want[0, :, 5:7] = True
     assert (torch.isnan(dw) == want).all() and torch.isfinite(dw[~want]).all()
+
+
+@pytest.mark.parametrize("name", ["few", "few y"])
+def test_few_rows_with_operands_of_any_scale(name):
+    x, w, off, dy, r = _normal(name, 6)
+    n, k = w.shape[1:]
+    few_dx = SHAPES[name][4]
+
+    def check(x, w, dy, label):
+        say(f"{name}: {label}")
+        x, w, dy = dev(x), dev(w), dev(dy)
+        y = mx.grouped_matmul(x, w, off)
+        dx = mx.grouped_matmul_backward(x, w, off, dy, need_dw=False)[0]
+        torch.cuda.synchronize()
+        X, W, DY = host(x), host(w), host(dy)
+        for e, (a, b) in enumerate(ref.group_rows(off.cpu().numpy(), len(X))):
+            _same(y[a:b], X[a:b] @ W[e].T, _tol(np.abs(X[a:b]), np.abs(W[e]), k), f"{label} y {e}")
+            if few_dx:
+                t = _tol(np.abs(DY[a:b]), np.abs(W[e]).T, n)
+                _same(dx[a:b], DY[a:b] @ W[e], t, f"{label} dx {e}")
+
+    # small weights against large rows: ordinary results out of parts near the range's end
+    for p in (110, 120, 126, 138):                       # (subnormal weights from 2^-126 down)
+        check(x * 2.0 ** 100, w * 2.0 ** -p, dy * 2.0 ** 100, f"weights at 2^-{p}")
+    # rows, and channels of the contraction whose factors are each other's opposite
+    sr = 2.0 ** np.floor(r.uniform(-60, 60, (len(x), 1)))
+    check(x * sr, w, dy * sr, "rows")
+    s = 2.0 ** np.floor(r.uniform(-60, 60, k))
+    check(x * s, w / s, dy, "channels")
+    s = 2.0 ** np.floor(r.uniform(-60, 60, n))
+    check(x, w / s[:, None], dy * s, "output channels")
