@@ -286,10 +286,8 @@ moe_status_t moe_grouped_matmul(const void* x, const void* w, const int32_t* off
  *   dw[e] = sum over e's rows of dy[r] x[r]^T  [E][n][k] float32, may be NULL
  * (not both NULL unless M = 0).  A group without rows gets a zero dw, M = 0 included; dx
  * outside the groups as y above.  x may be NULL without dw, w without dx.
- * float32 dw: products of three-bfloat16 splits, float32 accuracy however much
- * experts, rows and channels differ.  float32 dx: w is scaled per expert, and a
- * value of w is held to 2^-38 of its expert's largest, one of dy to 2^-38 of its
- * row's (float32 accuracy down to 2^-14 of those, none at 2^-38). */
+ * float32: products of three-bfloat16 splits, float32 accuracy however much
+ * experts, rows and channels differ. */
 moe_status_t moe_grouped_matmul_backward_workspace_size(int M, int E, int n, int k, int dtype,
                                                         int want_dx, int want_dw, size_t* bytes);
 moe_status_t moe_grouped_matmul_backward(const void* x, const void* w, const int32_t* offsets,

@@ -13,12 +13,11 @@
 // ends there by a bounded buffer range.
 //
 // bfloat16 operands are read where they are (the transposed products through
-// transposing LDS reads).  float32 operands of y and dx are first written as two
-// float16 each (tile_gemm.h), with a power-of-two scale per row of x, dy and, in the
-// forward, w; per expert for w in dx, whose product contracts over w's rows.  The
-// weight gradient contracts over the rows of both dy and x, where no scale of a row can
-// be taken out again and experts, rows and channels differ by any factor: its operands
-// are written as three bfloat16 each, which need no scale.
+// transposing LDS reads).  float32 operands of y are first written as two float16 each
+// (tile_gemm.h), with a power-of-two scale per row of x and w.  The gradients contract over
+// rows of w, and of dy and x, where no scale of a row can be taken out again and
+// experts, rows and channels differ by any factor: their operands are written as three
+// bfloat16 each, which need no scale.
 //
 // The parts of an infinity are an infinity and NaN, so a float32 result with one among its
 // operands comes out as NaN, and what leaves float32's range on the way as either.  Every
@@ -133,8 +132,8 @@ struct GroupedProduct {
   uint32_t plane_a, plane_b;  // three parts: bytes of one in a row
   const int32_t* offsets;
   void* out;
-  const int32_t* ea;       // two parts: exponents of A's rows, and of
-  const int32_t* eb;       //   w's rows (forward), experts (dx)
+  const int32_t* ea;       // two parts: exponents of x's rows, and
+  const int32_t* eb;       //   of w's
   GroupDims g;
   int zero_rest;
   const float *ra, *rb;    // float32: A's and B's operands as the caller gave them
@@ -235,18 +234,18 @@ struct GroupedTiles {
       // a lane holds four consecutive columns of one row
       const int N = DIR == GR_FWD ? g.n : g.k;
       bool bad = false;
-      const bool vec = N % (C::SPLIT ? 4 : 8) == 0;  // whole 16-byte runs
+      const bool vec = N % (C::PARTS > 1 ? 4 : 8) == 0;  // whole 16-byte runs
 #pragma unroll
       for (int fm = 0; fm < C::FM; ++fm) {
         const int mr = tg_row<C>(wm, fm, lane, 0);
         if (mr >= t.rows) continue;
         const size_t row = (size_t)(t.row0 + t.m0 + mr);
-        const int ea = C::SPLIT ? p.ea[row] + (DIR == GR_DX ? p.eb[t.hint] : 0) : 0;
+        const int ea = C::SPLIT ? p.ea[row] : 0;
 #pragma unroll
         for (int fn = 0; fn < C::FN; ++fn) {
           const int n0 = t.n0 + tg_col<C>(wn, fn, 0, 0);  // the fragment's first column
           if (n0 >= N) continue;
-          if constexpr (C::SPLIT) {
+          if constexpr (C::PARTS > 1) {
             float* c = (float*)p.out + row * N;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -256,7 +255,8 @@ struct GroupedTiles {
               for (int e = 0; e < 4; ++e) {
                 v[e] = acc[fm][fn][4 * q + e];
                 if (n + e < N) {
-                  v[e] = ldexpf(v[e], -ea - (DIR == GR_FWD ? p.eb[(size_t)t.hint * g.n + n + e] : 0));
+                  if constexpr (C::SPLIT) v[e] = ldexpf(v[e], -ea - p.eb[(size_t)t.hint * g.n + n + e]);
+                  else v[e] *= kTgUnlift;
                   bad |= not_finite(v[e]);
                 }
               }
@@ -294,7 +294,7 @@ struct GroupedTiles {
           }
         }
       }
-      if (C::SPLIT && bad) again(t, wm, wn, lane);
+      if (C::PARTS > 1 && bad) again(t, wm, wn, lane);
     }
   }
 
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void grouped_kernel(
   group_tables<DIR>(p.g, p.offsets, C::BM, t);
   if (DIR != GR_DW && p.zero_rest) {
     const int width = DIR == GR_FWD ? p.g.n : p.g.k;
-    if (C::SPLIT) zero_rows((float*)p.out, p.g.M, width, t.off[0], t.off[p.g.E]);
+    if (C::PARTS > 1) zero_rows((float*)p.out, p.g.M, width, t.off[0], t.off[p.g.E]);
     else zero_rows((uint16_t*)p.out, p.g.M, width, t.off[0], t.off[p.g.E]);
   }
   if (DIR == GR_DW) {  // groups without rows have no tiles
@@ -368,10 +368,9 @@ __device__ __forceinline__ float chunk_max(const float (&f)[8]) {
   for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]) <= FLT_MAX ? fabsf(f[e]) : 0.f);
   return m;
 }
-// Splits one row; `exponent` gives the scale from the row's largest magnitude.
-template <class F>
+// Splits one row; returns its exponent.
 __device__ __forceinline__ int split_row(const float* __restrict__ src, int width,
-                                         uint8_t* __restrict__ dst, int lane, F exponent) {
+                                         uint8_t* __restrict__ dst, int lane) {
   const int padded = (width + 31) & ~31;
   float f[kRowChunks][8], m = 0.f;
 #pragma unroll
@@ -383,7 +382,7 @@ __device__ __forceinline__ int split_row(const float* __restrict__ src, int widt
     load_chunk<ElemF32>(src, j, width, g);
     m = fmaxf(m, chunk_max(g));
   }
-  const int ex = exponent(wave_max(m));
+  const int ex = split_exponent(wave_max(m));
 #pragma unroll
   for (int c = 0; c < kRowChunks; ++c) {
     const int j = 8 * (lane + 64 * c);
@@ -412,7 +411,7 @@ __device__ __forceinline__ void split_rows(const SplitRows& a, unsigned block) {
   const int lane = threadIdx.x & 63;
   if (r >= a.rows) return;
   const float* src = a.src + r * a.width;
-  const int ex = split_row(src, a.width, a.dst + r * a.pitch, lane, [](float m) { return split_exponent(m); });
+  const int ex = split_row(src, a.width, a.dst + r * a.pitch, lane);
   if (lane == 0) a.ex[r] = ex;
 }
 // The forward's operands, in one launch.
@@ -420,56 +419,6 @@ __global__ __launch_bounds__(256) void split_two_kernel(SplitRows a, SplitRows b
   const unsigned n = blocks_of(a.rows);
   if (blockIdx.x < n) split_rows(a, blockIdx.x);
   else split_rows(b, blockIdx.x - n);
-}
-
-// w by expert: partial maxima of kMaxChunks row ranges per expert, then the rows
-// with their expert's scale.
-constexpr int kMaxChunks = 64;
-struct SplitExperts {
-  const float* w;
-  float* part;      // [E][kMaxChunks]
-  uint8_t* dst;
-  int32_t* ex;      // [E]
-  long long rows;   // E * n
-  uint32_t pitch;
-  int E, n, k;
-};
-__device__ __forceinline__ void expert_max(const SplitExperts& a, unsigned block) {
-  __shared__ float s[4];
-  const int e = block / kMaxChunks, c = block % kMaxChunks, lane = threadIdx.x & 63;
-  const float* src = a.w + (long long)e * a.n * a.k;
-  const int lo = (int)((long long)a.n * c / kMaxChunks), hi = (int)((long long)a.n * (c + 1) / kMaxChunks);
-  float m = 0.f;
-  for (int r = lo + (threadIdx.x >> 6); r < hi; r += 4)
-    for (int j = 8 * lane; j < a.k; j += 512) {
-      float g[8];
-      load_chunk<ElemF32>(src + (long long)r * a.k, j, a.k, g);
-      m = fmaxf(m, chunk_max(g));
-    }
-  m = wave_max(m);
-  if (lane == 0) s[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x == 0) a.part[block] = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-}
-__device__ __forceinline__ void split_expert_rows(const SplitExperts& a, unsigned block) {
-  const long long r = (long long)block * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (r >= a.rows) return;
-  const int e = (int)(r / a.n);
-  static_assert(kMaxChunks == 64, "one partial maximum per lane");
-  const int x = split_exponent(wave_max(a.part[e * kMaxChunks + lane]));
-  if (lane == 0 && r % a.n == 0) a.ex[e] = x;
-  split_row(a.w + r * a.k, a.k, a.dst + r * a.pitch, lane, [&](float) { return x; });
-}
-
-// dx's operands in two launches: dy's rows and w's maxima, then w's rows.
-__global__ __launch_bounds__(256) void dx_first_kernel(SplitRows dy, SplitExperts w) {
-  const unsigned n = blocks_of(dy.rows);
-  if (blockIdx.x < n) split_rows(dy, blockIdx.x);
-  else expert_max(w, blockIdx.x - n);
-}
-__global__ __launch_bounds__(256) void dx_second_kernel(SplitExperts w) {
-  split_expert_rows(w, blockIdx.x);
 }
 
 // float32 rows as three bfloat16 each (tile_gemm.h), times kTgLift, zeros behind the last
@@ -482,6 +431,9 @@ struct PartRows {
   int width, shift;
   unsigned blocks;
 };
+// dy is dx's A too, whose k-steps read 64 elements of a row.
+uint32_t part_plane_dy(int n) { return (uint32_t)((n + 63) / 64 * 128); }
+uint32_t part_plane(int k) { return (uint32_t)((k + 7) / 8 * 16); }
 PartRows part_rows(const void* src, uint8_t* dst, long long rows, int width, uint32_t plane) {
   PartRows a{(const float*)src, dst, rows, plane, width, 0, 0};
   while (a.shift < 6 && (16u << a.shift) < plane) ++a.shift;
@@ -507,9 +459,12 @@ __device__ __forceinline__ void part_rows(const PartRows& a, unsigned block) {
     *(u32x4*)(to + 2 * (size_t)a.plane) = s.lo;
   }
 }
-__global__ __launch_bounds__(256) void parts_kernel(PartRows a, PartRows b) {
-  if (blockIdx.x < a.blocks) part_rows(a, blockIdx.x);
-  else part_rows(b, blockIdx.x - a.blocks);
+// The gradients' operands, in one launch (x is dw's, w dx's: no blocks without them).
+__global__ __launch_bounds__(256) void parts_kernel(PartRows dy, PartRows x, PartRows w) {
+  const unsigned b = blockIdx.x;
+  if (b < dy.blocks) part_rows(dy, b);
+  else if (b < dy.blocks + x.blocks) part_rows(x, b - dy.blocks);
+  else part_rows(w, b - dy.blocks - x.blocks);
 }
 
 // bfloat16 rows whose length does not suit the loads, copied into rows of whole
@@ -787,7 +742,6 @@ struct Carve {
 };
 
 uint32_t pad_pitch(int n) { return (uint32_t)((n + 63) / 64 * 128); }
-uint32_t part_plane(int n) { return (uint32_t)((n + 7) / 8 * 16); }
 
 // About how many tiles of b x b a product has: the offsets are on the device, so half a
 // tile's rows are taken as lost per group, and every row as in a group.
@@ -831,10 +785,8 @@ unsigned row_blocks(long long rows) { return blocks_of(rows); }
 // The workspace's regions: which are needed, and where they lie.
 struct GroupedPlan {
   uint8_t *x = nullptr, *w = nullptr, *dy = nullptr;        // prepared operands
-  uint8_t* dyp = nullptr;                                   // dy in three parts
   uint8_t* few = nullptr;                                   // dy, few rows per group
-  int32_t *ex = nullptr, *ew = nullptr, *ey = nullptr;      // exponents
-  float* wmax = nullptr;
+  int32_t *ex = nullptr, *ew = nullptr;                     // exponents
   size_t bytes = 0;
 };
 GroupedPlan plan_forward(int dtype, int M, int E, int n, int k, void* ws) {
@@ -863,17 +815,9 @@ GroupedPlan plan_backward(int dtype, int M, int E, int n, int k, bool dx, bool d
     dx = false;
   }
   if (dtype == 0) {
-    if (dx) {
-      p.dy = c.take((size_t)M * split_pitch(n));
-      p.ey = (int32_t*)c.take((size_t)M * 4);
-      p.w = c.take((size_t)E * n * split_pitch(k));
-      p.ew = (int32_t*)c.take((size_t)E * 4);
-      p.wmax = (float*)c.take((size_t)E * kMaxChunks * 4);
-    }
-    if (dw) {
-      p.dyp = c.take(3 * (size_t)M * part_plane(n));
-      p.x = c.take(3 * (size_t)M * part_plane(k));
-    }
+    if (dx || dw) p.dy = c.take(3 * (size_t)M * part_plane_dy(n));
+    if (dx) p.w = c.take(3 * (size_t)E * n * part_plane(k));
+    if (dw) p.x = c.take(3 * (size_t)M * part_plane(k));
   } else if (dtype != 0) {
     if (n % (dx ? 64 : 8) != 0) p.dy = c.take((size_t)M * pad_pitch(n));
     if (dx && k % 8 != 0) p.w = c.take((size_t)E * n * pad_pitch(k));
@@ -955,21 +899,20 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   const uint8_t *x = (const uint8_t*)a.x, *wt = (const uint8_t*)a.w, *dy = (const uint8_t*)a.dy;
   uint32_t px = a.k * 2, pw = a.k * 2, py = a.n * 2;
   if (dtype == 0) {
-    if (dx && a.M > 0) {
-      pw = (uint32_t)split_pitch(a.k);
-      py = (uint32_t)split_pitch(a.n);
-      const SplitRows ry{(const float*)a.dy, w.dy, w.ey, a.M, py, a.n};
-      const SplitExperts we{(const float*)a.w, w.wmax, w.w, w.ew, wr, pw, a.E, a.n, a.k};
-      dx_first_kernel<<<row_blocks(a.M) + a.E * kMaxChunks, 256, 0, st>>>(ry, we);
-      dx_second_kernel<<<row_blocks(wr), 256, 0, st>>>(we);
-    }
-    if (dw && a.M > 0) {
-      const PartRows ry = part_rows(a.dy, w.dyp, a.M, a.n, part_plane(a.n));
-      const PartRows rx = part_rows(a.x, w.x, a.M, a.k, part_plane(a.k));
-      parts_kernel<<<ry.blocks + rx.blocks, 256, 0, st>>>(ry, rx);
+    p.plane_a = part_plane_dy(a.n);
+    p.plane_b = part_plane(a.k);
+    py = 3 * p.plane_a;
+    px = pw = 3 * p.plane_b;
+    if (a.M > 0) {
+      const PartRows ry = part_rows(a.dy, w.dy, a.M, a.n, p.plane_a);
+      PartRows rx{}, rw{};
+      if (dw) rx = part_rows(a.x, w.x, a.M, a.k, p.plane_b);
+      if (dx) rw = part_rows(a.w, w.w, wr, a.k, p.plane_b);
+      parts_kernel<<<ry.blocks + rx.blocks + rw.blocks, 256, 0, st>>>(ry, rx, rw);
     }
     dy = w.dy;
     wt = w.w;
+    x = w.x;
   } else {
     if (w.dy != nullptr && a.M > 0) {
       py = pad_pitch(a.n);
@@ -989,38 +932,23 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  p.A = dy;
+  p.pitch_a = py;
+  p.ra = (const float*)a.dy;
   if (dx && a.M > 0) {
-    p.A = dy;
-    p.pitch_a = py;
-    p.ea = w.ey;
     p.B = wt;
     p.pitch_b = pw;
-    p.eb = w.ew;
-    p.ra = (const float*)a.dy;
     p.rb = (const float*)a.w;
     p.out = a.dx;
-    e = dtype == 0 ? pick_product<GR_DX, 2>(a, p, st) : pick_product<GR_DX, 1>(a, p, st);
+    e = dtype == 0 ? pick_product<GR_DX, 3>(a, p, st) : pick_product<GR_DX, 1>(a, p, st);
     if (e != hipSuccess) return e;
   }
   if (dw) {
+    p.B = x;
+    p.pitch_b = px;
+    p.rb = (const float*)a.x;
     p.out = a.dw;
-    if (dtype == 0) {
-      p.A = w.dyp;
-      p.B = w.x;
-      p.plane_a = part_plane(a.n);
-      p.plane_b = part_plane(a.k);
-      p.pitch_a = 3 * p.plane_a;
-      p.pitch_b = 3 * p.plane_b;
-      p.ra = (const float*)a.dy;
-      p.rb = (const float*)a.x;
-      e = pick_product<GR_DW, 3>(a, p, st);
-    } else {
-      p.A = dy;
-      p.pitch_a = py;
-      p.B = x;
-      p.pitch_b = px;
-      e = pick_product<GR_DW, 1>(a, p, st);
-    }
+    e = dtype == 0 ? pick_product<GR_DW, 3>(a, p, st) : pick_product<GR_DW, 1>(a, p, st);
   }
   return e;
 }

@@ -130,6 +130,19 @@ def test_infinities_and_nan_come_out_as_in_float32(name):
     _check_all(dev(x), dev(w), off, dev(dy), name, floor=2.0 ** -37)
 
 
+@pytest.mark.parametrize("name", SHAPES)
+def test_sums_that_leave_the_range_on_the_way(name):
+    """Products past float32's range that cancel, results past it, and the largest values."""
+    x, w, off, dy, _ = _normal(name, 2)
+    x[2, :4], w[0, 5, :4] = [2e38, 2e38, -2e38, -2e38], [1.5, 1.5, 1.5, 1.2]
+    x[3, 0], w[0, 6, 0] = 3.4e38, -3.0
+    w[1, 1, 2] = 3.4028234e38                           # rounds up as a bfloat16
+    x[40, 2] = 0.25
+    dy[2, :4], w[0, :4, 9] = [2e38, 2e38, -2e38, -2e38], [1.5, 1.5, 1.5, 1.2]
+    dy[4:8, 8], x[4:8, 1] = [2e38, 2e38, -2e38, -2e38], [1.5, 1.5, 1.5, 1.2]
+    _check_all(dev(x), dev(w), off, dev(dy), name, floor=2.0 ** -37)
+
+
 # ---------------------------------------------------------------- operands of uneven scale
 def _check_dw(x, w, off, dy, label):
     say(label)
@@ -213,3 +226,32 @@ def test_few_rows_with_operands_of_any_scale(name):
     check(x * s, w / s, dy, "channels")
     s = 2.0 ** np.floor(r.uniform(-60, 60, n))
     check(x, w / s[:, None], dy * s, "output channels")
+
+
+def _check_dx(x, w, off, dy, label):
+    say(label)
+    dx, _ = mx.grouped_matmul_backward(x, w, off, dy, need_dw=False)
+    both = mx.grouped_matmul_backward(x, w, off, dy)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(_bits(dx), _bits(both))
+    W, DY = host(w), host(dy)
+    for e, (a, b) in enumerate(ref.group_rows(off.cpu().numpy(), len(DY))):
+        t = _tol(np.abs(DY[a:b]), np.abs(W[e]).T, dy.shape[1])
+        _same(dx[a:b], DY[a:b] @ W[e], t, f"{label} dx {e}")
+
+
+@pytest.mark.parametrize("name", SHAPES)
+def test_input_gradients_through_weights_of_any_scale(name):
+    x, w, off, dy, r = _normal(name, 5)
+    n, k = w.shape[1:]
+    x = dev(x)
+    # experts, columns of w, and rows of dy
+    se, sk = 2.0 ** np.array([0, -30, 20, 40, -60][:len(w)]), 2.0 ** np.floor(r.uniform(-40, 20, k))
+    sr = 2.0 ** np.floor(r.uniform(-40, 20, (len(dy), 1)))
+    _check_dx(x, dev(w * se[:, None, None] * sk), off, dev(dy * sr), f"{name}: experts, columns, rows")
+    # output channels whose w and dy are each other's opposite, and one row of w above all others
+    s = 2.0 ** np.floor(r.uniform(-60, 60, n))
+    _check_dx(x, dev(w / s[:, None]), off, dev(dy * s), f"{name}: balanced channels")
+    loud = w.copy()
+    loud[:, 3] *= 2.0 ** 40
+    _check_dx(x, dev(loud), off, dev(dy), f"{name}: one channel")
