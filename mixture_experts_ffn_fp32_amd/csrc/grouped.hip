@@ -405,14 +405,19 @@ struct SplitRows {
   uint32_t pitch;
   int width;
 };
-__host__ __device__ inline unsigned blocks_of(long long rows) { return (unsigned)((rows + 3) / 4); }
+// Blocks that prepare an operand.  A launch holds fewer than 2^32 threads: past kMostBlocks
+// each block takes further rows.
+constexpr long long kMostBlocks = 1 << 20;
+__host__ __device__ inline unsigned blocks_of(long long rows) {
+  const long long b = (rows + 3) / 4;
+  return (unsigned)(b < kMostBlocks ? b : kMostBlocks);
+}
 __device__ __forceinline__ void split_rows(const SplitRows& a, unsigned block) {
-  const long long r = (long long)block * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  if (r >= a.rows) return;
-  const float* src = a.src + r * a.width;
-  const int ex = split_row(src, a.width, a.dst + r * a.pitch, lane);
-  if (lane == 0) a.ex[r] = ex;
+  for (long long r = (long long)block * 4 + (threadIdx.x >> 6); r < a.rows; r += 4 * kMostBlocks) {
+    const int ex = split_row(a.src + r * a.width, a.width, a.dst + r * a.pitch, lane);
+    if (lane == 0) a.ex[r] = ex;
+  }
 }
 // The forward's operands, in one launch.
 __global__ __launch_bounds__(256) void split_two_kernel(SplitRows a, SplitRows b) {
@@ -438,25 +443,26 @@ PartRows part_rows(const void* src, uint8_t* dst, long long rows, int width, uin
   PartRows a{(const float*)src, dst, rows, plane, width, 0, 0};
   while (a.shift < 6 && (16u << a.shift) < plane) ++a.shift;
   const long long per = 4 << (6 - a.shift);  // rows per block
-  a.blocks = (unsigned)((rows + per - 1) / per);
+  a.blocks = (unsigned)std::min((rows + per - 1) / per, kMostBlocks);
   return a;
 }
 __device__ __forceinline__ void part_rows(const PartRows& a, unsigned block) {
   const int lane = threadIdx.x & 63;
-  const long long r = (((long long)block * 4 + (threadIdx.x >> 6)) << (6 - a.shift)) + (lane >> a.shift);
-  if (r >= a.rows) return;
-  const float* src = a.src + r * a.width;
-  uint8_t* dst = a.dst + 3 * r * a.plane;
-  for (int j = 8 * (lane & ((1 << a.shift) - 1)); j < (int)(a.plane / 2); j += 8 << a.shift) {
-    float f[8];
-    load_chunk<ElemF32>(src, j, a.width, f);
+  long long r = (((long long)block * 4 + (threadIdx.x >> 6)) << (6 - a.shift)) + (lane >> a.shift);
+  for (; r < a.rows; r += 4 * kMostBlocks << (6 - a.shift)) {
+    const float* src = a.src + r * a.width;
+    uint8_t* dst = a.dst + 3 * r * a.plane;
+    for (int j = 8 * (lane & ((1 << a.shift) - 1)); j < (int)(a.plane / 2); j += 8 << a.shift) {
+      float f[8];
+      load_chunk<ElemF32>(src, j, a.width, f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= kTgLift;
-    const Split3 s = split_three(f);
-    uint8_t* to = dst + 2 * (size_t)j;
-    *(u32x4*)to = s.hi;
-    *(u32x4*)(to + a.plane) = s.mid;
-    *(u32x4*)(to + 2 * (size_t)a.plane) = s.lo;
+      for (int e = 0; e < 8; ++e) f[e] *= kTgLift;
+      const Split3 s = split_three(f);
+      uint8_t* to = dst + 2 * (size_t)j;
+      *(u32x4*)to = s.hi;
+      *(u32x4*)(to + a.plane) = s.mid;
+      *(u32x4*)(to + 2 * (size_t)a.plane) = s.lo;
+    }
   }
 }
 // The gradients' operands, in one launch (x is dw's, w dx's: no blocks without them).
@@ -472,13 +478,13 @@ __global__ __launch_bounds__(256) void parts_kernel(PartRows dy, PartRows x, Par
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src,
                                                        long long rows, int width,
                                                        uint8_t* __restrict__ dst, uint32_t pitch) {
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  if (r >= rows) return;
-  const uint16_t* s = src + r * width;
-  for (int j = 2 * lane; j < (int)(pitch / 2); j += 128) {
-    const uint32_t a = j < width ? s[j] : 0, b = j + 1 < width ? s[j + 1] : 0;
-    *(uint32_t*)(dst + r * pitch + 2 * j) = a | (b << 16);
+  for (long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += 4 * kMostBlocks) {
+    const uint16_t* s = src + r * width;
+    for (int j = 2 * lane; j < (int)(pitch / 2); j += 128) {
+      const uint32_t a = j < width ? s[j] : 0, b = j + 1 < width ? s[j + 1] : 0;
+      *(uint32_t*)(dst + r * pitch + 2 * j) = a | (b << 16);
+    }
   }
 }
 
@@ -517,7 +523,7 @@ struct FewProduct {
 // Bytes of x's split row.
 __host__ __device__ inline long long few_pitch(int k) { return (long long)((k + 31) / 32) * 192; }
 
-// x's rows (of a multiple of 4 values), one wavefront each.
+// x's rows (of a multiple of 4 values; 64 kGroupedMaxE at most), one wavefront each.
 __global__ __launch_bounds__(256) void split_three_kernel(const float* __restrict__ x, int rows, int k,
                                                           u32x4* __restrict__ out) {
   const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -712,6 +718,7 @@ hipError_t run_few(const GroupedArgs& a, const void* in, uint8_t* planes, void* 
   const FewProduct p{(const float*)a.w, (const u32x4*)planes, a.offsets, (float*)out,
                      GroupDims{a.M, a.E, a.n, a.k}, a.zero_rest, (const float*)in};
   split_three_kernel<<<blocks_of(a.M), 256, 0, st>>>((const float*)in, a.M, length, (u32x4*)planes);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   const long long most =
       ((long long)a.M / kFewRows + std::min(a.M, a.E)) * ((width + kFewCols - 1) / kFewCols);
   const long long room = 2LL * device_cu_count();
@@ -779,8 +786,6 @@ hipError_t pick_product(const GroupedArgs& a, const GroupedProduct& p, hipStream
     return run_product<TgConfig<TgMid, AC, BC, PARTS, SW>, DIR>(p, st);
   return run_product<TgConfig<TgSmall, AC, BC, PARTS, SW>, DIR>(p, st);
 }
-
-unsigned row_blocks(long long rows) { return blocks_of(rows); }
 
 // The workspace's regions: which are needed, and where they lie.
 struct GroupedPlan {
@@ -863,7 +868,8 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
     p.pitch_a = p.pitch_b = (uint32_t)split_pitch(a.k);
     const SplitRows rx{(const float*)a.x, w.x, w.ex, a.M, p.pitch_a, a.k};
     const SplitRows rw{(const float*)a.w, w.w, w.ew, wr, p.pitch_b, a.k};
-    split_two_kernel<<<row_blocks(a.M) + row_blocks(wr), 256, 0, st>>>(rx, rw);
+    split_two_kernel<<<blocks_of(a.M) + blocks_of(wr), 256, 0, st>>>(rx, rw);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     p.A = w.x;
     p.B = w.w;
     p.ea = w.ex;
@@ -874,8 +880,9 @@ hipError_t launch_grouped(int dtype, const GroupedArgs& a, void* ws, hipStream_t
   }
   if (w.x != nullptr) {
     p.pitch_a = p.pitch_b = pad_pitch(a.k);
-    pad_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const uint16_t*)a.x, a.M, a.k, w.x, p.pitch_a);
-    pad_rows_kernel<<<row_blocks(wr), 256, 0, st>>>((const uint16_t*)a.w, wr, a.k, w.w, p.pitch_b);
+    pad_rows_kernel<<<blocks_of(a.M), 256, 0, st>>>((const uint16_t*)a.x, a.M, a.k, w.x, p.pitch_a);
+    pad_rows_kernel<<<blocks_of(wr), 256, 0, st>>>((const uint16_t*)a.w, wr, a.k, w.w, p.pitch_b);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     p.A = w.x;
     p.B = w.w;
   }
@@ -916,17 +923,17 @@ hipError_t launch_grouped_backward(int dtype, const GroupedArgs& a, void* ws, hi
   } else {
     if (w.dy != nullptr && a.M > 0) {
       py = pad_pitch(a.n);
-      pad_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const uint16_t*)a.dy, a.M, a.n, w.dy, py);
+      pad_rows_kernel<<<blocks_of(a.M), 256, 0, st>>>((const uint16_t*)a.dy, a.M, a.n, w.dy, py);
       dy = w.dy;
     }
     if (w.w != nullptr) {
       pw = pad_pitch(a.k);
-      pad_rows_kernel<<<row_blocks(wr), 256, 0, st>>>((const uint16_t*)a.w, wr, a.k, w.w, pw);
+      pad_rows_kernel<<<blocks_of(wr), 256, 0, st>>>((const uint16_t*)a.w, wr, a.k, w.w, pw);
       wt = w.w;
     }
     if (w.x != nullptr && a.M > 0) {
       px = pad_pitch(a.k);
-      pad_rows_kernel<<<row_blocks(a.M), 256, 0, st>>>((const uint16_t*)a.x, a.M, a.k, w.x, px);
+      pad_rows_kernel<<<blocks_of(a.M), 256, 0, st>>>((const uint16_t*)a.x, a.M, a.k, w.x, px);
       x = w.x;
     }
   }

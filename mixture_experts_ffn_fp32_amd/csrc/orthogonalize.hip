@@ -289,33 +289,33 @@ __global__ __launch_bounds__(256) void ns_start_kernel(const void* __restrict__ 
                                                        float scale, uint8_t* __restrict__ out,
                                                        uint32_t pitch, void* last,
                                                        long long last_stride, int last_dtype) {
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  if (r >= rows) return;
-  const long long i = r / m, row = r % m;
-  double sq = part[i * kNormParts + lane];
-  static_assert(kNormParts == 64, "one partial norm per lane");
+  for (long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += 4LL * gridDim.x) {
+    const long long i = r / m, row = r % m;
+    double sq = part[i * kNormParts + lane];
+    static_assert(kNormParts == 64, "one partial norm per lane");
 #pragma unroll
-  for (int k = 32; k > 0; k >>= 1) sq += __shfl_xor(sq, k);
-  const double norm = sqrt(sq) + (double)eps;
-  // an all-zero matrix stays zero
-  const double f = norm == 0.0 ? 0.0 : (double)scale / norm;
-  const typename E::T* src = (const typename E::T*)x + i * stride + row * n;
-  if (last != nullptr) {
-    for (int j = lane; j < n; j += 64) {
-      const float v = (float)((double)load_as_f32<E>(src + j) * f);
-      if (last_dtype == 0) ((float*)last)[i * last_stride + row * n + j] = v;
-      else ((uint16_t*)last)[i * last_stride + row * n + j] = f32_to_bf16(v);
+    for (int k = 32; k > 0; k >>= 1) sq += __shfl_xor(sq, k);
+    const double norm = sqrt(sq) + (double)eps;
+    // an all-zero matrix stays zero
+    const double f = norm == 0.0 ? 0.0 : (double)scale / norm;
+    const typename E::T* src = (const typename E::T*)x + i * stride + row * n;
+    if (last != nullptr) {
+      for (int j = lane; j < n; j += 64) {
+        const float v = (float)((double)load_as_f32<E>(src + j) * f);
+        if (last_dtype == 0) ((float*)last)[i * last_stride + row * n + j] = v;
+        else ((uint16_t*)last)[i * last_stride + row * n + j] = f32_to_bf16(v);
+      }
+      continue;
     }
-    return;
-  }
-  const int padded = (n + 31) & ~31;
-  for (int j = 8 * lane; j < padded; j += 512) {
-    float v[8];
-    load_chunk<E>(src, j, n, v);
+    const int padded = (n + 31) & ~31;
+    for (int j = 8 * lane; j < padded; j += 512) {
+      float v[8];
+      load_chunk<E>(src, j, n, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (float)((double)v[e] * f);
-    store_chunk(v, out + r * pitch, j);
+      for (int e = 0; e < 8; ++e) v[e] = (float)((double)v[e] * f);
+      store_chunk(v, out + r * pitch, j);
+    }
   }
 }
 
@@ -438,7 +438,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, void* ws, hipStream_t st) {
   const int claims = a.steps * 3 * kTgCounters;
   const uint32_t px = (uint32_t)split_pitch(a.n), pa = (uint32_t)split_pitch(std::min(a.m, a.n));
   void* direct = a.steps == 0 ? a.out : nullptr;
-  const dim3 gn(kNormParts, a.B), gs((unsigned)((rows + 3) / 4));
+  // (a launch holds fewer than 2^32 threads: past 2^20 blocks each takes further rows)
+  const dim3 gn(kNormParts, a.B), gs((unsigned)std::min((rows + 3) / 4, 1LL << 20));
   if (a.dtype == 0) {
     ns_norm_kernel<ElemF32><<<gn, 256, 0, st>>>(a.x, a.x_stride, per, part,
                                                 counters, claims);

@@ -207,6 +207,89 @@ def test_layer_norm_past_4_gib():
         assert torch.equal(rstd[rows], s) and torch.equal(_bits(dx[rows]), _bits(again))
 
 
+# ---------------------------------------------------------------- past 2^26 rows
+# (a launch of one wavefront per row would hold 2^32 threads, of which some would never run)
+def _every_row(got, want, tol):
+    """On the GPU: |got - want| <= tol for every element (float64 tensors)."""
+    return bool(((got.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_grouped_past_2_26_rows(dtype):
+    M, n, k = (1 << 26) + 5, 8, 24
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    torch.manual_seed(4)
+    x = torch.randn(M, k, device="cuda").to(dt)
+    w = torch.randn(2, n, k, device="cuda").to(dt)
+    off = torch.tensor([1, M - 1000, M - 2], dtype=torch.int32, device="cuda")
+    say(f"grouped y of 2^26 rows {dtype}")
+    y = mx.grouped_matmul(x, w, off)
+    torch.cuda.synchronize()
+    for a in range(0, M, 1 << 24):
+        b = min(M, a + (1 << 24))
+        e = (torch.arange(a, b, device="cuda") >= M - 1000).long()
+        want = torch.zeros(b - a, n, dtype=torch.float64, device="cuda")
+        size = torch.zeros_like(want)
+        for g in (0, 1):
+            X, W = x[a:b].double(), w[g].double()
+            want += (X @ W.t().contiguous()) * (e == g)[:, None]
+            size += (X.abs() @ W.abs().t().contiguous()) * (e == g)[:, None]
+        t = (2 * (k + 8) + 8) * U * size
+        if a == 0:
+            want[0], t[0] = 0, 0
+        if b == M:
+            want[-2:], t[-2:] = 0, 0
+        assert _every_row(y[a:b], want, t + STORE[dtype] * (want.abs() + t)), a
+    del y
+    dy = torch.randn(M, n, device="cuda").to(dt)
+    off = torch.tensor([M - 900, M - 300, M - 2], dtype=torch.int32, device="cuda")
+    say(f"grouped gradients of 2^26 rows {dtype}")
+    dx, dw = mx.grouped_matmul_backward(x, w, off, dy)
+    torch.cuda.synchronize()
+    assert not dx[:M - 900].any() and not dx[M - 2:].any()
+    for e, (a, b) in enumerate([(M - 900, M - 300), (M - 300, M - 2)]):
+        X, W, DY = host(x[a:b]), host(w[e]), host(dy[a:b])
+        t = (12 * (n + 8) + 8) * U * (np.abs(DY) @ np.abs(W))
+        within(dx[a:b], DY @ W, t + STORE[dtype] * (np.abs(DY @ W) + t), f"dx {e}")
+        t = (12 * (b - a + 8) + 8) * U * (np.abs(DY).T @ np.abs(X))
+        within(dw[e], DY.T @ X, t + U * np.abs(DY.T @ X), f"dw {e}")
+
+
+def test_grouped_past_2_26_weight_rows():
+    """As many rows of w: E * n."""
+    E, n, k, M = 1024, 1 << 16, 8, 40
+    torch.manual_seed(5)
+    w = torch.randn(E, n, k, device="cuda", dtype=torch.bfloat16)
+    w = torch.cat([w, w[:, :128]], 1).contiguous()
+    x = torch.randn(M, k, device="cuda", dtype=torch.bfloat16)
+    sizes = np.zeros(E, int)
+    sizes[[0, 500, 1023]] = 30, 1, 9
+    off = torch.from_numpy(_offsets(sizes)).cuda()
+    say("grouped y with 2^26 rows of w")
+    y = mx.grouped_matmul(x, w, off)
+    torch.cuda.synchronize()
+    for e, (a, b) in enumerate(ref.group_rows(off.cpu().numpy(), M)):
+        if a < b:
+            X, W = host(x[a:b]), host(w[e])
+            _rows_match(y[a:b], X @ W.T, X, W, k, "bf16", f"y {e}")
+
+
+def test_orthogonalize_past_2_26_rows():
+    torch.manual_seed(6)
+    x = torch.randn(65535, 1100, 1, device="cuda")
+    say("orthogonalize of 72e6 rows, no steps")
+    out = mx.orthogonalize(x, steps=0)
+    want = x.double() / (x.double().square().sum((1, 2), keepdim=True).sqrt() + 1e-7)
+    assert _every_row(out, want, 2 * U * want.abs())
+    del x, out, want
+    x = torch.randn(64, 1 << 20, 1, device="cuda")
+    say("orthogonalize of 2^26 rows")
+    out = mx.orthogonalize(x)
+    torch.cuda.synchronize()
+    for i in (0, 63):
+        _check_update(out[i], host(x[i]), 5, (3.4445, -4.7750, 2.0315), "f32", i)
+
+
 # ---------------------------------------------------------------- captured graphs
 def test_graphs_that_share_a_workspace():
     """Every operator that needs one, captured into graphs of its own over one workspace and
