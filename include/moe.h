@@ -264,7 +264,7 @@ moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* 
  *   y[r] = w[e] x[r]     for every row r of group e
  *   x [M][k] dtype, w [E][n][k] dtype, y [M][n] dtype.
  * Groups may be empty.  Rows outside every group (before offsets[0], from
- * offsets[E] on) are not read; their y is zero with zero_rest != 0 and left as
+ * offsets[E] on) reach no result; their y is zero with zero_rest != 0 and left as
  * it was with zero_rest == 0.  Offsets outside [0, M] are clamped into it, and
  * one below its predecessor counts as equal to it.
  * bfloat16: exact products, float32 sums, one rounding.  float32: products of

@@ -40,7 +40,7 @@ struct NsSmall {
   static constexpr int SLOTS = 3;               // chunks of X
   static constexpr int NI = 2 * PP / 8 / NW;    // loads per wavefront per chunk
   static constexpr int TA = RB / 2;             // tiles of A per wavefront
-  // lo lo' too: where sums are short, what it leaves out (2^-24.5 of a product) is what their
+  // lo lo' too: where sums are short, what it leaves out (2^-24.5 of a product typically) is what their
   // error consists of (8 x 16: 1.2e-6 -> 1.0e-6 relative, 64 x 64 1.4e-6 -> 1.2e-6, where float32 products
   // have 0.7e-6 and 1.2e-6; 5% of the time).  For sides past 64 it costs 12% and their error is
   // that of float32 products without it.

@@ -12,11 +12,12 @@
 // and in one of three precisions (1, 2 or 3 parts a value):
 //   single  bfloat16, 64 contraction indices per k-step.
 //   split   a float32 value v as two float16, hi = f16(v), lo = f16(v - hi):
-//           22 bits of v survive (|v - hi - lo| <= 2^-24 |v| while lo is a
-//           normal float16), and hi hi' + hi lo' + lo hi' leaves out only lo
-//           lo' <= 2^-24 |v v'|.  Three float16 products at the full matrix
-//           rate thus give float32 accuracy at a third of it, against a
-//           sixteenth for the float32 matrix instructions.  Values are scaled
+//           22 bits of v survive (|lo| <= 2^-11 |v|, |v - hi - lo| <= 2^-23 |v|
+//           while lo is a normal float16), and hi hi' + hi lo' + lo hi' leaves
+//           out lo lo' <= 2^-22 |v v'| (root mean square 2^-24.5).  Three float16
+//           products at the full matrix rate thus give float32 accuracy, to two
+//           or three bits at worst, at a third of that rate, against a ninth
+//           that the float32 matrix instructions reach.  Values are scaled
 //           by powers of two beforehand so that neither part leaves the
 //           float16 range.  Stored per row in units of 128 bytes: 32 hi, then
 //           the 32 lo of the same indices; a k-step is one unit of each row
