@@ -255,3 +255,113 @@ def test_input_gradients_through_weights_of_any_scale(name):
     loud = w.copy()
     loud[:, 3] *= 2.0 ** 40
     _check_dx(x, dev(loud), off, dev(dy), f"{name}: one channel")
+
+
+# ---------------------------------------------------------------- the path with two parts
+@pytest.mark.parametrize("name", [s for s in SHAPES if not SHAPES[s][3]])
+def test_products_of_rows_of_any_scale(name):
+    """Rows of x and of w scaled by factors from 1e-30 to 1e20: each y keeps its own accuracy."""
+    x, w, off, _, r = _normal(name, 7)
+    x *= 10.0 ** r.uniform(-30, 8, (len(x), 1))
+    w *= 10.0 ** r.uniform(-8, 20, (*w.shape[:2], 1))
+    x, w = dev(x), dev(w)
+    say(f"{name}: rows of any scale")
+    y = mx.grouped_matmul(x, w, off)
+    torch.cuda.synchronize()
+    X, W = host(x), host(w)
+    for e, (a, b) in enumerate(ref.group_rows(off.cpu().numpy(), len(X))):
+        ax, aw = np.abs(X[a:b]), np.abs(W[e])
+        t = _tol(ax, aw, x.shape[1]) + 2.0 ** -37.9 * (ax.max(1, initial=0)[:, None] * aw.sum(1) +
+                                                       ax.sum(1)[:, None] * aw.max(1))
+        _same(y[a:b], X[a:b] @ W[e].T, t, f"{name} y {e}")
+
+
+def test_products_with_prepared_weights_past_4_gib():
+    E, n, k = 600, 1024, 2046                            # (a width that goes without the few rows' path)
+    torch.manual_seed(2)
+    sizes = np.zeros(E, int)
+    sizes[[0, 300, 598, 599]] = 3, 70, 1, 6
+    M = int(sizes.sum())
+    _side(M, E, n, k, False, False)
+    x, w = torch.randn(M, k, device="cuda"), torch.randn(E, n, k, device="cuda")
+    dy = torch.randn(M, n, device="cuda")
+    off = torch.from_numpy(_offsets(sizes)).cuda()
+    say("grouped f32, w of 5 GB and its parts")
+    y = mx.grouped_matmul(x, w, off)
+    dx, dw = mx.grouped_matmul_backward(x, w, off, dy)
+    torch.cuda.synchronize()
+    for e, (a, b) in enumerate(ref.group_rows(off.cpu().numpy(), M)):
+        if a < b:
+            X, W, DY = host(x[a:b]), host(w[e]), host(dy[a:b])
+            ax, aw, ady = np.abs(X), np.abs(W), np.abs(DY)
+            _same(y[a:b], X @ W.T, _tol(ax, aw, k), f"y {e}")
+            _same(dx[a:b], DY @ W, _tol(ady, aw.T, n), f"dx {e}")
+            _same(dw[e], DY.T @ X, _tol(ady.T, ax.T, b - a), f"dw {e}")
+    assert not dw[1:300].any() and not dw[301:598].any()
+
+
+# ---------------------------------------------------------------- on both sides of the rules
+@pytest.mark.parametrize("name", SHAPES)
+def test_bad_offsets_are_clamped(name):
+    x, w, _, dy, _ = _normal(name, 8)
+    x, w, dy, M = dev(x), dev(w), dev(dy), len(x)
+    a, b = M // 3, M // 2
+    bad, good = [-9, a, a - 5, M + 1000], [0, a, a, M]
+    tail = len(w) + 1 - len(bad)
+    say(f"{name}: bad offsets")
+    res = []
+    for o in (bad + [b] * tail, good + [M] * tail):
+        o = torch.tensor(o, dtype=torch.int32, device="cuda")
+        res.append((mx.grouped_matmul(x, w, o), *mx.grouped_matmul_backward(x, w, o, dy)))
+    torch.cuda.synchronize()
+    for p, q in zip(*res):
+        assert torch.equal(_bits(p), _bits(q))
+
+
+def _all_calls(ws=None):
+    calls = []
+    for name in SHAPES:
+        if not name.startswith("tiles"):
+            x, w, off, dy, _ = _normal(name, 9)
+            x, w, dy = dev(x), dev(w), dev(dy)
+            calls += [lambda x=x, w=w, off=off: (mx.grouped_matmul(x, w, off, workspace=ws),),
+                      lambda x=x, w=w, off=off, dy=dy: mx.grouped_matmul_backward(x, w, off, dy, workspace=ws),
+                      lambda x=x, w=w, off=off, dy=dy: mx.grouped_matmul_backward(
+                          x, w, off, dy, need_dw=False, workspace=ws)[:1]]
+    return calls
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_repeated_on_another_stream_and_captured(shared):
+    """Every path's calls, with a workspace each or one that all graphs share: the same bits on
+    another stream and in graphs replayed in changing order with eager calls between."""
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda") if shared else None
+    calls = _all_calls(ws)
+    want = [[t.clone() for t in c()] for c in calls]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [c() for c in calls]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for g, v in zip(got, want):
+        assert all(torch.equal(_bits(p), _bits(q)) for p, q in zip(g, v))
+    graphs, outs = [], []
+    for i, c in enumerate(calls):
+        say(f"capture {i}")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+    order = np.random.default_rng(10)
+    for k in range(3):
+        if shared:
+            ws.fill_(255)                        # what other calls left there does not matter
+        for i in order.permutation(len(calls)):
+            for t in outs[i]:
+                t.zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(_bits(p), _bits(q)) for p, q in zip(outs[i], want[i])), (k, i)
+            assert all(torch.equal(_bits(p), _bits(q)) for p, q in zip(calls[i](), want[i])), (k, i)
