@@ -633,18 +633,15 @@ __device__ __forceinline__ void tg_run(const P& p, int tiles, int32_t* counters,
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    if constexpr (C::FM == 2) {
-      constexpr int H = C::FN / 2;
-      const bool hm = t.rows <= C::BM / 2, hn = t.cols <= C::BN / 2;
-      if (hm && hn) tg_tile<C, 1, H, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
-      else if (hm) tg_tile<C, 1, C::FN, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
-      else if (hn) tg_tile<C, 2, H, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
-      else if (P::SYM && p.tri(t))
-        tg_tile<C, 2, C::FN, P::SYM>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
-      else tg_tile<C, 2, C::FN, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
-    } else {
-      tg_tile<C, C::FM, C::FN, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
-    }
+    static_assert(C::FM == 2, "half tiles leave out whole fragments");
+    constexpr int H = C::FN / 2;
+    const bool hm = t.rows <= C::BM / 2, hn = t.cols <= C::BN / 2;
+    if (hm && hn) tg_tile<C, 1, H, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
+    else if (hm) tg_tile<C, 1, C::FN, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
+    else if (hn) tg_tile<C, 2, H, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
+    else if (P::SYM && p.tri(t))
+      tg_tile<C, 2, C::FN, P::SYM>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
+    else tg_tile<C, 2, C::FN, false>(p, t.steps, ph, wave, lane, next, c, ld, off, acc, lds);
     // the loads in flight are waited for here (the next tile's first k-steps; the very
     // first one landed before the last barrier): its loop needs no wait for them
     MOE_WAIT_VMCNT(0);
