@@ -523,7 +523,7 @@ struct FewProduct {
 // Bytes of x's split row.
 __host__ __device__ inline long long few_pitch(int k) { return (long long)((k + 31) / 32) * 192; }
 
-// x's rows (of a multiple of 4 values; 64 kGroupedMaxE at most), one wavefront each.
+// x's rows (of a multiple of 4 values; 128 kGroupedMaxE at most), one wavefront each.
 __global__ __launch_bounds__(256) void split_three_kernel(const float* __restrict__ x, int rows, int k,
                                                           u32x4* __restrict__ out) {
   const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -726,16 +726,21 @@ hipError_t run_few(const GroupedArgs& a, const void* in, uint8_t* planes, void* 
   return hipGetLastError();
 }
 
-// Up to 64 rows per group on average; w 2048 x 1408 and 64 groups, general path -> this one: 6 rows
-// 432 -> 174 us (4.3 TB/s), 1 row 161 us (4.6 TB/s); 1408 x 2048, 32 rows 470 -> 221 us, 64 rows
-// 499 -> 368 us; of 96 rows it would read w three times (513 | 532 us).  dx, 6 rows 580 -> 162 us, 32 rows
-// 559 -> 199 us, 64 rows 576 -> 310 us, 96 rows 595 us either way.  The widths keep the
-// workspace of fewer rows the smaller one, and the tile's 64 columns in use.
+// y: up to 64 rows per group on average.  w 1408 x 2048 and 64 groups, general path -> this one: 6 rows
+// 461 -> 175 us (4.2 TB/s), 32 rows 482 -> 222 us, 64 rows 473 -> 384 us; 65 rows 491 | 477 us and 96
+// rows, for which it reads w three times, 499 | 541 us; 128 groups of 65 rows, 1000 x 1000, 373 | 482 us.
+// Uneven groups read w more often, on either path: of 64 rows on average with sizes as 1 / rank
+// (the largest 881 rows) 495 -> 432 us, all rows in one group 363 -> 283 us.
+// dx: up to 128 rows, as the general path has six products there: 6 rows 625 -> 157 us, 64 rows 663 -> 311
+// us, 96 rows 712 -> 464 us, 128 rows 735 -> 570 us, 160 rows 784 | 779 us (2048 x 1408: 905 | 834 us, 128
+// groups of 1000 x 1000: 641 | 720 us); uneven, 64 rows, the largest 881, 747 -> 360 us.
+// The widths keep the workspace of fewer rows the smaller one (few_pitch(n) M against w's parts),
+// and the tile's 64 columns in use.
 bool few_rows(int dtype, int M, int E, int n, int k) {
   return dtype == 0 && k % 4 == 0 && n >= 32 && M <= 64LL * E;
 }
 bool few_rows_dx(int dtype, int M, int E, int n, int k) {
-  return few_rows(dtype, M, E, n, k) && n % 4 == 0 && k >= 192;
+  return dtype == 0 && k % 4 == 0 && n % 4 == 0 && n >= 32 && k >= 192 && M <= (k >= 256 ? 128LL : 64LL) * E;
 }
 
 struct Carve {

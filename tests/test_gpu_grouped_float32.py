@@ -30,7 +30,7 @@ def _few(M, E, n, k):
 
 
 def _few_dx(M, E, n, k):
-    return _few(M, E, n, k) and n % 4 == 0 and k >= 192
+    return k % 4 == 0 and n % 4 == 0 and n >= 32 and k >= 192 and M <= E * (128 if k >= 256 else 64)
 
 
 def _size(query, *args):
@@ -90,11 +90,12 @@ def _check_all(x, w, off, dy, label, floor=0.0):
             _same(dw[e], DY[a:b].T @ X[a:b], _tol(fdy[a:b].T, fx[a:b].T, b - a), f"{label} dw {e}")
 
 
-# rows of the groups, n, k, and the sides of the rules: few rows, few rows with a width for y only, an odd
-# width, many rows (tiles of 64), and of tiles of 128 and 256
+# rows of the groups, n, k, and the sides of the rules: few rows, few rows with a width for y only, and for
+# dx only, an odd width, many rows (tiles of 64), and of tiles of 128 and 256
 SHAPES = {
     "few": ([30, 64, 0, 9], 48, 200, True, True),
     "few y": ([30, 64, 0, 9], 48, 72, True, False),
+    "few dx": ([100, 200, 0, 130], 72, 260, False, True),
     "odd width": ([30, 64, 0, 9], 50, 203, False, False),
     "many rows": ([300, 150, 0, 9], 72, 200, False, False),
     "tiles of 128": ([900, 830, 0, 1100, 900], 1000, 780, False, False),

@@ -162,6 +162,17 @@ def test_workspaces_grow_with_the_rows(lib):
             assert [b for _, b in got] == sorted(b for _, b in got), (E, n, k, dt, args)
 
 
+def test_float32_workspaces_grow_across_the_few_rows_rules(lib):
+    for n, k in itertools.product((32, 33, 36, 64, 68, 100, 1408), (4, 96, 192, 252, 256, 260, 2048)):
+        for E in (1, 3, 64):
+            rows = sorted({r * E + d for r in (1, 63, 64, 65, 127, 128, 129, 300) for d in (-1, 0, 1)})
+            for args in ((), (1, 0), (0, 1), (1, 1)):
+                query = (lib.moe_grouped_matmul_backward_workspace_size if args
+                         else lib.moe_grouped_matmul_workspace_size)
+                got = [size(query, M, E, n, k, 0, *args)[1] for M in rows]
+                assert got == sorted(got), (E, n, k, args, got)
+
+
 # ---------------------------------------------------------------- orthogonalised update
 def _ortho(lib, x=1 << 30, xs=64 * 128, B=2, m=64, n=128, dt=0, steps=5, eps=1e-7, a=3.4445,
            b=-4.7750, c=2.0315, out=1 << 34, os_=64 * 128, odt=0, ws=BIG, wsb=1 << 40):
