@@ -287,7 +287,7 @@ moe_status_t moe_grouped_matmul(const void* x, const void* w, const int32_t* off
  * (not both NULL unless M = 0).  A group without rows gets a zero dw, M = 0 included; dx
  * outside the groups as y above.  x may be NULL without dw, w without dx.
  * float32: products of three-bfloat16 splits, float32 accuracy however much
- * experts, rows and channels differ. */
+ * experts, rows and channels differ; results that are not finite as for y. */
 moe_status_t moe_grouped_matmul_backward_workspace_size(int M, int E, int n, int k, int dtype,
                                                         int want_dx, int want_dw, size_t* bytes);
 moe_status_t moe_grouped_matmul_backward(const void* x, const void* w, const int32_t* offsets,

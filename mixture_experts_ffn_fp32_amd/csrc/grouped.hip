@@ -22,8 +22,9 @@
 // The parts of an infinity are an infinity and NaN, so a float32 result with one among its
 // operands comes out as NaN, and what leaves float32's range on the way as either.  Every
 // float32 result that is not finite is therefore summed again from the operands themselves,
-// in float64 (grouped_again).  The search of the results in registers takes up to 1% of y's and
-// dx's time where all are finite.
+// in float64 (grouped_again).  The search of the results in registers takes up to 1% of y's
+// time where all are finite; an infinity in every row of x, 28665 of 1280 values, takes y
+// from 0.4 to 79 ms.
 //
 // Measured: y of 49152 rows in 64 groups, 1408 x 2048 bfloat16, 315 us (902 TFLOP/s of the 1338 that one
 // dense product reaches here; MFMAs busy 45%); of 384 rows, 2048 x 1408, 69 us (HBM bound, 5.4

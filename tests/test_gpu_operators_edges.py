@@ -207,6 +207,38 @@ def test_layer_norm_past_4_gib():
         assert torch.equal(rstd[rows], s) and torch.equal(_bits(dx[rows]), _bits(again))
 
 
+# ---------------------------------------------------------------- the widest rows
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,k", [(100, 1 << 20), (1 << 20, 100), (96, (1 << 20) - 1), (1, 1 << 20)])
+def test_grouped_widest_rows(n, k, dtype):
+    """n and k up to 2^20, against the definition in float64 on the GPU (one group and a rest)."""
+    M, a, b = 300, 7, 297
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    torch.manual_seed(7)
+    x, w = torch.randn(M, k, device="cuda").to(dt), torch.randn(1, n, k, device="cuda").to(dt)
+    dy = torch.randn(M, n, device="cuda").to(dt)
+    off = torch.tensor([a, b], dtype=torch.int32, device="cuda")
+    say(f"grouped n={n} k={k} {dtype}")
+    y = mx.grouped_matmul(x, w, off)
+    dx, dw = mx.grouped_matmul_backward(x, w, off, dy)
+    torch.cuda.synchronize()
+    X, W, DY = x[a:b].double(), w[0].double(), dy[a:b].double()
+
+    def check(got, p, q, terms, store, label):
+        """got = p q within the bounds of test_gpu_grouped_float32.py."""
+        want, t = p @ q, (12 * (terms + 8) + 8) * U * (p.abs() @ q.abs())
+        if dtype == "f32" and label == "y":
+            t += 2.0 ** -37.9 * (p.abs().amax(1)[:, None] * q.abs().sum(0) +
+                                 p.abs().sum(1)[:, None] * q.abs().amax(0))
+        assert _every_row(got, want, t + store * (want.abs() + t)), label
+
+    check(y[a:b], X, W.t().contiguous(), k, STORE[dtype], "y")
+    check(dx[a:b], DY, W, n, STORE[dtype], "dx")
+    check(dw[0], DY.t().contiguous(), X, b - a, U, "dw")
+    for t in (y, dx):
+        assert not t[:a].any() and not t[b:].any()
+
+
 # ---------------------------------------------------------------- past 2^26 rows
 # (a launch of one wavefront per row would hold 2^32 threads, of which some would never run)
 def _every_row(got, want, tol):
