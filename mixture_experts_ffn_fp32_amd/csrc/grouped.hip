@@ -26,11 +26,12 @@
 // time where all are finite; an infinity in every row of x, 28665 of 1280 values, takes y
 // from 0.4 to 79 ms.
 //
-// Measured: y of 49152 rows in 64 groups, 1408 x 2048 bfloat16, 315 us (902 TFLOP/s of the 1338 that one
-// dense product reaches here; MFMAs busy 45%); of 384 rows, 2048 x 1408, 69 us (HBM bound, 5.4
-// TB/s); both gradients of 28672 rows in 63 groups, 896 x 1280, 245 us (dw's 289 MB written at
-// 2.1 TB/s, dx 590 TFLOP/s); float32 y of 8190 rows in 16 groups, 896 x 1280, 115 us, of which
-// 44 us split x and w at 5.2 TB/s.
+// Measured: y of 49152 rows in 64 groups, 1408 x 2048 bfloat16, 313 to 331 us (905 to 856 TFLOP/s of the
+// 1338 that one dense product reaches here; MFMAs busy 47%); of 384 rows, 2048 x 1408, 69 us (HBM
+// bound, 5.4 TB/s); both gradients of 28672 rows in 63 groups, 896 x 1280, 240 to 251 us (dw's 289 MB
+// written at 2.2 TB/s, dx 635 TFLOP/s); float32 y of 8190 rows in 16 groups, 896 x 1280, 108 us, of
+// which 38 us split x and w.  float32 gradients of those 28672 rows: 228 us for the parts of dy, x
+// and w (1.08 GB, 4.7 TB/s), dx 423 us and dw 447 us (930 and 880 TFLOP/s of bfloat16 products).
 #include <float.h>
 
 #include <algorithm>

@@ -24,9 +24,11 @@
 // epilogue writes the next one's operand directly.  The norm is summed in
 // float64 (squares of small gradients leave float32's range).
 //
-// Measured, five steps: 64 float32 matrices of 1408 x 2048 15.0 ms (960 TFLOP/s of float16 products, of
-// the 1415 that one dense product reaches here; power holds the clock at 1.9 GHz); 4 bfloat16
-// ones of 1280 x 896 460 us, where each of the 15 products is about one tile per CU.
+// Measured, five steps: 64 float32 matrices of 1408 x 2048 14.9 to 15.9 ms (970 to 908 TFLOP/s of float16
+// products, from card to card, of the 1415 that one dense product reaches here; X's product 1.46 ms, 1.32 times what
+// that rate gives, the symmetric ones 0.82 ms, 1.77 times: their 21 tiles a matrix end unevenly and
+// are written twice); 4 bfloat16 ones of 1280 x 896 428 to 470 us, where each of the 15
+// products is about one tile per CU.
 #include <math.h>
 
 #include <algorithm>
