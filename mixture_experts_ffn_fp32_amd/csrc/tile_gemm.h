@@ -30,9 +30,11 @@
 //           parts need no scale, so a product is as exact as a float32 one whatever its
 //           neighbours along the contraction or in other rows are; that costs six bfloat16
 //           products for the three of `split`.  Values are stored times 2^24 (kTgLift), which
-//           keeps the parts of the smallest ones normal numbers.  The parts of a matrix are
-//           planes in its rows, and a block of 64 contraction indices takes six k-steps of the
-//           single kind, one per product (tg_offset).
+//           keeps the parts of the smallest ones normal numbers (and takes values from 2^104 and
+//           sums from 2^80 on out of the range, as infinities and NaN, which the caller has to
+//           replace).  The parts of a matrix are planes in its rows, and a block of 64
+//           contraction indices takes six k-steps of the single kind, one per product
+//           (tg_offset).
 #pragma once
 
 #include "lds_dma.h"
