@@ -311,11 +311,11 @@ def run(state):
         import mixture_experts_ffn_fp32_amd as moe
 
         if op == "f8":
-            return moe.grouped_matmul_f8(s["x"], s["xs"], s["w"], s["ws"], s["offsets"],
-                                         out_dtype=s["dtype"])
+            return moe.grouped_matmul_quantized(s["x"], s["xs"], s["w"], s["ws"], s["offsets"],
+                                                out_dtype=s["dtype"])
         if op == "f8_dx":
-            return moe.grouped_matmul_f8_dx(s["x"], s["xs"], s["w"], s["ws"], s["offsets"],
-                                            out_dtype=s["dtype"])
+            return moe.grouped_matmul_quantized_dx(s["x"], s["xs"], s["w"], s["ws"], s["offsets"],
+                                                   out_dtype=s["dtype"])
         if op == "quantize_rows":
             q, scales = moe.quantize_rows(s["x"], s["f8"])
             return dict(q=q, scales=scales)
