@@ -45,7 +45,12 @@
 extern "C" {
 #endif
 
-typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 } moe_dtype_t;
+typedef enum {
+  MOE_DTYPE_F32 = 0,
+  MOE_DTYPE_BF16 = 1,
+  MOE_DTYPE_E4M3 = 2, /* 8 bits, OCP: largest value 448, no infinity (8-bit operators only) */
+  MOE_DTYPE_E5M2 = 3  /* 8 bits, OCP: largest value 57344 (8-bit operators only)            */
+} moe_dtype_t;
 
 typedef enum {
   MOE_OK = 0,
@@ -226,6 +231,17 @@ moe_status_t moe_layer_backward(const void* u, const void* E_gate, const void* W
                                 float* dW_shared, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* The same with losses beside h: dlogits [T][N] float32 (or NULL), the gradient of the
+ * router's logits (bias included) that they give, as moe_balance_loss_backward
+ * writes it, is added to dz before du, dE_gate and dgate_bias are formed.  It must
+ * not overlap an output or the workspace (moe_backward_workspace_size() bytes). */
+moe_status_t moe_layer_backward_aux(const void* u, const void* E_gate, const void* W_routed,
+                                    const void* W_shared, int N, int K, int K_s, int T, int d,
+                                    int I, int dtype, const float* gate_bias, const void* dh,
+                                    const float* dlogits, void* du, float* dE_gate,
+                                    float* dgate_bias, float* dW_routed, float* dW_shared,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* ================================================================
  * Operators beside the layer, for the block around it and for experts of a
  * caller's own making.  They share the conventions above except the limits:
@@ -316,6 +332,111 @@ moe_status_t moe_orthogonalize(const void* x, int64_t x_stride, int B, int m, in
                                int steps, float eps, float a, float b, float c, void* out,
                                int64_t out_stride, int out_dtype, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/* ---- root-mean-square norm, with the residual's addition and an output in 8 bits ----
+ *   h = x + residual, rounded to dtype (h = x without residual)
+ *   rstd_t = 1 / sqrt((1/d) sum_j h_tj^2 + eps),  y_tj = h_tj rstd_t weight_j
+ *   x, residual (or NULL), h [T][d] dtype, weight [d] dtype or NULL (ones), rstd [T]
+ *   float32 or NULL (the backward needs h and rstd).  h may be NULL (not wanted), and
+ *   may be x or residual itself.
+ * y_dtype = dtype: y [T][d], scales NULL.  y_dtype MOE_DTYPE_E4M3 or _E5M2: y [T][d] in
+ * 8 bits with scales [T][ceil(d / 128)], quantised as moe_quantize_rows does from
+ * the float32 values.
+ * Any T >= 0; 1 <= d <= 2^24.  A row's sum of squares has to stay inside float32. */
+moe_status_t moe_rms_norm(const void* x, const void* residual, const void* weight, int T, int d,
+                          float eps, int dtype, int y_dtype, void* h, void* y, float* scales,
+                          float* rstd, void* stream);
+
+/* Gradients of sum_t dy_t . y_t + dh_t . h_t (g = dy weight, hh = h rstd):
+ *   dx = rstd (g - hh mean_j(g hh)) + dh   [T][d] dtype, of x and of residual alike
+ *   dweight = sum_t dy hh                  [d] float32, may be NULL
+ * dh [T][d] dtype is what reaches h from later layers, or NULL; dx may be dh itself.
+ * rstd is the forward's.  An 8-bit y has the gradient of the values it stands for.
+ * T = 0 gives a zero dweight.  The workspace is needed where dweight is given (not
+ * for T = 0). */
+moe_status_t moe_rms_norm_backward_workspace_size(int T, int d, int dtype, size_t* bytes);
+moe_status_t moe_rms_norm_backward(const void* dy, const void* h, const void* weight,
+                                   const float* rstd, const void* dh, int T, int d, int dtype,
+                                   void* dx, float* dweight, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* ---- 8 bits with a scale for each block of 128 ----
+ *   scale = max |v| / most over the block's finite values (most: 448 or 57344; 1 for a
+ *   block of zeros, never below 2^-126),  q = v / scale rounded to nearest even
+ * A value that is not finite becomes NaN and leaves the others of its block alone.
+ * Rows: x [T][d] dtype -> q [T][d] q_dtype, scales [T][ceil(d / 128)] float32, one for
+ * each 128 columns of a row.  Any T >= 0; 1 <= d <= 2^24. */
+moe_status_t moe_quantize_rows(const void* x, int T, int d, int dtype, int q_dtype, void* q,
+                               float* scales, void* stream);
+/* Matrices: w [E][n][k] dtype -> q [E][n][k] q_dtype, scales [E][ceil(n / 128)][ceil(k / 128)],
+ * one for each 128 x 128 of a matrix.  E >= 0; n, k <= 2^20, at most 2^23 blocks. */
+moe_status_t moe_quantize_blocks(const void* w, int E, int n, int k, int dtype, int q_dtype,
+                                 void* q, float* scales, void* stream);
+/* Rows read back: x = q scale, rounded to dtype (for a weight gradient from rows that were
+ * kept in 8 bits: moe_grouped_matmul_backward takes x). */
+moe_status_t moe_dequantize_rows(const void* q, const float* scales, int T, int d, int q_dtype,
+                                 int dtype, void* x, void* stream);
+
+/* ---- products of 8-bit operands grouped by expert, ragged ----
+ * moe_grouped_matmul for 8-bit rows and weights:
+ *   y[r][i] = sum_b xs[r][b] ws[e][i / 128][b] sum_{j in block b} x[r][j] w[e][i][j]
+ *   x [M][k] x_dtype (MOE_DTYPE_E4M3 or _E5M2), xs [M][ceil(k / 128)],
+ *   w [E][n][k] MOE_DTYPE_E4M3, ws [E][ceil(n / 128)][ceil(k / 128)],
+ *   y [M][n] out_dtype (MOE_DTYPE_F32 or _BF16).
+ * Groups, offsets and zero_rest as in moe_grouped_matmul; offsets NULL with E = 1: one
+ * group of all the rows.  Scales may be any float32 values; a product of two scales
+ * below 2^-126 loses digits.  Exact products; a float32 result has float32 sums, a
+ * bfloat16 result sums in which eight neighbours along the contraction are added first,
+ * each cut off 13 bits below the largest product of the eight (far below the
+ * result's rounding, unless almost everything cancels).
+ * Limits: 1 <= E <= 1024; n, k <= 2^20. */
+moe_status_t moe_grouped_matmul_quantized_workspace_size(int M, int E, int n, int k,
+                                                         size_t* bytes);
+moe_status_t moe_grouped_matmul_quantized(const void* x, const float* xs, const void* w,
+                                          const float* ws, const int32_t* offsets, int M, int E,
+                                          int n, int k, int x_dtype, int out_dtype, int zero_rest,
+                                          void* y, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+/* The rows' gradient, from 8-bit rows of dy (quantised along n) and the same weights:
+ *   dx[r][j] = sum_b dys[r][b] ws[e][b][j / 128] sum_{i in block b} dy[r][i] w[e][i][j]
+ *   dy [M][n] dy_dtype, dys [M][ceil(n / 128)], dx [M][k] out_dtype. */
+moe_status_t moe_grouped_matmul_quantized_dx_workspace_size(int M, int E, int n, int k,
+                                                            size_t* bytes);
+moe_status_t moe_grouped_matmul_quantized_dx(const void* dy, const float* dys, const void* w,
+                                             const float* ws, const int32_t* offsets, int M, int E,
+                                             int n, int k, int dy_dtype, int out_dtype,
+                                             int zero_rest, void* dx, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/* ---- balance loss with its gradient, per batch or per sequence ----
+ * The losses of moe_balance_stats for S sequences of rows, sequence s being rows
+ * offsets[s] .. offsets[s+1] - 1 (device, int32, treated as in moe_grouped_matmul; NULL
+ * with S = 1: all rows), over its n rows that mask keeps (device, one byte a row, not
+ * zero: counts; NULL: all).  Masked rows and rows of no sequence are not read.
+ *   counts_si = #{(t, k) : idx[t][k] = i} (entries outside [0, N) are not counted),
+ *   f_si = N counts_si / (K n),  P_si = (1/n) sum_t scores_ti
+ *   losses_s0 = alpha1 sum_i f_si P_si,  losses_s1 = alpha2 sum_g f'_sg P'_sg
+ * with device_of [N] int32 (device; an entry outside [0, D) puts its expert on no
+ * device), f' the mean and P' the sum over a device's experts; device_of NULL:
+ * losses_s1 = 0.  A sequence without rows gives zeros.
+ *   counts [S][N] int32; P [S][N], losses [S][2] float32;
+ *   slopes [S][2][N] float32: d losses / d scores, the same in each of the n rows.
+ * Sums are float64.  Limits: 1 <= K <= N <= 256, 1 <= S <= 1024, 0 <= D <= 256. */
+moe_status_t moe_balance_loss_workspace_size(int T, int N, int S, size_t* bytes);
+moe_status_t moe_balance_loss(const float* scores, const int32_t* idx, const int32_t* offsets,
+                              const uint8_t* mask, const int32_t* device_of, int T, int N, int K,
+                              int S, int D, float alpha1, float alpha2, int32_t* counts, float* P,
+                              float* losses, float* slopes, void* workspace,
+                              size_t workspace_bytes, void* stream);
+/* Gradient of sum_s dlosses_s . losses_s by the logits behind scores = softmax(logits), the
+ * selection idx held fixed:
+ *   c = dlosses_s0 slopes_s0 + dlosses_s1 slopes_s1,  dlogits_ti = s_ti (c_i - sum_j s_tj c_j)
+ *   dlosses [S][2] float32 or NULL (ones); dlogits [T][N] float32, zero for masked rows
+ *   and rows of no sequence.  moe_layer_backward_aux takes dlogits on to u and E_gate. */
+moe_status_t moe_balance_loss_backward(const float* scores, const float* slopes,
+                                       const float* dlosses, const int32_t* offsets,
+                                       const uint8_t* mask, int T, int N, int S, float* dlogits,
+                                       void* stream);
 
 /* ---- per-stage timing (for profiling; off by default) ----
  * When enabled, moe_layer_forward records a HIP event pair around each of its

@@ -3,8 +3,10 @@
 The library (libmoe.so, built by ``python -m mixture_experts_ffn_fp32_amd.build``)
 does all of the layer's work; this package only marshals arguments to it.
 """
-from .moe import (MoEError, STAGE_NAMES, backward_workspace_size, balance_stats, combine,  # noqa: F401
-                  dispatch, expert_ffn, grouped_matmul, grouped_matmul_backward, layer_backward,
-                  layer_forward, layer_forward_static, layer_norm, layer_norm_backward,
-                  load_library, orthogonalize, route,
-                  timing_enable, timing_read, workspace_size)
+from .moe import (MoEError, STAGE_NAMES, backward_workspace_size, balance_loss,  # noqa: F401
+                  balance_loss_backward, balance_stats, combine, dequantize_rows, dispatch,
+                  expert_ffn, grouped_matmul, grouped_matmul_backward, grouped_matmul_quantized,
+                  grouped_matmul_quantized_dx, layer_backward, layer_forward,
+                  layer_forward_static, layer_norm, layer_norm_backward, load_library,
+                  orthogonalize, quantize_blocks, quantize_rows, rms_norm, rms_norm_backward,
+                  rms_norm_quantized, route, timing_enable, timing_read, workspace_size)

@@ -419,7 +419,8 @@ __global__ void bw_slot_of_kernel(const int32_t* __restrict__ sorted_pair, int T
 }
 
 // Softmax backward per token (one 64-lane wavefront per token): dz from the
-// scores and the K gate gradients; dz kept in float32 and in the storage type.
+// scores and the K gate gradients, and what losses beside h (the balance loss)
+// add to it; dz kept in float32 and in the storage type.
 template <class E>
 __global__ __launch_bounds__(256) void bw_softmax_kernel(BwdArgs a, const float* __restrict__ s,
                                                          const int32_t* __restrict__ idx,
@@ -441,6 +442,7 @@ __global__ __launch_bounds__(256) void bw_softmax_kernel(BwdArgs a, const float*
       for (int k = 0; k < a.K; ++k)
         if (idx[(size_t)t * a.K + k] == i) dsi = ds_pair[(size_t)t * a.K + k];
       v = s[(size_t)t * a.N + i] * (dsi - dot);
+      if (a.dlogits != nullptr) v += a.dlogits[(size_t)t * a.N + i];
       dz[(size_t)t * a.N + i] = v;
     }
     store_from_f32<E>((Tp*)a.dzE + (size_t)t * a.NP + i, v);

@@ -1,0 +1,223 @@
+// Balance loss of the routing with its gradient, per batch or per sequence (DeepSeekMoE paper
+// summary, papercache.org, sec. 3.3, expert-level and device-level balance losses), over the n
+// rows of a sequence that are not masked:
+//
+//   count_i = #{(t, k) : idx[t][k] = i},  f_i = N count_i / (K n),  P_i = (1/n) sum_t s_ti
+//   L_0 = alpha1 sum_i f_i P_i,  L_1 = alpha2 sum_g f'_g P'_g
+//   f'_g = mean of f_i, P'_g = sum of P_i over the experts of device g
+//
+// The counts are whole numbers that no score's small change moves, so the losses are linear in
+// the scores, with the same slopes in every row of a sequence:
+//
+//   dL_0 / ds_ti = alpha1 f_i / n,  dL_1 / ds_ti = alpha2 f'_{g(i)} / n
+//
+// and through the softmax  dlogits_ti = s_ti (c_i - sum_j s_tj c_j),  c = the slopes times the
+// losses' own gradients.
+//
+// Small passes over the scores (16384 x 128: 8 MB each way), bound by launches and, for the
+// large ones, by HBM.  Forward: one launch for partial sums of kBlRows rows (float64, counts as
+// whole numbers), one that joins a sequence's partial sums in order.  Backward: one launch, a
+// wavefront per row.  Every sum has a fixed order.
+#include <algorithm>
+
+#include "groups.h"
+#include "ops_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kBlRows = 64;
+
+// Partial sums of one chunk of a sequence: block b takes the b-th chunk of kBlRows rows.
+__global__ __launch_bounds__(256) void balance_loss_partial_kernel(BalanceLossArgs a) {
+  __shared__ GroupTables t;
+  __shared__ int cnt[256], valid[kBlRows];
+  __shared__ double sum[256];
+  const int tid = threadIdx.x, N = a.N;
+  group_tables<GR_FWD>(GroupDims{a.T, a.S, 0, 0}, a.offsets, kBlRows, t);
+  const int b = blockIdx.x;
+  if (b >= t.tiles[a.S]) return;
+  const int s = group_of(t.tiles, a.S, b, 0);
+  const int t0 = t.off[s] + (b - t.tiles[s]) * kBlRows, rows = min(kBlRows, t.off[s + 1] - t0);
+  if (tid < N) cnt[tid] = 0;
+  if (tid < kBlRows) valid[tid] = tid < rows && (a.mask == nullptr || a.mask[t0 + tid] != 0);
+  __syncthreads();
+  for (int j = tid; j < rows * a.K; j += 256) {
+    const int e = a.idx[(size_t)t0 * a.K + j];
+    if (valid[j / a.K] && (unsigned)e < (unsigned)N) atomicAdd(&cnt[e], 1);
+  }
+  // 256 / NP rows at a time, NP columns each
+  const int NP = N <= 64 ? 64 : N <= 128 ? 128 : 256, c = tid & (NP - 1), g = tid / NP;
+  double p = 0.0;
+  if (c < N)
+    for (int r = g; r < rows; r += 256 / NP)
+      if (valid[r]) p += (double)a.scores[(size_t)(t0 + r) * N + c];
+  sum[tid] = p;
+  __syncthreads();
+  if (tid < N) {
+    for (int q = NP; q < 256; q += NP) p += sum[q + tid];
+    a.psum[(size_t)b * N + tid] = p;
+    a.pcnt[(size_t)b * (N + 1) + tid] = cnt[tid];
+  }
+  if (tid < 64) {
+    const int n = __popcll(__ballot(valid[tid] != 0));
+    if (tid == 0) a.pcnt[(size_t)b * (N + 1) + N] = n;
+  }
+}
+static_assert(kBlRows == 64, "a wavefront counts a chunk's rows");
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) v += __shfl_xor(v, k);
+  return v;
+}
+
+// One block per sequence.
+__global__ __launch_bounds__(1024) void balance_loss_final_kernel(BalanceLossArgs a) {
+  __shared__ GroupTables t;
+  __shared__ double sum[1024], l0[4], l1[4];
+  __shared__ int cnt[1024], dev_cnt[256], dev_size[256], s_n;
+  const int tid = threadIdx.x, N = a.N, s = blockIdx.x;
+  group_tables<GR_FWD>(GroupDims{a.T, a.S, 0, 0}, a.offsets, kBlRows, t);
+  const int b0 = t.tiles[s], b1 = t.tiles[s + 1];
+  const int NP = N <= 64 ? 64 : N <= 128 ? 128 : 256, c = tid & (NP - 1), g = tid / NP;
+  double p = 0.0;
+  int n = 0;
+  if (c < N)
+    for (int b = b0 + g; b < b1; b += 1024 / NP) {
+      p += a.psum[(size_t)b * N + c];
+      n += a.pcnt[(size_t)b * (N + 1) + c];
+    }
+  sum[tid] = p;
+  cnt[tid] = n;
+  if (tid < 256) dev_cnt[tid] = dev_size[tid] = 0;
+  if (tid < 64) {
+    int v = 0;
+    for (int b = b0 + tid; b < b1; b += 64) v += a.pcnt[(size_t)b * (N + 1) + N];
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) v += __shfl_xor(v, k);
+    if (tid == 0) s_n = v;
+  }
+  __syncthreads();
+  const double rows = s_n > 0 ? (double)s_n : 1.0;  // no rows: every sum is zero
+  int of = -1;
+  if (tid < N) {
+    for (int q = NP; q < 1024; q += NP) {
+      p += sum[q + tid];
+      n += cnt[q + tid];
+    }
+    if (a.device_of != nullptr) {
+      of = a.device_of[tid];
+      if ((unsigned)of >= (unsigned)a.D) of = -1;
+    }
+    if (of >= 0) {
+      atomicAdd(&dev_cnt[of], n);
+      atomicAdd(&dev_size[of], 1);
+    }
+  }
+  __syncthreads();
+  double v0 = 0.0, v1 = 0.0;
+  if (tid < N) {
+    const double unit = (double)N / ((double)a.K * rows), P = p / rows;
+    const double f = (double)a.alpha1 * unit * n;
+    const double fd = of >= 0 ? (double)a.alpha2 * unit * dev_cnt[of] / dev_size[of] : 0.0;
+    const size_t at = (size_t)s * N + tid;
+    a.counts[at] = n;
+    a.P[at] = (float)P;
+    a.slopes[2 * (size_t)s * N + tid] = (float)(f / rows);
+    a.slopes[(2 * (size_t)s + 1) * N + tid] = (float)(fd / rows);
+    v0 = f * P;
+    v1 = fd * P;
+  }
+  if (tid < 256) {
+    v0 = wave_sum_f64(v0);
+    v1 = wave_sum_f64(v1);
+    if ((tid & 63) == 0) {
+      l0[tid >> 6] = v0;
+      l1[tid >> 6] = v1;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    a.losses[2 * s] = (float)(l0[0] + l0[1] + l0[2] + l0[3]);
+    a.losses[2 * s + 1] = (float)(l1[0] + l1[1] + l1[2] + l1[3]);
+  }
+}
+
+// One wavefront per row, four columns a lane at most; rows of no sequence and masked ones are
+// zeros.
+__global__ __launch_bounds__(256) void balance_loss_backward_kernel(BalanceLossArgs a) {
+  __shared__ GroupTables t;
+  const int lane = threadIdx.x & 63, N = a.N;
+  group_tables<GR_FWD>(GroupDims{a.T, a.S, 0, 0}, a.offsets, kBlRows, t);
+  const int first = t.off[0], last = t.off[a.S];
+  int known = -1;  // the sequence whose slopes c holds
+  float c[4] = {0.f, 0.f, 0.f, 0.f};
+  for (long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); r < a.T;
+       r += (long long)gridDim.x * 4) {
+    const int row = uni((int)r);
+    const bool on = row >= first && row < last && (a.mask == nullptr || a.mask[row] != 0);
+    float* out = a.dlogits + (size_t)row * N;
+    if (!on) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane + 64 * i < N) out[lane + 64 * i] = 0.f;
+      continue;
+    }
+    const int s = uni(group_of(t.off, a.S, row, max(known, 0)));
+    if (s != known) {
+      known = s;
+      const float d0 = a.dlosses != nullptr ? a.dlosses[2 * s] : 1.f;
+      const float d1 = a.dlosses != nullptr ? a.dlosses[2 * s + 1] : 1.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = lane + 64 * i;
+        c[i] = j < N ? d0 * a.slopes[2 * (size_t)s * N + j] + d1 * a.slopes[(2 * (size_t)s + 1) * N + j]
+                     : 0.f;
+      }
+    }
+    const float* from = a.scores + (size_t)row * N;
+    float v[4], dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = lane + 64 * i;
+      v[i] = j < N ? from[j] : 0.f;
+      dot += v[i] * c[i];
+    }
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) dot += __shfl_xor(dot, k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (lane + 64 * i < N) out[lane + 64 * i] = v[i] * (c[i] - dot);
+  }
+}
+
+long long balance_loss_chunks(int T, int S) { return (T + kBlRows - 1LL) / kBlRows + S; }
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t balance_loss_workspace_bytes(int T, int N, int S) {
+  const size_t b = (size_t)balance_loss_chunks(T, S);
+  return align256(b * N * 8) + b * (N + 1) * 4;
+}
+
+hipError_t launch_balance_loss(BalanceLossArgs a, void* ws, hipStream_t st) {
+  const long long chunks = balance_loss_chunks(a.T, a.S);
+  a.psum = (double*)ws;
+  a.pcnt = (int32_t*)((char*)ws + align256((size_t)chunks * a.N * 8));
+  if (a.T > 0) {
+    balance_loss_partial_kernel<<<(unsigned)chunks, 256, 0, st>>>(a);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  balance_loss_final_kernel<<<a.S, 1024, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_loss_backward(const BalanceLossArgs& a, hipStream_t st) {
+  const unsigned grid = (unsigned)std::min<long long>((a.T + 3LL) / 4, 2048);
+  balance_loss_backward_kernel<<<grid, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

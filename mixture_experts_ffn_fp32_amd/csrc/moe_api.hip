@@ -747,6 +747,17 @@ moe_status_t moe_layer_backward(const void* u, const void* E_gate, const void* W
                                 float* dE_gate, float* dgate_bias, float* dW_routed,
                                 float* dW_shared, void* workspace, size_t workspace_bytes,
                                 void* stream) {
+  return moe_layer_backward_aux(u, E_gate, W_routed, W_shared, N, K, K_s, T, d, I, dtype, gate_bias,
+                                dh, nullptr, du, dE_gate, dgate_bias, dW_routed, dW_shared,
+                                workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_layer_backward_aux(const void* u, const void* E_gate, const void* W_routed,
+                                    const void* W_shared, int N, int K, int K_s, int T, int d,
+                                    int I, int dtype, const float* gate_bias, const void* dh,
+                                    const float* dlogits, void* du, float* dE_gate,
+                                    float* dgate_bias, float* dW_routed, float* dW_shared,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
   moe_status_t s = check_bwd_shapes(T, d, I, N, K, K_s, dtype);
   if (s != MOE_OK) return s;
   if (T == 0) return ok();
@@ -756,6 +767,7 @@ moe_status_t moe_layer_backward(const void* u, const void* E_gate, const void* W
   if ((s = check_ptr("W_shared", W_shared, K_s > 0)) != MOE_OK) return s;
   if ((s = check_ptr("gate_bias", gate_bias, false)) != MOE_OK) return s;
   if ((s = check_ptr("dh", dh, true)) != MOE_OK) return s;
+  if ((s = check_ptr("dlogits", dlogits, false)) != MOE_OK) return s;
   if ((s = check_ptr("du", du, true)) != MOE_OK) return s;
   if ((s = check_ptr("dE_gate", dE_gate, true)) != MOE_OK) return s;
   if ((s = check_ptr("dgate_bias", dgate_bias, false)) != MOE_OK) return s;
@@ -773,6 +785,13 @@ moe_status_t moe_layer_backward(const void* u, const void* E_gate, const void* W
   const size_t wr = (size_t)N * 3 * I * d * 4;
   if (overlap(dW_routed, wr, workspace, L.total))
     return fail(MOE_ERR_INVALID_ARG, "dW_routed overlaps workspace");
+  const size_t dz = dlogits == nullptr ? 0 : (size_t)T * N * 4;
+  if (overlap(dlogits, dz, du, act) || overlap(dlogits, dz, workspace, L.total) ||
+      overlap(dlogits, dz, dE_gate, (size_t)N * d * 4) ||
+      (dgate_bias != nullptr && overlap(dlogits, dz, dgate_bias, (size_t)N * 4)) ||
+      overlap(dlogits, dz, dW_routed, wr) ||
+      (K_s > 0 && overlap(dlogits, dz, dW_shared, (size_t)K_s * 3 * I * d * 4)))
+    return fail(MOE_ERR_INVALID_ARG, "dlogits overlaps an output or the workspace");
 
   hipStream_t st = (hipStream_t)stream;
   char* ws = (char*)workspace;
@@ -821,6 +840,7 @@ moe_status_t moe_layer_backward(const void* u, const void* E_gate, const void* W
   a.K_s = K_s;
   a.NP = pad8(N);
   a.gate = gate;
+  a.dlogits = dlogits;
   int32_t* tabs = nullptr;
   if (L.pipe) {
     tabs = (int32_t*)(ws + L.tabs);

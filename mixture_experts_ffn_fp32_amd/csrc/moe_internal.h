@@ -270,6 +270,7 @@ struct BwdArgs {
   int32_t* pcol;               // [N+1] padded first column of each routed expert
   long long ldx;               // row pitch (elements) of XT and dhT
   int Tp;                      // T rounded up to 64: the shared experts' column count
+  const float* dlogits;        // [T][N] or NULL: gradient of the logits from losses beside h
 };
 int backward_de_chunks(int T);
 // Padded slot columns: every virtual expert's slots rounded up to 64.

@@ -18,18 +18,26 @@ MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
 NUM_STAGES = 7
 STAGE_NAMES = ("router", "tile_rank", "dispatch_scan", "scatter", "expert_gemm1_swiglu",
                "expert_gemm2_down", "combine")
+MOE_DTYPE_E4M3, MOE_DTYPE_E5M2 = 2, 3
 _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16}
+_F8 = {torch.float8_e4m3fn: MOE_DTYPE_E4M3, torch.float8_e5m2: MOE_DTYPE_E5M2}
 
 EXPORTED = ("moe_last_error", "moe_workspace_size", "moe_layer_forward",
             "moe_layer_forward_static", "moe_route",
             "moe_dispatch_workspace_size", "moe_dispatch", "moe_expert_ffn_workspace_size",
             "moe_expert_ffn", "moe_combine", "moe_balance_workspace_size", "moe_balance_stats",
-            "moe_backward_workspace_size", "moe_layer_backward", "moe_layer_norm",
+            "moe_backward_workspace_size", "moe_layer_backward", "moe_layer_backward_aux",
+            "moe_layer_norm",
             "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
             "moe_grouped_matmul_workspace_size", "moe_grouped_matmul",
             "moe_grouped_matmul_backward_workspace_size", "moe_grouped_matmul_backward",
-            "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_timing_enable",
-            "moe_timing_read", "moe_timing_stages")
+            "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_rms_norm",
+            "moe_rms_norm_backward_workspace_size", "moe_rms_norm_backward", "moe_quantize_rows",
+            "moe_quantize_blocks", "moe_dequantize_rows",
+            "moe_grouped_matmul_quantized_workspace_size", "moe_grouped_matmul_quantized",
+            "moe_grouped_matmul_quantized_dx_workspace_size", "moe_grouped_matmul_quantized_dx",
+            "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
+            "moe_timing_enable", "moe_timing_read", "moe_timing_stages")
 
 
 class MoEError(RuntimeError):
@@ -71,6 +79,8 @@ def load_library(path: str = LIB_PATH):
         "moe_backward_workspace_size": [i, i, i, i, i, i, i, szp],
         "moe_layer_backward": [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp, vp, vp, vp, vp, vp,
                                sz, vp],
+        "moe_layer_backward_aux": [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp, vp, vp, vp, vp,
+                                   vp, vp, sz, vp],
         "moe_layer_norm": [vp, vp, vp, i, i, fl, i, vp, vp, vp, vp],
         "moe_layer_norm_backward_workspace_size": [i, i, i, szp],
         "moe_layer_norm_backward": [vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, vp, sz, vp],
@@ -80,6 +90,19 @@ def load_library(path: str = LIB_PATH):
         "moe_grouped_matmul_backward": [vp, vp, vp, vp, i, i, i, i, i, i, vp, vp, vp, sz, vp],
         "moe_orthogonalize_workspace_size": [i, i, i, szp],
         "moe_orthogonalize": [vp, i64, i, i, i, i, i, fl, fl, fl, fl, vp, i64, i, vp, sz, vp],
+        "moe_rms_norm": [vp, vp, vp, i, i, fl, i, i, vp, vp, vp, vp, vp],
+        "moe_rms_norm_backward_workspace_size": [i, i, i, szp],
+        "moe_rms_norm_backward": [vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, sz, vp],
+        "moe_quantize_rows": [vp, i, i, i, i, vp, vp, vp],
+        "moe_quantize_blocks": [vp, i, i, i, i, i, vp, vp, vp],
+        "moe_dequantize_rows": [vp, vp, i, i, i, i, vp, vp],
+        "moe_grouped_matmul_quantized_workspace_size": [i, i, i, i, szp],
+        "moe_grouped_matmul_quantized": [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, sz, vp],
+        "moe_grouped_matmul_quantized_dx_workspace_size": [i, i, i, i, szp],
+        "moe_grouped_matmul_quantized_dx": [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, sz, vp],
+        "moe_balance_loss_workspace_size": [i, i, i, szp],
+        "moe_balance_loss": [vp, vp, vp, vp, vp, i, i, i, i, i, fl, fl, vp, vp, vp, vp, vp, sz, vp],
+        "moe_balance_loss_backward": [vp, vp, vp, vp, vp, i, i, i, vp, vp],
         "moe_timing_enable": [i],
         "moe_timing_read": [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int)],
         "moe_timing_stages": [ctypes.c_uint],
@@ -184,8 +207,11 @@ def backward_workspace_size(T, d, I, N, K, K_s, dtype_code) -> int:
 
 
 def layer_backward(u, E_gate, W_routed, W_shared, N: int, K: int, K_s: int, dh, gate_bias=None,
-                   workspace=None):
+                   workspace=None, dlogits=None):
     """Gradients of sum(dh * h) for h = layer_forward(u, ...); see include/moe.h.
+
+    dlogits [T][N] float32 (balance_loss_backward's) is the logits' gradient from losses
+    beside h, and joins du, dE_gate and dgate_bias.
 
     Returns (du, dE_gate, dgate_bias, dW_routed, dW_shared or None); every gradient
     but du is float32, the weight gradients in the layout of their weights.  The
@@ -195,7 +221,9 @@ def layer_backward(u, E_gate, W_routed, W_shared, N: int, K: int, K_s: int, dh, 
     T, d = u.shape
     dt = _dtype_code(u)
     _dev(u, E_gate, W_routed, W_shared, dh, dtype=u.dtype)
-    _dev(gate_bias, dtype=torch.float32)
+    _dev(gate_bias, dlogits, dtype=torch.float32)
+    if dlogits is not None:
+        _typed("dlogits", dlogits, torch.float32, (T, N))
     I = _infer_I(W_routed, N, d)
     dev = u.device
     # an empty batch writes nothing: its weight gradients are zeros
@@ -209,10 +237,10 @@ def layer_backward(u, E_gate, W_routed, W_shared, N: int, K: int, K_s: int, dh, 
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     _dev(workspace)
-    _check(L.moe_layer_backward(_p(u), _p(E_gate), _p(W_routed), _p(W_shared), N, K, K_s, T, d, I,
-                                dt, _p(gate_bias), _p(dh), _p(du), _p(dE), _p(db), _p(dWr),
-                                _p(dWs), _p(workspace),
-                                workspace.numel() * workspace.element_size(), _stream()))
+    _check(L.moe_layer_backward_aux(_p(u), _p(E_gate), _p(W_routed), _p(W_shared), N, K, K_s, T, d,
+                                    I, dt, _p(gate_bias), _p(dh), _p(dlogits), _p(du), _p(dE),
+                                    _p(db), _p(dWr), _p(dWs), _p(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream()))
     return du, dE, db, dWr, dWs
 
 
@@ -545,6 +573,234 @@ def orthogonalize(x, steps: int = 5, eps: float = 1e-7,
         _check(L.moe_orthogonalize(_p(x), xs, B, m, n, dt, steps, eps, a, b, c, _p(out), os_,
                                    _dtype_code(out), _p(ws), _bytes(ws), _stream_of(x.device)))
     return out
+
+
+# ---------------------------------------------------------------- experts in 8 bits
+F8_BLOCK = 128
+
+
+def _f8_code(name: str, dtype) -> int:
+    if dtype not in _F8:
+        raise MoEError(2, f"{name}: expected torch.float8_e4m3fn or torch.float8_e5m2, got {dtype}")
+    return _F8[dtype]
+
+
+def _f8_blocks(n: int) -> int:
+    return (n + F8_BLOCK - 1) // F8_BLOCK
+
+
+def _rms_norm(x, weight, residual, eps, q_dtype, h_out, out):
+    L = load_library()
+    T, d = _dims("x", x, 2)
+    dt = _dtype_code(x)
+    yt = dt if q_dtype is None else _f8_code("q_dtype", q_dtype)
+    _typed("weight", weight, x.dtype, (d,))
+    _typed("residual", residual, x.dtype, (T, d))
+    _typed("h_out", h_out, x.dtype, (T, d))
+    _typed("out", out, x.dtype if q_dtype is None else q_dtype, (T, d))
+    dev = _operands(x, weight, residual, h_out, out)
+    with _on(dev):
+        h = h_out
+        if h is None and residual is not None:
+            h = torch.empty_like(x)
+        y = torch.empty((T, d), dtype=q_dtype or x.dtype, device=dev) if out is None else out
+        scales = None
+        if q_dtype is not None:
+            scales = torch.empty((T, _f8_blocks(d)), dtype=torch.float32, device=dev)
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        _check(L.moe_rms_norm(_p(x), _p(residual), _p(weight), T, d, eps, dt, yt, _p(h), _p(y),
+                              _p(scales), _p(rstd), _stream_of(dev)))
+    return y, scales, x if h is None else h, rstd
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, h_out=None, out=None):
+    """(y, h, rstd): root-mean-square norm of h = x + residual over the last dimension of
+    x [T][d] (see include/moe.h); without residual and h_out, h is x itself.
+
+    weight [d] has x's dtype (None: ones), rstd [T] is float32; h and rstd are what
+    rms_norm_backward needs.  h_out may be x or residual."""
+    y, _, h, rstd = _rms_norm(x, weight, residual, eps, None, h_out, out)
+    return y, h, rstd
+
+
+def rms_norm_quantized(x, weight=None, residual=None, eps: float = 1e-6,
+                       q_dtype=torch.float8_e4m3fn, h_out=None, out=None):
+    """(q, scales, h, rstd): rms_norm with y in 8 bits, quantised as quantize_rows does from the
+    float32 values: q [T][d] q_dtype, scales [T][ceil(d / 128)] float32."""
+    return _rms_norm(x, weight, residual, eps, q_dtype, h_out, out)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dh=None, out=None, workspace=None):
+    """(dx, dweight) of sum(dy * y) + sum(dh * h) for y, h, rstd = rms_norm(x, weight, residual):
+    dx, of x and of residual alike, has h's dtype, dweight [d] is float32.  weight may be None
+    (ones); dh, what reaches h from later layers, may be None; out may be dh."""
+    L = load_library()
+    T, d = _dims("h", h, 2)
+    dt = _dtype_code(h)
+    _typed("dy", dy, h.dtype, (T, d))
+    _typed("weight", weight, h.dtype, (d,))
+    _typed("rstd", rstd, torch.float32, (T,))
+    _typed("dh", dh, h.dtype, (T, d))
+    _typed("out", out, h.dtype, (T, d))
+    dev = _operands(h, dy, weight, rstd, dh, out)
+    with _on(dev):
+        dx = torch.empty_like(h) if out is None else out
+        dw = torch.empty(d, dtype=torch.float32, device=dev)
+        ws = _scratch(workspace, _size(L.moe_rms_norm_backward_workspace_size, T, d, dt), dev)
+        _check(L.moe_rms_norm_backward(_p(dy), _p(h), _p(weight), _p(rstd), _p(dh), T, d, dt,
+                                       _p(dx), _p(dw), _p(ws), _bytes(ws), _stream_of(dev)))
+    return dx, dw
+
+
+def quantize_rows(x, q_dtype=torch.float8_e4m3fn):
+    """(q, scales): x [T][d] in 8 bits with one float32 scale for each 128 columns of a row
+    (see include/moe.h): q [T][d] q_dtype, scales [T][ceil(d / 128)]."""
+    L = load_library()
+    T, d = _dims("x", x, 2)
+    dt, qt = _dtype_code(x), _f8_code("q_dtype", q_dtype)
+    dev = _operands(x)
+    with _on(dev):
+        q = torch.empty((T, d), dtype=q_dtype, device=dev)
+        scales = torch.empty((T, _f8_blocks(d)), dtype=torch.float32, device=dev)
+        _check(L.moe_quantize_rows(_p(x), T, d, dt, qt, _p(q), _p(scales), _stream_of(dev)))
+    return q, scales
+
+
+def quantize_blocks(w, q_dtype=torch.float8_e4m3fn):
+    """(q, scales): matrices w [E][n][k] in 8 bits with one float32 scale for each 128 x 128:
+    q [E][n][k] q_dtype, scales [E][ceil(n / 128)][ceil(k / 128)]."""
+    L = load_library()
+    E, n, k = _dims("w", w, 3)
+    dt, qt = _dtype_code(w), _f8_code("q_dtype", q_dtype)
+    dev = _operands(w)
+    with _on(dev):
+        q = torch.empty((E, n, k), dtype=q_dtype, device=dev)
+        scales = torch.empty((E, _f8_blocks(n), _f8_blocks(k)), dtype=torch.float32, device=dev)
+        _check(L.moe_quantize_blocks(_p(w), E, n, k, dt, qt, _p(q), _p(scales), _stream_of(dev)))
+    return q, scales
+
+
+def dequantize_rows(q, scales, dtype=torch.bfloat16):
+    """x [T][d] = q * scales in dtype, for q, scales = quantize_rows(..)."""
+    L = load_library()
+    T, d = _dims("q", q, 2)
+    qt = _f8_code("q", q.dtype)
+    if dtype not in _DTYPES:
+        raise MoEError(2, f"unsupported dtype {dtype}")
+    _typed("scales", scales, torch.float32, (T, _f8_blocks(d)))
+    dev = _operands(q, scales)
+    with _on(dev):
+        x = torch.empty((T, d), dtype=dtype, device=dev)
+        _check(L.moe_dequantize_rows(_p(q), _p(scales), T, d, qt, _DTYPES[dtype], _p(x),
+                                     _stream_of(dev)))
+    return x
+
+
+def _quantized(dx, x, xs, w, ws, offsets, out_dtype, out, workspace):
+    L = load_library()
+    name = "dy" if dx else "x"
+    M, into = _dims(name, x, 2)
+    E, n, k = _dims("w", w, 3)
+    width = k if dx else n
+    if into != (n if dx else k):
+        raise MoEError(1, f"{name} has rows of {into}, w is {n} x {k}")
+    code = _f8_code(name, x.dtype)
+    if w.dtype != torch.float8_e4m3fn:
+        raise MoEError(2, f"w: expected torch.float8_e4m3fn, got {w.dtype}")
+    if out_dtype not in _DTYPES:
+        raise MoEError(2, f"unsupported out_dtype {out_dtype}")
+    _typed(name + "s", xs, torch.float32, (M, _f8_blocks(into)))
+    _typed("ws", ws, torch.float32, (E, _f8_blocks(n), _f8_blocks(k)))
+    if offsets is None and E != 1:
+        raise MoEError(1, "offsets are needed where w holds more than one matrix")
+    _typed("offsets", offsets, torch.int32, (E + 1,))
+    _typed("out", out, out_dtype, (M, width))
+    dev = _operands(x, xs, w, ws, offsets, out)
+    size, call = ((L.moe_grouped_matmul_quantized_dx_workspace_size,
+                   L.moe_grouped_matmul_quantized_dx) if dx else
+                  (L.moe_grouped_matmul_quantized_workspace_size, L.moe_grouped_matmul_quantized))
+    with _on(dev):
+        y = torch.empty((M, width), dtype=out_dtype, device=dev) if out is None else out
+        scratch = _scratch(workspace, _size(size, M, E, n, k), dev)
+        _check(call(_p(x), _p(xs), _p(w), _p(ws), _p(offsets), M, E, n, k, code,
+                    _DTYPES[out_dtype], 1 if out is None else 0, _p(y), _p(scratch),
+                    _bytes(scratch), _stream_of(dev)))
+    return y
+
+
+def grouped_matmul_quantized(x, xs, w, ws, offsets=None, out_dtype=torch.bfloat16, out=None,
+                             workspace=None):
+    """y [M][n] in out_dtype: grouped_matmul of 8-bit rows and weights, x, xs = quantize_rows(..)
+    (or rms_norm_quantized's), w, ws = quantize_blocks(..) in e4m3; see include/moe.h.
+
+    offsets [E+1] as grouped_matmul's (None: all rows by the one matrix).  Rows outside every
+    group are zero in a new y and left as they were in a given `out`."""
+    return _quantized(False, x, xs, w, ws, offsets, out_dtype, out, workspace)
+
+
+def grouped_matmul_quantized_dx(dy, dys, w, ws, offsets=None, out_dtype=torch.bfloat16, out=None,
+                                workspace=None):
+    """dx [M][k] in out_dtype: the rows' gradient of grouped_matmul_quantized for
+    dy, dys = quantize_rows(dy [M][n], ..) and the forward's w, ws.  The weights' gradient is
+    grouped_matmul_backward's, from rows in x's dtype (dequantize_rows reads them back)."""
+    return _quantized(True, dy, dys, w, ws, offsets, out_dtype, out, workspace)
+
+
+# ---------------------------------------------------------------- balance loss
+def _sequences(T, offsets, mask):
+    S = 1
+    if offsets is not None:
+        S = _dims("offsets", offsets, 1)[0] - 1
+        _typed("offsets", offsets, torch.int32, (S + 1,))
+    _typed("mask", mask, torch.bool, (T,))
+    return S
+
+
+def balance_loss(scores, idx, offsets=None, mask=None, device_of=None, devices: int = 0,
+                 alpha1: float = 1.0, alpha2: float = 1.0, workspace=None):
+    """The balance losses of a routed batch with what their gradient needs (see include/moe.h):
+    a dict of counts [S][N] int32, P [S][N], losses [S][2] (expert-level, device-level) and
+    slopes [S][2][N], float32.
+
+    scores [T][N] and idx [T][K] are route()'s.  offsets [S+1] int32 cuts the rows into
+    sequences with losses of their own (None: one), mask [T] bool says which rows count (None:
+    all), device_of [N] int32 puts experts on `devices` devices (None: no device-level loss)."""
+    L = load_library()
+    T, N = _dims("scores", scores, 2)
+    K = _dims("idx", idx, 2)[1]
+    _typed("scores", scores, torch.float32, (T, N))
+    _typed("idx", idx, torch.int32, (T, K))
+    _typed("device_of", device_of, torch.int32, (N,))
+    S = _sequences(T, offsets, mask)
+    dev = _operands(scores, idx, offsets, mask, device_of)
+    with _on(dev):
+        counts = torch.empty((S, N), dtype=torch.int32, device=dev)
+        P = torch.empty((S, N), dtype=torch.float32, device=dev)
+        losses = torch.empty((S, 2), dtype=torch.float32, device=dev)
+        slopes = torch.empty((S, 2, N), dtype=torch.float32, device=dev)
+        ws = _scratch(workspace, _size(L.moe_balance_loss_workspace_size, T, N, S), dev)
+        _check(L.moe_balance_loss(_p(scores), _p(idx), _p(offsets), _p(mask), _p(device_of), T, N,
+                                  K, S, devices, alpha1, alpha2, _p(counts), _p(P), _p(losses),
+                                  _p(slopes), _p(ws), _bytes(ws), _stream_of(dev)))
+    return {"counts": counts, "P": P, "losses": losses, "slopes": slopes}
+
+
+def balance_loss_backward(scores, slopes, dlosses=None, offsets=None, mask=None):
+    """dlogits [T][N] float32: the gradient of sum(dlosses * losses) by the logits behind the
+    scores, for slopes of balance_loss(scores, .., offsets, mask); dlosses [S][2] float32 (None:
+    ones).  layer_backward takes it as `dlogits`."""
+    L = load_library()
+    T, N = _dims("scores", scores, 2)
+    _typed("scores", scores, torch.float32, (T, N))
+    S = _sequences(T, offsets, mask)
+    _typed("slopes", slopes, torch.float32, (S, 2, N))
+    _typed("dlosses", dlosses, torch.float32, (S, 2))
+    dev = _operands(scores, slopes, dlosses, offsets, mask)
+    with _on(dev):
+        dlogits = torch.empty((T, N), dtype=torch.float32, device=dev)
+        _check(L.moe_balance_loss_backward(_p(scores), _p(slopes), _p(dlosses), _p(offsets),
+                                           _p(mask), T, N, S, _p(dlogits), _stream_of(dev)))
+    return dlogits
 
 
 def timing_enable(on: bool = True, stages=None):
