@@ -1,8 +1,8 @@
 // Products of 8-bit operands grouped by expert with ragged sizes (gfx950), the grouped products
 // of grouped.hip for experts held in 8 bits with a float32 scale for each block of 128 (f8.h):
 //
-//   forward   y[r]  = sum over blocks b of k  xs[r][b] ws[e][n/128][b] sum_{k in b} xq[r][k] wq[e][n][k]
-//   gradient  dx[r] = sum over blocks b of n  dys[r][b] ws[e][b][k/128] sum_{n in b} dyq[r][n] wq[e][n][k]
+//   forward   y[r][n]  = sum_b xs[r][b] ws[e][n / 128][b] sum_{k in b} x[r][k] w[e][n][k]
+//   gradient  dx[r][k] = sum_b dys[r][b] ws[e][b][k / 128] sum_{n in b} dy[r][n] w[e][n][k]
 //
 // A block's sum and the sum over blocks are float32, the result is rounded once.  The weights'
 // scales hold for 128 x 128 elements, so both directions read the same weights.
@@ -15,178 +15,258 @@
 // at twice the bfloat16 rate.  A float32 result is computed from the same operands as bfloat16,
 // which hold every 8-bit value, by the bfloat16 instructions, whose sums keep float32's bits
 // (8e-9 in the same measurement).
+//
+// One launch covers every group, as in grouped.hip.  Operands are read where they are: rows end
+// inside their last k-step by loads that lie outside every range, w is read along k or, for dx,
+// across it.  Rows whose length is no whole number of 16 bytes are copied to ones that are first.
+
 #include <algorithm>
 
-#include "f8.h"
 #include "groups.h"
 #include "ops_internal.h"
+#include "tile_f8.h"
 
 namespace moe {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
 struct F8Product {
   const uint8_t* x;        // x or dy: rows of the groups
   const float* xs;
-  const uint8_t* w;        // [E][n][k]
-  const float* ws;         // [E][nb][kb]
+  const uint8_t* w;        // [E][n] rows
+  const float* ws;         // [E][blocks of n][blocks of k]
+  uint32_t pitch_x, pitch_w;
   const int32_t* offsets;
   void* out;
   GroupDims g;
   int zero_rest;
 };
 
-// Eight 8-bit values (two words) as bfloat16, which is exact.
-template <int Q>
-__device__ __forceinline__ bf16x8 f8_widen(int lo, int hi) {
-  bf16x8 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int w = i < 2 ? lo : hi;
-    bf16x2 two;
-    if constexpr (Q == F8_E4M3)
-      two = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true)
-                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false);
-    else
-      two = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.f, true)
-                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.f, false);
-    v[2 * i] = two[0];
-    v[2 * i + 1] = two[1];
+template <class C, int DIR>
+struct F8Tiles {
+  const F8Product& p;
+  const GroupTables& g_;
+
+  struct Tile {
+    F8Operand X, W;
+    int m0, n0, steps, length, rows, cols, hint, row0;
+  };
+  __device__ __forceinline__ int width() const { return DIR == GR_FWD ? p.g.n : p.g.k; }
+  __device__ __forceinline__ int columns() const { return (width() + C::BN - 1) / C::BN; }
+  __device__ __forceinline__ Tile tile(int L, int e) const {  // group by group, m fastest
+    const GroupDims& g = p.g;
+    const int nt = columns(), nb = f8_blocks(g.n), kb = f8_blocks(g.k);
+    e = uni(group_of(g_.tiles, g.E, L / nt, e));
+    const int first = uni(g_.tiles[e]), mt = uni(g_.tiles[e + 1]) - first, local = L - first * nt;
+    const int m = local % mt, n = local / mt;
+    Tile t;
+    t.hint = e;
+    t.row0 = uni(g_.off[e]);
+    t.m0 = m * C::BM;
+    t.n0 = n * C::BN;
+    t.length = DIR == GR_FWD ? g.k : g.n;
+    t.steps = f8_blocks(t.length);
+    t.X.p = p.x + (size_t)t.row0 * p.pitch_x;
+    t.X.s = p.xs + (size_t)t.row0 * t.steps;
+    t.X.pitch = p.pitch_x;
+    t.X.s_row = t.steps;
+    t.X.s_step = 1;
+    t.X.rows = uni(g_.off[e + 1]) - t.row0;
+    t.X.width = 0;
+    t.W.p = p.w + (size_t)e * g.n * p.pitch_w;
+    t.W.s = p.ws + (size_t)e * nb * kb;
+    t.W.pitch = p.pitch_w;
+    t.W.s_row = DIR == GR_FWD ? kb : 1;
+    t.W.s_step = DIR == GR_FWD ? 1 : kb;
+    t.W.rows = g.n;
+    t.W.width = p.pitch_w;
+    t.rows = t.X.rows - t.m0;
+    t.cols = width() - t.n0;
+    return t;
   }
-  return v;
-}
 
-// w fragment times x fragment of one block of 128, from zero: a lane holds four consecutive
-// columns (w's rows) 4 (lane / 16) .. of row lane % 16.
-template <int Q, bool EXACT>
-__device__ __forceinline__ f32x4 f8_mfma(const i32x8& w, const i32x8& x) {
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (!EXACT)
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, sum, 0, Q == F8_E5M2 ? 1 : 0, 0,
-                                                            0x7f7f7f7f, 0, 0x7f7f7f7f);
+  __device__ __forceinline__ void store(const Tile& t, int wm, int wn, int lane,
+                                        f32x16 (&acc)[C::FM][C::FN]) const {
+    // a lane holds four consecutive columns of one row
+    const int N = width();
+    const bool vec = N % (C::EXACT ? 4 : 8) == 0;  // whole 16-byte runs
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen<F8_E4M3>(w[2 * i], w[2 * i + 1]),
-                                                  f8_widen<Q>(x[2 * i], x[2 * i + 1]), sum, 0, 0, 0);
-  return sum;
-}
+    for (int fm = 0; fm < C::FM; ++fm) {
+      const int mr = tg_row<C>(wm, fm, lane, 0);
+      if (mr >= t.rows) continue;
+      const size_t row = (size_t)(t.row0 + t.m0 + mr);
+#pragma unroll
+      for (int fn = 0; fn < C::FN; ++fn) {
+        const int n0 = t.n0 + tg_col<C>(wn, fn, 0, 0);  // the fragment's first column
+        if (n0 >= N) continue;
+        if constexpr (C::EXACT) {
+          float* c = (float*)p.out + row * N;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = n0 + 8 * q + 4 * (lane >> 5);
+            if (vec) {
+              if (n < N)
+                *(f32x4*)(c + n) = f32x4{acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1],
+                                         acc[fm][fn][4 * q + 2], acc[fm][fn][4 * q + 3]};
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n + e < N) c[n + e] = acc[fm][fn][4 * q + e];
+            }
+          }
+        } else {
+          uint16_t* c = (uint16_t*)p.out + row * N;
+          uint2 w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[q] = uint2{pack_bf16x2(acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1]),
+                         pack_bf16x2(acc[fm][fn][4 * q + 2], acc[fm][fn][4 * q + 3])};
+          if (vec) {
+            u32x4 r0, r1;
+            tg_runs16(w, r0, r1);
+            const int n = n0 + 8 * (lane >> 5);
+            if (n < N) *(u32x4*)(c + n) = r0;
+            if (n + 16 < N) *(u32x4*)(c + n + 16) = r1;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int n = n0 + 8 * q + 4 * (lane >> 5);
+              const uint32_t b[2] = {w[q].x, w[q].y};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n + e < N) c[n + e] = (uint16_t)(b[e >> 1] >> (16 * (e & 1)));
+            }
+          }
+        }
+      }
+    }
+  }
+};
 
-constexpr int kF8Tile = 64;
-
-template <int DIR, int Q, bool F32>
-__global__ __launch_bounds__(256) void grouped_f8_kernel(F8Product p) {
+template <class C, int DIR>
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void grouped_f8_kernel(F8Product p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS];
   __shared__ GroupTables t;
-  __shared__ __attribute__((aligned(16))) uint8_t sx[kF8Tile * 128], sw[kF8Tile * 128];
-  const GroupDims& g = p.g;
-  group_tables<GR_FWD>(g, p.offsets, kF8Tile, t);
-  const int N = DIR == GR_FWD ? g.n : g.k, K = DIR == GR_FWD ? g.k : g.n;
+  group_tables<GR_FWD>(p.g, p.offsets, C::BM, t);
+  const F8Tiles<C, DIR> tiles{p, t};
   if (p.zero_rest) {
-    if (F32) zero_rows((float*)p.out, g.M, N, t.off[0], t.off[g.E]);
-    else zero_rows((uint16_t*)p.out, g.M, N, t.off[0], t.off[g.E]);
+    if (C::EXACT) zero_rows((float*)p.out, p.g.M, tiles.width(), t.off[0], t.off[p.g.E]);
+    else zero_rows((uint16_t*)p.out, p.g.M, tiles.width(), t.off[0], t.off[p.g.E]);
   }
-  const int nt = (N + kF8Tile - 1) / kF8Tile, nb = f8_blocks(g.n), kb = f8_blocks(g.k);
-  const int steps = DIR == GR_FWD ? kb : nb;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  const long long tiles = (long long)t.tiles[g.E] * nt;
-  for (long long L = blockIdx.x; L < tiles; L += gridDim.x) {
-    const int mt = uni((int)(L / nt)), n0 = uni((int)(L % nt)) * kF8Tile;
-    const int e = uni(group_of(t.tiles, g.E, mt, 0));
-    const int m0 = t.off[e] + (mt - t.tiles[e]) * kF8Tile, rows = min(kF8Tile, t.off[e + 1] - m0);
-    f32x4 acc[2][2];
+  const int n = uni(t.tiles[p.g.E]) * tiles.columns();
+  if constexpr (C::SMALL) f8_run_small<C>(tiles, n, lds);
+  else f8_run<C>(tiles, n, lds);
+}
+
+// Rows of `width` bytes to rows of `pitch` (the next multiple of 16), zeros behind their last
+// byte: 16 bytes a thread, from any address.
+struct PadRows {
+  const uint8_t* src;
+  uint8_t* dst;
+  long long rows;
+  int width;
+  uint32_t pitch;
+};
+typedef uint32_t pad_u32 __attribute__((aligned(1)));
+__global__ __launch_bounds__(256) void pad_bytes_kernel(PadRows a) {
+  const long long per = a.pitch / 16, all = a.rows * per;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+    const long long r = i / per;
+    const int j = (int)(i - r * per) * 16;
+    const uint8_t* src = a.src + r * a.width;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (j + 16 <= a.width) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int e = 0; e < 4; ++e) v[e] = *(const pad_u32*)(src + j + 4 * e);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < steps; ++s) {
-      __syncthreads();
-      for (int i = tid; i < kF8Tile * 128; i += 256) {
-        const int r = i >> 7, j = i & 127, kk = s * 128 + j;
-        const int at = lds_chunk_offset(r, j >> 4) + (j & 15);
-        sx[at] = r < rows && kk < K ? p.x[(size_t)(m0 + r) * K + kk] : 0;
-        const size_t we = (size_t)e * g.n * g.k;
-        if (DIR == GR_FWD) sw[at] = n0 + r < N && kk < K ? p.w[we + (size_t)(n0 + r) * g.k + kk] : 0;
-        else sw[at] = n0 + r < N && kk < K ? p.w[we + (size_t)kk * g.k + n0 + r] : 0;
-      }
-      __syncthreads();
-      const float wscale = DIR == GR_FWD ? p.ws[((size_t)e * nb + n0 / 128) * kb + s]
-                                         : p.ws[((size_t)e * nb + s) * kb + n0 / 128];
-      i32x8 xf[2], wf[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = 2 * (lane >> 4);
-        const int rx = wm * 32 + 16 * i + (lane & 15), rw = wn * 32 + 16 * i + (lane & 15);
-        const u32x4 a = *(const u32x4*)(sx + lds_chunk_offset(rx, c));
-        const u32x4 b = *(const u32x4*)(sx + lds_chunk_offset(rx, c + 1));
-        const u32x4 d = *(const u32x4*)(sw + lds_chunk_offset(rw, c));
-        const u32x4 f = *(const u32x4*)(sw + lds_chunk_offset(rw, c + 1));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          xf[i][q] = a[q];
-          xf[i][4 + q] = b[q];
-          wf[i][q] = d[q];
-          wf[i][4 + q] = f[q];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = wm * 32 + 16 * i + (lane & 15);
-        const float scale = r < rows ? p.xs[(size_t)(m0 + r) * steps + s] * wscale : 0.f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const f32x4 part = f8_mfma<Q, F32>(wf[j], xf[i]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][j][q] += scale * part[q];
-        }
-      }
+      for (int e = 0; e < 16; ++e)
+        if (j + e < a.width) v[e >> 2] |= (uint32_t)src[j + e] << (8 * (e & 3));
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = wm * 32 + 16 * i + (lane & 15);
-      if (r >= rows) continue;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = n0 + wn * 32 + 16 * j + 4 * (lane >> 4) + q;
-          if (c >= N) continue;
-          const size_t at = (size_t)(m0 + r) * N + c;
-          if (F32) ((float*)p.out)[at] = acc[i][j][q];
-          else ((uint16_t*)p.out)[at] = f32_to_bf16(acc[i][j][q]);
-        }
-    }
+    *(u32x4*)(a.dst + r * a.pitch + j) = v;
   }
+}
+hipError_t pad_bytes(const PadRows& a, hipStream_t st) {
+  const long long blocks = (a.rows * (a.pitch / 16) + 255) / 256;
+  pad_bytes_kernel<<<(unsigned)std::min<long long>(blocks, 1 << 16), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+uint32_t pitch16(int width) { return ((uint32_t)width + 15) & ~15u; }
+
+// The workspace: copies of operands whose rows are no whole number of 16 bytes.
+struct F8Plan {
+  uint8_t *x = nullptr, *w = nullptr;
+  size_t bytes = 0;
+};
+F8Plan f8_plan(int M, int E, int n, int k, bool dx, void* ws) {
+  F8Plan p;
+  auto take = [&](size_t n) {
+    uint8_t* at = (uint8_t*)ws + p.bytes;
+    p.bytes += (n + 255) & ~size_t(255);
+    return at;
+  };
+  const int length = dx ? n : k;
+  if (length % 16 != 0) p.x = take((size_t)M * pitch16(length));
+  if (k % 16 != 0) p.w = take((size_t)E * n * pitch16(k));
+  return p;
+}
+
+long long f8_tiles(const GroupedF8Args& a, bool dx, int b) {
+  return (a.M / b + (long long)std::min(a.E, a.M)) * (((dx ? a.k : a.n) + b - 1) / b);
+}
+template <class Shape, int DIR, int Q, bool F32>
+hipError_t run_f8(const F8Product& p, const GroupedF8Args& a, hipStream_t st) {
+  using C = F8Config<Shape, DIR == GR_DX, Q, F32>;
+  const long long blocks = (long long)device_cu_count() * C::BPC;
+  const long long tiles = f8_tiles(a, DIR == GR_DX, C::BM);
+  grouped_f8_kernel<C, DIR><<<(unsigned)std::max(1LL, std::min(tiles, blocks)), C::THREADS, 0, st>>>(p);
+  return hipGetLastError();
+}
+template <int DIR, int Q>
+hipError_t pick_f8(const F8Product& p, const GroupedF8Args& a, hipStream_t st) {
+  const int cus = device_cu_count();
+  const bool dx = DIR == GR_DX;
+  if (!a.out_f32 && 4 * f8_tiles(a, dx, 256) >= 3 * cus && a.M > 128LL * a.E)
+    return run_f8<TgBig, DIR, Q, false>(p, a, st);
+  if (4 * f8_tiles(a, dx, 128) >= 3 * cus)
+    return a.out_f32 ? run_f8<TgMid, DIR, Q, true>(p, a, st) : run_f8<TgMid, DIR, Q, false>(p, a, st);
+  return a.out_f32 ? run_f8<TgSmall, DIR, Q, true>(p, a, st) : run_f8<TgSmall, DIR, Q, false>(p, a, st);
 }
 
 }  // namespace
 
-size_t grouped_f8_workspace_bytes(int, int, int, int, bool) { return 0; }
+size_t grouped_f8_workspace_bytes(int M, int E, int n, int k, bool dx) {
+  return f8_plan(M, E, n, k, dx, nullptr).bytes;
+}
 
-hipError_t launch_grouped_f8(int f8, bool dx, const GroupedF8Args& a, void*, hipStream_t st) {
+hipError_t launch_grouped_f8(int f8, bool dx, const GroupedF8Args& a, void* ws, hipStream_t st) {
+  const F8Plan plan = f8_plan(a.M, a.E, a.n, a.k, dx, ws);
   F8Product p{};
   p.x = (const uint8_t*)a.x;
   p.xs = a.xs;
   p.w = (const uint8_t*)a.w;
   p.ws = a.ws;
+  p.pitch_x = dx ? a.n : a.k;
+  p.pitch_w = a.k;
   p.offsets = a.offsets;
   p.out = a.out;
   p.g = GroupDims{a.M, a.E, a.n, a.k};
   p.zero_rest = a.zero_rest;
-  const long long tiles =
-      (a.M / kF8Tile + 1LL + a.E) * (((dx ? a.k : a.n) + kF8Tile - 1) / kF8Tile);
-  const unsigned grid = (unsigned)std::min<long long>(tiles, 4LL * device_cu_count());
-  const int which = (dx ? 4 : 0) + (f8 == F8_E5M2 ? 2 : 0) + (a.out_f32 ? 1 : 0);
-  switch (which) {
-    case 0: grouped_f8_kernel<GR_FWD, F8_E4M3, false><<<grid, 256, 0, st>>>(p); break;
-    case 1: grouped_f8_kernel<GR_FWD, F8_E4M3, true><<<grid, 256, 0, st>>>(p); break;
-    case 2: grouped_f8_kernel<GR_FWD, F8_E5M2, false><<<grid, 256, 0, st>>>(p); break;
-    case 3: grouped_f8_kernel<GR_FWD, F8_E5M2, true><<<grid, 256, 0, st>>>(p); break;
-    case 4: grouped_f8_kernel<GR_DX, F8_E4M3, false><<<grid, 256, 0, st>>>(p); break;
-    case 5: grouped_f8_kernel<GR_DX, F8_E4M3, true><<<grid, 256, 0, st>>>(p); break;
-    case 6: grouped_f8_kernel<GR_DX, F8_E5M2, false><<<grid, 256, 0, st>>>(p); break;
-    default: grouped_f8_kernel<GR_DX, F8_E5M2, true><<<grid, 256, 0, st>>>(p); break;
+  if (plan.x != nullptr) {
+    const PadRows r{p.x, plan.x, a.M, (int)p.pitch_x, pitch16(p.pitch_x)};
+    if (const hipError_t e = pad_bytes(r, st); e != hipSuccess) return e;
+    p.x = r.dst;
+    p.pitch_x = r.pitch;
   }
-  return hipGetLastError();
+  if (plan.w != nullptr) {
+    const PadRows r{p.w, plan.w, (long long)a.E * a.n, a.k, pitch16(a.k)};
+    if (const hipError_t e = pad_bytes(r, st); e != hipSuccess) return e;
+    p.w = r.dst;
+    p.pitch_w = r.pitch;
+  }
+  if (dx)
+    return f8 == F8_E4M3 ? pick_f8<GR_DX, F8_E4M3>(p, a, st) : pick_f8<GR_DX, F8_E5M2>(p, a, st);
+  return f8 == F8_E4M3 ? pick_f8<GR_FWD, F8_E4M3>(p, a, st) : pick_f8<GR_FWD, F8_E5M2>(p, a, st);
 }
 
 }  // namespace moe

@@ -1,0 +1,557 @@
+// MFMA tile pipeline of products of 8-bit operands with a float32 scale for each block of 128
+// (gfx950): one (BM x BN) tile of C = X W per block at a time, in the shapes, LDS rings and
+// tile order of tile_gemm.h.  A k-step is 128 contraction indices, which are 128 bytes of a row
+// as the k-steps there are, and one block of scales:
+//
+//   acc += xs[row] ws[column block] (sum over the k-step of x w)
+//
+// The k-step's sum comes from the matrix instructions in registers of its own (a pair of
+// 32x32x64, the second one on top of the first) and is added to acc by 16 multiply-adds per
+// fragment while the next pair runs: 64 of its 128 cycles.  acc therefore has to lie in registers
+// that the vector ALU reaches, which bounds a wavefront's tile to 64 x 128.
+//
+// x is read in row layout (rows contiguous along the contraction).  w is read in row layout
+// (forward: its rows run along k) or in column layout (input gradient: its rows are the
+// contraction's), where a k-step is 128 rows of BN bytes and fragments come from transposing
+// LDS reads.  The scales ride in the ring beside their k-step, one float per row and column.
+#pragma once
+
+#include "f8.h"
+#include "tile_gemm.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+// Q: x's type (w is e4m3); WCOL: w in column layout; EXACT: through bfloat16 (see
+// grouped_f8.hip).
+template <class Shape, bool WCOL_, int Q_, bool EXACT_>
+struct F8Config : Shape {
+  static constexpr bool WCOL = WCOL_, EXACT = EXACT_, SWAP = true;
+  static constexpr int Q = Q_;
+  static constexpr bool SMALL = Shape::BM == TgSmall::BM;
+  static constexpr int DATA = Shape::SLOT;                       // bytes of x and w in a slot,
+  static constexpr int SLOT = DATA + 4 * (Shape::BM + Shape::BN);  // and of their scales
+  static constexpr int LDS = Shape::S * SLOT * (SMALL ? TgSmall::WAVES : 1);
+  static constexpr int WAVES_PER_SIMD = Shape::BPC * Shape::THREADS / 256;
+};
+
+// A tile's operands.  Row layout: `rows` rows of `pitch` bytes, of which the first `length` are
+// the contraction.  Column layout: `rows` contraction rows of `pitch` bytes, `width` columns (a
+// multiple of 16 up to pitch).  Scales: those of row r (column c: c / 128) and k-step s lie at
+// r * s_row + s * s_step (floats).
+struct F8Operand {
+  const uint8_t* p;
+  const float* s;
+  uint32_t pitch, s_row, s_step;
+  int rows, width;
+};
+
+// Loading state of one wavefront: its data loads (16 bytes a lane) and its load of 64 scales.
+struct F8Load {
+  const uint8_t *base, *scales;
+  uint32_t step, s_step;   // bytes from one k-step to the next
+  int rows;                // column layout: contraction rows; row layout: -(k-steps)
+  uint32_t pitch;
+  int tail;                // row layout: bytes of the last k-step that exist
+};
+
+// One direct-to-LDS load of 4 bytes per lane (dma16 otherwise).
+__device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint8_t* __restrict__ wr,
+                                     int nrec) {
+  const __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, nrec, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)wr, 4, off,
+                                           0, 0, 0);
+}
+
+// Column layout: the 16-byte chunk c of contraction row k lies at position c ^ f8_rotation(k),
+// so that a transposing read of 32 lanes (two neighbouring chunks of eight consecutive rows)
+// touches every bank once.  It depends on the row's place among eight alone.
+template <int W>
+__device__ __forceinline__ int f8_rotation(int k) {
+  return 2 * (W == 256 ? k & 7 : W == 128 ? (k >> 1) & 3 : (k >> 2) & 1);
+}
+// Row layout: the byte of a row's k-step that load i of this lane takes.
+template <class C>
+__device__ __forceinline__ int f8_chunk_byte(int w, int i, int lane) {
+  const int r = (w * C::NI + i) * 8 + (lane >> 3);
+  return ((lane & 7) ^ ((r >> 1) & 7)) << 4;
+}
+
+// Loads of wavefront w (of those on this side) of the tile's side at t0.
+template <class C, bool COL>
+__device__ __forceinline__ F8Load f8_prepare(const F8Operand& o, int t0, int steps, int length,
+                                             int w, int lane, uint32_t (&off)[C::NI],
+                                             uint32_t& s_off) {
+  constexpr int W = C::BM;
+  F8Load l;
+  l.pitch = uni((int)o.pitch);
+  l.s_step = uni((int)o.s_step) * 4;
+  if constexpr (COL) {
+    constexpr int RPI = 1024 / W, CPR = W / 16;  // rows per load instruction, chunks per row
+    l.base = uni(o.p);
+    l.step = l.pitch * kF8Block;
+    l.rows = uni(o.rows);
+    l.tail = 0;
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) {
+      const int k = (w * C::NI + i) * RPI + lane / CPR;
+      // columns past the last one reread the last chunk (never stored)
+      off[i] = (uint32_t)k * l.pitch +
+               min(t0 + 16 * ((lane % CPR) ^ f8_rotation<W>(k)), o.width - 16);
+    }
+    l.scales = uni((const uint8_t*)o.s);
+    s_off = 4 * o.s_row * (uint32_t)(min(t0 + 64 * w + lane, o.width - 1) / kF8Block);
+  } else {
+    const int r0 = min(t0, o.rows - 1);
+    l.base = uni(o.p + (size_t)r0 * o.pitch);
+    l.step = kF8Block;
+    // a wavefront whose rows all lie past the last one loads nothing (range 0)
+    l.rows = t0 + w * C::NI * 8 < o.rows ? -uni(steps) : 0;
+    l.tail = uni(length - (steps - 1) * kF8Block);
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) {
+      const int r = (w * C::NI + i) * 8 + (lane >> 3);
+      // rows past the last one reread it (never stored)
+      off[i] = (uint32_t)(min(t0 + r, o.rows - 1) - r0) * l.pitch + f8_chunk_byte<C>(w, i, lane);
+    }
+    l.scales = uni((const uint8_t*)o.s);
+    s_off = 0;
+  }
+  return l;
+}
+// x's scales are those of rows, w's (forward) of blocks of 128 of its rows.
+template <class C>
+__device__ __forceinline__ void f8_scale_place(const F8Operand& o, bool blocks, int t0, int w, int lane,
+                                               F8Load& l, uint32_t& s_off) {
+  const int r0 = min(t0, o.rows - 1);
+  const int r = min(t0 + 64 * w + lane, o.rows - 1);
+  if (blocks) {
+    s_off = 4 * o.s_row * (uint32_t)(r / kF8Block);
+  } else {
+    l.scales = uni((const uint8_t*)(o.s + (size_t)r0 * o.s_row));
+    s_off = 4 * o.s_row * (uint32_t)(r - r0);
+  }
+}
+
+// Bytes from the k-step's base that its loads may touch; later ones read zeros.
+__device__ __forceinline__ int f8_range(const F8Load& l, int s) {
+  if (l.rows <= 0) return s < -l.rows ? 0x7fffffff : 0;
+  return min(max(l.rows - kF8Block * s, 0), kF8Block) * (int)l.pitch;
+}
+
+// The last k-step of a row ends with the row: chunks behind it read zeros (their offset lies
+// outside every range).  Only k-steps of zeros follow it.
+template <class C>
+__device__ __forceinline__ void f8_mask_tail(const F8Load& l, int s, int w, int lane,
+                                             uint32_t (&off)[C::NI]) {
+  if (l.rows < 0 && s == -l.rows - 1 && l.tail < kF8Block) {
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i)
+      if (f8_chunk_byte<C>(w, i, lane) >= l.tail) off[i] = 0x7fffffffu;
+  }
+}
+
+// 32 rows (columns) of a tile, half h (64 indices) of a k-step: lane l holds row l % 32,
+// indices 64 h + 16 (l / 32) + 0 .. 15 and the same 32 further on.
+__device__ __forceinline__ i32x8 f8_join(const u32x4& a, const u32x4& b) {
+  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+template <class C, bool COL>
+__device__ __forceinline__ i32x8 f8_frag(const uint8_t* rd, int h, int u_const, int u_wave, int lane) {
+  if constexpr (COL) {
+    constexpr int W = C::BN;
+    const int l16 = lane & 15, k = 16 * (lane >> 5) + (l16 >> 1);
+    const int c = (2 * (u_const + u_wave) + ((lane >> 4) & 1)) ^ f8_rotation<W>(k);
+    const uint8_t* p = rd + k * W + c * 16 + 8 * (l16 & 1) + 64 * h * W;
+    i32x8 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // rows + 0, 8, 32, 40
+      const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (__attribute__((address_space(3))) i32x2*)(__attribute__((address_space(3)))
+                                                     const uint8_t*)(p + (8 * (j & 1) + 32 * (j >> 1)) * W));
+      v[2 * j] = t[0];
+      v[2 * j + 1] = t[1];
+    }
+    return v;
+  } else {
+    const int r = u_wave * 32 + (lane & 31);
+    const u32x4 a = *(const u32x4*)(rd + lds_chunk_offset(r, 4 * h + (lane >> 5)) + u_const * 32 * 128);
+    const u32x4 b = *(const u32x4*)(rd + lds_chunk_offset(r, 4 * h + 2 + (lane >> 5)) + u_const * 32 * 128);
+    return f8_join(a, b);
+  }
+}
+
+struct F8Frag {
+  i32x8 h[2];
+};
+template <class C>
+__device__ __forceinline__ F8Frag f8_frag_x(const uint8_t* rd, int fm, int wm, int lane) {
+  return F8Frag{{f8_frag<C, false>(rd, 0, C::WM * fm, wm, lane),
+                 f8_frag<C, false>(rd, 1, C::WM * fm, wm, lane)}};
+}
+template <class C>
+__device__ __forceinline__ F8Frag f8_frag_w(const uint8_t* rd, int fn, int wn, int lane) {
+  rd += C::BM * 128;
+  return F8Frag{{f8_frag<C, C::WCOL>(rd, 0, C::WN * fn, wn, lane),
+                 f8_frag<C, C::WCOL>(rd, 1, C::WN * fn, wn, lane)}};
+}
+
+// Eight 8-bit values (two words) as bfloat16, which is exact.
+template <int Q>
+__device__ __forceinline__ bf16x8 f8_widen(int lo, int hi) {
+  bf16x8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int w = i < 2 ? lo : hi;
+    bf16x2 two;
+    if constexpr (Q == F8_E4M3)
+      two = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true)
+                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false);
+    else
+      two = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.f, true)
+                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.f, false);
+    v[2 * i] = two[0];
+    v[2 * i + 1] = two[1];
+  }
+  return v;
+}
+
+// The sum of a k-step's products: a lane holds 16 columns (w's) of one row (x's).
+template <class C>
+__device__ __forceinline__ f32x16 f8_products(const F8Frag& w, const F8Frag& x) {
+  f32x16 part;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) part[r] = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (C::EXACT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            f8_widen<F8_E4M3>(w.h[h][2 * i], w.h[h][2 * i + 1]),
+            f8_widen<C::Q>(x.h[h][2 * i], x.h[h][2 * i + 1]), part, 0, 0, 0);
+    } else {
+      part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          w.h[h], x.h[h], part, 0, C::Q == F8_E5M2 ? 1 : 0, 0, 0, 0, 0);
+    }
+  }
+  return part;
+}
+__device__ __forceinline__ void f8_add(f32x16& acc, const f32x16& part, float scale) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = fmaf(part[r], scale, acc[r]);
+  // (here and not later: the compiler would sink the additions and keep every pair's sum)
+  asm volatile("" : "+v"(acc));
+}
+
+// A k-step's scales as a wavefront needs them: of its rows, one a lane, and of the tile's
+// blocks of 128 columns.
+template <class C>
+struct F8Scales {
+  static constexpr int NB = C::BN > kF8Block ? C::BN / kF8Block : 1;
+  float x[C::FM], w[NB];
+};
+template <class C>
+__device__ __forceinline__ F8Scales<C> f8_scales(const uint8_t* rd, int wm, int lane) {
+  const float* s = (const float*)(rd + C::DATA);
+  F8Scales<C> v;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) v.x[i] = s[(C::WM * i + wm) * 32 + (lane & 31)];
+#pragma unroll
+  for (int j = 0; j < F8Scales<C>::NB; ++j) v.w[j] = s[C::BM + j * kF8Block];
+  return v;
+}
+template <class C>
+__device__ __forceinline__ float f8_scale_of(const F8Scales<C>& s, int fm, int fn) {
+  return s.x[fm] * s.w[C::WN * 32 * fn / kF8Block];
+}
+
+// What passes from one k-step to the next: x's fragments and w's first one, the scales, and the
+// last pair's sum, which is added behind the next pair's start.
+template <class C>
+struct F8State {
+  F8Frag x[C::FM], w[2];
+  F8Scales<C> s;
+  f32x16 part;
+  float scale;
+};
+
+// One k-step out of ring slot `rd`.  The barrier stands before the last of w's fragments, when
+// every read of `rd` has been made: `rd` is free, the next k-step (slot `nx`) has landed, and
+// the last fragment's products cover the reads of the next k-step's first ones, each into the
+// registers that its last use has freed.  `wr` is `rd` again (see tg_step).
+template <class C, int FMA, int FNA>
+__device__ __forceinline__ void f8_step(const uint8_t* __restrict__ rd, const uint8_t* __restrict__ nx,
+                                        int wm, int wn, int lane, F8State<C>& f,
+                                        f32x16 (&acc)[C::FM][C::FN], const uint8_t* db,
+                                        const uint32_t (&off)[C::NI], const uint8_t* sb,
+                                        uint32_t s_off, uint8_t* __restrict__ wr, int wave, int nrec,
+                                        int s_nrec, bool landed) {
+  const F8Scales<C> s = f.s;
+#pragma unroll
+  for (int fn = 0; fn < FNA; ++fn) {
+    if (fn + 1 < FNA) {
+      f.w[(fn + 1) & 1] = f8_frag_w<C>(rd, fn + 1, wn, lane);
+    } else {
+      if (!landed) MOE_WAIT_VMCNT((C::S - 2) * (C::NI + 1));
+      lds_sync();
+      f.s = f8_scales<C>(nx, wm, lane);
+      if (FNA > 1) f.w[0] = f8_frag_w<C>(nx, 0, wn, lane);
+#pragma unroll
+      for (int i = 0; i < C::NI; ++i) dma16(db, off[i], wr + (wave * C::NI + i) * 1024, nrec);
+      dma4(sb, s_off, wr + C::DATA + wave * 256, s_nrec);
+    }
+#pragma unroll
+    for (int fm = 0; fm < FMA; ++fm) {
+      const f32x16 part = f8_products<C>(f.w[fn & 1], f.x[fm]);
+      const int pm = fm > 0 ? fm - 1 : FMA - 1, pn = fm > 0 ? fn : fn > 0 ? fn - 1 : FNA - 1;
+      f8_add(acc[pm][pn], f.part, f.scale);
+      f.part = part;
+      f.scale = f8_scale_of<C>(s, fm, fn);
+      if (fn + 1 == FNA) f.x[fm] = f8_frag_x<C>(nx, fm, wm, lane);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (FNA == 1) f.w[0] = f8_frag_w<C>(nx, 0, wn, lane);
+  }
+}
+
+// The loads of this wavefront: x in the first half of them, w in the other.
+template <class C, class Tile>
+__device__ __forceinline__ F8Load f8_prepare_wave(const Tile& t, int wave, int lane,
+                                                  uint32_t (&off)[C::NI], uint32_t& s_off) {
+  constexpr int H = C::WM * C::WN / 2;
+  F8Load l;
+  if (wave < H) {
+    l = f8_prepare<C, false>(t.X, t.m0, t.steps, t.length, wave, lane, off, s_off);
+    f8_scale_place<C>(t.X, false, t.m0, wave, lane, l, s_off);
+  } else {
+    l = f8_prepare<C, C::WCOL>(t.W, t.n0, t.steps, t.length, wave - H, lane, off, s_off);
+    if (!C::WCOL) f8_scale_place<C>(t.W, true, t.n0, wave - H, lane, l, s_off);
+  }
+  return l;
+}
+
+struct F8Cursor {
+  int hint;
+  int s, steps;      // the tile's next k-step, its k-steps (0: the stream has ended)
+  int real;          // those that exist
+};
+template <class C, class P>
+__device__ __forceinline__ void f8_seek(const P& p, int L, F8Cursor& c, F8Load& ld,
+                                        uint32_t (&off)[C::NI], uint32_t& s_off, int wave, int lane) {
+  c.s = c.steps = c.real = 0;
+  if (L < 0) return;
+  const typename P::Tile t = p.tile(L, c.hint);
+  c.hint = uni(t.hint);
+  c.real = uni(t.steps);
+  c.steps = max(c.real, C::S + 1);
+  ld = f8_prepare_wave<C>(t, wave, lane, off, s_off);
+}
+template <class C>
+__device__ __forceinline__ int f8_side(int wave) {
+  constexpr int H = C::WM * C::WN / 2;
+  return wave < H ? wave : wave - H;
+}
+
+// The k-steps of a tile (as tg_tile).
+template <class C, int FMA, int FNA, class P, class Next>
+__device__ __forceinline__ void f8_tile(const P& p, int steps, int& ph, int wave, int lane, Next next,
+                                        F8Cursor& c, F8Load& ld, uint32_t (&off)[C::NI],
+                                        uint32_t& s_off, f32x16 (&acc)[C::FM][C::FN],
+                                        uint8_t* __restrict__ lds) {
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  asm volatile("" : "+v"(lane));  // (see tg_tile)
+  const int all = max(steps, C::S + 1);
+  F8State<C> f;
+  const uint8_t* first = lds + ph * C::SLOT;
+  f.s = f8_scales<C>(first, wm, lane);
+#pragma unroll
+  for (int fm = 0; fm < FMA; ++fm) f.x[fm] = f8_frag_x<C>(first, fm, wm, lane);
+  f.w[0] = f8_frag_w<C>(first, 0, wn, lane);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) f.part[r] = 0.f;
+  f.scale = 0.f;
+  for (int s = 0; s < all; ++s) {
+    const int after = ph + 1 < C::S ? ph + 1 : 0;
+    f8_mask_tail<C>(ld, c.s, f8_side<C>(wave), lane, off);
+    const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
+    const uint8_t* sb = uni(ld.scales + (size_t)c.s * ld.s_step);
+    const int nrec = uni(c.steps > 0 ? f8_range(ld, c.s) : 0);
+    const int s_nrec = uni(c.s < c.real ? 0x7fffffff : 0);
+    uint8_t* rd = lds + ph * C::SLOT;
+    f8_step<C, FMA, FNA>(rd, lds + after * C::SLOT, wm, wn, lane, f, acc, db, off, sb, s_off, rd,
+                         wave, nrec, s_nrec, s < C::S - 1);
+    c.s = uni(c.s + 1);
+    if (c.s == c.steps) f8_seek<C>(p, next(), c, ld, off, s_off, wave, lane);
+    ph = after;
+  }
+  f8_add(acc[FMA - 1][FNA - 1], f.part, f.scale);
+}
+
+// The persistent loop over a block's tiles of problem P (as tg_run):
+//   P::Tile   { F8Operand X, W; int m0, n0, steps, length, rows, cols, hint; .. }
+template <class C, class P>
+__device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restrict__ lds) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uni(tid >> 6), wm = wave / C::WN, wn = wave % C::WN;
+  TgTiles q;
+  q.init(tiles, nullptr);
+  int mine = q.own;
+  int L = q.at(q.x, mine);
+  if (L < 0) return;
+  F8Cursor c{0, 0, 0, 0};
+  F8Load ld{};
+  uint32_t off[C::NI] = {}, s_off = 0;
+  f8_seek<C>(p, L, c, ld, off, s_off, wave, lane);
+  int ph = 0;  // ring slot of the next k-step
+#pragma unroll
+  for (int k = 0; k < C::S; ++k) {
+    f8_mask_tail<C>(ld, c.s, f8_side<C>(wave), lane, off);
+    uint8_t* w = lds + k * C::SLOT;
+    const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
+    const uint8_t* sb = uni(ld.scales + (size_t)c.s * ld.s_step);
+    const int nrec = uni(f8_range(ld, c.s)), s_nrec = uni(c.s < c.real ? 0x7fffffff : 0);
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) dma16(db, off[i], w + (wave * C::NI + i) * 1024, nrec);
+    dma4(sb, s_off, w + C::DATA + wave * 256, s_nrec);
+    c.s = uni(c.s + 1);
+  }
+  pipe_sync();
+  int L1 = -1;
+  auto next = [&]() -> int { return L1 = q.at(q.x, mine += q.blocks(q.x)); };
+  int hint = 0;
+  while (true) {
+    const typename P::Tile t = p.tile(L, hint);
+    hint = t.hint;
+    f32x16 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    static_assert(C::FM == 2, "half tiles leave out whole fragments");
+    constexpr int H = C::FN / 2;
+    const bool hm = t.rows <= C::BM / 2, hn = t.cols <= C::BN / 2;
+    if (hm && hn) f8_tile<C, 1, H>(p, t.steps, ph, wave, lane, next, c, ld, off, s_off, acc, lds);
+    else if (hm) f8_tile<C, 1, C::FN>(p, t.steps, ph, wave, lane, next, c, ld, off, s_off, acc, lds);
+    else if (hn) f8_tile<C, 2, H>(p, t.steps, ph, wave, lane, next, c, ld, off, s_off, acc, lds);
+    else f8_tile<C, 2, C::FN>(p, t.steps, ph, wave, lane, next, c, ld, off, s_off, acc, lds);
+    // the loads in flight are waited for here, as in tg_run
+    MOE_WAIT_VMCNT(0);
+    p.store(t, wm, wn, lane, acc);
+    if (L1 < 0) break;
+    L = L1;
+  }
+}
+
+// The same for TgSmall: the k-steps dealt to the four wavefronts, each with a ring of its own
+// (as tg_run_small).
+template <class C>
+struct F8One : C {
+  static constexpr int WM = 1, WN = 1, FM = 2, FN = 2;
+};
+template <class C, class P>
+__device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __restrict__ lds) {
+  constexpr int W = TgSmall::WAVES, NI = C::NI;
+  using One = F8One<C>;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uni(tid >> 6);
+  uint8_t* ring = lds + wave * (C::S * C::SLOT);
+  TgTiles q;
+  q.init(tiles, nullptr);
+  int hint = 0;
+  for (int j = q.own;; j += q.blocks(q.x)) {
+    const int L = q.at(q.x, j);
+    if (L < 0) break;
+    const typename P::Tile t = p.tile(L, hint);
+    hint = t.hint;
+    uint32_t ox[NI], ow[NI], sx, sw;
+    F8Load lx = f8_prepare<C, false>(t.X, t.m0, t.steps, t.length, 0, lane, ox, sx);
+    f8_scale_place<C>(t.X, false, t.m0, 0, lane, lx, sx);
+    F8Load lw = f8_prepare<C, C::WCOL>(t.W, t.n0, t.steps, t.length, 0, lane, ow, sw);
+    if (!C::WCOL) f8_scale_place<C>(t.W, true, t.n0, 0, lane, lw, sw);
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][k][r] = 0.f;
+    const int mine = t.steps > wave ? (t.steps - wave + W - 1) / W : 0;
+    auto issue = [&](int i, uint8_t* slot) {
+      const int s = wave + W * i;
+      const bool on = i < mine;
+      f8_mask_tail<C>(lx, s, 0, lane, ox);
+      f8_mask_tail<C>(lw, s, 0, lane, ow);
+      const int nx = uni(on ? f8_range(lx, s) : 0), nw = uni(on ? f8_range(lw, s) : 0);
+      const int ns = uni(on ? 0x7fffffff : 0);
+      const uint8_t *dx = uni(lx.base + (size_t)s * lx.step), *dw = uni(lw.base + (size_t)s * lw.step);
+#pragma unroll
+      for (int k = 0; k < NI; ++k) dma16(dx, ox[k], slot + k * 1024, nx);
+#pragma unroll
+      for (int k = 0; k < NI; ++k) dma16(dw, ow[k], slot + C::BM * 128 + k * 1024, nw);
+      dma4(uni(lx.scales + (size_t)s * lx.s_step), sx, slot + C::DATA, ns);
+      dma4(uni(lw.scales + (size_t)s * lw.s_step), sw, slot + C::DATA + 256, ns);
+    };
+    issue(0, ring);
+    issue(1, ring + C::SLOT);
+    for (int i = 0; i < mine; ++i) {
+      uint8_t* slot = ring + (i & 1) * C::SLOT;
+      MOE_WAIT_VMCNT(2 * NI + 2);  // this k-step has landed, the next one may be in flight
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      F8Frag x[2], w[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        x[k] = f8_frag_x<One>(slot, k, 0, lane);
+        w[k] = f8_frag_w<One>(slot, k, 0, lane);
+      }
+      const F8Scales<One> s = f8_scales<One>(slot, 0, lane);
+      MOE_WAIT_LGKMCNT0();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      issue(i + 2, slot);
+#pragma unroll
+      for (int fn = 0; fn < 2; ++fn)
+#pragma unroll
+        for (int fm = 0; fm < 2; ++fm)
+          f8_add(acc[fm][fn], f8_products<One>(w[fn], x[fm]), f8_scale_of<One>(s, fm, fn));
+    }
+    MOE_WAIT_VMCNT(0);  // the sums go through the ring
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    // the four sums through this wavefront's ring, every fragment as 16-byte runs
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *(f32x4*)(ring + f * 4096 + r * 1024 + lane * 16) =
+            f32x4{acc[f >> 1][f & 1][4 * r], acc[f >> 1][f & 1][4 * r + 1],
+                  acc[f >> 1][f & 1][4 * r + 2], acc[f >> 1][f & 1][4 * r + 3]};
+    __syncthreads();
+    f32x16 sum[1][1];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int o = 0; o < W; ++o) {
+        const f32x4 a =
+            *(const f32x4*)(lds + o * (C::S * C::SLOT) + wave * 4096 + r * 1024 + lane * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += a[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[0][0][4 * r + e] = v[e];
+    }
+    __syncthreads();  // the rings take the next tile's loads
+    p.store(t, wave / C::WN, wave % C::WN, lane, sum);
+  }
+}
+
+}  // namespace
+}  // namespace moe
