@@ -50,11 +50,14 @@ struct F8Operand {
 };
 
 // Loading state of one wavefront: its data loads (16 bytes a lane) and its load of 64 scales.
+// Load i of a k-step starts i * i_step bytes behind the first one; the lanes' offsets repeat
+// every second load.
 struct F8Load {
   const uint8_t *base, *scales;
-  uint32_t step, s_step;   // bytes from one k-step to the next
+  uint32_t step, s_step, i_step;  // bytes from one k-step to the next, from one load to the next
   int rows;                // column layout: contraction rows; row layout: -(k-steps)
   uint32_t pitch;
+  int range;               // row layout: bytes from base to the end of the tile's rows
   int tail;                // row layout: bytes of the last k-step that exist
 };
 
@@ -74,17 +77,16 @@ template <int W>
 __device__ __forceinline__ int f8_rotation(int k) {
   return 2 * (W == 256 ? k & 7 : W == 128 ? (k >> 1) & 3 : (k >> 2) & 1);
 }
-// Row layout: the byte of a row's k-step that load i of this lane takes.
-template <class C>
-__device__ __forceinline__ int f8_chunk_byte(int w, int i, int lane) {
-  const int r = (w * C::NI + i) * 8 + (lane >> 3);
-  return ((lane & 7) ^ ((r >> 1) & 7)) << 4;
+// Row layout: the byte of a row's k-step that load i of this lane takes (of the rows 8 i ..).
+__device__ __forceinline__ int f8_chunk_byte(int i, int lane) {
+  return ((lane & 7) ^ ((4 * i + (lane >> 4)) & 7)) << 4;
 }
 
-// Loads of wavefront w (of those on this side) of the tile's side at t0.
+// Loads of wavefront w (of those on this side) of the tile's side at t0; `blocks`: the scales
+// are those of blocks of 128 rows (w), else of rows (x).
 template <class C, bool COL>
-__device__ __forceinline__ F8Load f8_prepare(const F8Operand& o, int t0, int steps, int length,
-                                             int w, int lane, uint32_t (&off)[C::NI],
+__device__ __forceinline__ F8Load f8_prepare(const F8Operand& o, bool blocks, int t0, int steps,
+                                             int length, int w, int lane, uint32_t (&off)[2],
                                              uint32_t& s_off) {
   constexpr int W = C::BM;
   F8Load l;
@@ -94,64 +96,63 @@ __device__ __forceinline__ F8Load f8_prepare(const F8Operand& o, int t0, int ste
     constexpr int RPI = 1024 / W, CPR = W / 16;  // rows per load instruction, chunks per row
     l.base = uni(o.p);
     l.step = l.pitch * kF8Block;
+    l.i_step = l.pitch * RPI;
     l.rows = uni(o.rows);
-    l.tail = 0;
+    l.range = l.tail = 0;
 #pragma unroll
-    for (int i = 0; i < C::NI; ++i) {
-      const int k = (w * C::NI + i) * RPI + lane / CPR;
+    for (int i = 0; i < 2; ++i) {
+      const int k = lane / CPR;
       // columns past the last one reread the last chunk (never stored)
-      off[i] = (uint32_t)k * l.pitch +
-               min(t0 + 16 * ((lane % CPR) ^ f8_rotation<W>(k)), o.width - 16);
+      off[i] = (uint32_t)(w * C::NI * RPI + k) * l.pitch +
+               min(t0 + 16 * ((lane % CPR) ^ f8_rotation<W>(k + i * RPI)), o.width - 16);
     }
     l.scales = uni((const uint8_t*)o.s);
     s_off = 4 * o.s_row * (uint32_t)(min(t0 + 64 * w + lane, o.width - 1) / kF8Block);
   } else {
-    const int r0 = min(t0, o.rows - 1);
-    l.base = uni(o.p + (size_t)r0 * o.pitch);
+    // rows past the last one lie outside the range: they read zeros
+    const int r0 = t0 + w * C::NI * 8, rows = min(max(o.rows - r0, 0), C::NI * 8);
+    l.base = uni(o.p + (size_t)min(r0, o.rows - 1) * o.pitch);
     l.step = kF8Block;
-    // a wavefront whose rows all lie past the last one loads nothing (range 0)
-    l.rows = t0 + w * C::NI * 8 < o.rows ? -uni(steps) : 0;
+    l.i_step = l.pitch * 8;
+    l.rows = -uni(steps);
+    l.range = uni(rows) * (int)l.pitch;
     l.tail = uni(length - (steps - 1) * kF8Block);
 #pragma unroll
-    for (int i = 0; i < C::NI; ++i) {
-      const int r = (w * C::NI + i) * 8 + (lane >> 3);
-      // rows past the last one reread it (never stored)
-      off[i] = (uint32_t)(min(t0 + r, o.rows - 1) - r0) * l.pitch + f8_chunk_byte<C>(w, i, lane);
-    }
-    l.scales = uni((const uint8_t*)o.s);
-    s_off = 0;
+    for (int i = 0; i < 2; ++i)
+      off[i] = (uint32_t)(lane >> 3) * l.pitch + f8_chunk_byte(i, lane);
+    const int first = min(t0, o.rows - 1), r = min(t0 + 64 * w + lane, o.rows - 1);
+    l.scales = uni((const uint8_t*)(o.s + (blocks ? 0 : (size_t)first * o.s_row)));
+    s_off = 4 * o.s_row * (uint32_t)(blocks ? r / kF8Block : r - first);
   }
   return l;
-}
-// x's scales are those of rows, w's (forward) of blocks of 128 of its rows.
-template <class C>
-__device__ __forceinline__ void f8_scale_place(const F8Operand& o, bool blocks, int t0, int w, int lane,
-                                               F8Load& l, uint32_t& s_off) {
-  const int r0 = min(t0, o.rows - 1);
-  const int r = min(t0 + 64 * w + lane, o.rows - 1);
-  if (blocks) {
-    s_off = 4 * o.s_row * (uint32_t)(r / kF8Block);
-  } else {
-    l.scales = uni((const uint8_t*)(o.s + (size_t)r0 * o.s_row));
-    s_off = 4 * o.s_row * (uint32_t)(r - r0);
-  }
 }
 
 // Bytes from the k-step's base that its loads may touch; later ones read zeros.
 __device__ __forceinline__ int f8_range(const F8Load& l, int s) {
-  if (l.rows <= 0) return s < -l.rows ? 0x7fffffff : 0;
+  if (l.rows < 0) return s < -l.rows ? max(l.range - kF8Block * s, 0) : 0;
   return min(max(l.rows - kF8Block * s, 0), kF8Block) * (int)l.pitch;
+}
+// A k-step's data into `wr`.
+template <class C>
+__device__ __forceinline__ void f8_issue(const F8Load& l, int s, bool on, const uint32_t (&off)[2],
+                                         uint8_t* __restrict__ wr) {
+  const uint8_t* db = uni(l.base + (size_t)s * l.step);
+  int nrec = uni(on ? f8_range(l, s) : 0);
+#pragma unroll
+  for (int i = 0; i < C::NI; ++i) {
+    dma16(db, off[i & 1], wr + i * 1024, nrec);
+    db += l.i_step;
+    nrec = max(nrec - (int)l.i_step, 0);
+  }
 }
 
 // The last k-step of a row ends with the row: chunks behind it read zeros (their offset lies
 // outside every range).  Only k-steps of zeros follow it.
-template <class C>
-__device__ __forceinline__ void f8_mask_tail(const F8Load& l, int s, int w, int lane,
-                                             uint32_t (&off)[C::NI]) {
+__device__ __forceinline__ void f8_mask_tail(const F8Load& l, int s, int lane, uint32_t (&off)[2]) {
   if (l.rows < 0 && s == -l.rows - 1 && l.tail < kF8Block) {
 #pragma unroll
-    for (int i = 0; i < C::NI; ++i)
-      if (f8_chunk_byte<C>(w, i, lane) >= l.tail) off[i] = 0x7fffffffu;
+    for (int i = 0; i < 2; ++i)
+      if (f8_chunk_byte(i, lane) >= l.tail) off[i] = 0x7fffffffu;
   }
 }
 
@@ -270,12 +271,11 @@ __device__ __forceinline__ float f8_scale_of(const F8Scales<C>& s, int fm, int f
   return s.x[fm] * s.w[C::WN * 32 * fn / kF8Block];
 }
 
-// What passes from one k-step to the next: x's fragments and w's first one, the scales, and the
-// last pair's sum, which is added behind the next pair's start.
+// What passes from one k-step to the next: x's fragments and w's first one, and the last pair's
+// sum, which is added behind the next pair's start.
 template <class C>
 struct F8State {
   F8Frag x[C::FM], w[2];
-  F8Scales<C> s;
   f32x16 part;
   float scale;
 };
@@ -283,15 +283,13 @@ struct F8State {
 // One k-step out of ring slot `rd`.  The barrier stands before the last of w's fragments, when
 // every read of `rd` has been made: `rd` is free, the next k-step (slot `nx`) has landed, and
 // the last fragment's products cover the reads of the next k-step's first ones, each into the
-// registers that its last use has freed.  `wr` is `rd` again (see tg_step).
-template <class C, int FMA, int FNA>
+// registers that its last use has freed.  issue() loads into `rd` (under a name of its own, see
+// tg_step).
+template <class C, int FMA, int FNA, class Issue>
 __device__ __forceinline__ void f8_step(const uint8_t* __restrict__ rd, const uint8_t* __restrict__ nx,
                                         int wm, int wn, int lane, F8State<C>& f,
-                                        f32x16 (&acc)[C::FM][C::FN], const uint8_t* db,
-                                        const uint32_t (&off)[C::NI], const uint8_t* sb,
-                                        uint32_t s_off, uint8_t* __restrict__ wr, int wave, int nrec,
-                                        int s_nrec, bool landed) {
-  const F8Scales<C> s = f.s;
+                                        f32x16 (&acc)[C::FM][C::FN], Issue issue, bool landed) {
+  const F8Scales<C> s = f8_scales<C>(rd, wm, lane);
 #pragma unroll
   for (int fn = 0; fn < FNA; ++fn) {
     if (fn + 1 < FNA) {
@@ -299,11 +297,8 @@ __device__ __forceinline__ void f8_step(const uint8_t* __restrict__ rd, const ui
     } else {
       if (!landed) MOE_WAIT_VMCNT((C::S - 2) * (C::NI + 1));
       lds_sync();
-      f.s = f8_scales<C>(nx, wm, lane);
       if (FNA > 1) f.w[0] = f8_frag_w<C>(nx, 0, wn, lane);
-#pragma unroll
-      for (int i = 0; i < C::NI; ++i) dma16(db, off[i], wr + (wave * C::NI + i) * 1024, nrec);
-      dma4(sb, s_off, wr + C::DATA + wave * 256, s_nrec);
+      issue();
     }
 #pragma unroll
     for (int fm = 0; fm < FMA; ++fm) {
@@ -322,17 +317,10 @@ __device__ __forceinline__ void f8_step(const uint8_t* __restrict__ rd, const ui
 // The loads of this wavefront: x in the first half of them, w in the other.
 template <class C, class Tile>
 __device__ __forceinline__ F8Load f8_prepare_wave(const Tile& t, int wave, int lane,
-                                                  uint32_t (&off)[C::NI], uint32_t& s_off) {
+                                                  uint32_t (&off)[2], uint32_t& s_off) {
   constexpr int H = C::WM * C::WN / 2;
-  F8Load l;
-  if (wave < H) {
-    l = f8_prepare<C, false>(t.X, t.m0, t.steps, t.length, wave, lane, off, s_off);
-    f8_scale_place<C>(t.X, false, t.m0, wave, lane, l, s_off);
-  } else {
-    l = f8_prepare<C, C::WCOL>(t.W, t.n0, t.steps, t.length, wave - H, lane, off, s_off);
-    if (!C::WCOL) f8_scale_place<C>(t.W, true, t.n0, wave - H, lane, l, s_off);
-  }
-  return l;
+  if (wave < H) return f8_prepare<C, false>(t.X, false, t.m0, t.steps, t.length, wave, lane, off, s_off);
+  return f8_prepare<C, C::WCOL>(t.W, true, t.n0, t.steps, t.length, wave - H, lane, off, s_off);
 }
 
 struct F8Cursor {
@@ -342,7 +330,7 @@ struct F8Cursor {
 };
 template <class C, class P>
 __device__ __forceinline__ void f8_seek(const P& p, int L, F8Cursor& c, F8Load& ld,
-                                        uint32_t (&off)[C::NI], uint32_t& s_off, int wave, int lane) {
+                                        uint32_t (&off)[2], uint32_t& s_off, int wave, int lane) {
   c.s = c.steps = c.real = 0;
   if (L < 0) return;
   const typename P::Tile t = p.tile(L, c.hint);
@@ -351,16 +339,20 @@ __device__ __forceinline__ void f8_seek(const P& p, int L, F8Cursor& c, F8Load& 
   c.steps = max(c.real, C::S + 1);
   ld = f8_prepare_wave<C>(t, wave, lane, off, s_off);
 }
+// The cursor's k-step into `slot`, with its scales.
 template <class C>
-__device__ __forceinline__ int f8_side(int wave) {
-  constexpr int H = C::WM * C::WN / 2;
-  return wave < H ? wave : wave - H;
+__device__ __forceinline__ void f8_issue_step(const F8Cursor& c, const F8Load& ld,
+                                              const uint32_t (&off)[2], uint32_t s_off, int wave,
+                                              uint8_t* __restrict__ slot) {
+  f8_issue<C>(ld, c.s, c.steps > 0, off, slot + wave * C::NI * 1024);
+  dma4(uni(ld.scales + (size_t)c.s * ld.s_step), s_off, slot + C::DATA + wave * 256,
+       uni(c.s < c.real ? 0x7fffffff : 0));
 }
 
 // The k-steps of a tile (as tg_tile).
 template <class C, int FMA, int FNA, class P, class Next>
 __device__ __forceinline__ void f8_tile(const P& p, int steps, int& ph, int wave, int lane, Next next,
-                                        F8Cursor& c, F8Load& ld, uint32_t (&off)[C::NI],
+                                        F8Cursor& c, F8Load& ld, uint32_t (&off)[2],
                                         uint32_t& s_off, f32x16 (&acc)[C::FM][C::FN],
                                         uint8_t* __restrict__ lds) {
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -368,7 +360,6 @@ __device__ __forceinline__ void f8_tile(const P& p, int steps, int& ph, int wave
   const int all = max(steps, C::S + 1);
   F8State<C> f;
   const uint8_t* first = lds + ph * C::SLOT;
-  f.s = f8_scales<C>(first, wm, lane);
 #pragma unroll
   for (int fm = 0; fm < FMA; ++fm) f.x[fm] = f8_frag_x<C>(first, fm, wm, lane);
   f.w[0] = f8_frag_w<C>(first, 0, wn, lane);
@@ -377,14 +368,10 @@ __device__ __forceinline__ void f8_tile(const P& p, int steps, int& ph, int wave
   f.scale = 0.f;
   for (int s = 0; s < all; ++s) {
     const int after = ph + 1 < C::S ? ph + 1 : 0;
-    f8_mask_tail<C>(ld, c.s, f8_side<C>(wave), lane, off);
-    const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
-    const uint8_t* sb = uni(ld.scales + (size_t)c.s * ld.s_step);
-    const int nrec = uni(c.steps > 0 ? f8_range(ld, c.s) : 0);
-    const int s_nrec = uni(c.s < c.real ? 0x7fffffff : 0);
+    f8_mask_tail(ld, c.s, lane, off);
     uint8_t* rd = lds + ph * C::SLOT;
-    f8_step<C, FMA, FNA>(rd, lds + after * C::SLOT, wm, wn, lane, f, acc, db, off, sb, s_off, rd,
-                         wave, nrec, s_nrec, s < C::S - 1);
+    f8_step<C, FMA, FNA>(rd, lds + after * C::SLOT, wm, wn, lane, f, acc,
+                         [&]() { f8_issue_step<C>(c, ld, off, s_off, wave, rd); }, s < C::S - 1);
     c.s = uni(c.s + 1);
     if (c.s == c.steps) f8_seek<C>(p, next(), c, ld, off, s_off, wave, lane);
     ph = after;
@@ -405,19 +392,13 @@ __device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restric
   if (L < 0) return;
   F8Cursor c{0, 0, 0, 0};
   F8Load ld{};
-  uint32_t off[C::NI] = {}, s_off = 0;
+  uint32_t off[2] = {}, s_off = 0;
   f8_seek<C>(p, L, c, ld, off, s_off, wave, lane);
   int ph = 0;  // ring slot of the next k-step
 #pragma unroll
   for (int k = 0; k < C::S; ++k) {
-    f8_mask_tail<C>(ld, c.s, f8_side<C>(wave), lane, off);
-    uint8_t* w = lds + k * C::SLOT;
-    const uint8_t* db = uni(ld.base + (size_t)c.s * ld.step);
-    const uint8_t* sb = uni(ld.scales + (size_t)c.s * ld.s_step);
-    const int nrec = uni(f8_range(ld, c.s)), s_nrec = uni(c.s < c.real ? 0x7fffffff : 0);
-#pragma unroll
-    for (int i = 0; i < C::NI; ++i) dma16(db, off[i], w + (wave * C::NI + i) * 1024, nrec);
-    dma4(sb, s_off, w + C::DATA + wave * 256, s_nrec);
+    f8_mask_tail(ld, c.s, lane, off);
+    f8_issue_step<C>(c, ld, off, s_off, wave, lds + k * C::SLOT);
     c.s = uni(c.s + 1);
   }
   pipe_sync();
@@ -470,11 +451,9 @@ __device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __r
     if (L < 0) break;
     const typename P::Tile t = p.tile(L, hint);
     hint = t.hint;
-    uint32_t ox[NI], ow[NI], sx, sw;
-    F8Load lx = f8_prepare<C, false>(t.X, t.m0, t.steps, t.length, 0, lane, ox, sx);
-    f8_scale_place<C>(t.X, false, t.m0, 0, lane, lx, sx);
-    F8Load lw = f8_prepare<C, C::WCOL>(t.W, t.n0, t.steps, t.length, 0, lane, ow, sw);
-    if (!C::WCOL) f8_scale_place<C>(t.W, true, t.n0, 0, lane, lw, sw);
+    uint32_t ox[2], ow[2], sx, sw;
+    const F8Load lx = f8_prepare<C, false>(t.X, false, t.m0, t.steps, t.length, 0, lane, ox, sx);
+    const F8Load lw = f8_prepare<C, C::WCOL>(t.W, true, t.n0, t.steps, t.length, 0, lane, ow, sw);
     f32x16 acc[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -486,15 +465,11 @@ __device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __r
     auto issue = [&](int i, uint8_t* slot) {
       const int s = wave + W * i;
       const bool on = i < mine;
-      f8_mask_tail<C>(lx, s, 0, lane, ox);
-      f8_mask_tail<C>(lw, s, 0, lane, ow);
-      const int nx = uni(on ? f8_range(lx, s) : 0), nw = uni(on ? f8_range(lw, s) : 0);
+      f8_mask_tail(lx, s, lane, ox);
+      f8_mask_tail(lw, s, lane, ow);
       const int ns = uni(on ? 0x7fffffff : 0);
-      const uint8_t *dx = uni(lx.base + (size_t)s * lx.step), *dw = uni(lw.base + (size_t)s * lw.step);
-#pragma unroll
-      for (int k = 0; k < NI; ++k) dma16(dx, ox[k], slot + k * 1024, nx);
-#pragma unroll
-      for (int k = 0; k < NI; ++k) dma16(dw, ow[k], slot + C::BM * 128 + k * 1024, nw);
+      f8_issue<C>(lx, s, on, ox, slot);
+      f8_issue<C>(lw, s, on, ow, slot + C::BM * 128);
       dma4(uni(lx.scales + (size_t)s * lx.s_step), sx, slot + C::DATA, ns);
       dma4(uni(lw.scales + (size_t)s * lw.s_step), sw, slot + C::DATA + 256, ns);
     };
