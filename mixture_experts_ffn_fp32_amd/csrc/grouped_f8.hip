@@ -144,8 +144,10 @@ struct F8Tiles {
 
 template <class C, int DIR>
 __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void grouped_f8_kernel(F8Product p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS];
-  __shared__ GroupTables t;
+  // (one array: accesses to several would lose the scopes that tell reads of the ring from the
+  // loads into it, see f8_step)
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS + sizeof(GroupTables)];
+  GroupTables& t = *(GroupTables*)(lds + C::LDS);
   group_tables<GR_FWD>(p.g, p.offsets, C::BM, t);
   const F8Tiles<C, DIR> tiles{p, t};
   if (p.zero_rest) {

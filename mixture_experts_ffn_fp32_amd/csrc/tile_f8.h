@@ -36,6 +36,9 @@ struct F8Config : Shape {
   static constexpr int SLOT = DATA + 4 * (Shape::BM + Shape::BN);  // and of their scales
   static constexpr int LDS = Shape::S * SLOT * (SMALL ? TgSmall::WAVES : 1);
   static constexpr int WAVES_PER_SIMD = Shape::BPC * Shape::THREADS / 256;
+  // Loads of a k-step per wavefront (its data and 64 scales), and how many of them follow the
+  // barrier that frees their slot at once (f8_step).
+  static constexpr int LOADS = Shape::NI + 1, FIRST = Shape::NI / 2 - 1;
 };
 
 // A tile's operands.  Row layout: `rows` rows of `pitch` bytes, of which the first `length` are
@@ -132,18 +135,29 @@ __device__ __forceinline__ int f8_range(const F8Load& l, int s) {
   if (l.rows < 0) return s < -l.rows ? max(l.range - kF8Block * s, 0) : 0;
   return min(max(l.rows - kF8Block * s, 0), kF8Block) * (int)l.pitch;
 }
-// A k-step's data into `wr`.
+// A k-step that is being loaded: where its data and scales come from, uniform.
+struct F8Source {
+  const uint8_t *data, *scales;
+  int range, s_range;
+};
+__device__ __forceinline__ F8Source f8_source(const F8Load& l, int s, bool on) {
+  F8Source f;
+  f.data = uni(l.base + (size_t)s * l.step);
+  f.scales = uni(l.scales + (size_t)s * l.s_step);
+  f.range = uni(on ? f8_range(l, s) : 0);
+  f.s_range = uni(on ? 0x7fffffff : 0);
+  return f;
+}
+// Load i of it (the last one the scales) of wavefront `part` into ring slot `wr`.
 template <class C>
-__device__ __forceinline__ void f8_issue(const F8Load& l, int s, bool on, const uint32_t (&off)[2],
-                                         uint8_t* __restrict__ wr) {
-  const uint8_t* db = uni(l.base + (size_t)s * l.step);
-  int nrec = uni(on ? f8_range(l, s) : 0);
-#pragma unroll
-  for (int i = 0; i < C::NI; ++i) {
-    dma16(db, off[i & 1], wr + i * 1024, nrec);
-    db += l.i_step;
-    nrec = max(nrec - (int)l.i_step, 0);
-  }
+__device__ __forceinline__ void f8_load(const F8Source& f, const F8Load& l, int i,
+                                        const uint32_t (&off)[2], uint32_t s_off,
+                                        uint8_t* __restrict__ wr, int part) {
+  if (i == C::NI)
+    dma4(f.scales, s_off, wr + C::DATA + part * 256, f.s_range);
+  else
+    dma16(f.data + (size_t)i * l.i_step, off[i & 1], wr + (part * C::NI + i) * 1024,
+          max(f.range - i * (int)l.i_step, 0));
 }
 
 // The last k-step of a row ends with the row: chunks behind it read zeros (their offset lies
@@ -156,49 +170,67 @@ __device__ __forceinline__ void f8_mask_tail(const F8Load& l, int s, int lane, u
   }
 }
 
-// 32 rows (columns) of a tile, half h (64 indices) of a k-step: lane l holds row l % 32,
+// A k-step of 32 rows (columns) of a tile: lane l holds row l % 32, in half h (64 indices)
 // indices 64 h + 16 (l / 32) + 0 .. 15 and the same 32 further on.
-__device__ __forceinline__ i32x8 f8_join(const u32x4& a, const u32x4& b) {
-  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-template <class C, bool COL>
-__device__ __forceinline__ i32x8 f8_frag(const uint8_t* rd, int h, int u_const, int u_wave, int lane) {
-  if constexpr (COL) {
-    constexpr int W = C::BN;
-    const int l16 = lane & 15, k = 16 * (lane >> 5) + (l16 >> 1);
-    const int c = (2 * (u_const + u_wave) + ((lane >> 4) & 1)) ^ f8_rotation<W>(k);
-    const uint8_t* p = rd + k * W + c * 16 + 8 * (l16 & 1) + 64 * h * W;
-    i32x8 v;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {  // rows + 0, 8, 32, 40
-      const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-          (__attribute__((address_space(3))) i32x2*)(__attribute__((address_space(3)))
-                                                     const uint8_t*)(p + (8 * (j & 1) + 32 * (j >> 1)) * W));
-      v[2 * j] = t[0];
-      v[2 * j + 1] = t[1];
-    }
-    return v;
-  } else {
-    const int r = u_wave * 32 + (lane & 31);
-    const u32x4 a = *(const u32x4*)(rd + lds_chunk_offset(r, 4 * h + (lane >> 5)) + u_const * 32 * 128);
-    const u32x4 b = *(const u32x4*)(rd + lds_chunk_offset(r, 4 * h + 2 + (lane >> 5)) + u_const * 32 * 128);
-    return f8_join(a, b);
-  }
-}
-
 struct F8Frag {
   i32x8 h[2];
 };
+// A lane's place in the first of its wavefront's fragments (fragment WN f + u is the f-th).  Row
+// layout: its chunk 16 (l / 32); the other chunks are that xor 32 (the other 16 bytes of half 0),
+// 64 and 96.  Column layout: its column of contraction row 16 (l / 32) + (l % 16) / 2; the f-th
+// fragment's is that xor 32 WN f, as a fragment's columns are 32 bytes of the row.
+template <int W, bool COL>
+__device__ __forceinline__ int f8_place(int u, int lane) {
+  if constexpr (COL) {
+    const int l16 = lane & 15, k = 16 * (lane >> 5) + (l16 >> 1);
+    return k * W + ((2 * u + ((lane >> 4) & 1)) ^ f8_rotation<W>(k)) * 16 + 8 * (l16 & 1);
+  } else {
+    return lds_chunk_offset(u * 32 + (lane & 31), lane >> 5);
+  }
+}
+// The f-th fragment of the operand at rd, N being the wavefronts that share it out.
+template <int W, bool COL, int N>
+__device__ __forceinline__ F8Frag f8_frag(const uint8_t* rd, int place, int f) {
+  // (opaque: the few operations that make the addresses are repeated for every fragment, as
+  // kept addresses would push sums out of the registers)
+  asm volatile("" : "+v"(place));
+  F8Frag v;
+  if constexpr (COL) {
+    const uint8_t* p = rd + (place ^ (32 * N * f));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // rows + 0, 8, 32, 40 of each half
+      const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (__attribute__((address_space(3))) i32x2*)(__attribute__((address_space(3)))
+                                                     const uint8_t*)(p + (8 * (j & 1) + 32 * (j >> 1)) * W));
+      v.h[j >> 2][2 * (j & 3)] = t[0];
+      v.h[j >> 2][2 * (j & 3) + 1] = t[1];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 c = *(const u32x4*)(rd + (place ^ (32 * j)) + N * f * 32 * 128);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.h[j >> 1][4 * (j & 1) + e] = (int)c[e];
+    }
+  }
+  return v;
+}
+// Both places of a wavefront.
+struct F8Places {
+  int x, w;
+};
 template <class C>
-__device__ __forceinline__ F8Frag f8_frag_x(const uint8_t* rd, int fm, int wm, int lane) {
-  return F8Frag{{f8_frag<C, false>(rd, 0, C::WM * fm, wm, lane),
-                 f8_frag<C, false>(rd, 1, C::WM * fm, wm, lane)}};
+__device__ __forceinline__ F8Places f8_places(int wm, int wn, int lane) {
+  return F8Places{f8_place<C::BM, false>(wm, lane),
+                  C::BM * 128 + f8_place<C::BN, C::WCOL>(wn, lane)};
 }
 template <class C>
-__device__ __forceinline__ F8Frag f8_frag_w(const uint8_t* rd, int fn, int wn, int lane) {
-  rd += C::BM * 128;
-  return F8Frag{{f8_frag<C, C::WCOL>(rd, 0, C::WN * fn, wn, lane),
-                 f8_frag<C, C::WCOL>(rd, 1, C::WN * fn, wn, lane)}};
+__device__ __forceinline__ F8Frag f8_frag_x(const uint8_t* rd, const F8Places& at, int fm) {
+  return f8_frag<C::BM, false, C::WM>(rd, at.x, fm);
+}
+template <class C>
+__device__ __forceinline__ F8Frag f8_frag_w(const uint8_t* rd, const F8Places& at, int fn) {
+  return f8_frag<C::BN, C::WCOL, C::WN>(rd, at.w, fn);
 }
 
 // Eight 8-bit values (two words) as bfloat16, which is exact.
@@ -263,7 +295,8 @@ __device__ __forceinline__ F8Scales<C> f8_scales(const uint8_t* rd, int wm, int 
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) v.x[i] = s[(C::WM * i + wm) * 32 + (lane & 31)];
 #pragma unroll
-  for (int j = 0; j < F8Scales<C>::NB; ++j) v.w[j] = s[C::BM + j * kF8Block];
+  for (int j = 0; j < F8Scales<C>::NB; ++j)
+    v.w[j] = __uint_as_float(uni((int)__float_as_uint(s[C::BM + j * kF8Block])));
   return v;
 }
 template <class C>
@@ -280,38 +313,90 @@ struct F8State {
   float scale;
 };
 
+// Order of a pair's products: behind each MFMA its share of the loads and of the LDS reads, and
+// of the last pair's additions.
+template <int LOADS, int READS>
+__device__ __forceinline__ void f8_order() {
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+    for (int i = m * LOADS / 2; i < (m + 1) * LOADS / 2; ++i)
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+#pragma unroll
+    for (int i = m * READS / 2; i < (m + 1) * READS / 2; ++i)
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+  }
+}
+
 // One k-step out of ring slot `rd`.  The barrier stands before the last of w's fragments, when
 // every read of `rd` has been made: `rd` is free, the next k-step (slot `nx`) has landed, and
 // the last fragment's products cover the reads of the next k-step's first ones, each into the
-// registers that its last use has freed.  issue() loads into `rd` (under a name of its own, see
-// tg_step).
-template <class C, int FMA, int FNA, class Issue>
-__device__ __forceinline__ void f8_step(const uint8_t* __restrict__ rd, const uint8_t* __restrict__ nx,
-                                        int wm, int wn, int lane, F8State<C>& f,
-                                        f32x16 (&acc)[C::FM][C::FN], Issue issue, bool landed) {
+// registers that its last use has freed.
+//
+// The loads of the k-step after the next one go into `rd`: C::FIRST of them behind the barrier,
+// the others in the next call, each behind an MFMA.  (All of them behind the barrier they held
+// the wavefronts up: a load takes the address path 16 cycles, 72 of them of eight wavefronts
+// 1150, half a k-step, and a wavefront whose load waits issues no MFMA.)  load(i, slot) issues the
+// i-th load, advance() passes to the next k-step.  wr_rd and wr_nx are rd and nx again: with
+// the loads and the reads in separate restrict scopes the compiler does not make every fragment
+// read wait for the loads in flight, and the barrier's fences keep their order.
+template <class C, int FMA, int FNA, class Advance>
+__device__ __forceinline__ void f8_step(const uint8_t* __restrict__ rd,
+                                        const uint8_t* __restrict__ nx, uint8_t* __restrict__ wr_rd,
+                                        uint8_t* __restrict__ wr_nx, const F8Places& at, int wm,
+                                        int lane, int wave, F8State<C>& f,
+                                        f32x16 (&acc)[C::FM][C::FN], const F8Source& from,
+                                        const F8Load& ld, const uint32_t (&off)[2],
+                                        const uint32_t& s_off, Advance advance) {
+  constexpr int REST = C::LOADS - C::FIRST;         // of the k-step in `nx`
+  constexpr int SPREAD = FNA > 2 ? FNA - 2 : 1;     // over so many groups of products
   const F8Scales<C> s = f8_scales<C>(rd, wm, lane);
+  // the products of fragments (fm, fn), and the pair's before them added
+  auto pair = [&](int fn, int fm) {
+    const f32x16 part = f8_products<C>(f.w[fn & 1], f.x[fm]);
+    const int pm = fm > 0 ? fm - 1 : FMA - 1, pn = fm > 0 ? fn : fn > 0 ? fn - 1 : FNA - 1;
+    f8_add(acc[pm][pn], f.part, f.scale);
+    f.part = part;
+    f.scale = f8_scale_of<C>(s, fm, fn);
+  };
+  // (the last group apart: in one loop the reads of rd and of nx would be merged, and lose
+  // their scopes)
 #pragma unroll
-  for (int fn = 0; fn < FNA; ++fn) {
-    if (fn + 1 < FNA) {
-      f.w[(fn + 1) & 1] = f8_frag_w<C>(rd, fn + 1, wn, lane);
-    } else {
-      if (!landed) MOE_WAIT_VMCNT((C::S - 2) * (C::NI + 1));
-      lds_sync();
-      if (FNA > 1) f.w[0] = f8_frag_w<C>(nx, 0, wn, lane);
-      issue();
-    }
+  for (int fn = 0; fn + 1 < FNA; ++fn) {
+    f.w[(fn + 1) & 1] = f8_frag_w<C>(rd, at, fn + 1);
+    const int l0 = C::FIRST + (fn < SPREAD ? fn * REST / SPREAD : REST);
+    const int l1 = C::FIRST + (fn < SPREAD ? (fn + 1) * REST / SPREAD : REST);
 #pragma unroll
     for (int fm = 0; fm < FMA; ++fm) {
-      const f32x16 part = f8_products<C>(f.w[fn & 1], f.x[fm]);
-      const int pm = fm > 0 ? fm - 1 : FMA - 1, pn = fm > 0 ? fn : fn > 0 ? fn - 1 : FNA - 1;
-      f8_add(acc[pm][pn], f.part, f.scale);
-      f.part = part;
-      f.scale = f8_scale_of<C>(s, fm, fn);
-      if (fn + 1 == FNA) f.x[fm] = f8_frag_x<C>(nx, fm, wm, lane);
+#pragma unroll
+      for (int i = l0 + fm * (l1 - l0) / FMA; i < l0 + (fm + 1) * (l1 - l0) / FMA; ++i)
+        f8_load<C>(from, ld, i, off, s_off, wr_nx, wave);
+      pair(fn, fm);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (FNA == 1) f.w[0] = f8_frag_w<C>(nx, 0, wn, lane);
+    if (fn + 1 == SPREAD) advance();
   }
+  if (FNA == 1) {
+#pragma unroll
+    for (int i = C::FIRST; i < C::LOADS; ++i) f8_load<C>(from, ld, i, off, s_off, wr_nx, wave);
+    advance();
+  }
+  MOE_WAIT_VMCNT(0);
+  lds_sync();
+  if (FNA > 1) f.w[0] = f8_frag_w<C>(nx, at, 0);
+#pragma unroll
+  for (int fm = 0; fm < FMA; ++fm) {
+#pragma unroll
+    for (int i = fm * C::FIRST / FMA; i < (fm + 1) * C::FIRST / FMA; ++i)
+      f8_load<C>(from, ld, i, off, s_off, wr_rd, wave);
+    pair(FNA - 1, fm);
+    f.x[fm] = f8_frag_x<C>(nx, at, fm);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (FNA == 1) f.w[0] = f8_frag_w<C>(nx, at, 0);
 }
 
 // The loads of this wavefront: x in the first half of them, w in the other.
@@ -323,57 +408,67 @@ __device__ __forceinline__ F8Load f8_prepare_wave(const Tile& t, int wave, int l
   return f8_prepare<C, C::WCOL>(t.W, true, t.n0, t.steps, t.length, wave - H, lane, off, s_off);
 }
 
+// The loads' place in the stream of k-steps of a block's tiles (see TgCursor).
 struct F8Cursor {
   int hint;
   int s, steps;      // the tile's next k-step, its k-steps (0: the stream has ended)
   int real;          // those that exist
+  F8Source from;
 };
+// k-steps of a tile: two at least, so that the loads, which are a k-step ahead, pass to the next
+// tile while this one is multiplied (k-steps of zeros follow the last one).
+__device__ __forceinline__ int f8_steps(int steps) { return max(steps, 2); }
+
+// The cursor to tile L (-1: the stream has ended).
 template <class C, class P>
 __device__ __forceinline__ void f8_seek(const P& p, int L, F8Cursor& c, F8Load& ld,
                                         uint32_t (&off)[2], uint32_t& s_off, int wave, int lane) {
   c.s = c.steps = c.real = 0;
-  if (L < 0) return;
-  const typename P::Tile t = p.tile(L, c.hint);
-  c.hint = uni(t.hint);
-  c.real = uni(t.steps);
-  c.steps = max(c.real, C::S + 1);
-  ld = f8_prepare_wave<C>(t, wave, lane, off, s_off);
+  if (L >= 0) {
+    const typename P::Tile t = p.tile(L, c.hint);
+    c.hint = uni(t.hint);
+    c.real = uni(t.steps);
+    c.steps = f8_steps(c.real);
+    ld = f8_prepare_wave<C>(t, wave, lane, off, s_off);
+  }
 }
-// The cursor's k-step into `slot`, with its scales.
-template <class C>
-__device__ __forceinline__ void f8_issue_step(const F8Cursor& c, const F8Load& ld,
-                                              const uint32_t (&off)[2], uint32_t s_off, int wave,
-                                              uint8_t* __restrict__ slot) {
-  f8_issue<C>(ld, c.s, c.steps > 0, off, slot + wave * C::NI * 1024);
-  dma4(uni(ld.scales + (size_t)c.s * ld.s_step), s_off, slot + C::DATA + wave * 256,
-       uni(c.s < c.real ? 0x7fffffff : 0));
+// Ready to load the cursor's k-step.
+__device__ __forceinline__ void f8_ready(F8Cursor& c, const F8Load& ld, int lane,
+                                         uint32_t (&off)[2]) {
+  f8_mask_tail(ld, c.s, lane, off);
+  c.from = f8_source(ld, c.s, c.s < c.real);
 }
 
-// The k-steps of a tile (as tg_tile).
+// The k-steps of a tile.  On entry the first one lies in slot ph, and C::FIRST loads of the
+// second one have been issued; on return the same holds of the next tile (next()).
 template <class C, int FMA, int FNA, class P, class Next>
 __device__ __forceinline__ void f8_tile(const P& p, int steps, int& ph, int wave, int lane, Next next,
                                         F8Cursor& c, F8Load& ld, uint32_t (&off)[2],
                                         uint32_t& s_off, f32x16 (&acc)[C::FM][C::FN],
                                         uint8_t* __restrict__ lds) {
+  static_assert(C::S == 2, "one k-step is multiplied, one is loaded");
   const int wm = wave / C::WN, wn = wave % C::WN;
   asm volatile("" : "+v"(lane));  // (see tg_tile)
-  const int all = max(steps, C::S + 1);
+  const int all = f8_steps(steps);
+  const F8Places at = f8_places<C>(wm, wn, lane);
   F8State<C> f;
   const uint8_t* first = lds + ph * C::SLOT;
 #pragma unroll
-  for (int fm = 0; fm < FMA; ++fm) f.x[fm] = f8_frag_x<C>(first, fm, wm, lane);
-  f.w[0] = f8_frag_w<C>(first, 0, wn, lane);
+  for (int fm = 0; fm < FMA; ++fm) f.x[fm] = f8_frag_x<C>(first, at, fm);
+  f.w[0] = f8_frag_w<C>(first, at, 0);
 #pragma unroll
   for (int r = 0; r < 16; ++r) f.part[r] = 0.f;
   f.scale = 0.f;
   for (int s = 0; s < all; ++s) {
-    const int after = ph + 1 < C::S ? ph + 1 : 0;
-    f8_mask_tail(ld, c.s, lane, off);
-    uint8_t* rd = lds + ph * C::SLOT;
-    f8_step<C, FMA, FNA>(rd, lds + after * C::SLOT, wm, wn, lane, f, acc,
-                         [&]() { f8_issue_step<C>(c, ld, off, s_off, wave, rd); }, s < C::S - 1);
-    c.s = uni(c.s + 1);
-    if (c.s == c.steps) f8_seek<C>(p, next(), c, ld, off, s_off, wave, lane);
+    const int after = ph ^ 1;
+    f8_step<C, FMA, FNA>(
+        lds + ph * C::SLOT, lds + after * C::SLOT, lds + ph * C::SLOT, lds + after * C::SLOT, at, wm,
+        lane, wave, f, acc, c.from, ld, off, s_off,
+        [&]() {
+          c.s = uni(c.s + 1);
+          if (c.s >= c.steps) f8_seek<C>(p, next(), c, ld, off, s_off, wave, lane);
+          f8_ready(c, ld, lane, off);
+        });
     ph = after;
   }
   f8_add(acc[FMA - 1][FNA - 1], f.part, f.scale);
@@ -390,18 +485,20 @@ __device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restric
   int mine = q.own;
   int L = q.at(q.x, mine);
   if (L < 0) return;
-  F8Cursor c{0, 0, 0, 0};
+  F8Cursor c{};
   F8Load ld{};
   uint32_t off[2] = {}, s_off = 0;
   f8_seek<C>(p, L, c, ld, off, s_off, wave, lane);
-  int ph = 0;  // ring slot of the next k-step
 #pragma unroll
-  for (int k = 0; k < C::S; ++k) {
-    f8_mask_tail(ld, c.s, lane, off);
-    f8_issue_step<C>(c, ld, off, s_off, wave, lds + k * C::SLOT);
-    c.s = uni(c.s + 1);
+  for (int k = 0; k < 2; ++k) {
+    f8_ready(c, ld, lane, off);
+#pragma unroll
+    for (int i = 0; i < (k == 0 ? C::LOADS : C::FIRST); ++i)
+      f8_load<C>(c.from, ld, i, off, s_off, lds + k * C::SLOT, wave);
+    if (k == 0) c.s = 1;
   }
   pipe_sync();
+  int ph = 0;  // ring slot of the next k-step
   int L1 = -1;
   auto next = [&]() -> int { return L1 = q.at(q.x, mine += q.blocks(q.x)); };
   int hint = 0;
@@ -422,7 +519,8 @@ __device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restric
     else if (hm) f8_tile<C, 1, C::FN>(p, t.steps, ph, wave, lane, next, c, ld, off, s_off, acc, lds);
     else if (hn) f8_tile<C, 2, H>(p, t.steps, ph, wave, lane, next, c, ld, off, s_off, acc, lds);
     else f8_tile<C, 2, C::FN>(p, t.steps, ph, wave, lane, next, c, ld, off, s_off, acc, lds);
-    // the loads in flight are waited for here, as in tg_run
+    // the loads in flight are waited for here: to the compiler they could be any slot's, and
+    // every fragment read of the next tile's loop would wait for loads
     MOE_WAIT_VMCNT(0);
     p.store(t, wm, wn, lane, acc);
     if (L1 < 0) break;
@@ -443,6 +541,7 @@ __device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __r
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uni(tid >> 6);
   uint8_t* ring = lds + wave * (C::S * C::SLOT);
+  const F8Places at = f8_places<One>(0, 0, lane);
   TgTiles q;
   q.init(tiles, nullptr);
   int hint = 0;
@@ -467,11 +566,11 @@ __device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __r
       const bool on = i < mine;
       f8_mask_tail(lx, s, lane, ox);
       f8_mask_tail(lw, s, lane, ow);
-      const int ns = uni(on ? 0x7fffffff : 0);
-      f8_issue<C>(lx, s, on, ox, slot);
-      f8_issue<C>(lw, s, on, ow, slot + C::BM * 128);
-      dma4(uni(lx.scales + (size_t)s * lx.s_step), sx, slot + C::DATA, ns);
-      dma4(uni(lw.scales + (size_t)s * lw.s_step), sw, slot + C::DATA + 256, ns);
+      const F8Source fx = f8_source(lx, s, on), fw = f8_source(lw, s, on);
+#pragma unroll
+      for (int k = 0; k < C::LOADS; ++k) f8_load<C>(fx, lx, k, ox, sx, slot, 0);
+#pragma unroll
+      for (int k = 0; k < C::LOADS; ++k) f8_load<C>(fw, lw, k, ow, sw, slot, 1);
     };
     issue(0, ring);
     issue(1, ring + C::SLOT);
@@ -483,8 +582,8 @@ __device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __r
       F8Frag x[2], w[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        x[k] = f8_frag_x<One>(slot, k, 0, lane);
-        w[k] = f8_frag_w<One>(slot, k, 0, lane);
+        x[k] = f8_frag_x<One>(slot, at, k);
+        w[k] = f8_frag_w<One>(slot, at, k);
       }
       const F8Scales<One> s = f8_scales<One>(slot, 0, lane);
       MOE_WAIT_LGKMCNT0();
