@@ -84,11 +84,48 @@ struct F8Tiles {
     return t;
   }
 
+  // bfloat16 results, two neighbouring fragments at a time: four lanes exchange their runs of
+  // four rows, so that a store writes whole lines, 8 rows of 128 bytes (32 of 32 bytes before:
+  // 49152 rows in 64 groups, 1408 x 2048, 210 -> 204 us).
+  __device__ __forceinline__ void store_lines(const Tile& t, int wm, int wn, int lane,
+                                              f32x16 (&acc)[C::FM][C::FN]) const {
+    const int N = width();
+#pragma unroll
+    for (int fm = 0; fm < C::FM; ++fm) {
+      const int m = (C::WM * fm + wm) * 32 + (lane & 28);  // the first of the four rows
+#pragma unroll
+      for (int fn = 0; fn < C::FN; fn += 2) {
+        u32x4 c[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint2 w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[q] = uint2{pack_bf16x2(acc[fm][fn + h][4 * q], acc[fm][fn + h][4 * q + 1]),
+                         pack_bf16x2(acc[fm][fn + h][4 * q + 2], acc[fm][fn + h][4 * q + 3])};
+          tg_runs16(w, c[2 * h], c[2 * h + 1]);
+        }
+        f8_quad_transpose(c, lane);
+        const int n = t.n0 + 32 * (C::column(fn) + C::first(wn)) + 16 * (lane & 3) + 8 * (lane >> 5);
+        if (n >= N) continue;
+        uint16_t* to = (uint16_t*)p.out + (size_t)(t.row0 + t.m0 + m) * N + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (m + i < t.rows) *(u32x4*)(to + (size_t)i * N) = c[i];
+      }
+    }
+  }
   __device__ __forceinline__ void store(const Tile& t, int wm, int wn, int lane,
                                         f32x16 (&acc)[C::FM][C::FN]) const {
     // a lane holds four consecutive columns of one row
     const int N = width();
     const bool vec = N % (C::EXACT ? 4 : 8) == 0;  // whole 16-byte runs
+    if constexpr (C::PAIRS) {
+      if (vec) {
+        store_lines(t, wm, wn, lane, acc);
+        return;
+      }
+    }
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
       const int mr = tg_row<C>(wm, fm, lane, 0);
@@ -96,7 +133,7 @@ struct F8Tiles {
       const size_t row = (size_t)(t.row0 + t.m0 + mr);
 #pragma unroll
       for (int fn = 0; fn < C::FN; ++fn) {
-        const int n0 = t.n0 + tg_col<C>(wn, fn, 0, 0);  // the fragment's first column
+        const int n0 = t.n0 + 32 * (C::column(fn) + C::first(wn));  // the fragment's first column
         if (n0 >= N) continue;
         if constexpr (C::EXACT) {
           float* c = (float*)p.out + row * N;

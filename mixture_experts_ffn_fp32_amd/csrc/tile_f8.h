@@ -39,6 +39,15 @@ struct F8Config : Shape {
   // Loads of a k-step per wavefront (its data and 64 scales), and how many of them follow the
   // barrier that frees their slot at once (f8_step).
   static constexpr int LOADS = Shape::NI + 1, FIRST = Shape::NI / 2 - 1;
+  // Places of a wavefront's fragments of w among the tile's fragments of 32 columns: the f-th
+  // is column(f) + first(wn).  With four of them, two neighbours each: 128 bytes of a row of
+  // bfloat16 results, a whole line, lie in one wavefront.  With two they interleave, so that the
+  // wavefronts stay balanced where the matrix ends after half a tile's columns.
+  static constexpr bool PAIRS = Shape::FN == 4;
+  static __host__ __device__ constexpr int column(int f) {
+    return PAIRS ? 2 * Shape::WN * (f >> 1) + (f & 1) : Shape::WN * f;
+  }
+  static __host__ __device__ constexpr int first(int wn) { return PAIRS ? 2 * wn : wn; }
 };
 
 // A tile's operands.  Row layout: `rows` rows of `pitch` bytes, of which the first `length` are
@@ -177,8 +186,8 @@ struct F8Frag {
 };
 // A lane's place in the first of its wavefront's fragments (fragment WN f + u is the f-th).  Row
 // layout: its chunk 16 (l / 32); the other chunks are that xor 32 (the other 16 bytes of half 0),
-// 64 and 96.  Column layout: its column of contraction row 16 (l / 32) + (l % 16) / 2; the f-th
-// fragment's is that xor 32 WN f, as a fragment's columns are 32 bytes of the row.
+// 64 and 96.  Column layout: its column of contraction row 16 (l / 32) + (l % 16) / 2; a
+// fragment u places further on is that xor 32 u, as a fragment's columns are 32 bytes of the row.
 template <int W, bool COL>
 __device__ __forceinline__ int f8_place(int u, int lane) {
   if constexpr (COL) {
@@ -188,15 +197,15 @@ __device__ __forceinline__ int f8_place(int u, int lane) {
     return lds_chunk_offset(u * 32 + (lane & 31), lane >> 5);
   }
 }
-// The f-th fragment of the operand at rd, N being the wavefronts that share it out.
-template <int W, bool COL, int N>
-__device__ __forceinline__ F8Frag f8_frag(const uint8_t* rd, int place, int f) {
+// The fragment of the operand at rd that lies u places behind the wavefront's first one.
+template <int W, bool COL>
+__device__ __forceinline__ F8Frag f8_frag(const uint8_t* rd, int place, int u) {
   // (opaque: the few operations that make the addresses are repeated for every fragment, as
   // kept addresses would push sums out of the registers)
   asm volatile("" : "+v"(place));
   F8Frag v;
   if constexpr (COL) {
-    const uint8_t* p = rd + (place ^ (32 * N * f));
+    const uint8_t* p = rd + (place ^ (32 * u));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {  // rows + 0, 8, 32, 40 of each half
       const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
@@ -208,7 +217,7 @@ __device__ __forceinline__ F8Frag f8_frag(const uint8_t* rd, int place, int f) {
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const u32x4 c = *(const u32x4*)(rd + (place ^ (32 * j)) + N * f * 32 * 128);
+      const u32x4 c = *(const u32x4*)(rd + (place ^ (32 * j)) + u * 32 * 128);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v.h[j >> 1][4 * (j & 1) + e] = (int)c[e];
     }
@@ -222,15 +231,15 @@ struct F8Places {
 template <class C>
 __device__ __forceinline__ F8Places f8_places(int wm, int wn, int lane) {
   return F8Places{f8_place<C::BM, false>(wm, lane),
-                  C::BM * 128 + f8_place<C::BN, C::WCOL>(wn, lane)};
+                  C::BM * 128 + f8_place<C::BN, C::WCOL>(C::first(wn), lane)};
 }
 template <class C>
 __device__ __forceinline__ F8Frag f8_frag_x(const uint8_t* rd, const F8Places& at, int fm) {
-  return f8_frag<C::BM, false, C::WM>(rd, at.x, fm);
+  return f8_frag<C::BM, false>(rd, at.x, C::WM * fm);
 }
 template <class C>
 __device__ __forceinline__ F8Frag f8_frag_w(const uint8_t* rd, const F8Places& at, int fn) {
-  return f8_frag<C::BN, C::WCOL, C::WN>(rd, at.w, fn);
+  return f8_frag<C::BN, C::WCOL>(rd, at.w, C::column(fn));
 }
 
 // Eight 8-bit values (two words) as bfloat16, which is exact.
@@ -301,7 +310,28 @@ __device__ __forceinline__ F8Scales<C> f8_scales(const uint8_t* rd, int wm, int 
 }
 template <class C>
 __device__ __forceinline__ float f8_scale_of(const F8Scales<C>& s, int fm, int fn) {
-  return s.x[fm] * s.w[C::WN * 32 * fn / kF8Block];
+  return s.x[fm] * s.w[C::column(fn) * 32 / kF8Block];
+}
+
+// 16-byte chunks of four neighbouring lanes transposed: lane j of four holds chunks (j, 0 .. 3) and
+// receives (0 .. 3, j).
+__device__ __forceinline__ void f8_quad_transpose(u32x4 (&c)[4], int lane) {
+  const bool odd = lane & 1, up = lane & 2;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {  // with lane ^ 1
+      const uint32_t t = __builtin_amdgcn_mov_dpp(odd ? c[i][e] : c[i + 1][e], 0xB1, 0xf, 0xf, true);
+      c[i][e] = odd ? t : c[i][e];
+      c[i + 1][e] = odd ? c[i + 1][e] : t;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // with lane ^ 2
+      const uint32_t t = __builtin_amdgcn_mov_dpp(up ? c[i][e] : c[i + 2][e], 0x4E, 0xf, 0xf, true);
+      c[i][e] = up ? t : c[i][e];
+      c[i + 2][e] = up ? c[i + 2][e] : t;
+    }
+  }
 }
 
 // What passes from one k-step to the next: x's fragments and w's first one, and the last pair's
@@ -312,24 +342,6 @@ struct F8State {
   f32x16 part;
   float scale;
 };
-
-// Order of a pair's products: behind each MFMA its share of the loads and of the LDS reads, and
-// of the last pair's additions.
-template <int LOADS, int READS>
-__device__ __forceinline__ void f8_order() {
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-#pragma unroll
-    for (int i = m * LOADS / 2; i < (m + 1) * LOADS / 2; ++i)
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-#pragma unroll
-    for (int i = m * READS / 2; i < (m + 1) * READS / 2; ++i)
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
-  }
-}
 
 // One k-step out of ring slot `rd`.  The barrier stands before the last of w's fragments, when
 // every read of `rd` has been made: `rd` is free, the next k-step (slot `nx`) has landed, and
@@ -533,6 +545,8 @@ __device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restric
 template <class C>
 struct F8One : C {
   static constexpr int WM = 1, WN = 1, FM = 2, FN = 2;
+  static __host__ __device__ constexpr int column(int f) { return f; }
+  static __host__ __device__ constexpr int first(int) { return 0; }
 };
 template <class C, class P>
 __device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __restrict__ lds) {
