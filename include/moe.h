@@ -412,7 +412,7 @@ moe_status_t moe_grouped_matmul_quantized_dx(const void* dy, const float* dys, c
  * The losses of moe_balance_stats for S sequences of rows, sequence s being rows
  * offsets[s] .. offsets[s+1] - 1 (device, int32, treated as in moe_grouped_matmul; NULL
  * with S = 1: all rows), over its n rows that mask keeps (device, one byte a row, not
- * zero: counts; NULL: all).  Masked rows and rows of no sequence are not read.
+ * zero: counts; NULL: all).  Masked rows and rows of no sequence reach no result.
  *   counts_si = #{(t, k) : idx[t][k] = i} (entries outside [0, N) are not counted),
  *   f_si = N counts_si / (K n),  P_si = (1/n) sum_t scores_ti
  *   losses_s0 = alpha1 sum_i f_si P_si,  losses_s1 = alpha2 sum_g f'_sg P'_sg

@@ -17,7 +17,7 @@
 // Small passes over the scores (16384 x 128: 8 MB each way), bound by launches and, for the
 // large ones, by HBM.  Forward: one launch for partial sums of kBlRows rows (float64, counts as
 // whole numbers), one that joins a sequence's partial sums in order.  Backward: one launch, a
-// wavefront per row.  Every sum has a fixed order.
+// wavefront per four rows.  Every sum has a fixed order.
 #include <algorithm>
 
 #include "groups.h"
@@ -28,34 +28,46 @@ namespace {
 
 constexpr int kBlRows = 64;
 
-// Partial sums of one chunk of a sequence: block b takes the b-th chunk of kBlRows rows.
-__global__ __launch_bounds__(256) void balance_loss_partial_kernel(BalanceLossArgs a) {
+// Partial sums of one chunk of a sequence: block b takes the b-th chunk of kBlRows rows.  The
+// loads of a thread's column (every 512 / NP-th row) are made eight at a time, whatever the
+// mask says; a masked row's are left out of the sum.
+constexpr int kBlThreads = 512;
+__global__ __launch_bounds__(kBlThreads) void balance_loss_partial_kernel(BalanceLossArgs a) {
   __shared__ GroupTables t;
   __shared__ int cnt[256], valid[kBlRows];
-  __shared__ double sum[256];
+  __shared__ double sum[kBlThreads];
   const int tid = threadIdx.x, N = a.N;
   group_tables<GR_FWD>(GroupDims{a.T, a.S, 0, 0}, a.offsets, kBlRows, t);
   const int b = blockIdx.x;
   if (b >= t.tiles[a.S]) return;
   const int s = group_of(t.tiles, a.S, b, 0);
   const int t0 = t.off[s] + (b - t.tiles[s]) * kBlRows, rows = min(kBlRows, t.off[s + 1] - t0);
-  if (tid < N) cnt[tid] = 0;
+  if (tid < 256) cnt[tid] = 0;
   if (tid < kBlRows) valid[tid] = tid < rows && (a.mask == nullptr || a.mask[t0 + tid] != 0);
   __syncthreads();
-  for (int j = tid; j < rows * a.K; j += 256) {
+  for (int j = tid; j < rows * a.K; j += kBlThreads) {
     const int e = a.idx[(size_t)t0 * a.K + j];
     if (valid[j / a.K] && (unsigned)e < (unsigned)N) atomicAdd(&cnt[e], 1);
   }
-  // 256 / NP rows at a time, NP columns each
-  const int NP = N <= 64 ? 64 : N <= 128 ? 128 : 256, c = tid & (NP - 1), g = tid / NP;
+  // kBlThreads / NP rows at a time, NP columns each
+  const int NP = N <= 64 ? 64 : N <= 128 ? 128 : 256, G = kBlThreads / NP;
+  const int c = tid & (NP - 1), g = tid / NP;
   double p = 0.0;
-  if (c < N)
-    for (int r = g; r < rows; r += 256 / NP)
-      if (valid[r]) p += (double)a.scores[(size_t)(t0 + r) * N + c];
+  if (c < N) {
+    const float* from = a.scores + (size_t)t0 * N + c;
+    for (int r0 = g; r0 < rows; r0 += 8 * G) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = from[(size_t)min(r0 + i * G, rows - 1) * N];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r0 + i * G < rows && valid[r0 + i * G]) p += (double)v[i];
+    }
+  }
   sum[tid] = p;
   __syncthreads();
   if (tid < N) {
-    for (int q = NP; q < 256; q += NP) p += sum[q + tid];
+    for (int q = NP; q < kBlThreads; q += NP) p += sum[q + tid];
     a.psum[(size_t)b * N + tid] = p;
     a.pcnt[(size_t)b * (N + 1) + tid] = cnt[tid];
   }
@@ -83,11 +95,30 @@ __global__ __launch_bounds__(1024) void balance_loss_final_kernel(BalanceLossArg
   const int NP = N <= 64 ? 64 : N <= 128 ? 128 : 256, c = tid & (NP - 1), g = tid / NP;
   double p = 0.0;
   int n = 0;
-  if (c < N)
-    for (int b = b0 + g; b < b1; b += 1024 / NP) {
-      p += a.psum[(size_t)b * N + c];
-      n += a.pcnt[(size_t)b * (N + 1) + c];
+  int of = -1;
+  if (tid < N && a.device_of != nullptr) {
+    of = a.device_of[tid];
+    if ((unsigned)of >= (unsigned)a.D) of = -1;
+  }
+  if (c < N) {
+    const int G = 1024 / NP;
+    for (int b = b0 + g; b < b1; b += 4 * G) {
+      double v[4];
+      int k[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = min(b + i * G, b1 - 1);
+        v[i] = a.psum[(size_t)q * N + c];
+        k[i] = a.pcnt[(size_t)q * (N + 1) + c];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (b + i * G < b1) {
+          p += v[i];
+          n += k[i];
+        }
     }
+  }
   sum[tid] = p;
   cnt[tid] = n;
   if (tid < 256) dev_cnt[tid] = dev_size[tid] = 0;
@@ -100,15 +131,10 @@ __global__ __launch_bounds__(1024) void balance_loss_final_kernel(BalanceLossArg
   }
   __syncthreads();
   const double rows = s_n > 0 ? (double)s_n : 1.0;  // no rows: every sum is zero
-  int of = -1;
   if (tid < N) {
     for (int q = NP; q < 1024; q += NP) {
       p += sum[q + tid];
       n += cnt[q + tid];
-    }
-    if (a.device_of != nullptr) {
-      of = a.device_of[tid];
-      if ((unsigned)of >= (unsigned)a.D) of = -1;
     }
     if (of >= 0) {
       atomicAdd(&dev_cnt[of], n);
@@ -144,51 +170,67 @@ __global__ __launch_bounds__(1024) void balance_loss_final_kernel(BalanceLossArg
   }
 }
 
-// One wavefront per row, four columns a lane at most; rows of no sequence and masked ones are
-// zeros.
+// One wavefront for kBlAtOnce neighbouring rows, PER columns of each a lane; rows of no sequence
+// and masked ones are zeros.
+constexpr int kBlAtOnce = 4;
+template <int PER>
 __global__ __launch_bounds__(256) void balance_loss_backward_kernel(BalanceLossArgs a) {
   __shared__ GroupTables t;
   const int lane = threadIdx.x & 63, N = a.N;
   group_tables<GR_FWD>(GroupDims{a.T, a.S, 0, 0}, a.offsets, kBlRows, t);
   const int first = t.off[0], last = t.off[a.S];
   int known = -1;  // the sequence whose slopes c holds
-  float c[4] = {0.f, 0.f, 0.f, 0.f};
-  for (long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); r < a.T;
-       r += (long long)gridDim.x * 4) {
-    const int row = uni((int)r);
-    const bool on = row >= first && row < last && (a.mask == nullptr || a.mask[row] != 0);
-    float* out = a.dlogits + (size_t)row * N;
-    if (!on) {
+  float c[PER];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane + 64 * i < N) out[lane + 64 * i] = 0.f;
-      continue;
-    }
-    const int s = uni(group_of(t.off, a.S, row, max(known, 0)));
-    if (s != known) {
-      known = s;
-      const float d0 = a.dlosses != nullptr ? a.dlosses[2 * s] : 1.f;
-      const float d1 = a.dlosses != nullptr ? a.dlosses[2 * s + 1] : 1.f;
+  for (int i = 0; i < PER; ++i) c[i] = 0.f;
+  const long long stride = (long long)gridDim.x * 4 * kBlAtOnce;
+  for (long long r = ((long long)blockIdx.x * 4 + (threadIdx.x >> 6)) * kBlAtOnce; r < a.T; r += stride) {
+    float v[kBlAtOnce][PER], z[kBlAtOnce][PER], dot[kBlAtOnce];
+    bool on[kBlAtOnce];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+    for (int q = 0; q < kBlAtOnce; ++q) {
+      const int row = uni((int)min(r + q, a.T - 1LL));
+      on[q] = row >= first && row < last && (a.mask == nullptr || a.mask[row] != 0);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
         const int j = lane + 64 * i;
-        c[i] = j < N ? d0 * a.slopes[2 * (size_t)s * N + j] + d1 * a.slopes[(2 * (size_t)s + 1) * N + j]
-                     : 0.f;
+        v[q][i] = j < N ? a.scores[(size_t)row * N + j] : 0.f;
       }
     }
-    const float* from = a.scores + (size_t)row * N;
-    float v[4], dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = lane + 64 * i;
-      v[i] = j < N ? from[j] : 0.f;
-      dot += v[i] * c[i];
+    for (int q = 0; q < kBlAtOnce; ++q) {
+      const int row = uni((int)min(r + q, a.T - 1LL));
+      const int s = on[q] ? uni(group_of(t.off, a.S, row, max(known, 0))) : known;
+      if (s != known) {
+        known = s;
+        const float d0 = a.dlosses != nullptr ? a.dlosses[2 * s] : 1.f;
+        const float d1 = a.dlosses != nullptr ? a.dlosses[2 * s + 1] : 1.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int j = lane + 64 * i;
+          c[i] = j < N ? d0 * a.slopes[2 * (size_t)s * N + j] + d1 * a.slopes[(2 * (size_t)s + 1) * N + j]
+                       : 0.f;
+        }
+      }
+      dot[q] = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        z[q][i] = c[i];
+        dot[q] += v[q][i] * c[i];
+      }
     }
 #pragma unroll
-    for (int k = 32; k > 0; k >>= 1) dot += __shfl_xor(dot, k);
+    for (int k = 32; k > 0; k >>= 1)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i < N) out[lane + 64 * i] = v[i] * (c[i] - dot);
+      for (int q = 0; q < kBlAtOnce; ++q) dot[q] += __shfl_xor(dot[q], k);
+#pragma unroll
+    for (int q = 0; q < kBlAtOnce; ++q)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int j = lane + 64 * i;
+        if (r + q < a.T && j < N)
+          a.dlogits[(size_t)(r + q) * N + j] = on[q] ? v[q][i] * (z[q][i] - dot[q]) : 0.f;
+      }
   }
 }
 
@@ -207,7 +249,7 @@ hipError_t launch_balance_loss(BalanceLossArgs a, void* ws, hipStream_t st) {
   a.psum = (double*)ws;
   a.pcnt = (int32_t*)((char*)ws + align256((size_t)chunks * a.N * 8));
   if (a.T > 0) {
-    balance_loss_partial_kernel<<<(unsigned)chunks, 256, 0, st>>>(a);
+    balance_loss_partial_kernel<<<(unsigned)chunks, kBlThreads, 0, st>>>(a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   balance_loss_final_kernel<<<a.S, 1024, 0, st>>>(a);
@@ -215,8 +257,11 @@ hipError_t launch_balance_loss(BalanceLossArgs a, void* ws, hipStream_t st) {
 }
 
 hipError_t launch_balance_loss_backward(const BalanceLossArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)std::min<long long>((a.T + 3LL) / 4, 2048);
-  balance_loss_backward_kernel<<<grid, 256, 0, st>>>(a);
+  const unsigned grid =
+      (unsigned)std::min<long long>((a.T + 4LL * kBlAtOnce - 1) / (4 * kBlAtOnce), 2048);
+  if (a.N <= 64) balance_loss_backward_kernel<1><<<grid, 256, 0, st>>>(a);
+  else if (a.N <= 128) balance_loss_backward_kernel<2><<<grid, 256, 0, st>>>(a);
+  else balance_loss_backward_kernel<4><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -206,9 +206,9 @@ struct PadRows {
   uint32_t pitch;
 };
 typedef uint32_t pad_u32 __attribute__((aligned(1)));
-__global__ __launch_bounds__(256) void pad_bytes_kernel(PadRows a) {
+__device__ __forceinline__ void pad_rows(const PadRows& a, unsigned block, unsigned blocks) {
   const long long per = a.pitch / 16, all = a.rows * per;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+  for (long long i = (long long)block * 256 + threadIdx.x; i < all; i += (long long)blocks * 256) {
     const long long r = i / per;
     const int j = (int)(i - r * per) * 16;
     const uint8_t* src = a.src + r * a.width;
@@ -224,9 +224,16 @@ __global__ __launch_bounds__(256) void pad_bytes_kernel(PadRows a) {
     *(u32x4*)(a.dst + r * a.pitch + j) = v;
   }
 }
-hipError_t pad_bytes(const PadRows& a, hipStream_t st) {
-  const long long blocks = (a.rows * (a.pitch / 16) + 255) / 256;
-  pad_bytes_kernel<<<(unsigned)std::min<long long>(blocks, 1 << 16), 256, 0, st>>>(a);
+// Both operands' rows in one launch (either may have none).
+__global__ __launch_bounds__(256) void pad_two_kernel(PadRows a, PadRows b, unsigned blocks_a) {
+  if (blockIdx.x < blocks_a) pad_rows(a, blockIdx.x, blocks_a);
+  else pad_rows(b, blockIdx.x - blocks_a, gridDim.x - blocks_a);
+}
+hipError_t pad_two(const PadRows& a, const PadRows& b, hipStream_t st) {
+  auto blocks = [](const PadRows& r) {
+    return (unsigned)std::min<long long>((r.rows * (r.pitch / 16) + 255) / 256, 1 << 16);
+  };
+  pad_two_kernel<<<blocks(a) + blocks(b), 256, 0, st>>>(a, b, blocks(a));
   return hipGetLastError();
 }
 
@@ -291,17 +298,19 @@ hipError_t launch_grouped_f8(int f8, bool dx, const GroupedF8Args& a, void* ws, 
   p.out = a.out;
   p.g = GroupDims{a.M, a.E, a.n, a.k};
   p.zero_rest = a.zero_rest;
-  if (plan.x != nullptr) {
-    const PadRows r{p.x, plan.x, a.M, (int)p.pitch_x, pitch16(p.pitch_x)};
-    if (const hipError_t e = pad_bytes(r, st); e != hipSuccess) return e;
-    p.x = r.dst;
-    p.pitch_x = r.pitch;
-  }
-  if (plan.w != nullptr) {
-    const PadRows r{p.w, plan.w, (long long)a.E * a.n, a.k, pitch16(a.k)};
-    if (const hipError_t e = pad_bytes(r, st); e != hipSuccess) return e;
-    p.w = r.dst;
-    p.pitch_w = r.pitch;
+  if (plan.x != nullptr || plan.w != nullptr) {
+    PadRows rx{}, rw{};
+    if (plan.x != nullptr) rx = PadRows{p.x, plan.x, a.M, (int)p.pitch_x, pitch16(p.pitch_x)};
+    if (plan.w != nullptr) rw = PadRows{p.w, plan.w, (long long)a.E * a.n, a.k, pitch16(a.k)};
+    if (const hipError_t e = pad_two(rx, rw, st); e != hipSuccess) return e;
+    if (plan.x != nullptr) {
+      p.x = rx.dst;
+      p.pitch_x = rx.pitch;
+    }
+    if (plan.w != nullptr) {
+      p.w = rw.dst;
+      p.pitch_w = rw.pitch;
+    }
   }
   if (dx)
     return f8 == F8_E4M3 ? pick_f8<GR_DX, F8_E4M3>(p, a, st) : pick_f8<GR_DX, F8_E5M2>(p, a, st);
