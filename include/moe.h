@@ -421,7 +421,8 @@ moe_status_t moe_grouped_matmul_quantized_dx(const void* dy, const float* dys, c
  * losses_s1 = 0.  A sequence without rows gives zeros.
  *   counts [S][N] int32; P [S][N], losses [S][2] float32;
  *   slopes [S][2][N] float32: d losses / d scores, the same in each of the n rows.
- * Sums are float64.  Limits: 1 <= K <= N <= 256, 1 <= S <= 1024, 0 <= D <= 256. */
+ * Sums are float64.  Limits: 1 <= K <= N <= 256, 1 <= S <= 1024, 0 <= D <= 256 (D >= 1
+ * with device_of). */
 moe_status_t moe_balance_loss_workspace_size(int T, int N, int S, size_t* bytes);
 moe_status_t moe_balance_loss(const float* scores, const int32_t* idx, const int32_t* offsets,
                               const uint8_t* mask, const int32_t* device_of, int T, int N, int K,

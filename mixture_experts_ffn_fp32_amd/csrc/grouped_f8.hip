@@ -257,24 +257,42 @@ F8Plan f8_plan(int M, int E, int n, int k, bool dx, void* ws) {
   return p;
 }
 
-long long f8_tiles(const GroupedF8Args& a, bool dx, int b) {
-  return (a.M / b + (long long)std::min(a.E, a.M)) * (((dx ? a.k : a.n) + b - 1) / b);
+// Tiles of b x b: at most (a launch's blocks), and as expected, half a tile's rows being left over
+// in a group.
+long long f8_most_tiles(const GroupedF8Args& a, int width, int b) {
+  return (a.M / b + (long long)std::min(a.E, a.M)) * ((width + b - 1) / b);
+}
+double f8_tiles(const GroupedF8Args& a, int width, int b) {
+  const double groups = std::min(a.E, a.M);
+  const double rows = a.E == 1 ? (a.M + b - 1) / b : std::max(groups, (double)a.M / b + groups / 2);
+  return rows * ((width + b - 1) / b);
 }
 template <class Shape, int DIR, int Q, bool F32>
 hipError_t run_f8(const F8Product& p, const GroupedF8Args& a, hipStream_t st) {
   using C = F8Config<Shape, DIR == GR_DX, Q, F32>;
   const long long blocks = (long long)device_cu_count() * C::BPC;
-  const long long tiles = f8_tiles(a, DIR == GR_DX, C::BM);
+  const long long tiles = f8_most_tiles(a, DIR == GR_DX ? a.k : a.n, C::BM);
   grouped_f8_kernel<C, DIR><<<(unsigned)std::max(1LL, std::min(tiles, blocks)), C::THREADS, 0, st>>>(p);
   return hipGetLastError();
 }
+// Which tiles.  256^2 against 128^2 (bfloat16 results; one block per CU against two) by the time
+// that the expected tiles take at the measured rates, us per tile: 1.9 a k-step and 6 for its
+// start and its results, against 1.35 and 4 for two at once; a CU has one tile at least.
+// Measured, 256 | 128: 49152 rows in 64 uneven groups, 1408 x 2048, 207 | 227 us; dx of 28672 rows
+// in 63, 896 x 1280, 67 | 76; y of 4096^3 76 | 99; y of 64 groups of 128 rows, 1408 x 2048, 56 | 44,
+// of 64 rows 48 | 38; dx of 256 rows there 73 | 85; y of 4096 rows, 2048 x 2048, 36 | 28.  (Wrong by
+// most where groups just fill tiles: y of 200 and 256 rows there, 77 | 65 and 85 | 76.)
+// 64^2 where 128^2 give less than half of the CUs one: 128 | 64: y of 128 rows, 4096 x 4096 (32
+// tiles), 27 | 14 us; of one row, 2048 x 2048, 13 | 10; of 8 groups of 200 rows, 1024 x 1024 (128
+// tiles), 12 | 13; of 64 groups of 6 rows, 2048 x 1408, 33 | 51.
 template <int DIR, int Q>
 hipError_t pick_f8(const F8Product& p, const GroupedF8Args& a, hipStream_t st) {
-  const int cus = device_cu_count();
-  const bool dx = DIR == GR_DX;
-  if (!a.out_f32 && 4 * f8_tiles(a, dx, 256) >= 3 * cus && a.M > 128LL * a.E)
-    return run_f8<TgBig, DIR, Q, false>(p, a, st);
-  if (4 * f8_tiles(a, dx, 128) >= 3 * cus)
+  const double cus = device_cu_count();
+  const int width = DIR == GR_DX ? a.k : a.n, steps = f8_blocks(DIR == GR_DX ? a.n : a.k);
+  const double big = std::max(1.0, f8_tiles(a, width, 256) / cus) * (1.9 * steps + 6);
+  const double mid = std::max(1.0, f8_tiles(a, width, 128) / (2 * cus)) * (1.35 * steps + 4);
+  if (!a.out_f32 && big < mid) return run_f8<TgBig, DIR, Q, false>(p, a, st);
+  if (2 * f8_tiles(a, width, 128) >= cus)
     return a.out_f32 ? run_f8<TgMid, DIR, Q, true>(p, a, st) : run_f8<TgMid, DIR, Q, false>(p, a, st);
   return a.out_f32 ? run_f8<TgSmall, DIR, Q, true>(p, a, st) : run_f8<TgSmall, DIR, Q, false>(p, a, st);
 }

@@ -667,6 +667,8 @@ moe_status_t moe_balance_loss(const float* scores, const int32_t* idx, const int
     return fail(MOE_ERR_UNSUPPORTED, "T * K must stay below 2^31");
   if (D < 0) return fail(MOE_ERR_INVALID_ARG, "D must be >= 0");
   if (D > 256) return fail(MOE_ERR_UNSUPPORTED, "D > 256 devices is not supported");
+  if (device_of != nullptr && D == 0)
+    return fail(MOE_ERR_INVALID_ARG, "device_of needs the number of devices D");
   if (!isfinite(alpha1) || !isfinite(alpha2))
     return fail(MOE_ERR_INVALID_ARG, "alpha1 and alpha2 must be finite");
   if ((s = check_ptr("scores", scores, T > 0)) != MOE_OK) return s;

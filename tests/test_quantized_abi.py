@@ -190,6 +190,7 @@ def test_balance_loss_refusals(lib):
             assert call(**{name: None}) == INVALID, name
     assert fwd(K=0) == INVALID and fwd(K=9) == INVALID
     assert fwd(D=-1) == INVALID and fwd(D=257) == UNSUPPORTED
+    assert fwd(D=0) == INVALID and says(lib, "device_of needs")
     assert fwd(T=2 ** 30, K=2) == UNSUPPORTED
     for a in (NAN, INF):
         assert fwd(a1=a) == INVALID and fwd(a2=a) == INVALID
