@@ -37,10 +37,13 @@ __device__ __forceinline__ F8Scale f8_scale(float top) {
   s.inv = 1.f / s.scale;
   return s;
 }
-// v / scale before its rounding.  (inv's own rounding and the product's put the block's
-// largest value at most 3 * 2^-24 above `most`, which rounds back to it.)
+// v / scale as float32 division rounds it, before its rounding to 8 bits: the product with the
+// rounded reciprocal, and its rest divided once more.  (The product alone is off by an ulp now
+// and then, which moves values that lie between two of 8 bits, and bfloat16 values often do.)
+// The block's largest value is `most` but for the scale's own rounding, which rounds back to it.
 __device__ __forceinline__ float f8_scaled(float v, const F8Scale& s) {
-  return fabsf(v) <= FLT_MAX ? v * s.inv : __builtin_nanf("");
+  const float q = v * s.inv;
+  return fabsf(v) <= FLT_MAX ? fmaf(fmaf(-q, s.scale, v), s.inv, q) : __builtin_nanf("");
 }
 // Four values, rounded to nearest even, lowest byte first.
 template <int Q>
