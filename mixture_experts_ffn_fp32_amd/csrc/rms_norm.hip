@@ -323,7 +323,7 @@ __global__ __launch_bounds__(1024) void rms_bwd_long_kernel(RmsArgs a) {
 }
 // Partial column sums of rms_long_rows(T) rows: one thread per column.
 __host__ __device__ inline int rms_long_rows(int T) {
-  return T <= 64 * 1024 ? 64 : (T + 1023) / 1024;
+  return T <= 64 * 1024 ? 64 : (T - 1) / 1024 + 1;
 }
 template <class E>
 __global__ __launch_bounds__(256) void rms_cols_long_kernel(RmsArgs a) {
@@ -433,7 +433,7 @@ hipError_t launch_rms_norm(int dtype, int f8, RmsArgs a, hipStream_t st) {
 
 int rms_norm_chunks(int dtype, int T, int d) {
   const RmsPlan p = rms_plan(dtype, d);
-  if (p.nch == 0) return (T + rms_long_rows(T) - 1) / rms_long_rows(T);
+  if (p.nch == 0) return T == 0 ? 0 : (T - 1) / rms_long_rows(T) + 1;
   return (int)rms_grid(p, T, kRmsBwdBlocks);
 }
 

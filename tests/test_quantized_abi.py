@@ -79,6 +79,8 @@ def test_rms_norm_backward_refusals(lib):
     status, need = size(query, 4, 64, BF16)
     assert status == OK and need > 0
     assert size(query, 0, 64, BF16) == (OK, 0)
+    # rows too long for registers: partial rows of T / 1024 rows each, up to the largest T
+    assert size(query, 2 ** 31 - 1, 20000, F32) == (OK, 1024 * 20000 * 4)
     assert size(query, 4, 0, BF16)[0] == INVALID
     assert query(4, 64, BF16, None) == INVALID
     for name in ("dy", "h", "rstd", "dx", "ws"):
