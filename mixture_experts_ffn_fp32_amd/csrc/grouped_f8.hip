@@ -107,7 +107,7 @@ struct F8Tiles {
         }
         f8_quad_transpose(c, lane);
         const int n = t.n0 + 32 * (C::column(fn) + C::first(wn)) + 16 * (lane & 3) + 8 * (lane >> 5);
-        if (n >= N) continue;
+        if (n >= t.n0 + t.cols) continue;
         uint16_t* to = (uint16_t*)p.out + (size_t)(t.row0 + t.m0 + m) * N + n;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -134,7 +134,7 @@ struct F8Tiles {
 #pragma unroll
       for (int fn = 0; fn < C::FN; ++fn) {
         const int n0 = t.n0 + 32 * (C::column(fn) + C::first(wn));  // the fragment's first column
-        if (n0 >= N) continue;
+        if (n0 >= t.n0 + t.cols) continue;
         if constexpr (C::EXACT) {
           float* c = (float*)p.out + row * N;
 #pragma unroll

@@ -44,6 +44,11 @@ struct F8Config : Shape {
   // bfloat16 results, a whole line, lie in one wavefront.  With two they interleave, so that the
   // wavefronts stay balanced where the matrix ends after half a tile's columns.
   static constexpr bool PAIRS = Shape::FN == 4;
+  // Whether a round of few tiles is cut (F8Units), and half a tile's and a quarter's time then,
+  // percent of a tile's.  128^2 are not: two of them share a CU, and one alone there is as fast as
+  // its halves (4096 rows, 2048 -> 2560 x 2048, one round and a quarter, 54 us, cut 60).
+  static constexpr bool CUT = PAIRS;
+  static constexpr int HALF = 65, QUARTER = 50;
   static __host__ __device__ constexpr int column(int f) {
     return PAIRS ? 2 * Shape::WN * (f >> 1) + (f & 1) : Shape::WN * f;
   }
@@ -420,6 +425,62 @@ __device__ __forceinline__ F8Load f8_prepare_wave(const Tile& t, int wave, int l
   return f8_prepare<C, C::WCOL>(t.W, true, t.n0, t.steps, t.length, wave - H, lane, off, s_off);
 }
 
+// A block's tiles: every P-th of its XCD's range (TgTiles; P: the XCD's blocks), and of the last
+// round, if tiles are left for few of the blocks only, halves or quarters, so that more of them
+// have some.  Measured at 4096 rows and 256^2 tiles, k = 2048 (8192): one round 39 (127) us; 16, 64
+// or 128 tiles more in quarters, quarters and halves + 14, 15 and 20 (54, 61, 84) us, whole + 25
+// (86 .. 92).
+struct F8Unit {
+  int tile, ways, part;  // tile -1: none
+};
+template <class C>
+struct F8Units {
+  int first, whole, rest, ways, blocks;
+  __device__ __forceinline__ F8Units(const TgTiles& q) {
+    const int n = q.count(q.x);
+    first = q.at(q.x, 0);
+    blocks = q.blocks(q.x);
+    rest = n % blocks;
+    whole = n - rest;
+    ways = 1;
+    if constexpr (C::CUT) {
+      const int two = (2 * rest + blocks - 1) / blocks * C::HALF;
+      const int four = (4 * rest + blocks - 1) / blocks * C::QUARTER;
+      if (min(two, four) < 100) ways = four < two ? 4 : 2;
+    }
+  }
+  __device__ __forceinline__ F8Unit at(int j) const {
+    if (j < whole) return F8Unit{first + j, 1, 0};
+    const int u = j - whole;
+    if (u >= rest * ways) return F8Unit{-1, 1, 0};
+    return F8Unit{first + whole + u / ways, ways, u % ways};
+  }
+};
+// The tile's part: halves of its columns (of its rows, if it has half the columns only), quarters
+// of both.  A part without rows or columns has no k-steps.
+template <class C, class P>
+__device__ __forceinline__ typename P::Tile f8_unit(const P& p, const F8Unit& u, int hint) {
+  typename P::Tile t = p.tile(u.tile, hint);
+  if (C::CUT && u.ways > 1) {
+    constexpr int HM = C::BM / 2, HN = C::BN / 2;
+    const bool m = u.ways == 4 || t.cols <= HN, n = u.ways == 4 || !m;
+    if (m) {
+      t.m0 += (u.part & 1) * HM;
+      t.X.rows = min(t.X.rows, t.m0 + HM);
+      t.rows = t.X.rows - t.m0;
+    }
+    if (n) {
+      const int j = u.ways == 4 ? u.part >> 1 : u.part;
+      t.n0 += j * HN;
+      t.cols = min(t.cols - j * HN, HN);
+      if (C::WCOL) t.W.width = min(t.W.width, t.n0 + HN);
+      else t.W.rows = min(t.W.rows, t.n0 + HN);
+    }
+    if (t.rows <= 0 || t.cols <= 0) t.steps = 0;
+  }
+  return t;
+}
+
 // The loads' place in the stream of k-steps of a block's tiles (see TgCursor).
 struct F8Cursor {
   int hint;
@@ -431,13 +492,13 @@ struct F8Cursor {
 // tile while this one is multiplied (k-steps of zeros follow the last one).
 __device__ __forceinline__ int f8_steps(int steps) { return max(steps, 2); }
 
-// The cursor to tile L (-1: the stream has ended).
+// The cursor to unit u (without a tile: the stream has ended).
 template <class C, class P>
-__device__ __forceinline__ void f8_seek(const P& p, int L, F8Cursor& c, F8Load& ld,
+__device__ __forceinline__ void f8_seek(const P& p, const F8Unit& u, F8Cursor& c, F8Load& ld,
                                         uint32_t (&off)[2], uint32_t& s_off, int wave, int lane) {
   c.s = c.steps = c.real = 0;
-  if (L >= 0) {
-    const typename P::Tile t = p.tile(L, c.hint);
+  if (u.tile >= 0) {
+    const typename P::Tile t = f8_unit<C>(p, u, c.hint);
     c.hint = uni(t.hint);
     c.real = uni(t.steps);
     c.steps = f8_steps(c.real);
@@ -494,13 +555,14 @@ __device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restric
   const int wave = uni(tid >> 6), wm = wave / C::WN, wn = wave % C::WN;
   TgTiles q;
   q.init(tiles, nullptr);
+  const F8Units<C> units(q);
   int mine = q.own;
-  int L = q.at(q.x, mine);
-  if (L < 0) return;
+  F8Unit u = units.at(mine);
+  if (u.tile < 0) return;
   F8Cursor c{};
   F8Load ld{};
   uint32_t off[2] = {}, s_off = 0;
-  f8_seek<C>(p, L, c, ld, off, s_off, wave, lane);
+  f8_seek<C>(p, u, c, ld, off, s_off, wave, lane);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     f8_ready(c, ld, lane, off);
@@ -511,11 +573,11 @@ __device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restric
   }
   pipe_sync();
   int ph = 0;  // ring slot of the next k-step
-  int L1 = -1;
-  auto next = [&]() -> int { return L1 = q.at(q.x, mine += q.blocks(q.x)); };
+  F8Unit u1{-1, 1, 0};
+  auto next = [&]() -> F8Unit { return u1 = units.at(mine += units.blocks); };
   int hint = 0;
   while (true) {
-    const typename P::Tile t = p.tile(L, hint);
+    const typename P::Tile t = f8_unit<C>(p, u, hint);
     hint = t.hint;
     f32x16 acc[C::FM][C::FN];
 #pragma unroll
@@ -535,8 +597,8 @@ __device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restric
     // every fragment read of the next tile's loop would wait for loads
     MOE_WAIT_VMCNT(0);
     p.store(t, wm, wn, lane, acc);
-    if (L1 < 0) break;
-    L = L1;
+    if (u1.tile < 0) break;
+    u = u1;
   }
 }
 

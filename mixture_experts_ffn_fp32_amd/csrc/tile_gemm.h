@@ -475,6 +475,10 @@ struct TgTiles {
     const int a = (int)((long long)n * xcd / X), b = (int)((long long)n * (xcd + 1) / X);
     return j < b - a ? a + j : -1;
   }
+  // Its tiles.
+  __device__ __forceinline__ int count(int xcd) const {
+    return (int)((long long)n * (xcd + 1) / X) - (int)((long long)n * xcd / X);
+  }
   __device__ __forceinline__ void init(int tiles, int32_t* c) {
     n = tiles;
     counters = c;

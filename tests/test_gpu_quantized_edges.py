@@ -41,6 +41,22 @@ def test_every_kind_of_tail(length, dx):
             within(call(x, xs, w, ws, None, DT[out]), want, tol + STORE[out] * (np.abs(want) + tol), out)
 
 
+@pytest.mark.parametrize("dx", [False, True])
+@pytest.mark.parametrize("M,E,width", [(4096, 1, 4200), (4400, 3, 4000), (4500, 2, 3900), (5200, 4, 4200),
+                                       (5700, 9, 4096), (6300, 5, 4004), (4100, 30, 1408)])
+def test_last_rounds_of_few_tiles(M, E, width, dx):
+    """One round of 256 x 256 tiles and some: the rest is cut to halves or quarters, some of which
+    lie outside their group or the matrix.  A given out keeps the rows outside the groups."""
+    n, k = (160, width) if dx else (width, 160)
+    offsets = _ragged(M, E, M, 3)
+    x, xs, w, ws, off, y = _product_check(M, E, n, k, offsets, dx, "e4m3", "bf16", "few tiles left")
+    call = mx.grouped_matmul_quantized_dx if dx else mx.grouped_matmul_quantized
+    out = torch.full_like(y, 7.0)
+    call(x, xs, w, ws, off, out=out)
+    assert torch.equal(out[:offsets[-1]], y[:offsets[-1]]) and (out[offsets[-1]:] == 7).all()
+    _product_check(M, E, n, k, offsets, dx, "e5m2", "bf16", "few tiles left", 1)
+
+
 def test_product_of_rows_past_4_gib():
     """x past 2^32 bytes and, behind it, results: the last rows are as those of a small call."""
     M, n, k = (1 << 21) + 4096, 16, 2064
