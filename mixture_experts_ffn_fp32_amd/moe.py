@@ -603,7 +603,7 @@ def _rms_norm(x, weight, residual, eps, q_dtype, h_out, out):
         h = h_out
         if h is None and residual is not None:
             h = torch.empty_like(x)
-        y = torch.empty((T, d), dtype=q_dtype or x.dtype, device=dev) if out is None else out
+        y = torch.empty_like(x, dtype=q_dtype) if out is None else out
         scales = None
         if q_dtype is not None:
             scales = torch.empty((T, _f8_blocks(d)), dtype=torch.float32, device=dev)
@@ -660,7 +660,7 @@ def quantize_rows(x, q_dtype=torch.float8_e4m3fn):
     dt, qt = _dtype_code(x), _f8_code("q_dtype", q_dtype)
     dev = _operands(x)
     with _on(dev):
-        q = torch.empty((T, d), dtype=q_dtype, device=dev)
+        q = torch.empty_like(x, dtype=q_dtype)
         scales = torch.empty((T, _f8_blocks(d)), dtype=torch.float32, device=dev)
         _check(L.moe_quantize_rows(_p(x), T, d, dt, qt, _p(q), _p(scales), _stream_of(dev)))
     return q, scales
@@ -674,7 +674,7 @@ def quantize_blocks(w, q_dtype=torch.float8_e4m3fn):
     dt, qt = _dtype_code(w), _f8_code("q_dtype", q_dtype)
     dev = _operands(w)
     with _on(dev):
-        q = torch.empty((E, n, k), dtype=q_dtype, device=dev)
+        q = torch.empty_like(w, dtype=q_dtype)
         scales = torch.empty((E, _f8_blocks(n), _f8_blocks(k)), dtype=torch.float32, device=dev)
         _check(L.moe_quantize_blocks(_p(w), E, n, k, dt, qt, _p(q), _p(scales), _stream_of(dev)))
     return q, scales
@@ -690,7 +690,7 @@ def dequantize_rows(q, scales, dtype=torch.bfloat16):
     _typed("scales", scales, torch.float32, (T, _f8_blocks(d)))
     dev = _operands(q, scales)
     with _on(dev):
-        x = torch.empty((T, d), dtype=dtype, device=dev)
+        x = torch.empty_like(q, dtype=dtype)
         _check(L.moe_dequantize_rows(_p(q), _p(scales), T, d, qt, _DTYPES[dtype], _p(x),
                                      _stream_of(dev)))
     return x
@@ -797,7 +797,7 @@ def balance_loss_backward(scores, slopes, dlosses=None, offsets=None, mask=None)
     _typed("dlosses", dlosses, torch.float32, (S, 2))
     dev = _operands(scores, slopes, dlosses, offsets, mask)
     with _on(dev):
-        dlogits = torch.empty((T, N), dtype=torch.float32, device=dev)
+        dlogits = torch.empty_like(scores)
         _check(L.moe_balance_loss_backward(_p(scores), _p(slopes), _p(dlosses), _p(offsets),
                                            _p(mask), T, N, S, _p(dlogits), _stream_of(dev)))
     return dlogits
