@@ -19,7 +19,14 @@
 // One launch covers every group, as in grouped.hip.  Operands are read where they are: rows end
 // inside their last k-step by loads that lie outside every range, w is read along k or, for dx,
 // across it.  Rows whose length is no whole number of 16 bytes are copied to ones that are first.
-
+//
+// Measured (the same products in one library call without scales: 2600 TFLOP/s at 8192^3; copy 5.1
+// TB/s): y of 8192^3 1880 TFLOP/s, dx 1950, y with k = 16384 2000 to 2250; float32 results 1000.
+// 49152 rows in 64 uneven groups, 1408 x 2048, 200 us (1420 TFLOP/s, MFMAs busy 33% at 2.15 GHz: five
+// rounds of 256^2 tiles and a cut one); dx of 28672 rows in 63, 896 x 1280, from e5m2, 61 us (1080
+// TFLOP/s, busy 23% at 2.43 GHz: k-steps are seven a tile, results 73 MB); 384 rows in 64 groups, 2048
+// x 1408, 39.4 us (4.75 TB/s, every weight once); 1021 rows in 16 groups, 136 x 267, float32, 3.6 us
+// for the copies and 7.7.
 #include <algorithm>
 
 #include "groups.h"
@@ -278,10 +285,11 @@ hipError_t run_f8(const F8Product& p, const GroupedF8Args& a, hipStream_t st) {
 // Which tiles.  256^2 against 128^2 (bfloat16 results; one block per CU against two) by the time
 // that the expected tiles take at the measured rates, us per tile: 1.9 a k-step and 6 for its
 // start and its results, against 1.35 and 4 for two at once; a CU has one tile at least.
-// Measured, 256 | 128: 49152 rows in 64 uneven groups, 1408 x 2048, 207 | 227 us; dx of 28672 rows
-// in 63, 896 x 1280, 67 | 76; y of 4096^3 76 | 99; y of 64 groups of 128 rows, 1408 x 2048, 56 | 44,
-// of 64 rows 48 | 38; dx of 256 rows there 73 | 85; y of 4096 rows, 2048 x 2048, 36 | 28.  (Wrong by
-// most where groups just fill tiles: y of 200 and 256 rows there, 77 | 65 and 85 | 76.)
+// Measured, 256 | 128: 49152 rows in 64 uneven groups, 1408 x 2048, 200 | 227 us; dx of 28672 rows
+// in 63, 896 x 1280, 61 | 76; y of 4096^3 72 | 91; y of 64 groups of 64, 128, 160 and 256 rows, 1408 x
+// 2048, 48 | 39, 50 | 46, 60 | 72 and 64 | 72 us, dx 42 | 38, 46 | 44, 57 | 71 and 64 | 85; y of 4096
+// rows, 2048 x 2048, 36 | 29.  (Wrong by most where 128^2 just start a second round: y of 4096 rows,
+// 2560 x 2048, 36 | 42.)
 // 64^2 where 128^2 give less than half of the CUs one: 128 | 64: y of 128 rows, 4096 x 4096 (32
 // tiles), 27 | 14 us; of one row, 2048 x 2048, 13 | 10; of 8 groups of 200 rows, 1024 x 1024 (128
 // tiles), 12 | 13; of 64 groups of 6 rows, 2048 x 1408, 33 | 51.

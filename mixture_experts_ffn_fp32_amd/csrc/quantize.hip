@@ -5,7 +5,12 @@
 //
 // Bound by HBM: every value is read once, held in registers until its block's largest is known,
 // and written once.  A row's block is one 16-byte chunk of 16 (bfloat16) or 32 (float32) lanes;
-// a matrix's block is a workgroup's 256 threads.
+// a matrix's block is a workgroup's 256 threads, each with its 16 (float32) or 8 chunks in flight.
+// The rounding to 8 bits is the operator's own; scales and quotients are float32.
+//
+// Measured: 28672 x 896 bfloat16 rows to e5m2 16.5 us (4.7 TB/s; 15.1 with the launches of calls
+// back to back overlapping); 64 matrices of 1408 x 2048 float32 160 us (5.8 TB/s: four of five bytes
+// are reads, which run above a copy's rate).
 #include <algorithm>
 
 #include "f8.h"
