@@ -18,15 +18,15 @@
 //
 // One launch covers every group, as in grouped.hip.  Operands are read where they are: rows end
 // inside their last k-step by loads that lie outside every range, w is read along k or, for dx,
-// across it.  Rows whose length is no whole number of 16 bytes are copied to ones that are first.
+// across it.  Rows whose length is no whole number of 16 bytes are copied to ones that are first,
+// or, where there are few tiles, read from any byte through registers.
 //
 // Measured (the same products in one library call without scales: 2600 TFLOP/s at 8192^3; copy 5.1
 // TB/s): y of 8192^3 1880 TFLOP/s, dx 1950, y with k = 16384 2000 to 2250; float32 results 1000.
 // 49152 rows in 64 uneven groups, 1408 x 2048, 200 us (1420 TFLOP/s, MFMAs busy 33% at 2.15 GHz: five
 // rounds of 256^2 tiles and a cut one); dx of 28672 rows in 63, 896 x 1280, from e5m2, 61 us (1080
 // TFLOP/s, busy 23% at 2.43 GHz: k-steps are seven a tile, results 73 MB); 384 rows in 64 groups, 2048
-// x 1408, 39.4 us (4.75 TB/s, every weight once); 1021 rows in 16 groups, 136 x 267, float32, 3.6 us
-// for the copies and 7.7.
+// x 1408, 39.4 us (4.75 TB/s, every weight once); 1021 rows in 16 groups, 136 x 267, float32, 9.5 us.
 #include <algorithm>
 
 #include "groups.h"
@@ -212,7 +212,6 @@ struct PadRows {
   int width;
   uint32_t pitch;
 };
-typedef uint32_t pad_u32 __attribute__((aligned(1)));
 __device__ __forceinline__ void pad_rows(const PadRows& a, unsigned block, unsigned blocks) {
   const long long per = a.pitch / 16, all = a.rows * per;
   for (long long i = (long long)block * 256 + threadIdx.x; i < all; i += (long long)blocks * 256) {
@@ -221,8 +220,7 @@ __device__ __forceinline__ void pad_rows(const PadRows& a, unsigned block, unsig
     const uint8_t* src = a.src + r * a.width;
     u32x4 v = {0u, 0u, 0u, 0u};
     if (j + 16 <= a.width) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = *(const pad_u32*)(src + j + 4 * e);
+      v = *(const u32x4_at1*)(src + j);
     } else {
 #pragma unroll
       for (int e = 0; e < 16; ++e)
@@ -246,37 +244,49 @@ hipError_t pad_two(const PadRows& a, const PadRows& b, hipStream_t st) {
 
 uint32_t pitch16(int width) { return ((uint32_t)width + 15) & ~15u; }
 
-// The workspace: copies of operands whose rows are no whole number of 16 bytes.
-struct F8Plan {
-  uint8_t *x = nullptr, *w = nullptr;
-  size_t bytes = 0;
-};
-F8Plan f8_plan(int M, int E, int n, int k, bool dx, void* ws) {
-  F8Plan p;
-  auto take = [&](size_t n) {
-    uint8_t* at = (uint8_t*)ws + p.bytes;
-    p.bytes += (n + 255) & ~size_t(255);
-    return at;
-  };
-  const int length = dx ? n : k;
-  if (length % 16 != 0) p.x = take((size_t)M * pitch16(length));
-  if (k % 16 != 0) p.w = take((size_t)E * n * pitch16(k));
-  return p;
-}
-
 // Tiles of b x b: at most (a launch's blocks), and as expected, half a tile's rows being left over
 // in a group.
 long long f8_most_tiles(const GroupedF8Args& a, int width, int b) {
   return (a.M / b + (long long)std::min(a.E, a.M)) * ((width + b - 1) / b);
 }
-double f8_tiles(const GroupedF8Args& a, int width, int b) {
-  const double groups = std::min(a.E, a.M);
-  const double rows = a.E == 1 ? (a.M + b - 1) / b : std::max(groups, (double)a.M / b + groups / 2);
+double f8_tiles(int M, int E, int width, int b) {
+  const double groups = std::min(E, M);
+  const double rows = E == 1 ? (M + b - 1LL) / b : std::max(groups, (double)M / b + groups / 2);
   return rows * ((width + b - 1) / b);
 }
-template <class Shape, int DIR, int Q, bool F32>
+
+// The workspace: copies of operands whose rows are no whole number of 16 bytes.  None where such
+// rows are read where they are, by 64^2 tiles: where 128^2 tiles would be fewer than half of a
+// card's 256 CUs, and where up to 64 rows per group read w about once, so that a copy of it is most of
+// the work, if the contraction gives each wavefront a k-step.  Measured, copied | read in place (us):
+// y of 16 groups of 64 rows, 136 x 267, 15 | 10; of 8 of 100, 1001 x 1501, 24 | 15; of 64 of 6, 2041 x
+// 1409, 119 | 74; of 64 of 64, 1409 x 2041, 153 | 81, dx 160 | 93; of 31 of 60, 777 x 777, 32 | 21.
+// Outside: y of 1900 rows, 1023 x 2047, 32 | 33, dx (240 tiles) 31 | 39; y of 8 of 300, 777 x 777, 25 | 28; of
+// 100 of 2, 2041 x 200 (two k-steps), 44 | 54; of 1000 of 1, 300 x 300, 86 | 96.
+struct F8Plan {
+  uint8_t *x = nullptr, *w = nullptr;
+  bool odd = false;
+  size_t bytes = 0;
+};
+F8Plan f8_plan(int M, int E, int n, int k, bool dx, void* ws) {
+  F8Plan p;
+  const int into = dx ? n : k;
+  p.odd = (into % 16 != 0 || k % 16 != 0) && into >= 16 && k >= 16 &&
+          (2 * f8_tiles(M, E, dx ? k : n, 128) < 256 || (M <= 64LL * E && f8_blocks(into) >= 4));
+  if (p.odd) return p;
+  auto take = [&](size_t n) {
+    uint8_t* at = (uint8_t*)ws + p.bytes;
+    p.bytes += (n + 255) & ~size_t(255);
+    return at;
+  };
+  if (into % 16 != 0) p.x = take((size_t)M * pitch16(into));
+  if (k % 16 != 0) p.w = take((size_t)E * n * pitch16(k));
+  return p;
+}
+
+template <class Shape, int DIR, int Q, bool F32, bool ODD = false>
 hipError_t run_f8(const F8Product& p, const GroupedF8Args& a, hipStream_t st) {
-  using C = F8Config<Shape, DIR == GR_DX, Q, F32>;
+  using C = F8Config<Shape, DIR == GR_DX, Q, F32, ODD>;
   const long long blocks = (long long)device_cu_count() * C::BPC;
   const long long tiles = f8_most_tiles(a, DIR == GR_DX ? a.k : a.n, C::BM);
   grouped_f8_kernel<C, DIR><<<(unsigned)std::max(1LL, std::min(tiles, blocks)), C::THREADS, 0, st>>>(p);
@@ -294,13 +304,17 @@ hipError_t run_f8(const F8Product& p, const GroupedF8Args& a, hipStream_t st) {
 // tiles), 27 | 14 us; of one row, 2048 x 2048, 13 | 10; of 8 groups of 200 rows, 1024 x 1024 (128
 // tiles), 12 | 13; of 64 groups of 6 rows, 2048 x 1408, 33 | 51.
 template <int DIR, int Q>
-hipError_t pick_f8(const F8Product& p, const GroupedF8Args& a, hipStream_t st) {
+hipError_t pick_f8(const F8Product& p, const GroupedF8Args& a, bool odd, hipStream_t st) {
   const double cus = device_cu_count();
   const int width = DIR == GR_DX ? a.k : a.n, steps = f8_blocks(DIR == GR_DX ? a.n : a.k);
-  const double big = std::max(1.0, f8_tiles(a, width, 256) / cus) * (1.9 * steps + 6);
-  const double mid = std::max(1.0, f8_tiles(a, width, 128) / (2 * cus)) * (1.35 * steps + 4);
+  if (odd)
+    return a.out_f32 ? run_f8<TgSmall, DIR, Q, true, true>(p, a, st)
+                     : run_f8<TgSmall, DIR, Q, false, true>(p, a, st);
+  const double few = f8_tiles(a.M, a.E, width, 256), more = f8_tiles(a.M, a.E, width, 128);
+  const double big = std::max(1.0, few / cus) * (1.9 * steps + 6);
+  const double mid = std::max(1.0, more / (2 * cus)) * (1.35 * steps + 4);
   if (!a.out_f32 && big < mid) return run_f8<TgBig, DIR, Q, false>(p, a, st);
-  if (2 * f8_tiles(a, width, 128) >= cus)
+  if (2 * more >= cus)
     return a.out_f32 ? run_f8<TgMid, DIR, Q, true>(p, a, st) : run_f8<TgMid, DIR, Q, false>(p, a, st);
   return a.out_f32 ? run_f8<TgSmall, DIR, Q, true>(p, a, st) : run_f8<TgSmall, DIR, Q, false>(p, a, st);
 }
@@ -339,8 +353,10 @@ hipError_t launch_grouped_f8(int f8, bool dx, const GroupedF8Args& a, void* ws, 
     }
   }
   if (dx)
-    return f8 == F8_E4M3 ? pick_f8<GR_DX, F8_E4M3>(p, a, st) : pick_f8<GR_DX, F8_E5M2>(p, a, st);
-  return f8 == F8_E4M3 ? pick_f8<GR_FWD, F8_E4M3>(p, a, st) : pick_f8<GR_FWD, F8_E5M2>(p, a, st);
+    return f8 == F8_E4M3 ? pick_f8<GR_DX, F8_E4M3>(p, a, plan.odd, st)
+                          : pick_f8<GR_DX, F8_E5M2>(p, a, plan.odd, st);
+  return f8 == F8_E4M3 ? pick_f8<GR_FWD, F8_E4M3>(p, a, plan.odd, st)
+                       : pick_f8<GR_FWD, F8_E5M2>(p, a, plan.odd, st);
 }
 
 }  // namespace moe

@@ -31,10 +31,10 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 // Q: x's type (w is e4m3); WCOL: w in column layout; EXACT: through bfloat16 (see
-// grouped_f8.hip).
-template <class Shape, bool WCOL_, int Q_, bool EXACT_>
+// grouped_f8.hip); ODD: rows start at any byte (TgSmall).
+template <class Shape, bool WCOL_, int Q_, bool EXACT_, bool ODD_ = false>
 struct F8Config : Shape {
-  static constexpr bool WCOL = WCOL_, EXACT = EXACT_, SWAP = true;
+  static constexpr bool WCOL = WCOL_, EXACT = EXACT_, SWAP = true, ODD = ODD_;
   static constexpr int Q = Q_;
   static constexpr bool SMALL = Shape::BM == TgSmall::BM;
   static constexpr int DATA = Shape::SLOT;                       // bytes of x and w in a slot,
@@ -608,6 +608,49 @@ __device__ __forceinline__ void f8_run(const P& p, int tiles, uint8_t* __restric
   }
 }
 
+// Rows of 16 bytes and more that start at any byte: load i of a k-step (f8_load) through
+// registers.  A chunk that the row's end cuts is read as the row's last 16 bytes and shifted
+// when it has landed (f8_odd_cut), so that no load waits for another.
+typedef u32x4 u32x4_at1 __attribute__((aligned(1)));
+struct F8Place {
+  int row, byte, end;  // the row's bytes end at `end`
+};
+template <class C, bool COL>
+__device__ __forceinline__ F8Place f8_odd_place(const F8Operand& o, int t0, int length, int s, int i,
+                                                int lane) {
+  if constexpr (COL) {
+    constexpr int W = C::BM, CPR = W / 16;
+    const int k = i * (1024 / W) + lane / CPR;
+    return F8Place{s * kF8Block + k, t0 + 16 * ((lane % CPR) ^ f8_rotation<W>(k)), o.width};
+  } else {
+    return F8Place{t0 + 8 * i + (lane >> 3), s * kF8Block + f8_chunk_byte(i & 1, lane), length};
+  }
+}
+template <class C, bool COL>
+__device__ __forceinline__ u32x4 f8_odd_load(const F8Operand& o, int t0, int length, int s, int i,
+                                             int lane) {
+  const F8Place at = f8_odd_place<C, COL>(o, t0, length, s, i, lane);
+  return *(const u32x4_at1*)(o.p + (size_t)min(at.row, o.rows - 1) * o.pitch +
+                             min(at.byte, at.end - 16));
+}
+template <class C, bool COL>
+__device__ __forceinline__ u32x4 f8_odd_cut(u32x4 v, const F8Operand& o, int t0, int length, int s,
+                                            int i, int lane) {
+  const F8Place at = f8_odd_place<C, COL>(o, t0, length, s, i, lane);
+  const int valid = at.row < o.rows ? min(max(at.end - at.byte, 0), 16) : 0;
+  const int shift = 8 * (16 - valid);  // bits
+  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  if (shift >= 64) {
+    lo = hi;
+    hi = 0;
+  }
+  const int b = shift & 63;
+  lo = lo >> b | (b > 0 ? hi << (64 - b) : 0);
+  hi >>= b;
+  if (shift >= 128) lo = 0;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 // The same for TgSmall: the k-steps dealt to the four wavefronts, each with a ring of its own
 // (as tg_run_small).
 template <class C>
@@ -654,11 +697,43 @@ __device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __r
 #pragma unroll
       for (int k = 0; k < C::LOADS; ++k) f8_load<C>(fw, lw, k, ow, sw, slot, 1);
     };
-    issue(0, ring);
-    issue(1, ring + C::SLOT);
+    // ODD: through registers, as loads that go straight to LDS take whole words only
+    u32x4 vx[NI], vw[NI];
+    float fx = 0.f, fw = 0.f;
+    auto fetch = [&](int i) {
+      if (i >= mine) return;
+      const int s = wave + W * i;
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        vx[k] = f8_odd_load<C, false>(t.X, t.m0, t.length, s, k, lane);
+        vw[k] = f8_odd_load<C, C::WCOL>(t.W, t.n0, t.length, s, k, lane);
+      }
+      fx = *(const float*)(lx.scales + (size_t)s * lx.s_step + sx);
+      fw = *(const float*)(lw.scales + (size_t)s * lw.s_step + sw);
+    };
+    if constexpr (C::ODD) {
+      fetch(0);
+    } else {
+      issue(0, ring);
+      issue(1, ring + C::SLOT);
+    }
     for (int i = 0; i < mine; ++i) {
       uint8_t* slot = ring + (i & 1) * C::SLOT;
-      MOE_WAIT_VMCNT(2 * NI + 2);  // this k-step has landed, the next one may be in flight
+      if constexpr (C::ODD) {
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+          const int s = wave + W * i;
+          *(u32x4*)(slot + k * 1024 + lane * 16) =
+              f8_odd_cut<C, false>(vx[k], t.X, t.m0, t.length, s, k, lane);
+          *(u32x4*)(slot + (NI + k) * 1024 + lane * 16) =
+              f8_odd_cut<C, C::WCOL>(vw[k], t.W, t.n0, t.length, s, k, lane);
+        }
+        *(float*)(slot + C::DATA + lane * 4) = fx;
+        *(float*)(slot + C::DATA + 256 + lane * 4) = fw;
+        MOE_WAIT_LGKMCNT0();
+      } else {
+        MOE_WAIT_VMCNT(2 * NI + 2);  // this k-step has landed, the next one may be in flight
+      }
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
       F8Frag x[2], w[2];
@@ -671,7 +746,8 @@ __device__ __forceinline__ void f8_run_small(const P& p, int tiles, uint8_t* __r
       MOE_WAIT_LGKMCNT0();
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      issue(i + 2, slot);
+      if constexpr (C::ODD) fetch(i + 1);
+      else issue(i + 2, slot);
 #pragma unroll
       for (int fn = 0; fn < 2; ++fn)
 #pragma unroll

@@ -42,6 +42,25 @@ def test_every_kind_of_tail(length, dx):
 
 
 @pytest.mark.parametrize("dx", [False, True])
+@pytest.mark.parametrize("M,E,n,k", [(200, 40, 601, 1001), (90, 30, 1409, 519), (64, 1, 17, 31), (1, 1, 16, 17),
+                                     (7, 2, 31, 16), (30, 3, 2000, 2047), (130, 2, 515, 16), (640, 10, 517, 530)])
+def test_odd_rows_read_in_place(M, E, n, k, dx):
+    """Rows that start at any byte, few of them per group; every operand ends with its tensor."""
+    off = _ragged(M, E, M)
+    _product_check(M, E, n, k, off, dx, "e4m3", "f32", "in place")
+    x, xs, w, ws, o, y = _product_check(M, E, n, k, off, dx, "e5m2", "bf16", "in place", 3)
+    # what lies before and behind the operands in memory reaches no result
+    call = mx.grouped_matmul_quantized_dx if dx else mx.grouped_matmul_quantized
+
+    def inside(t):
+        big = torch.full((t.numel() + 64,), 0x7f, dtype=torch.uint8, device="cuda")
+        big[32:32 + t.numel()] = t.view(torch.uint8).reshape(-1)
+        return big[32:32 + t.numel()].view(t.dtype).view(t.shape)
+
+    assert torch.equal(call(inside(x), xs, inside(w), ws, o), y)
+
+
+@pytest.mark.parametrize("dx", [False, True])
 @pytest.mark.parametrize("M,E,width", [(4096, 1, 4200), (4400, 3, 4000), (4500, 2, 3900), (5200, 4, 4200),
                                        (5700, 9, 4096), (6300, 5, 4004), (4100, 30, 1408)])
 def test_last_rounds_of_few_tiles(M, E, width, dx):
@@ -167,9 +186,9 @@ def test_infinities_of_e5m2_rows(out):
                                                 (sign * np.inf)[sign != 0])
 
 
-def test_two_calls_at_once():
+@pytest.mark.parametrize("M,E,n,k", [(600, 3, 270, 333), (5000, 3, 1030, 333)])
+def test_two_calls_at_once(M, E, n, k):
     """The same operands on two streams, each call with a workspace of its own."""
-    M, E, n, k = 600, 3, 270, 333
     x, xs, w, ws, off, y = _product_check(M, E, n, k, _ragged(M, E, 1), False, "e4m3", "bf16", "one call")
     s, idx = _routing(3000, 64, 6, 1)
     s, idx = dev(s), torch.from_numpy(idx).cuda()
@@ -186,14 +205,14 @@ def test_two_calls_at_once():
         assert torch.equal(yy, y) and all(torch.equal(bb[i], b[i]) for i in b)
 
 
-def test_padded_operands_in_a_graph():
-    """Rows of no whole number of 16 bytes are copied to a workspace first: captured, replayed on
-    new inputs with eager calls in between, two graphs with one workspace in turn."""
-    M, E, n, k = 300, 2, 136, 267
-    ws_ = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+@pytest.mark.parametrize("M,E,n,k", [(300, 2, 136, 267), (9000, 2, 1100, 267)])
+def test_odd_operands_in_a_graph(M, E, n, k):
+    """Rows of no whole number of 16 bytes, read in place or copied to a workspace first: captured,
+    replayed on new inputs with eager calls in between, two graphs with one workspace in turn."""
+    ws_ = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
     t = dict(zip(("x", "xs"), _quantized((M, k), 1, "e4m3")))
     t |= dict(zip(("w", "ws"), _quantized((E, n, k), 2, "e4m3", True)))
-    t |= dict(zip(("dy", "dys"), _quantized((M, n), 3, "e5m2")), off=ints([0, 170, 300]))
+    t |= dict(zip(("dy", "dys"), _quantized((M, n), 3, "e5m2")), off=ints([0, M // 2 + 20, M]))
 
     def step(**kw):
         return [mx.grouped_matmul_quantized(t["x"], t["xs"], t["w"], t["ws"], t["off"], **kw),
