@@ -30,52 +30,56 @@ namespace {
 
 constexpr int kBlRows = 64;
 
-// Partial sums of one chunk of a sequence: block b takes the b-th chunk of kBlRows rows.  The
-// loads of a thread's column (every 512 / NP-th row) are made eight at a time, whatever the
-// mask says; a masked row's are left out of the sum.
+// Partial sums of the chunks of kBlRows rows of the sequences, chunk b in partial row b: one chunk
+// a block, and past kBlMostBlocks, as a launch holds fewer than 2^32 threads, each block takes
+// further ones.  The loads of a thread's column (every 512 / NP-th row) are made eight at a time,
+// whatever the mask says; a masked row's are left out of the sum.
 constexpr int kBlThreads = 512;
+constexpr long long kBlMostBlocks = 1 << 20;
 __global__ __launch_bounds__(kBlThreads) void balance_loss_partial_kernel(BalanceLossArgs a) {
   __shared__ GroupTables t;
   __shared__ int cnt[256], valid[kBlRows];
   __shared__ double sum[kBlThreads];
   const int tid = threadIdx.x, N = a.N;
   group_tables<GR_FWD>(GroupDims{a.T, a.S, 0, 0}, a.offsets, kBlRows, t);
-  const int b = blockIdx.x;
-  if (b >= t.tiles[a.S]) return;
-  const int s = group_of(t.tiles, a.S, b, 0);
-  const int t0 = t.off[s] + (b - t.tiles[s]) * kBlRows, rows = min(kBlRows, t.off[s + 1] - t0);
-  if (tid < 256) cnt[tid] = 0;
-  if (tid < kBlRows) valid[tid] = tid < rows && (a.mask == nullptr || a.mask[t0 + tid] != 0);
-  __syncthreads();
-  for (int j = tid; j < rows * a.K; j += kBlThreads) {
-    const int e = a.idx[(size_t)t0 * a.K + j];
-    if (valid[j / a.K] && (unsigned)e < (unsigned)N) atomicAdd(&cnt[e], 1);
-  }
-  // kBlThreads / NP rows at a time, NP columns each
-  const int NP = N <= 64 ? 64 : N <= 128 ? 128 : 256, G = kBlThreads / NP;
-  const int c = tid & (NP - 1), g = tid / NP;
-  double p = 0.0;
-  if (c < N) {
-    const float* from = a.scores + (size_t)t0 * N + c;
-    for (int r0 = g; r0 < rows; r0 += 8 * G) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = from[(size_t)min(r0 + i * G, rows - 1) * N];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (r0 + i * G < rows && valid[r0 + i * G]) p += (double)v[i];
+  const int chunks = uni(t.tiles[a.S]);
+  for (int b = blockIdx.x; b < chunks; b += gridDim.x) {
+    const int s = group_of(t.tiles, a.S, b, 0);
+    const int t0 = t.off[s] + (b - t.tiles[s]) * kBlRows, rows = min(kBlRows, t.off[s + 1] - t0);
+    if (tid < 256) cnt[tid] = 0;
+    if (tid < kBlRows) valid[tid] = tid < rows && (a.mask == nullptr || a.mask[t0 + tid] != 0);
+    __syncthreads();
+    for (int j = tid; j < rows * a.K; j += kBlThreads) {
+      const int e = a.idx[(size_t)t0 * a.K + j];
+      if (valid[j / a.K] && (unsigned)e < (unsigned)N) atomicAdd(&cnt[e], 1);
     }
-  }
-  sum[tid] = p;
-  __syncthreads();
-  if (tid < N) {
-    for (int q = NP; q < kBlThreads; q += NP) p += sum[q + tid];
-    a.psum[(size_t)b * N + tid] = p;
-    a.pcnt[(size_t)b * (N + 1) + tid] = cnt[tid];
-  }
-  if (tid < 64) {
-    const int n = __popcll(__ballot(valid[tid] != 0));
-    if (tid == 0) a.pcnt[(size_t)b * (N + 1) + N] = n;
+    // kBlThreads / NP rows at a time, NP columns each
+    const int NP = N <= 64 ? 64 : N <= 128 ? 128 : 256, G = kBlThreads / NP;
+    const int c = tid & (NP - 1), g = tid / NP;
+    double p = 0.0;
+    if (c < N) {
+      const float* from = a.scores + (size_t)t0 * N + c;
+      for (int r0 = g; r0 < rows; r0 += 8 * G) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = from[(size_t)min(r0 + i * G, rows - 1) * N];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + i * G < rows && valid[r0 + i * G]) p += (double)v[i];
+      }
+    }
+    sum[tid] = p;
+    __syncthreads();
+    if (tid < N) {
+      for (int q = NP; q < kBlThreads; q += NP) p += sum[q + tid];
+      a.psum[(size_t)b * N + tid] = p;
+      a.pcnt[(size_t)b * (N + 1) + tid] = cnt[tid];
+    }
+    if (tid < 64) {
+      const int n = __popcll(__ballot(valid[tid] != 0));
+      if (tid == 0) a.pcnt[(size_t)b * (N + 1) + N] = n;
+    }
+    __syncthreads();  // the next chunk's counts and rows
   }
 }
 static_assert(kBlRows == 64, "a wavefront counts a chunk's rows");
@@ -252,7 +256,8 @@ hipError_t launch_balance_loss(BalanceLossArgs a, void* ws, hipStream_t st) {
   a.psum = (double*)ws;
   a.pcnt = (int32_t*)((char*)ws + align256((size_t)chunks * a.N * 8));
   if (a.T > 0) {
-    balance_loss_partial_kernel<<<(unsigned)chunks, kBlThreads, 0, st>>>(a);
+    const unsigned blocks = (unsigned)std::min(chunks, kBlMostBlocks);
+    balance_loss_partial_kernel<<<blocks, kBlThreads, 0, st>>>(a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   balance_loss_final_kernel<<<a.S, 1024, 0, st>>>(a);
