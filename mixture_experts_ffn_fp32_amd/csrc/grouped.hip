@@ -108,7 +108,7 @@ struct GroupedTiles {
       t.B.p = p.B + (size_t)t.row0 * p.pitch_b;
       t.B.rows = t.size;
       t.B.width = (g.k + 31) & ~31;
-      t.steps = (t.size + C::KS - 1) / C::KS;
+      t.steps = t.size / C::KS + (t.size % C::KS != 0);
     } else {
       t.B.p = p.B + (size_t)t.hint * g.n * p.pitch_b;
       t.B.rows = g.n;

@@ -115,7 +115,7 @@ struct F8Tiles {
         f8_quad_transpose(c, lane);
         const int n = t.n0 + 32 * (C::column(fn) + C::first(wn)) + 16 * (lane & 3) + 8 * (lane >> 5);
         if (n >= t.n0 + t.cols) continue;
-        uint16_t* to = (uint16_t*)p.out + (size_t)(t.row0 + t.m0 + m) * N + n;
+        uint16_t* to = (uint16_t*)p.out + ((size_t)t.row0 + (t.m0 + m)) * N + n;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (m + i < t.rows) *(u32x4*)(to + (size_t)i * N) = c[i];

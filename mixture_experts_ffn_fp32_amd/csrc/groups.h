@@ -20,8 +20,9 @@ struct GroupTables {
 };
 
 template <int DIR>
-__device__ __forceinline__ int group_tiles(const GroupDims& g, int rows, int bm) {
-  return ((DIR == GR_DW ? (rows > 0 ? g.n : 0) : rows) + bm - 1) / bm;
+__host__ __device__ __forceinline__ int group_tiles(const GroupDims& g, int rows, int bm) {
+  const int v = DIR == GR_DW ? (rows > 0 ? g.n : 0) : rows;  // (up to 2^31 - 1)
+  return v / bm + (v % bm != 0);
 }
 
 __device__ __forceinline__ int wave_prefix(int v, int lane) {  // inclusive

@@ -201,7 +201,9 @@ template <class C>
 __device__ __forceinline__ int tg_range(const TgLoad& l, int s) {
   if (l.rows < 0) return s < -l.rows ? 0x7fffffff : 0;
   if constexpr (C::PARTS == 3) s /= kTgProducts;
-  return min(max(l.rows - C::KS * s, 0), C::KS) * (int)l.pitch;
+  // (up to 2^31 - 1 rows, and k-steps of zeros behind them: their product may pass 2^31)
+  const int left = (int)((uint32_t)l.rows - (uint32_t)C::KS * (uint32_t)s);
+  return min(max(left, 0), C::KS) * (int)l.pitch;
 }
 
 __device__ __forceinline__ uint2 tg_read_tr(const uint8_t* p) {

@@ -1,0 +1,114 @@
+// Launch code of the operators beside the layer under sanitizers, on the CPU: their host objects
+// are linked with the few runtime calls below, which take a launch's sizes and run nothing.  Every
+// launch has to hold fewer than 2^32 threads along each of its sides (beyond, blocks are left
+// out without an error).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <initializer_list>
+#include <string>
+
+#include "groups.h"
+#include "moe.h"
+
+static int failures = 0;
+static std::string what, error;
+static long long launches = 0;
+static dim3 grid, block;
+
+namespace moe {
+void set_last_error(const char* msg) { error = msg; }
+}  // namespace moe
+
+extern "C" {
+hipError_t __hipPushCallConfiguration(dim3 g, dim3 b, size_t, hipStream_t) {
+  grid = g;
+  block = b;
+  return hipSuccess;
+}
+hipError_t __hipPopCallConfiguration(dim3* g, dim3* b, size_t* shared, hipStream_t* st) {
+  *g = grid;
+  *b = block;
+  *shared = 0;
+  *st = nullptr;
+  return hipSuccess;
+}
+hipError_t hipLaunchKernel(const void*, dim3 g, dim3 b, void**, size_t, hipStream_t) {
+  ++launches;
+  const uint64_t n[3] = {(uint64_t)g.x * b.x, (uint64_t)g.y * b.y, (uint64_t)g.z * b.z};
+  if (n[0] == 0 || n[1] == 0 || n[2] == 0 || (n[0] | n[1] | n[2]) >> 32 != 0 || g.y > 65535 || g.z > 65535 ||
+      b.x * b.y * b.z > 1024) {
+    printf("%s: %u x %u x %u blocks of %u x %u x %u threads\n", what.c_str(), g.x, g.y, g.z, b.x, b.y, b.z);
+    ++failures;
+  }
+  return hipSuccess;
+}
+void** __hipRegisterFatBinary(const void*) { return nullptr; }
+void __hipUnregisterFatBinary(void**) {}
+void __hipRegisterFunction(void**, const void*, char*, const char*, unsigned, void*, void*, dim3*, dim3*, int*) {}
+hipError_t hipGetLastError(void) { return hipSuccess; }
+const char* hipGetErrorString(hipError_t) { return ""; }
+hipError_t hipGetDevice(int* d) {
+  *d = 0;
+  return hipSuccess;
+}
+hipError_t hipDeviceGetAttribute(int* v, hipDeviceAttribute_t, int) {
+  *v = 256;
+  return hipSuccess;
+}
+}
+
+// Buffers of up to 2^40 bytes.
+static void* at(int i) { return (void*)((uintptr_t)(i + 1) << 40); }
+static float* fl(int i) { return (float*)at(i); }
+static int32_t* in(int i) { return (int32_t*)at(i); }
+
+static void took(int status, const std::string& call) {
+  if (status != MOE_OK) {
+    printf("%s: status %d (%s)\n", call.c_str(), status, error.c_str());
+    ++failures;
+  }
+}
+#define RUN(name, call)                                        \
+  do {                                                         \
+    what = name;                                               \
+    const long long before = launches;                         \
+    took(call, what);                                          \
+    if (launches == before) {                                  \
+      printf("%s: nothing was launched\n", what.c_str());      \
+      ++failures;                                              \
+    }                                                          \
+  } while (0)
+
+static const size_t kRoom = (size_t)1 << 40;
+static const int kMost = 2147483647;
+static std::string of(const char* name, std::initializer_list<long long> v) {
+  std::string s = name;
+  for (long long x : v) s += " " + std::to_string(x);
+  return s;
+}
+
+// Tiles of a group of any number of rows: none is lost, none too many.
+static void tiles() {
+  for (int bm : {32, 64, 128, 256})
+    for (long long rows : {0LL, 1LL, bm - 1LL, (long long)bm, bm + 1LL, kMost - 256LL, kMost - 255LL, kMost - 63LL,
+                           kMost - 1LL, (long long)kMost}) {
+      const int got = moe::group_tiles<moe::GR_FWD>(moe::GroupDims{kMost, 1, 16, 16}, (int)rows, bm);
+      if (got != (rows + bm - 1) / bm) {
+        printf("%lld rows in tiles of %d: %d\n", rows, bm, got);
+        ++failures;
+      }
+      const int w = moe::group_tiles<moe::GR_DW>(moe::GroupDims{kMost, 1, 1 << 20, 16}, (int)rows, bm);
+      if (w != (rows > 0 ? (1 << 20) / bm : 0)) ++failures;
+    }
+}
+
+int main(int argc, char** argv) {
+  for (int i = 1; i < argc; ++i) {
+    if (!strcmp(argv[i], "tiles")) tiles();
+  }
+  if (failures == 0) printf("ALL OK\n");
+  return failures != 0;
+}

@@ -44,3 +44,42 @@ def test_balance_loss_of_more_chunks_than_one_launch_has_blocks():
         row = scores[at0].double()
         assert torch.allclose(z[at0].double(), row * (slope - row @ slope), rtol=0, atol=8 * 2.0 ** -24 *
                               float(slope.max()))
+
+
+def _rows_of_the_most(M, k, dtype, seed):
+    """M rows of k zeros whose last ones are whole numbers, and those."""
+    tail = np.random.default_rng(seed).integers(-3, 4, size=(300, k))
+    x = torch.zeros((M, k), dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype, device="cuda").view(dtype)
+    last = torch.from_numpy(tail.astype(np.float32)).to(dtype).cuda()
+    (x.view(torch.uint8) if dtype == torch.float8_e4m3fn else x)[-300:] = (
+        last.view(torch.uint8) if dtype == torch.float8_e4m3fn else last)
+    return x, tail
+
+
+@pytest.mark.parametrize("dx", [False, True])
+def test_eight_bit_product_of_the_most_rows(dx):
+    """One group of 2^31 - 1 rows: its tiles are counted without an overflow."""
+    M, n, k = 2147483647, 16, 16
+    say(f"8-bit product of {M} rows dx={dx}")
+    x, tail = _rows_of_the_most(M, 16, torch.float8_e4m3fn, 1)
+    xs = torch.ones((M, 1), device="cuda")
+    wv = np.random.default_rng(2).integers(-3, 4, size=(n, k))
+    w = torch.from_numpy(wv[None].astype(np.float32)).to(torch.float8_e4m3fn).cuda()
+    call = mx.grouped_matmul_quantized_dx if dx else mx.grouped_matmul_quantized
+    out = torch.full((M, 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    call(x, xs, w, torch.ones((1, 1, 1), device="cuda"), None, out=out)
+    want = tail @ (wv if dx else wv.T)              # at most 144: exact in bfloat16
+    assert np.array_equal(out[-300:].float().cpu().numpy(), want)
+    for a in range(0, M - 300, 1 << 28):
+        assert not out[a:min(a + (1 << 28), M - 300)].any(), a
+
+
+def test_weight_gradient_of_the_most_rows():
+    """The same of bfloat16 rows: a contraction of 2^31 - 1 indices (y and dx of so many rows need
+    more memory than there is)."""
+    M, n = 2147483647, 8
+    say(f"weight gradient of {M} rows")
+    x, tail = _rows_of_the_most(M, n, torch.bfloat16, 3)
+    w = torch.zeros((1, n, n), dtype=torch.bfloat16, device="cuda")
+    _, dw = mx.grouped_matmul_backward(x, w, ints([0, M]), x, need_dx=False)
+    assert np.array_equal(dw[0].cpu().numpy(), tail.T @ tail)      # at most 2700: exact
