@@ -241,7 +241,7 @@ __global__ __launch_bounds__(256) void balance_loss_backward_kernel(BalanceLossA
   }
 }
 
-long long balance_loss_chunks(int T, int S) { return (T + kBlRows - 1LL) / kBlRows + S; }
+long long balance_loss_chunks(int T, int S) { return (T + (kBlRows - 1LL)) / kBlRows + S; }
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace

@@ -105,9 +105,30 @@ static void tiles() {
     }
 }
 
+static void balance() {
+  for (int T : {1, 64, 65, 1 << 29, kMost - 64, kMost - 63, kMost - 1, kMost})
+    for (int S : {1, 1024}) {
+      size_t bytes = 0;
+      took(moe_balance_loss_workspace_size(T, 3, S, &bytes), of("balance loss size", {T, S}));
+      const size_t chunks = ((size_t)T + 63) / 64 + S;
+      if (bytes < chunks * 40 || bytes > chunks * 40 + 256) {
+        printf("balance loss %d %d: %zu bytes for %zu chunks\n", T, S, bytes, chunks);
+        ++failures;
+      }
+    }
+  for (int T : {1, 64, 1 << 20, 1 << 26, (1 << 29) - 64, 1 << 29, kMost - 63, kMost})
+    for (int S : {1, 1024}) {
+      RUN(of("balance loss", {T, S}), moe_balance_loss(fl(0), in(1), in(2), 0, 0, T, 3, 1, S, 0, 1.f, 1.f, in(3), fl(4),
+                                                       fl(5), fl(6), at(7), kRoom, 0));
+      RUN(of("its gradient", {T, S}),
+          moe_balance_loss_backward(fl(0), fl(6), 0, in(2), 0, T, 3, S, fl(8), 0));
+    }
+}
+
 int main(int argc, char** argv) {
   for (int i = 1; i < argc; ++i) {
     if (!strcmp(argv[i], "tiles")) tiles();
+    if (!strcmp(argv[i], "balance")) balance();
   }
   if (failures == 0) printf("ALL OK\n");
   return failures != 0;

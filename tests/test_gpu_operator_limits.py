@@ -83,3 +83,16 @@ def test_weight_gradient_of_the_most_rows():
     w = torch.zeros((1, n, n), dtype=torch.bfloat16, device="cuda")
     _, dw = mx.grouped_matmul_backward(x, w, ints([0, M]), x, need_dx=False)
     assert np.array_equal(dw[0].cpu().numpy(), tail.T @ tail)      # at most 2700: exact
+
+
+def test_balance_loss_of_the_most_rows():
+    T = 2147483647
+    say(f"balance loss T={T}")
+    s = torch.ones((T, 1), device="cuda")
+    idx = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    b = mx.balance_loss(s, idx)
+    assert b["counts"].item() == T and b["P"].item() == 1 and b["losses"][0].tolist() == [1, 0]
+    assert b["slopes"][0, 0].item() == np.float32(1 / T)
+    z = mx.balance_loss_backward(s, b["slopes"])
+    for a in range(0, T, 1 << 28):
+        assert not z[a:a + (1 << 28)].any(), a              # s (c - s c) with s = 1
