@@ -275,7 +275,7 @@ F8Plan f8_plan(int M, int E, int n, int k, bool dx, void* ws) {
           (2 * f8_tiles(M, E, dx ? k : n, 128) < 256 || (M <= 64LL * E && f8_blocks(into) >= 4));
   if (p.odd) return p;
   auto take = [&](size_t n) {
-    uint8_t* at = (uint8_t*)ws + p.bytes;
+    uint8_t* at = ws != nullptr ? (uint8_t*)ws + p.bytes : nullptr;  // (NULL: sizes only)
     p.bytes += (n + 255) & ~size_t(255);
     return at;
   };

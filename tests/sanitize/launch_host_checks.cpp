@@ -125,10 +125,57 @@ static void balance() {
     }
 }
 
+static void products() {
+  const int Q = MOE_DTYPE_E4M3, R = MOE_DTYPE_E5M2, F = MOE_DTYPE_F32, B = MOE_DTYPE_BF16;
+  struct Shape {
+    int M, E, n, k;
+    size_t copy;  // bytes of the operands' copies: w's rows, for y
+  };
+  const Shape shapes[] = {{1, 1, 1, 1, 256 + 256}, {1, 1, 2048, 2048, 0}, {1021, 16, 136, 267, 0},
+                          {20000, 1, 8, 8, 20000 * 16 + 256}, {49152, 64, 1408, 2048, 0},
+                          {9000, 2, 1100, 267, 9000 * 272 + 2 * 1100 * 272}, {kMost, 1024, 16, 16, 0}, {1 << 20, 1024, 64, 48, 0},
+                          {3, 1, 1 << 20, 1 << 20, 0}, {64, 1024, 1 << 20, 1, 0}};
+  for (const Shape& s : shapes)
+    for (int dx : {0, 1})
+      for (int x : {Q, R})
+        for (int out : {F, B}) {
+          const std::string name = of(dx ? "8-bit dx" : "8-bit y", {s.M, s.E, s.n, s.k});
+          size_t bytes = 0;
+          took(dx ? moe_grouped_matmul_quantized_dx_workspace_size(s.M, s.E, s.n, s.k, &bytes)
+                  : moe_grouped_matmul_quantized_workspace_size(s.M, s.E, s.n, s.k, &bytes), name);
+          // none for whole 16 bytes; else up to both operands' rows of whole 16 bytes
+          const int into = dx ? s.n : s.k;
+          const size_t most = (into % 16 ? (size_t)s.M * ((into + 15) / 16 * 16) + 255 : 0) +
+                              (s.k % 16 ? (size_t)s.E * s.n * ((s.k + 15) / 16 * 16) + 255 : 0);
+          if (bytes > most || (!dx && s.copy != 0 && bytes < s.copy - 512)) {
+            printf("%s: workspace of %zu bytes\n", name.c_str(), bytes);
+            ++failures;
+          }
+          if (bytes > kRoom) continue;
+          RUN(name, dx ? moe_grouped_matmul_quantized_dx(at(0), fl(1), at(2), fl(3), in(4), s.M, s.E, s.n, s.k, x, out, 1,
+                                                         at(5), at(6), kRoom, 0)
+                       : moe_grouped_matmul_quantized(at(0), fl(1), at(2), fl(3), in(4), s.M, s.E, s.n, s.k, x, out, 1,
+                                                      at(5), at(6), kRoom, 0));
+        }
+  for (const Shape& s : shapes)
+    for (int dt : {F, B}) {
+      const std::string name = of("grouped", {s.M, s.E, s.n, s.k, dt});
+      size_t bytes = 0;
+      took(moe_grouped_matmul_workspace_size(s.M, s.E, s.n, s.k, dt, &bytes), name);
+      if (bytes > kRoom || (size_t)s.E * s.n * s.k * 4 > kRoom) continue;
+      RUN(name, moe_grouped_matmul(at(0), at(1), in(2), s.M, s.E, s.n, s.k, dt, 1, at(3), at(4), kRoom, 0));
+      took(moe_grouped_matmul_backward_workspace_size(s.M, s.E, s.n, s.k, dt, 1, 1, &bytes), name);
+      if (bytes > kRoom) continue;
+      RUN(name + " gradients", moe_grouped_matmul_backward(at(0), at(1), in(2), at(3), s.M, s.E, s.n, s.k, dt, 1, at(4),
+                                                           fl(5), at(6), kRoom, 0));
+    }
+}
+
 int main(int argc, char** argv) {
   for (int i = 1; i < argc; ++i) {
     if (!strcmp(argv[i], "tiles")) tiles();
     if (!strcmp(argv[i], "balance")) balance();
+    if (!strcmp(argv[i], "products")) products();
   }
   if (failures == 0) printf("ALL OK\n");
   return failures != 0;
