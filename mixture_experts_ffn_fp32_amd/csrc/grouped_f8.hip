@@ -251,7 +251,7 @@ long long f8_most_tiles(const GroupedF8Args& a, int width, int b) {
 }
 double f8_tiles(int M, int E, int width, int b) {
   const double groups = std::min(E, M);
-  const double rows = E == 1 ? (M + b - 1LL) / b : std::max(groups, (double)M / b + groups / 2);
+  const double rows = E == 1 ? (M + (b - 1LL)) / b : std::max(groups, (double)M / b + groups / 2);
   return rows * ((width + b - 1) / b);
 }
 

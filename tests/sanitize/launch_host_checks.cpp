@@ -133,7 +133,8 @@ static void products() {
   };
   const Shape shapes[] = {{1, 1, 1, 1, 256 + 256}, {1, 1, 2048, 2048, 0}, {1021, 16, 136, 267, 0},
                           {20000, 1, 8, 8, 20000 * 16 + 256}, {49152, 64, 1408, 2048, 0},
-                          {9000, 2, 1100, 267, 9000 * 272 + 2 * 1100 * 272}, {kMost, 1024, 16, 16, 0}, {1 << 20, 1024, 64, 48, 0},
+                          {9000, 2, 1100, 267, 9000 * 272 + 2 * 1100 * 272}, {kMost, 1, 16, 16, 0},
+                          {kMost, 1024, 16, 16, 0}, {kMost, 1, 17, 17, 0}, {1 << 20, 1024, 64, 48, 0},
                           {3, 1, 1 << 20, 1 << 20, 0}, {64, 1024, 1 << 20, 1, 0}};
   for (const Shape& s : shapes)
     for (int dx : {0, 1})
