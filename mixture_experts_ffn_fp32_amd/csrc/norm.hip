@@ -276,7 +276,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormArgs a) {
   }
 }
 // Partial column sums of long_rows(T) rows: one thread per column.
-__host__ __device__ inline int long_rows(int T) { return T <= 64 * 1024 ? 64 : (T + 1023) / 1024; }
+__host__ __device__ inline int long_rows(int T) { return T <= 64 * 1024 ? 64 : (T - 1) / 1024 + 1; }
 template <class E>
 __global__ __launch_bounds__(256) void norm_cols_long_kernel(NormArgs a) {
   using T = typename E::T;
@@ -384,7 +384,7 @@ hipError_t launch_layer_norm(int dtype, const NormArgs& a, hipStream_t st) {
 
 int layer_norm_chunks(int dtype, int T, int d) {
   const NormPlan p = norm_plan(dtype, d);
-  if (p.nch == 0) return (T + long_rows(T) - 1) / long_rows(T);
+  if (p.nch == 0) return T == 0 ? 0 : (T - 1) / long_rows(T) + 1;
   return (int)norm_grid(p, T, kNormBwdBlocks);
 }
 

@@ -172,11 +172,55 @@ static void products() {
     }
 }
 
+static void rows() {
+  const int F = MOE_DTYPE_F32, B = MOE_DTYPE_BF16;
+  struct Shape {
+    int T, d;
+  };
+  for (const Shape& s : {Shape{1, 1}, {1, 1 << 24}, {4096, 8192}, {3001, 1283}, {70000, 20000}, {kMost, 1}, {kMost, 8},
+                         {kMost, 128}, {1 << 20, 1 << 17}, {(1 << 24) + 5, 2049}})
+    for (int dt : {F, B}) {
+      for (int q : {dt, (int)MOE_DTYPE_E4M3, (int)MOE_DTYPE_E5M2})
+        RUN(of("RMS norm", {s.T, s.d, dt, q}), moe_rms_norm(at(0), at(1), at(2), s.T, s.d, 0.f, dt, q, at(3), at(4),
+                                                            q == dt ? nullptr : fl(5), fl(6), 0));
+      RUN(of("RMS norm gradients", {s.T, s.d, dt}),
+          moe_rms_norm_backward(at(0), at(1), at(2), fl(3), at(4), s.T, s.d, dt, at(5), fl(6), at(7), kRoom, 0));
+      RUN(of("layer norm", {s.T, s.d, dt}), moe_layer_norm(at(0), at(1), at(2), s.T, s.d, 0.f, dt, at(3), fl(4), fl(5), 0));
+      RUN(of("layer norm gradients", {s.T, s.d, dt}),
+          moe_layer_norm_backward(at(0), at(1), at(2), fl(3), fl(4), s.T, s.d, dt, at(5), fl(6), fl(7), at(8), kRoom, 0));
+      for (int q : {MOE_DTYPE_E4M3, MOE_DTYPE_E5M2}) {
+        RUN(of("quantise", {s.T, s.d, dt}), moe_quantize_rows(at(0), s.T, s.d, dt, q, at(1), fl(2), 0));
+        RUN(of("read back", {s.T, s.d, dt}), moe_dequantize_rows(at(0), fl(1), s.T, s.d, q, dt, at(2), 0));
+      }
+    }
+  for (int T : {0, 1, 64 * 1024, 64 * 1024 + 1, kMost - 1023, kMost - 1, kMost})
+    for (int d : {1, 16384, 16385, 1 << 24})
+      for (int dt : {F, B}) {
+        size_t r = 0, l = 0;
+        took(moe_rms_norm_backward_workspace_size(T, d, dt, &r), of("RMS norm size", {T, d, dt}));
+        took(moe_layer_norm_backward_workspace_size(T, d, dt, &l), of("layer norm size", {T, d, dt}));
+        // partial rows of d (2 d) floats: none without rows, at most 1024
+        const size_t row = (size_t)d * 4;
+        if ((r == 0) != (T == 0) || r % row != 0 || r > 1024 * row || (l == 0) != (T == 0) || l % (2 * row) != 0 ||
+            l > 1024 * 2 * row) {
+          printf("partial rows of %d x %d: %zu and %zu bytes\n", T, d, r, l);
+          ++failures;
+        }
+      }
+  for (int q : {MOE_DTYPE_E4M3, MOE_DTYPE_E5M2})
+    for (int dt : {F, B}) {
+      RUN("quantise matrices", moe_quantize_blocks(at(0), 1 << 23, 1, 1, dt, q, at(1), fl(2), 0));
+      RUN("quantise matrices", moe_quantize_blocks(at(0), 1, 1 << 20, 1 << 17, dt, q, at(1), fl(2), 0));
+      RUN("quantise matrices", moe_quantize_blocks(at(0), 64, 1408, 2047, dt, q, at(1), fl(2), 0));
+    }
+}
+
 int main(int argc, char** argv) {
   for (int i = 1; i < argc; ++i) {
     if (!strcmp(argv[i], "tiles")) tiles();
     if (!strcmp(argv[i], "balance")) balance();
     if (!strcmp(argv[i], "products")) products();
+    if (!strcmp(argv[i], "rows")) rows();
   }
   if (failures == 0) printf("ALL OK\n");
   return failures != 0;

@@ -53,6 +53,6 @@ def checks(tmp_path_factory):
     return run
 
 
-@pytest.mark.parametrize("part", ["tiles", "balance", "products"])
+@pytest.mark.parametrize("part", ["tiles", "balance", "products", "rows"])
 def test_launches_and_plans(checks, part):
     checks(part)
