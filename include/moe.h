@@ -385,7 +385,8 @@ moe_status_t moe_dequantize_rows(const void* q, const float* scales, int T, int 
  *   y [M][n] out_dtype (MOE_DTYPE_F32 or _BF16).
  * Groups, offsets and zero_rest as in moe_grouped_matmul; offsets NULL with E = 1: one
  * group of all the rows.  Scales may be any float32 values; a product of two scales
- * below 2^-126 loses digits.  Exact products; a float32 result has float32 sums, a
+ * below 2^-126 loses digits, and results that one past float32's range reaches are summed
+ * again in float64.  Exact products; a float32 result has float32 sums, a
  * bfloat16 result sums in which eight neighbours along the contraction are added first,
  * each cut off 13 bits below the largest product of the eight (far below the
  * result's rounding, unless almost everything cancels).

@@ -45,6 +45,12 @@ __device__ __forceinline__ float f8_scaled(float v, const F8Scale& s) {
   const float q = v * s.inv;
   return fabsf(v) <= FLT_MAX ? fmaf(fmaf(-q, s.scale, v), s.inv, q) : __builtin_nanf("");
 }
+// The value of a byte, exactly.
+template <int Q>
+__device__ __forceinline__ float f8_value(uint32_t byte) {
+  if constexpr (Q == F8_E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
+  else return __builtin_amdgcn_cvt_f32_bf8((int)byte, 0);
+}
 // Four values, rounded to nearest even, lowest byte first.
 template <int Q>
 __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {

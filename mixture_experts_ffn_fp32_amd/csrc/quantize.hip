@@ -91,11 +91,6 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const typename E::
 }
 
 // Four columns a thread.
-template <int Q>
-__device__ __forceinline__ float f8_value(uint32_t byte) {
-  if constexpr (Q == F8_E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
-  else return __builtin_amdgcn_cvt_f32_bf8((int)byte, 0);
-}
 template <class E, int Q>
 __global__ __launch_bounds__(256) void dequantize_rows_kernel(const uint8_t* __restrict__ q,
                                                               const float* __restrict__ scales,
