@@ -12,8 +12,9 @@ pytestmark = pytest.mark.gpu
 
 mx = pytest.importorskip("mixture_experts_ffn_fp32_amd")
 
-# M, E, n, k: tiles of 64^2, odd rows in place, 128^2, copied odd rows, 256^2, 256^2 with a cut last round
-SHAPES = [(40, 2, 144, 272), (70, 1, 130, 261), (700, 3, 1040, 1040), (5000, 2, 1030, 1037), (5000, 3, 2064, 2064),
+# M, E, n, k: tiles of 64^2, odd rows in place, 64^2, copied odd rows in 128^2, 128^2, 256^2 and y of 256^2
+# with a cut last round (bfloat16 results)
+SHAPES = [(40, 2, 144, 272), (70, 1, 130, 261), (700, 3, 1040, 1040), (5000, 2, 1030, 1037), (5000, 3, 2064, 2064), (6000, 3, 2064, 2064),
           (5200, 4, 4208, 272)]
 TOP = {"f32": float(np.finfo(np.float32).max), "bf16": float(torch.finfo(torch.bfloat16).max)}
 
