@@ -362,14 +362,16 @@ moe_status_t moe_rms_norm_backward(const void* dy, const void* h, const void* we
 
 /* ---- 8 bits with a scale for each block of 128 ----
  *   scale = max |v| / most over the block's finite values (most: 448 or 57344; 1 for a
- *   block of zeros, never below 2^-126),  q = v / scale rounded to nearest even
+ *   block of zeros, never below 2^-126),  q = v / scale, the float32 quotient, rounded to
+ *   nearest even
  * A value that is not finite becomes NaN and leaves the others of its block alone.
  * Rows: x [T][d] dtype -> q [T][d] q_dtype, scales [T][ceil(d / 128)] float32, one for
  * each 128 columns of a row.  Any T >= 0; 1 <= d <= 2^24. */
 moe_status_t moe_quantize_rows(const void* x, int T, int d, int dtype, int q_dtype, void* q,
                                float* scales, void* stream);
 /* Matrices: w [E][n][k] dtype -> q [E][n][k] q_dtype, scales [E][ceil(n / 128)][ceil(k / 128)],
- * one for each 128 x 128 of a matrix.  E >= 0; n, k <= 2^20, at most 2^23 blocks. */
+ * one for each 128 x 128 of a matrix.  E >= 0; n, k <= 2^20, at most 2^23 blocks.  (The
+ * products below take matrices in MOE_DTYPE_E4M3.) */
 moe_status_t moe_quantize_blocks(const void* w, int E, int n, int k, int dtype, int q_dtype,
                                  void* q, float* scales, void* stream);
 /* Rows read back: x = q scale, rounded to dtype (for a weight gradient from rows that were
@@ -422,8 +424,8 @@ moe_status_t moe_grouped_matmul_quantized_dx(const void* dy, const float* dys, c
  * losses_s1 = 0.  A sequence without rows gives zeros.
  *   counts [S][N] int32; P [S][N], losses [S][2] float32;
  *   slopes [S][2][N] float32: d losses / d scores, the same in each of the n rows.
- * Sums are float64.  Limits: 1 <= K <= N <= 256, 1 <= S <= 1024, 0 <= D <= 256 (D >= 1
- * with device_of). */
+ * Sums are float64.  Limits: 1 <= K <= N <= 256, T K < 2^31, 1 <= S <= 1024, 0 <= D <= 256
+ * (D >= 1 with device_of). */
 moe_status_t moe_balance_loss_workspace_size(int T, int N, int S, size_t* bytes);
 moe_status_t moe_balance_loss(const float* scores, const int32_t* idx, const int32_t* offsets,
                               const uint8_t* mask, const int32_t* device_of, int T, int N, int K,

@@ -18,8 +18,8 @@
 // kBlRows rows (float64, counts as whole numbers), one that joins a sequence's partial sums in
 // order.  Backward: one launch, a wavefront per four rows.  Every sum has a fixed order.
 //
-// Measured: 4096 x 63 in one sequence 5.0, 4.6 and 5.1 us; 16384 x 128 in eight sequences (8 MB each
-// way) 7.6, 6.0 and 8.4 us (with loads row by row, and a wavefront per row, 32 us for the three).
+// Measured: 4096 x 63 in one sequence 5.1, 4.5 and 5.2 us; 16384 x 128 in eight sequences (8 MB each
+// way) 8.0, 5.7 and 8.3 us (with loads row by row, and a wavefront per row, 32 us for the three).
 #include <algorithm>
 
 #include "groups.h"

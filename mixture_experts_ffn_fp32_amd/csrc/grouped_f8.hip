@@ -26,7 +26,8 @@
 // or, where there are few tiles, read from any byte through registers.
 //
 // Measured (the same products in one library call without scales: 2600 TFLOP/s at 8192^3; copy 5.1
-// TB/s): y of 8192^3 1880 TFLOP/s, dx 1950, y with k = 16384 2000 to 2250; float32 results 1000.
+// TB/s): y of 8192^3 1880 to 2070 TFLOP/s, dx 1950 to 2110, y with k = 16384 2000 to 2250; float32 results
+// 960 and 980 (bfloat16 library product 1402), y of 49152 rows in 64 groups, 1408 x 2048, 327 us.
 // 49152 rows in 64 uneven groups, 1408 x 2048, 200 us (1420 TFLOP/s, MFMAs busy 33% at 2.15 GHz: five
 // rounds of 256^2 tiles and a cut one); dx of 28672 rows in 63, 896 x 1280, from e5m2, 61 us (1080
 // TFLOP/s, busy 23% at 2.43 GHz: k-steps are seven a tile, results 73 MB); 384 rows in 64 groups, 2048
@@ -319,7 +320,8 @@ double f8_tiles(int M, int E, int width, int b) {
 // y of 16 groups of 64 rows, 136 x 267, 15 | 10; of 8 of 100, 1001 x 1501, 24 | 15; of 64 of 6, 2041 x
 // 1409, 119 | 74; of 64 of 64, 1409 x 2041, 153 | 81, dx 160 | 93; of 31 of 60, 777 x 777, 32 | 21.
 // Outside: y of 1900 rows, 1023 x 2047, 32 | 33, dx (240 tiles) 31 | 39; y of 8 of 300, 777 x 777, 25 | 28; of
-// 100 of 2, 2041 x 200 (two k-steps), 44 | 54; of 1000 of 1, 300 x 300, 86 | 96.
+// 100 of 2, 2041 x 200 (two k-steps), 44 | 54; of 1000 of 1, 300 x 300, 86 | 96.  (256 and not the
+// device's count: a size asked for without a device, or on another one, has to hold.)
 struct F8Plan {
   uint8_t *x = nullptr, *w = nullptr;
   bool odd = false;

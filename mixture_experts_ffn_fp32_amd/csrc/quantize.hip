@@ -10,7 +10,7 @@
 //
 // Measured: 28672 x 896 bfloat16 rows to e5m2 16.5 us (4.7 TB/s; 15.1 with the launches of calls
 // back to back overlapping); 64 matrices of 1408 x 2048 float32 160 us (5.8 TB/s: four of five bytes
-// are reads, which run above a copy's rate).
+// are reads, which run above a copy's rate); 28672 x 896 e4m3 rows read back to bfloat16 15.6 us (5.0 TB/s).
 #include <algorithm>
 
 #include "f8.h"
